@@ -1,7 +1,7 @@
 /*
  * kda.h -- C ABI of libkda, the GB300 (sm_103a) KDA token-generation library.
  *
- * Two operations, each with variants:
+ * The KDA operations, each with variants:
  *   kda_decode     the Kimi Delta Attention decode recurrence over a
  *                  slot-indexed fp32 state pool, varlen tokens per request;
  *                  kda_decode_ex chooses the state layout (K-first or V-first)
@@ -11,6 +11,13 @@
  *                  fused projection, short convolutions, gates, recurrence,
  *                  gated output RMSNorm, output projection), n >= 1 tokens per
  *                  request; kda_block_tkg_static needs no caller workspace.
+ * and what a token-generation step runs next to them, for a model that keeps
+ * full-attention layers between its KDA layers and drafts its tokens:
+ *   kda_cache_append, kda_cache_read  K and V rows into a paged cache (bf16 or
+ *                  e4m3 with one scale per row) and back
+ *   kda_paged_attention  new tokens (one, a drafted window, a chunk) over it
+ *   kda_verify_draft  drafted tokens against the target's probabilities, from
+ *                  given uniform numbers
  *
  * Conventions shared by every call:
  *   - Every tensor pointer is a DEVICE pointer (cudaMalloc'd or equivalent),
@@ -60,7 +67,7 @@ typedef enum kda_status {
   KDA_ERR_NULL = -1,        /* a required pointer is NULL                         */
   KDA_ERR_SHAPE = -2,       /* a size is out of range or sizes are inconsistent  */
   KDA_ERR_UNSUPPORTED = -3, /* valid sizes this build does not implement         */
-  KDA_ERR_ENUM = -4,        /* unknown gate_mode, state_layout or output_dtype   */
+  KDA_ERR_ENUM = -4,        /* unknown gate_mode, state_layout, output or cache dtype */
   KDA_ERR_CUDA = -5,        /* a CUDA runtime call (launch) failed                */
   KDA_ERR_ALIGN = -6,       /* a pointer is not aligned as documented             */
   KDA_ERR_VALUE = -7,       /* a scalar argument is not finite / out of range     */
@@ -83,6 +90,9 @@ typedef enum kda_status {
                                 KDA_DEBUG_BOUNDS=1): an index the kernels derived fell outside
                                 its tensor; that access was skipped.  Never set by libkda.so,
                                 whose kernels carry no such checks.                              */
+#define KDA_DEV_BAD_PAGE 16  /* a page_table entry that a position needs is outside 0..num_pages-1 */
+#define KDA_DEV_BAD_TOKEN 32 /* a draft token outside 0..V-1: rejected where it stands            */
+#define KDA_DEV_BAD_PROB 64  /* weights to draw from that sum to zero or not to a finite number   */
 
 /*
  * kda_decode -- advance each request's recurrent state over its new tokens.
@@ -290,6 +300,146 @@ kda_status kda_block_tkg_static(float* out, const float* hidden, const float* ga
 /* Bytes of device workspace kda_block_tkg needs for these sizes (0 when the
  * sizes are invalid).  Host-only, no CUDA call. */
 size_t kda_block_tkg_workspace_size(int B, int n, int Hd, int nh, int K, int V, int Kc);
+
+/* ------------------------------------------------------------------------
+ * Paged K/V cache, attention over it, and verification of drafted tokens.
+ *
+ * A cache is two tensors [num_pages, HKV, page_size, D], K and V.  cache_dtype:
+ *   KDA_CACHE_BF16   bf16 rows; k_scale and v_scale are NULL.
+ *   KDA_CACHE_E4M3   e4m3 codes (8 bits) and fp32 scales [num_pages, HKV,
+ *                    page_size], one per row: the row is code * scale.
+ * D is 64 or 128, page_size 16, 32, 64 or 128.
+ *   page_table  [B, max_pages] int32: the page that holds request b's positions
+ *               i * page_size .. (i + 1) * page_size - 1.  Entries that no
+ *               position in use needs are not read.
+ *   cu_seqlens  [B + 1] int32: request b's new tokens are the packed rows
+ *               cu[b] .. cu[b+1]-1 (n_b of them, 0 allowed), cu[0] = 0, cu[B] = T.
+ *   seq_lens    [B] int32: positions in use, the new tokens' included: token i of
+ *               request b is at position seq_lens[b] - n_b + i.  A token at a
+ *               negative position is padding: it is not written to the cache and
+ *               attends to nothing.  0 <= seq_lens[b] <= max_pages * page_size.
+ * A request that breaks one of these sets KDA_DEV_BAD_SEQLEN and is skipped.
+ * A position whose page_table entry is outside 0..num_pages-1 sets
+ * KDA_DEV_BAD_PAGE: it is not written, reads back as zeros, and takes part in
+ * attention as a zero key and a zero value.
+ * ------------------------------------------------------------------------ */
+#define KDA_CACHE_BF16 0
+#define KDA_CACHE_E4M3 1
+
+/*
+ * kda_cache_append -- write the new tokens' K and V rows into the cache.
+ *
+ * KDA_CACHE_E4M3, per row of D entries x:
+ *   scale = max|x| / 448   (1 for a row of zeros; NaN for a row with an infinity
+ *                          or a NaN, which so reads back as NaN throughout)
+ *   code  = e4m3(x / scale)   both quotients rounded to nearest in fp32, the
+ *                             code to nearest even
+ * KDA_CACHE_BF16 rows are copied.
+ *
+ *   k, v         [T, HKV, D] bf16 with k_stride, v_stride elements between two
+ *                tokens (multiples of 8, at least HKV * D; views of a fused
+ *                projection's output need no copy).  Alignment 16 B.
+ *   k_cache, v_cache  written.  Alignment 16 B.   k_scale, v_scale  written.
+ *   seq_lens     the lengths WITH the new tokens.
+ * Rows of the cache that no new token names are left as they are.  Two tokens
+ * of one call must not name the same page row.
+ */
+kda_status kda_cache_append(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                            const kda_bf16* k, const kda_bf16* v, const int32_t* cu_seqlens,
+                            const int32_t* seq_lens, const int32_t* page_table, int cache_dtype,
+                            int B, int T, int HKV, int D, int page_size, int num_pages,
+                            int max_pages, long long k_stride, long long v_stride,
+                            int32_t* dev_status, void* stream);
+
+/*
+ * kda_cache_read -- rows of the cache back as dense bf16 rows.
+ *
+ *   k_rows, v_rows  [T, HKV, D] bf16, written: packed row cu_rows[b] + i is
+ *                request b's position starts[b] + i (e4m3: code * scale in fp32,
+ *                rounded to bf16).  Alignment 16 B.
+ *   cu_rows      [B + 1] int32 as cu_seqlens.
+ *   starts       [B] int32 first position of each request, or NULL for 0.
+ *                starts[b] + n_b <= max_pages * page_size, else KDA_DEV_BAD_SEQLEN;
+ *                the rows of a skipped request are zeroed.
+ */
+kda_status kda_cache_read(kda_bf16* k_rows, kda_bf16* v_rows, const void* k_cache,
+                          const void* v_cache, const float* k_scale, const float* v_scale,
+                          const int32_t* cu_rows, const int32_t* starts, const int32_t* page_table,
+                          int cache_dtype, int B, int T, int HKV, int D, int page_size,
+                          int num_pages, int max_pages, int32_t* dev_status, void* stream);
+
+/*
+ * kda_paged_attention -- softmax attention of the new tokens over the cache.
+ * The new tokens' own rows are read from the cache too: append them first.
+ *
+ * For token i of request b at position p = seq_lens[b] - n_b + i >= 0, query head
+ * h, key head h / (H / HKV):
+ *   x_j = scale * q . k_j  for the positions j it sees: 0 <= j < seq_lens[b], and
+ *         j <= p if causal, and j > p - window if window > 0
+ *   out = sum_j e^(x_j - m) v_j / sum_j e^(x_j - m),  m = max_j x_j
+ *   lse = ln sum_j e^(x_j)
+ * A token that sees nothing gets out = 0, lse = -inf.  Scores, sums and outputs
+ * are accumulated in fp32; the weights e^(x_j - m) are rounded to bf16 for the
+ * product with V.  What a position beyond seq_lens[b] or outside every token's
+ * window holds (not a number, an infinity) has no influence.
+ *
+ *   out          [T, H, D] bf16, written.  Alignment 16 B.
+ *   lse          [T, H] fp32, written, or NULL.
+ *   q            [T, H, D] bf16, q_stride elements between tokens (a multiple of
+ *                8, at least H * D).  Alignment 16 B.
+ *   max_tokens   no request has more new tokens than this (a host-side bound
+ *                that chooses the kernels; a request with more is skipped with
+ *                KDA_DEV_BAD_SEQLEN).
+ *   scale        finite.       causal  0 or 1.       window  >= 0 (0: none).
+ *   H            a multiple of HKV, at most 128 query heads per key head.
+ *   workspace    device scratch of kda_paged_attention_workspace_size(...)
+ *                bytes, 256-byte aligned, contents need not be initialised.
+ * The rows of a skipped request are not written.
+ */
+kda_status kda_paged_attention(kda_bf16* out, float* lse, const kda_bf16* q, const void* k_cache,
+                               const void* v_cache, const float* k_scale, const float* v_scale,
+                               const int32_t* cu_seqlens, const int32_t* seq_lens,
+                               const int32_t* page_table, float scale, int causal, int window,
+                               int cache_dtype, int B, int T, int max_tokens, int H, int HKV,
+                               int D, int page_size, int num_pages, int max_pages,
+                               long long q_stride, void* workspace, size_t workspace_bytes,
+                               int32_t* dev_status, void* stream);
+
+/* Bytes of device workspace kda_paged_attention needs for these sizes (0 when the
+ * sizes are invalid); it does not decrease in B, T or max_tokens.  Host-only, no
+ * CUDA call. */
+size_t kda_paged_attention_workspace_size(int B, int T, int max_tokens, int H, int HKV, int D);
+
+/*
+ * kda_verify_draft -- accept a prefix of each request's drafted tokens and draw
+ * the token after it, so that the tokens are distributed as the target's.
+ *
+ * Request b drafted n_b tokens x_0 .. x_{n_b-1} (0 allowed); the target's
+ * probabilities p_i are given at n_b + 1 places, the draft's q_i at n_b:
+ *   x_i is accepted iff x_0 .. x_{i-1} were and u_i q_i(x_i) < p_i(x_i)
+ *   j of them accepted: w = max(p_j - q_j, 0) if j < n_b, w = p_j if j = n_b
+ *   drawn: the smallest v with w(0) + .. + w(v) > u' (w(0) + .. + w(V - 1))
+ * The products, the comparisons and the sums are exact to 48 bits or more, so
+ * the tokens do not depend on the order of summation.  Entries of w that are
+ * not positive, or not a number, count as 0.
+ *
+ *   tokens       [N + B] int32, written: request b's at cu_drafts[b] + b: its
+ *                accepted drafts, the drawn token, then -1.
+ *   accepted     [B] int32, written: j.
+ *   target_probs [N + B, V] fp32, target_stride elements between rows (>= V).
+ *   draft_probs  [N, V] fp32, draft_stride between rows, or NULL: every draft
+ *                was proposed with probability 1 (q_i(x_i) = 1, else 0).
+ *   draft_tokens [N] int32.  One outside 0..V-1 is rejected, KDA_DEV_BAD_TOKEN.
+ *   accept_u     [N] fp32, sample_u [B] fp32, in [0, 1): u and u'.
+ *   cu_drafts    [B + 1] int32, cu[0] = 0, cu[B] = N (else KDA_DEV_BAD_SEQLEN; a
+ *                request with a bad range is skipped).
+ * Weights that sum to zero or to nothing finite draw -1, KDA_DEV_BAD_PROB.
+ */
+kda_status kda_verify_draft(int32_t* tokens, int32_t* accepted, const float* target_probs,
+                            const float* draft_probs, const int32_t* draft_tokens,
+                            const float* accept_u, const float* sample_u, const int32_t* cu_drafts,
+                            int B, int N, int V, long long target_stride, long long draft_stride,
+                            int32_t* dev_status, void* stream);
 
 /* Static description of a status code.  Host-only. */
 const char* kda_status_string(kda_status status);

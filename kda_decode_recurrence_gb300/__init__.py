@@ -21,6 +21,16 @@ KdaDeviceError when any bit is set.
                   dt_bias, gamma_o, W_o, S, conv_state, scale, lower_bound,
                   rms_norm_eps, l2_eps, workspace)
     block_workspace_size(B, n, Hd, nh, K, V, Kc)
+
+Next to the KDA layers, for a model's full-attention layers and drafted tokens:
+
+    kda_cache_append(k_cache, v_cache, k, v, cu_seqlens, seq_lens, page_table)
+    kda_cache_read(k_rows, v_rows, k_cache, v_cache, cu_rows, starts, page_table)
+    kda_paged_attention(out, q, k_cache, v_cache, cu_seqlens, seq_lens,
+                        page_table, max_tokens)
+    paged_attention_workspace_size(B, T, max_tokens, H, HKV, D)
+    kda_verify_draft(tokens, accepted, target_probs, draft_probs, draft_tokens,
+                     accept_u, sample_u, cu_drafts)
 """
 from __future__ import annotations
 
@@ -38,6 +48,11 @@ DEV_BAD_SLOT = 1
 DEV_BAD_SEQLEN = 2
 DEV_TIMEOUT = 4
 DEV_BOUNDS = 8  # debug builds only (libkda_debugbounds.so)
+DEV_BAD_PAGE = 16
+DEV_BAD_TOKEN = 32
+DEV_BAD_PROB = 64
+CACHE_BF16 = 0
+CACHE_E4M3 = 1
 
 
 class KdaError(RuntimeError):
@@ -53,7 +68,10 @@ class KdaDeviceError(RuntimeError):
         names = [n for b, n in ((DEV_BAD_SLOT, "KDA_DEV_BAD_SLOT"),
                                 (DEV_BAD_SEQLEN, "KDA_DEV_BAD_SEQLEN"),
                                 (DEV_TIMEOUT, "KDA_DEV_TIMEOUT"),
-                                (DEV_BOUNDS, "KDA_DEV_BOUNDS")) if bits & b]
+                                (DEV_BOUNDS, "KDA_DEV_BOUNDS"),
+                                (DEV_BAD_PAGE, "KDA_DEV_BAD_PAGE"),
+                                (DEV_BAD_TOKEN, "KDA_DEV_BAD_TOKEN"),
+                                (DEV_BAD_PROB, "KDA_DEV_BAD_PROB")) if bits & b]
         super().__init__(f"{what}: device status {bits} ({' | '.join(names) or 'unknown bits'})")
 
 
@@ -239,6 +257,199 @@ def kda_block_tkg(out, hidden, gamma_in, W_in, W_fb, W_gb, conv_w, A_log, dt_bia
         float(lower_bound), float(rms_norm_eps), float(l2_eps), B, n, Hd, nh, K, V, Kc,
         workspace.data_ptr(), workspace.numel(), status.data_ptr(), _stream_handle(stream))
     return _finish(rc, status, "kda_block_tkg", check, check_device, stream)
+
+
+def _check_rows(t: torch.Tensor, name: str, heads: int, D: int, device) -> int:
+    """A [T, heads, D] bf16 tensor whose tokens may be strided (a view of a fused
+    projection's output); returns the elements between two tokens."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected device {device}, got {t.device}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+        raise ValueError(f"{name} shape {tuple(t.shape)} != [T, {heads}, {D}]")
+    T = t.shape[0]
+    s = t.stride()
+    if (D > 1 and s[2] != 1) or (heads > 1 and s[1] != D):
+        raise ValueError(f"{name}: a token's rows must be contiguous (strides {s})")
+    return s[0] if T > 1 else heads * D
+
+
+def _check_cache(k_cache, v_cache, k_scale, v_scale, page_table, cu, what):
+    """The tensors every call on a paged cache takes; returns (cache_dtype, B, HKV,
+    D, page_size, num_pages, max_pages)."""
+    dev = k_cache.device
+    if k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise TypeError(f"k_cache: expected bfloat16 or float8_e4m3fn, got {k_cache.dtype}")
+    e4m3 = k_cache.dtype == torch.float8_e4m3fn
+    _check(k_cache, "k_cache", k_cache.dtype, dev)
+    _check(v_cache, "v_cache", k_cache.dtype, dev)
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} must be "
+                         "the same [num_pages, HKV, page_size, D]")
+    if e4m3:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an e4m3 cache needs k_scale and v_scale")
+        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _check(t, n, torch.float32, dev)
+            if t.shape != k_cache.shape[:3]:
+                raise ValueError(f"{n} shape {tuple(t.shape)} != {tuple(k_cache.shape[:3])}")
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("a bf16 cache takes no scales")
+    _check(page_table, "page_table", torch.int32, dev)
+    _check(cu, what, torch.int32, dev)
+    B = page_table.shape[0]
+    if page_table.dim() != 2 or cu.numel() != B + 1:
+        raise ValueError(f"page_table must be [B, max_pages] and {what} have B + 1 entries")
+    N, HKV, page, D = k_cache.shape
+    return (CACHE_E4M3 if e4m3 else CACHE_BF16), B, HKV, D, page, N, page_table.shape[1]
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def kda_cache_append(k_cache, v_cache, k, v, cu_seqlens, seq_lens, page_table, k_scale=None,
+                     v_scale=None, dev_status=None, stream=None, check=True,
+                     check_device=False) -> torch.Tensor:
+    """Write the new tokens' K and V rows into a paged cache (see include/kda.h).
+
+    Shapes: k_cache, v_cache [num_pages, HKV, page_size, D] bf16 or
+    float8_e4m3fn (then with k_scale, v_scale [num_pages, HKV, page_size] fp32);
+    k, v [T, HKV, D] bf16, tokens may be strided; cu_seqlens [B+1] int32;
+    seq_lens [B] int32 (the new tokens included); page_table [B, max_pages] int32.
+    """
+    dev = k_cache.device
+    dtype, B, HKV, D, page, N, max_pages = _check_cache(k_cache, v_cache, k_scale, v_scale,
+                                                        page_table, cu_seqlens, "cu_seqlens")
+    ks, vs = _check_rows(k, "k", HKV, D, dev), _check_rows(v, "v", HKV, D, dev)
+    if v.shape[0] != k.shape[0]:
+        raise ValueError(f"k has {k.shape[0]} tokens, v {v.shape[0]}")
+    _check(seq_lens, "seq_lens", torch.int32, dev)
+    if seq_lens.numel() != B:
+        raise ValueError("seq_lens must have B entries")
+    status = _status_word(dev_status, dev, stream)
+    rc = _lib.load().kda_cache_append(
+        k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale), k.data_ptr(),
+        v.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), dtype, B,
+        k.shape[0], HKV, D, page, N, max_pages, ks, vs, status.data_ptr(), _stream_handle(stream))
+    return _finish(rc, status, "kda_cache_append", check, check_device, stream)
+
+
+def kda_cache_read(k_rows, v_rows, k_cache, v_cache, cu_rows, starts, page_table, k_scale=None,
+                   v_scale=None, dev_status=None, stream=None, check=True,
+                   check_device=False) -> torch.Tensor:
+    """Rows of a paged cache back as dense bf16 rows: k_rows, v_rows [T, HKV, D]
+    take request b's positions starts[b] .. (0 .. when ``starts`` is None)."""
+    dev = k_cache.device
+    dtype, B, HKV, D, page, N, max_pages = _check_cache(k_cache, v_cache, k_scale, v_scale,
+                                                        page_table, cu_rows, "cu_rows")
+    for t, n in ((k_rows, "k_rows"), (v_rows, "v_rows")):
+        _check(t, n, torch.bfloat16, dev)
+        if t.dim() != 3 or t.shape[1:] != (HKV, D) or t.shape != k_rows.shape:
+            raise ValueError(f"{n} shape {tuple(t.shape)} != [T, {HKV}, {D}]")
+    if starts is not None:
+        _check(starts, "starts", torch.int32, dev)
+        if starts.numel() != B:
+            raise ValueError("starts must have B entries")
+    status = _status_word(dev_status, dev, stream)
+    rc = _lib.load().kda_cache_read(
+        k_rows.data_ptr(), v_rows.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        _ptr(k_scale), _ptr(v_scale), cu_rows.data_ptr(), _ptr(starts), page_table.data_ptr(),
+        dtype, B, k_rows.shape[0], HKV, D, page, N, max_pages, status.data_ptr(),
+        _stream_handle(stream))
+    return _finish(rc, status, "kda_cache_read", check, check_device, stream)
+
+
+def paged_attention_workspace_size(B, T, max_tokens, H, HKV, D) -> int:
+    return int(_lib.load().kda_paged_attention_workspace_size(B, T, max_tokens, H, HKV, D))
+
+
+def kda_paged_attention(out, q, k_cache, v_cache, cu_seqlens, seq_lens, page_table, max_tokens,
+                        scale=None, causal=True, window=0, k_scale=None, v_scale=None, lse=None,
+                        workspace=None, dev_status=None, stream=None, check=True,
+                        check_device=False) -> torch.Tensor:
+    """Softmax attention of the new tokens over a paged cache that holds their own
+    rows too (see include/kda.h).
+
+    Shapes: out [T, H, D] bf16; q [T, H, D] bf16, tokens may be strided; the cache,
+    cu_seqlens, seq_lens and page_table as kda_cache_append; lse [T, H] fp32 or None.
+    ``max_tokens`` bounds every request's new tokens; ``scale`` defaults to
+    D ** -0.5.  ``workspace`` is a uint8 CUDA tensor of at least
+    paged_attention_workspace_size(...) bytes; when None one is allocated here.
+    """
+    dev = k_cache.device
+    dtype, B, HKV, D, page, N, max_pages = _check_cache(k_cache, v_cache, k_scale, v_scale,
+                                                        page_table, cu_seqlens, "cu_seqlens")
+    T, H = out.shape[0], out.shape[1]
+    _check(out, "out", torch.bfloat16, dev)
+    qs = _check_rows(q, "q", H, D, dev)
+    if tuple(out.shape) != (q.shape[0], H, D):
+        raise ValueError(f"out shape {tuple(out.shape)} != {tuple(q.shape)}")
+    _check(seq_lens, "seq_lens", torch.int32, dev)
+    if seq_lens.numel() != B:
+        raise ValueError("seq_lens must have B entries")
+    if lse is not None:
+        _check(lse, "lse", torch.float32, dev)
+        if tuple(lse.shape) != (T, H):
+            raise ValueError(f"lse shape {tuple(lse.shape)} != [{T}, {H}]")
+    if workspace is None:
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
+            workspace = torch.empty(max(paged_attention_workspace_size(B, T, max_tokens, H, HKV, D), 1),
+                                    dtype=torch.uint8, device=dev)
+    else:
+        _check(workspace, "workspace", torch.uint8, dev)
+    status = _status_word(dev_status, dev, stream)
+    rc = _lib.load().kda_paged_attention(
+        out.data_ptr(), _ptr(lse), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        _ptr(k_scale), _ptr(v_scale), cu_seqlens.data_ptr(), seq_lens.data_ptr(),
+        page_table.data_ptr(), float(D ** -0.5 if scale is None else scale), int(causal),
+        int(window), dtype, B, T, int(max_tokens), H, HKV, D, page, N, max_pages, qs,
+        workspace.data_ptr(), workspace.numel(), status.data_ptr(), _stream_handle(stream))
+    return _finish(rc, status, "kda_paged_attention", check, check_device, stream)
+
+
+def kda_verify_draft(tokens, accepted, target_probs, draft_probs, draft_tokens, accept_u, sample_u,
+                     cu_drafts, dev_status=None, stream=None, check=True,
+                     check_device=False) -> torch.Tensor:
+    """Accept a prefix of each request's drafted tokens and draw the token after it
+    (see include/kda.h).
+
+    Shapes: tokens [N + B] int32, accepted [B] int32 (written); target_probs
+    [N + B, V] fp32; draft_probs [N, V] fp32 or None (drafts proposed with
+    certainty); draft_tokens [N] int32; accept_u [N], sample_u [B] fp32;
+    cu_drafts [B+1] int32.  Rows of probabilities may be strided.
+    """
+    dev = target_probs.device
+    B, N = accepted.shape[0], draft_tokens.shape[0]
+    for t, n, dt, size in ((tokens, "tokens", torch.int32, N + B),
+                           (accepted, "accepted", torch.int32, B),
+                           (draft_tokens, "draft_tokens", torch.int32, N),
+                           (accept_u, "accept_u", torch.float32, N),
+                           (sample_u, "sample_u", torch.float32, B),
+                           (cu_drafts, "cu_drafts", torch.int32, B + 1)):
+        _check(t, n, dt, dev)
+        if t.numel() != size:
+            raise ValueError(f"{n}: expected {size} entries, got {t.numel()}")
+    V = target_probs.shape[-1]
+    strides = []
+    for t, n, rows in ((target_probs, "target_probs", N + B), (draft_probs, "draft_probs", N)):
+        if t is None:
+            strides.append(V)
+            continue
+        if t.dtype != torch.float32:
+            raise TypeError(f"{n}: expected {torch.float32}, got {t.dtype}")
+        if t.device != dev:
+            raise ValueError(f"{n}: expected device {dev}, got {t.device}")
+        if tuple(t.shape) != (rows, V) or (V > 1 and t.stride(1) != 1):
+            raise ValueError(f"{n}: expected [{rows}, {V}] with contiguous rows, got {tuple(t.shape)}")
+        strides.append(t.stride(0) if rows > 1 else V)
+    status = _status_word(dev_status, dev, stream)
+    rc = _lib.load().kda_verify_draft(
+        tokens.data_ptr(), accepted.data_ptr(), target_probs.data_ptr(), _ptr(draft_probs),
+        draft_tokens.data_ptr(), accept_u.data_ptr(), sample_u.data_ptr(), cu_drafts.data_ptr(),
+        B, N, V, strides[0], strides[1], status.data_ptr(), _stream_handle(stream))
+    return _finish(rc, status, "kda_verify_draft", check, check_device, stream)
 
 
 def version() -> str:

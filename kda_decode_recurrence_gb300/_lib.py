@@ -15,7 +15,9 @@ _lib = None
 
 # Every symbol include/kda.h declares.
 EXPORTS = ("kda_decode", "kda_decode_ex", "kda_prefill", "kda_block_tkg", "kda_block_tkg_static",
-           "kda_block_tkg_workspace_size", "kda_status_string", "kda_version")
+           "kda_block_tkg_workspace_size", "kda_cache_append", "kda_cache_read",
+           "kda_paged_attention", "kda_paged_attention_workspace_size", "kda_verify_draft",
+           "kda_status_string", "kda_version")
 
 STATUS = {
     0: "KDA_OK", -1: "KDA_ERR_NULL", -2: "KDA_ERR_SHAPE", -3: "KDA_ERR_UNSUPPORTED",
@@ -38,6 +40,17 @@ def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.kda_block_tkg_static.argtypes = [vp] * 13 + [f] * 4 + [i] * 7 + [vp, vp]
     lib.kda_block_tkg_workspace_size.restype = ctypes.c_size_t
     lib.kda_block_tkg_workspace_size.argtypes = [i] * 7
+    ll = ctypes.c_longlong
+    lib.kda_cache_append.restype = i
+    lib.kda_cache_append.argtypes = [vp] * 9 + [i] * 8 + [ll, ll, vp, vp]
+    lib.kda_cache_read.restype = i
+    lib.kda_cache_read.argtypes = [vp] * 9 + [i] * 8 + [vp, vp]
+    lib.kda_paged_attention.restype = i
+    lib.kda_paged_attention.argtypes = ([vp] * 10 + [f] + [i] * 12 + [ll, vp, ctypes.c_size_t, vp, vp])
+    lib.kda_paged_attention_workspace_size.restype = ctypes.c_size_t
+    lib.kda_paged_attention_workspace_size.argtypes = [i] * 6
+    lib.kda_verify_draft.restype = i
+    lib.kda_verify_draft.argtypes = [vp] * 8 + [i] * 3 + [ll, ll, vp, vp]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_status_string.argtypes = [i]
     lib.kda_version.restype = ctypes.c_char_p

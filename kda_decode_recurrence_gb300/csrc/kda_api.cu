@@ -5,6 +5,7 @@
 
 #include "kda.h"
 #include "kda_internal.h"
+#include "kda_paged.h"
 
 namespace {
 
@@ -20,7 +21,7 @@ const char* kda_status_string(kda_status status) {
     case KDA_ERR_NULL: return "a required pointer is NULL";
     case KDA_ERR_SHAPE: return "a size is out of range or sizes are inconsistent";
     case KDA_ERR_UNSUPPORTED: return "sizes not implemented by this build";
-    case KDA_ERR_ENUM: return "unknown gate_mode, state_layout or output_dtype";
+    case KDA_ERR_ENUM: return "unknown gate_mode, state_layout, output_dtype or cache_dtype";
     case KDA_ERR_CUDA: return "a CUDA runtime call failed";
     case KDA_ERR_ALIGN: return "a pointer is not aligned as documented";
     case KDA_ERR_VALUE: return "a scalar argument is not finite or out of range";
@@ -199,6 +200,184 @@ kda_status kda_block_tkg(float* out, const float* hidden, const float* gamma_in,
   if (kda::launch_kda_block(a, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return KDA_ERR_CUDA;
   return KDA_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// What every call on a paged cache checks first; fills `c` when it returns KDA_OK.
+kda_status check_cache(kda::PagedCache& c, const void* k, const void* v, const float* k_scale,
+                       const float* v_scale, const int32_t* page_table, int cache_dtype, int B,
+                       int T, int HKV, int D, int page_size, int num_pages, int max_pages) {
+  if (B < 0 || T < 0 || HKV < 1 || D < 1 || page_size < 1 || num_pages < 1 || max_pages < 1)
+    return KDA_ERR_SHAPE;
+  if (cache_dtype != KDA_CACHE_BF16 && cache_dtype != KDA_CACHE_E4M3) return KDA_ERR_ENUM;
+  if ((D != 64 && D != 128) ||
+      (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128))
+    return KDA_ERR_UNSUPPORTED;
+  // Positions are 32-bit, and so are row numbers of the cache (a copy's coordinate).
+  if ((long long)max_pages * page_size > 0x7fffffffLL - 128 ||
+      (long long)num_pages * HKV > (0x7fffffffLL - 128) / page_size || (long long)T * HKV > 0x3fffffffLL)
+    return KDA_ERR_UNSUPPORTED;
+  if (B == 0 || T == 0) return KDA_OK;
+  const bool e4m3 = cache_dtype == KDA_CACHE_E4M3;
+  if (!k || !v || !page_table || (e4m3 && (!k_scale || !v_scale))) return KDA_ERR_NULL;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(page_table, 4) || !aligned(k_scale, 4) ||
+      !aligned(v_scale, 4))
+    return KDA_ERR_ALIGN;
+  c.k = const_cast<void*>(k);
+  c.v = const_cast<void*>(v);
+  c.k_scale = e4m3 ? const_cast<float*>(k_scale) : nullptr;
+  c.v_scale = e4m3 ? const_cast<float*>(v_scale) : nullptr;
+  c.page_table = page_table;
+  c.e4m3 = e4m3;
+  c.HKV = HKV;
+  c.D = D;
+  c.page_size = page_size;
+  c.num_pages = num_pages;
+  c.max_pages = max_pages;
+  return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status kda_cache_append(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                            const kda_bf16* k, const kda_bf16* v, const int32_t* cu_seqlens,
+                            const int32_t* seq_lens, const int32_t* page_table, int cache_dtype,
+                            int B, int T, int HKV, int D, int page_size, int num_pages,
+                            int max_pages, long long k_stride, long long v_stride,
+                            int32_t* dev_status, void* stream) {
+  kda::CacheRowsArgs a = {};
+  const kda_status st = check_cache(a.c, k_cache, v_cache, k_scale, v_scale, page_table,
+                                    cache_dtype, B, T, HKV, D, page_size, num_pages, max_pages);
+  if (st != KDA_OK) return st;
+  const long long row = (long long)HKV * D;
+  if (k_stride < row || v_stride < row) return KDA_ERR_SHAPE;
+  if (B == 0 || T == 0) return KDA_OK;
+  if (!k || !v || !cu_seqlens || !seq_lens) return KDA_ERR_NULL;
+  if (!aligned(k, 16) || !aligned(v, 16) || k_stride % 8 != 0 || v_stride % 8 != 0 ||
+      !aligned(cu_seqlens, 4) || !aligned(seq_lens, 4))
+    return KDA_ERR_ALIGN;
+  a.k_rows = const_cast<kda_bf16*>(k);
+  a.v_rows = const_cast<kda_bf16*>(v);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.cu = cu_seqlens;
+  a.at = seq_lens;
+  a.B = B;
+  a.T = T;
+  a.dev_status = dev_status;
+  return kda::launch_cache_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_cache_read(kda_bf16* k_rows, kda_bf16* v_rows, const void* k_cache,
+                          const void* v_cache, const float* k_scale, const float* v_scale,
+                          const int32_t* cu_rows, const int32_t* starts, const int32_t* page_table,
+                          int cache_dtype, int B, int T, int HKV, int D, int page_size,
+                          int num_pages, int max_pages, int32_t* dev_status, void* stream) {
+  kda::CacheRowsArgs a = {};
+  const kda_status st = check_cache(a.c, k_cache, v_cache, k_scale, v_scale, page_table,
+                                    cache_dtype, B, T, HKV, D, page_size, num_pages, max_pages);
+  if (st != KDA_OK || B == 0 || T == 0) return st;
+  if (!k_rows || !v_rows || !cu_rows) return KDA_ERR_NULL;
+  if (!aligned(k_rows, 16) || !aligned(v_rows, 16) || !aligned(cu_rows, 4) || !aligned(starts, 4))
+    return KDA_ERR_ALIGN;
+  a.k_rows = k_rows;
+  a.v_rows = v_rows;
+  a.k_stride = a.v_stride = (long long)HKV * D;
+  a.cu = cu_rows;
+  a.at = starts;
+  a.B = B;
+  a.T = T;
+  a.dev_status = dev_status;
+  return kda::launch_cache_read(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? KDA_OK : KDA_ERR_CUDA;
+}
+
+size_t kda_paged_attention_workspace_size(int B, int T, int max_tokens, int H, int HKV, int D) {
+  return kda::attention_workspace_bytes(B, T, max_tokens, H, HKV, D);
+}
+
+kda_status kda_paged_attention(kda_bf16* out, float* lse, const kda_bf16* q, const void* k_cache,
+                               const void* v_cache, const float* k_scale, const float* v_scale,
+                               const int32_t* cu_seqlens, const int32_t* seq_lens,
+                               const int32_t* page_table, float scale, int causal, int window,
+                               int cache_dtype, int B, int T, int max_tokens, int H, int HKV,
+                               int D, int page_size, int num_pages, int max_pages,
+                               long long q_stride, void* workspace, size_t workspace_bytes,
+                               int32_t* dev_status, void* stream) {
+  kda::AttentionArgs a = {};
+  const kda_status st = check_cache(a.c, k_cache, v_cache, k_scale, v_scale, page_table,
+                                    cache_dtype, B, T, HKV, D, page_size, num_pages, max_pages);
+  if (st != KDA_OK) return st;
+  if (H < 1 || H % HKV != 0 || max_tokens < 0 || q_stride < (long long)H * D) return KDA_ERR_SHAPE;
+  if (H / HKV > 128 || (long long)T * H > 0x3fffffffLL) return KDA_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale) || window < 0 || (causal != 0 && causal != 1)) return KDA_ERR_VALUE;
+  if (B == 0 || T == 0) return KDA_OK;
+  if (!out || !q || !cu_seqlens || !seq_lens) return KDA_ERR_NULL;
+  if (!aligned(out, 16) || !aligned(q, 16) || q_stride % 8 != 0 || !aligned(lse, 4) ||
+      !aligned(cu_seqlens, 4) || !aligned(seq_lens, 4))
+    return KDA_ERR_ALIGN;
+  if (!workspace || workspace_bytes < kda::attention_workspace_bytes(B, T, max_tokens, H, HKV, D))
+    return KDA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return KDA_ERR_ALIGN;
+  a.out = out;
+  a.lse = lse;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.cu = cu_seqlens;
+  a.lens = seq_lens;
+  a.scale = scale;
+  a.causal = causal;
+  a.window = window;
+  a.B = B;
+  a.T = T;
+  a.max_tokens = max_tokens;
+  a.H = H;
+  a.G = H / HKV;
+  a.workspace = workspace;
+  a.dev_status = dev_status;
+  return kda::launch_paged_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_verify_draft(int32_t* tokens, int32_t* accepted, const float* target_probs,
+                            const float* draft_probs, const int32_t* draft_tokens,
+                            const float* accept_u, const float* sample_u, const int32_t* cu_drafts,
+                            int B, int N, int V, long long target_stride, long long draft_stride,
+                            int32_t* dev_status, void* stream) {
+  if (B < 0 || N < 0 || V < 1 || target_stride < V || (draft_probs && draft_stride < V))
+    return KDA_ERR_SHAPE;
+  if (B > 0x7fffffff / 8 || V > 0x7fffffff - 4096 || (long long)N + B > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+  if (B == 0) return KDA_OK;
+  if (!tokens || !accepted || !target_probs || !sample_u || !cu_drafts ||
+      (N > 0 && (!draft_tokens || !accept_u)))
+    return KDA_ERR_NULL;
+  const void* ptrs[] = {tokens, accepted, target_probs, draft_probs, draft_tokens,
+                        accept_u, sample_u, cu_drafts};
+  for (const void* p : ptrs)
+    if (!aligned(p, 4)) return KDA_ERR_ALIGN;
+  kda::VerifyArgs a = {};
+  a.tokens = tokens;
+  a.accepted = accepted;
+  a.target = target_probs;
+  a.draft = draft_probs;
+  a.draft_tokens = draft_tokens;
+  a.accept_u = accept_u;
+  a.sample_u = sample_u;
+  a.cu = cu_drafts;
+  a.target_stride = target_stride;
+  a.draft_stride = draft_stride;
+  a.B = B;
+  a.N = N;
+  a.V = V;
+  a.dev_status = dev_status;
+  return kda::launch_verify_draft(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? KDA_OK : KDA_ERR_CUDA;
 }
 
 }  // extern "C"

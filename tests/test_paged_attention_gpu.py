@@ -1,0 +1,259 @@
+"""kda_paged_attention against softmax attention in 64 bits, position by position
+(tolerances: see _paged.attention).  Rows of the cache that no position in use owns
+hold NaN throughout."""
+import pytest
+import torch
+
+import kda_decode_recurrence_gb300 as kda
+
+from _paged import Case, attention
+from _parity import Guarded
+
+pytestmark = pytest.mark.gpu
+
+
+def queries(case, H, seed=1, amplitude=1.0):
+    g = torch.Generator().manual_seed(seed)
+    wide = (torch.randn(case.T, H + 2, case.D, generator=g) * amplitude).to(torch.bfloat16).cuda()
+    return wide[:, :H]                      # tokens strided by (H + 2) D
+
+
+def attend(case, q, causal=True, window=0, scale=None, max_tokens=None, table=None, with_lse=True,
+           seq_lens=None, stream=None):
+    """The call on guarded outputs and workspace; returns (out, lse, status)."""
+    T, H, D = q.shape
+    out = Guarded((T, H, D), torch.bfloat16, fill=float("nan"))
+    lse = Guarded((T, H), torch.float32, fill=float("nan"))
+    most = max(case.n) if max_tokens is None else max_tokens
+    work = Guarded((kda.paged_attention_workspace_size(case.B, T, most, H, case.HKV, D),), torch.uint8, fill=0xFF)
+    caches, scales = case.args()
+    status = kda.kda_paged_attention(out.t, q, *caches, case.cu, case.seq_lens if seq_lens is None else seq_lens,
+                                     case.table if table is None else table, most, scale=scale, causal=causal,
+                                     window=window, **scales, lse=lse.t if with_lse else None, workspace=work.t,
+                                     stream=stream)
+    torch.cuda.synchronize()
+    assert out.intact() and lse.intact() and work.intact()
+    return out.t, lse.t, int(status.item())
+
+
+def check(case, q, causal=True, window=0, scale=None, table=None, **kw):
+    out, lse, status = attend(case, q, causal, window, scale, table=table, **kw)
+    assert status == 0
+    want, wlse, tol, ltol = attention(case, q, q.shape[2] ** -0.5 if scale is None else scale, causal, window, table)
+    off = (out.double() - want).abs()
+    assert bool((off <= tol).all()), f"off by {float((off / tol.clamp_min(1e-300)).max()):.3g} tolerances"
+    empty = torch.isneginf(wlse)
+    assert torch.equal(torch.isneginf(lse), empty) and bool((out[empty] == 0).all())
+    off = (lse.double() - wlse)[~empty].abs()
+    assert bool((off <= ltol[~empty]).all()), f"lse off by {float((off / ltol[~empty]).max()):.3g} tolerances"
+
+
+SHAPES = [
+    # single tokens: one key, page and tile edges
+    dict(n=[1], lens=[1], H=1, HKV=1, D=128, page=16),
+    dict(n=[1] * 7, lens=[1, 15, 16, 17, 63, 64, 65], H=8, HKV=2, D=128, page=16),
+    dict(n=[1] * 5, lens=[127, 128, 129, 255, 257], H=12, HKV=1, D=128, page=64),
+    dict(n=[1] * 4, lens=[300, 1, 700, 33], H=6, HKV=2, D=64, page=32),
+    dict(n=[1, 1], lens=[1500, 2], H=32, HKV=2, D=128, page=128),
+    dict(n=[1], lens=[5000], H=4, HKV=1, D=64, page=16),
+    dict(n=[1], lens=[4099], H=16, HKV=1, D=128, page=64),
+    # drafted windows, empty requests, padding (more new tokens than positions)
+    dict(n=[1, 2, 3, 4, 5, 6, 7, 8], lens=[9, 2, 100, 64, 130, 6, 65, 257], H=8, HKV=2, D=128, page=16),
+    dict(n=[0, 5, 0, 3], lens=[0, 40, 12, 3], H=5, HKV=5, D=64, page=16),
+    dict(n=[4, 6, 3], lens=[2, 0, 50], H=4, HKV=2, D=128, page=16),
+    dict(n=[8, 8], lens=[520, 41], H=24, HKV=2, D=128, page=32),
+    dict(n=[7], lens=[300], H=7, HKV=1, D=64, page=64),
+    # chunks: rows of several tiles, with and without a cached prefix
+    dict(n=[40], lens=[40], H=4, HKV=2, D=128, page=16),
+    dict(n=[100, 33], lens=[230, 33], H=8, HKV=2, D=128, page=64),
+    dict(n=[130], lens=[390], H=2, HKV=2, D=64, page=32),
+    dict(n=[257], lens=[257], H=3, HKV=1, D=128, page=128),
+    dict(n=[70, 1, 0, 20], lens=[64, 900, 5, 300], H=12, HKV=1, D=128, page=16),
+    dict(n=[65, 2], lens=[80, 90], H=20, HKV=4, D=64, page=16),
+]
+IDS = [f"n{max(s['n'])}_L{max(s['lens'])}_H{s['H']}_{s['HKV']}_D{s['D']}_p{s['page']}" for s in SHAPES]
+
+
+def make(shape, **kw):
+    shape = dict(shape)
+    H = shape.pop("H")
+    case = Case(**shape, **kw)
+    return case, queries(case, H)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_causal(shape, cache):
+    case, q = make(shape, cache=cache, seed=11)
+    check(case, q)
+
+
+@pytest.mark.parametrize("window", [1, 16, 100, 129])
+@pytest.mark.parametrize("shape", [SHAPES[i] for i in (1, 4, 5, 7, 9, 13, 15, 16)], ids=lambda s: f"L{max(s['lens'])}")
+def test_window(shape, window):
+    case, q = make(shape, cache="bf16" if window % 2 else "e4m3", seed=12)
+    check(case, q, window=window)
+
+
+@pytest.mark.parametrize("window", [0, 37])
+@pytest.mark.parametrize("shape", [SHAPES[i] for i in (0, 4, 8, 9, 13, 16)], ids=lambda s: f"L{max(s['lens'])}")
+def test_not_causal(shape, window):
+    case, q = make(shape, cache="e4m3" if window else "bf16", seed=13)
+    check(case, q, causal=False, window=window)
+
+
+@pytest.mark.parametrize("shape", [SHAPES[4], SHAPES[7], SHAPES[13]], ids=["token", "window", "chunk"])
+def test_large_scores_and_another_scale(shape):
+    """Scores in the hundreds: one weight near 1, the rest below fp32's range."""
+    case, q = make(shape, seed=14)
+    check(case, q * 8, scale=0.5)
+    check(case, q, scale=-0.1)
+    check(case, q, scale=0.0)
+
+
+@pytest.mark.parametrize("shape", [SHAPES[3], SHAPES[10], SHAPES[14]], ids=["token", "window", "chunk"])
+def test_values_of_extreme_size(shape):
+    """Values near bf16's ends: the weights' product with V neither overflows nor vanishes."""
+    for amplitude in (1e-30, 1e30):
+        case, q = make(shape, seed=15)
+        v = case.tensors["v"][0]
+        v.copy_((v.float() * amplitude).to(torch.bfloat16))
+        check(case, q)
+    case, q = make(shape, cache="e4m3", seed=15)
+    for amplitude in (1e-20, 1e20):
+        scale = case.tensors["v"][1].clone()
+        case.tensors["v"][1].mul_(amplitude)
+        check(case, q)
+        case.tensors["v"][1].copy_(scale)
+
+
+@pytest.mark.parametrize("n,lens,G", [(1, 300, 4), (6, 300, 8), (90, 300, 4), (150, 150, 2)])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_not_a_number_in_masked_places(n, lens, G, cache):
+    """K and V of positions outside a token's window or after it hold NaN and infinity,
+    and pages wholly before the window are gone: tokens that do not see them are as before."""
+    window = 64
+    case, q = make(dict(n=[n, n], lens=[lens, lens - 3], H=2 * G, HKV=2, D=128, page=16), cache=cache, seed=16)
+    want, wlse, _ = attend(case, q, window=window)
+    table = case.table.clone()
+    for b in range(2):
+        first = max(0, case.lens[b] - n - window + 1)          # the first position any token sees
+        table[b, :first // 16] = -1
+        for pos in range(first // 16 * 16, first):
+            for name, bad in (("k", float("nan")), ("v", float("inf"))):
+                x, s = case.tensors[name]
+                row = (int(case.table[b, pos // 16]), slice(None), pos % 16)
+                if s is None:
+                    x[row] = bad
+                else:
+                    s[row] = bad
+    out, lse, status = attend(case, q, window=window, table=table)
+    assert status == 0
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
+@pytest.mark.parametrize("n,lens,G", [(5, 70, 4), (8, 200, 8), (90, 300, 4), (150, 150, 2), (300, 300, 1)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_bad_value_reaches_only_the_tokens_that_see_it(n, lens, G, bad):
+    """A later token's V that is not finite: earlier tokens of the chunk are as before."""
+    case, q = make(dict(n=[n], lens=[lens], H=2 * G, HKV=2, D=128, page=16), seed=17)
+    want, wlse, _ = attend(case, q)
+    i = (2 * n) // 3                                            # its position becomes bad
+    pos = lens - n + i
+    case.tensors["v"][0][int(case.table[0, pos // 16]), :, pos % 16, 5] = bad
+    out, lse, status = attend(case, q)
+    assert status == 0
+    assert torch.equal(out[:i], want[:i]) and torch.equal(lse, wlse)
+    keep = torch.arange(128, device="cuda") != 5
+    assert torch.equal(out[i:][..., keep], want[i:][..., keep])
+    assert not bool(torch.isfinite(out[i:][..., 5]).any())
+
+
+def test_without_lse_and_on_another_stream():
+    case, q = make(SHAPES[13], seed=18)
+    want, _, _ = attend(case, q)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    out, _, status = attend(case, q, with_lse=False, stream=stream)
+    assert status == 0 and torch.equal(out, want)
+
+
+def test_max_tokens_only_chooses_kernels():
+    """A larger bound than needed: the same values, within the tolerance of either."""
+    for shape in (SHAPES[2], SHAPES[7], SHAPES[16]):
+        case, q = make(shape, seed=19)
+        for most in (max(case.n), max(case.n) + 1, 5000):
+            check(case, q, max_tokens=most)
+
+
+def test_same_call_same_bits_and_graph_replay():
+    for shape in (SHAPES[5], SHAPES[7], SHAPES[13], SHAPES[16]):
+        case, q = make(shape, seed=20)
+        want, wlse, _ = attend(case, q)
+        again, alse, _ = attend(case, q)
+        assert torch.equal(want, again) and torch.equal(wlse, alse)
+        caches, scales = case.args()
+        out, lse = torch.zeros_like(want), torch.zeros_like(wlse)
+        work = torch.empty(kda.paged_attention_workspace_size(case.B, case.T, max(case.n), q.shape[1], case.HKV, case.D),
+                           dtype=torch.uint8, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            kda.kda_paged_attention(out, q, *caches, case.cu, case.seq_lens, case.table, max(case.n), **scales,
+                                    lse=lse, workspace=work, dev_status=status)
+        for _ in range(2):
+            out.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want) and torch.equal(lse, wlse) and int(status.item()) == 0
+
+
+@pytest.mark.parametrize("shape", [SHAPES[3], SHAPES[7], SHAPES[13]], ids=["token", "window", "chunk"])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_a_bad_page_counts_as_zero_rows(shape, cache):
+    case, q = make(shape, cache=cache, seed=21)
+    table = case.table.clone()
+    table[0, 0] = case.num_pages
+    table[case.B - 1, 0] = -5
+    out, lse, status = attend(case, q, table=table)
+    assert status == kda.DEV_BAD_PAGE
+    want, wlse, tol, ltol = attention(case, q, case.D ** -0.5, table=table)
+    assert bool(((out.double() - want).abs() <= tol).all())
+    some = ~torch.isneginf(wlse)
+    assert bool(((lse.double() - wlse)[some].abs() <= ltol[some]).all())
+
+
+def test_bad_lengths_are_reported_and_skipped():
+    case, q = make(SHAPES[13], seed=22)       # n = 100, 33
+    want, _, _ = attend(case, q)
+    lens = case.seq_lens.clone()
+    lens[1] = case.max_pages * case.page + 1
+    out, _, status = attend(case, q, seq_lens=lens)
+    assert status == kda.DEV_BAD_SEQLEN
+    assert torch.equal(out[:100], want[:100]) and bool(torch.isnan(out[100:]).all())
+    out, _, status = attend(case, q, max_tokens=50)
+    assert status == kda.DEV_BAD_SEQLEN
+    assert bool(torch.isnan(out[:100]).all()) and bool(torch.isfinite(out[100:]).all())
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_offsets_beyond_32_bits(n):
+    """Pages past 2^31 elements of the cache (the last ones of 4.9 GB)."""
+    small, q = make(dict(n=[n], lens=[200], H=8, HKV=8, D=128, page=128), seed=23, junk=0.0)
+    pages = 18400
+    big = [torch.zeros(pages, 8, 128, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for i, x in enumerate(big):
+        x[-small.num_pages:] = small.tensors["kv"[i]][0]
+    table = torch.where(small.table >= 0, small.table + pages - small.num_pages, small.table)
+    want, _, _ = attend(small, q)
+    out = torch.empty_like(want)
+    status = kda.kda_paged_attention(out, q, *big, small.cu, small.seq_lens, table, n)
+    assert int(status.item()) == 0 and torch.equal(out, want)
+
+
+def test_many_requests():
+    """More requests than threads of a block, lengths from 0."""
+    g = torch.Generator().manual_seed(24)
+    lens = torch.randint(0, 60, (700,), generator=g).tolist()
+    case, q = make(dict(n=[min(1, x) for x in lens], lens=lens, H=2, HKV=1, D=64, page=16), seed=24)
+    check(case, q)

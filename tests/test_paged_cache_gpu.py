@@ -1,0 +1,200 @@
+"""kda_cache_append and kda_cache_read against their formula in 64 bits.
+
+The scales and the codes of kda_cache_append have one right value each (quotients
+rounded to nearest in fp32, the code to nearest even), so they are compared for
+equality; kda_cache_read is off by one rounding to fp32 and one to bf16."""
+import numpy as np
+import pytest
+import torch
+
+import kda_decode_recurrence_gb300 as kda
+
+from _paged import Case, E4M3_TABLE, U_BF16, U_F32, cumulative, quantise
+from _parity import Guarded, guarded_copy
+
+pytestmark = pytest.mark.gpu
+
+
+def bits(t):
+    return t.cpu().view(torch.uint8 if t.element_size() == 1 else torch.int16).numpy()
+
+
+def append(case, k, v, table=None, seq_lens=None, cu=None):
+    """Run kda_cache_append on guarded copies of the cache; returns them and the status."""
+    held = {}
+    for name in ("k", "v"):
+        x, s = case.tensors[name]
+        held[name] = guarded_copy(x)
+        held[name + "_scale"] = None if s is None else guarded_copy(s)
+    scales = {n: None if held[n] is None else held[n].t for n in ("k_scale", "v_scale")}
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kda.kda_cache_append(held["k"].t, held["v"].t, k, v, case.cu if cu is None else cu,
+                         case.seq_lens if seq_lens is None else seq_lens,
+                         case.table if table is None else table, **scales, dev_status=status)
+    torch.cuda.synchronize()
+    assert all(g is None or g.intact() for g in held.values())
+    return held, int(status.item())
+
+
+def rows(case, seed, wild=False):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(case.T, 2, case.HKV, case.D, generator=g)
+    x *= torch.exp2(torch.randint(-30, 30, (case.T, 2, case.HKV, 1), generator=g).float())
+    x = x.to(torch.bfloat16)
+    if wild and case.T >= 8:
+        x[0, 0, 0] = 0
+        x[1, 1, 0, 3] = float("inf")
+        x[2, 0, 0, 5] = float("nan")
+        x[3, :, :] = -0.0
+        x[4, 0, 0] = torch.finfo(torch.bfloat16).tiny     # scales below the normal range
+        x[5, 0, 0, :] = torch.tensor([2.0 ** -133, 0.0]).repeat(case.D // 2)
+        x[6, 0, 0] = torch.finfo(torch.bfloat16).max
+        x[7, 0, 0] = torch.linspace(-448, 448, case.D)    # ties of the code's rounding
+    x = x.cuda()
+    return x[:, 0], x[:, 1]                               # tokens strided by 2 HKV D
+
+
+SHAPES = [
+    dict(n=[1], lens=[1], HKV=1, D=128, page=16),
+    dict(n=[1, 1, 1], lens=[1, 64, 65], HKV=8, D=128, page=64),
+    dict(n=[0, 5, 0, 1, 0], lens=[0, 40, 7, 1, 300], HKV=3, D=64, page=16),
+    dict(n=[33, 17, 129], lens=[33, 150, 129], HKV=2, D=128, page=32),
+    dict(n=[300], lens=[300], HKV=1, D=64, page=128),
+    dict(n=[4, 9], lens=[2, 8], HKV=2, D=128, page=16),   # tokens before position 0
+    dict(n=list(range(40)), lens=[2 * i for i in range(40)], HKV=2, D=128, page=16),
+]
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("shape", SHAPES, ids=range(len(SHAPES)))
+def test_append(shape, cache):
+    case = Case(**shape, cache=cache, seed=3, junk=1.0)
+    k, v = rows(case, 5, wild=True)
+    held, status = append(case, k, v)
+    assert status == 0
+    for name, x in (("k", k), ("v", v)):
+        before, scale0 = case.tensors[name]
+        want = bits(before).copy()
+        codes, scales = quantise(x.float().cpu().numpy()) if cache == "e4m3" else (bits(x.contiguous()), None)
+        want_scale = None if scale0 is None else scale0.cpu().numpy().copy()
+        cu = cumulative(case.n)
+        for b in range(case.B):
+            for i in range(case.n[b]):
+                pos = case.lens[b] - case.n[b] + i
+                if pos < 0:
+                    continue
+                pg, off = int(case.table[b, pos // case.page]), pos % case.page
+                for h in range(case.HKV):
+                    nan = scales is not None and np.isnan(scales[cu[b] + i, h])
+                    want[pg, h, off] = bits(held[name].t)[pg, h, off] if nan else codes[cu[b] + i, h]
+                    if scales is not None:
+                        want_scale[pg, h, off] = scales[cu[b] + i, h]
+        assert np.array_equal(bits(held[name].t), want), name
+        if scales is not None:
+            assert np.array_equal(held[name + "_scale"].t.cpu().numpy(), want_scale, equal_nan=True), name
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("shape", SHAPES, ids=range(len(SHAPES)))
+@pytest.mark.parametrize("from_start", [True, False])
+def test_read(shape, cache, from_start):
+    case = Case(**shape, cache=cache, seed=4)
+    lens = [max(x, 0) for x in case.lens]
+    starts = [0] * case.B if from_start else [x // 3 for x in lens]
+    n = [x - s for x, s in zip(lens, starts)]
+    cu = torch.tensor(cumulative(n), dtype=torch.int32, device="cuda")
+    outs = [Guarded((sum(n), case.HKV, case.D), torch.bfloat16, fill=float("nan")) for _ in range(2)]
+    caches, scales = case.args()
+    status = kda.kda_cache_read(outs[0].t, outs[1].t, *caches, cu,
+                                None if from_start else torch.tensor(starts, dtype=torch.int32, device="cuda"),
+                                case.table, **scales)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and all(o.intact() for o in outs)
+    for name, o in zip(("k", "v"), outs):
+        want = torch.cat([case.dense(name, b)[starts[b]:] for b in range(case.B)])
+        off = (o.t.double() - want).abs()
+        assert bool((off <= (U_BF16 + 2 * U_F32) * want.abs() if cache == "e4m3" else off == 0).all())
+
+
+def test_round_trip_is_within_half_a_step():
+    case = Case(n=[500], lens=[500], HKV=4, D=128, page=64, cache="e4m3", seed=6)
+    k, v = rows(case, 7)
+    held, status = append(case, k, v)
+    assert status == 0
+    out = [torch.empty(500, 4, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    kda.kda_cache_read(*out, held["k"].t, held["v"].t, case.cu, None, case.table,
+                       k_scale=held["k_scale"].t, v_scale=held["v_scale"].t)
+    for x, y in ((k, out[0]), (v, out[1])):
+        x, y = x.double(), y.double()
+        scale = x.abs().amax(-1, keepdim=True) / 448
+        # e4m3 2^-4 of the value, half the smallest step 2^-10 of the scale; bf16 on top
+        bound = torch.maximum(2.0 ** -4 * x.abs(), 2.0 ** -10 * scale) * (1 + 1e-5) + U_BF16 * y.abs()
+        assert bool(((x - y).abs() <= bound).all())
+
+
+def test_a_row_that_is_not_finite_reads_back_as_nan():
+    case = Case(n=[9], lens=[9], HKV=1, D=64, page=16, cache="e4m3", junk=0.0)
+    k, v = rows(case, 5, wild=True)
+    held, _ = append(case, k, v)
+    out = [torch.empty(9, 1, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    kda.kda_cache_read(*out, held["k"].t, held["v"].t, case.cu, None, case.table,
+                       k_scale=held["k_scale"].t, v_scale=held["v_scale"].t)
+    for x, y in ((k, out[0]), (v, out[1])):
+        bad = ~torch.isfinite(x).all(-1)
+        assert int(bad.sum()) == 1
+        assert bool(torch.isnan(y[bad]).all()) and bool(torch.isfinite(y[~bad]).all())
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_bad_pages_and_lengths_are_reported_and_skipped(cache):
+    shape = dict(n=[3, 4, 5], lens=[20, 40, 30], HKV=2, D=128, page=16)
+    case = Case(**shape, cache=cache, junk=1.0)
+    k, v = rows(case, 9)
+    good, status = append(case, k, v)
+    assert status == 0
+    table = case.table.clone()
+    table[1, 2] = case.num_pages                       # request 1's new tokens: positions 36..39
+    held, status = append(case, k, v, table=table)
+    assert status == kda.DEV_BAD_PAGE
+    mine = int(case.table[1, 2])
+    for name in ("k", "v"):
+        want = good[name].t.clone()
+        want.view(torch.uint8)[mine] = case.tensors[name][0].view(torch.uint8)[mine]
+        assert np.array_equal(bits(held[name].t), bits(want))
+    lens = torch.tensor([20, case.max_pages * 16 + 1, -1], dtype=torch.int32, device="cuda")
+    held, status = append(case, k, v, seq_lens=lens)   # requests 1 and 2 are skipped
+    assert status == kda.DEV_BAD_SEQLEN
+    cu = torch.tensor([0, 3, 7, 999], dtype=torch.int32, device="cuda")
+    _, status = append(case, k, v, cu=cu)
+    assert status == kda.DEV_BAD_SEQLEN
+    caches, scales = case.args()
+    out = [torch.full((12, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    starts = torch.tensor([17, 36, 25], dtype=torch.int32, device="cuda")
+    status = kda.kda_cache_read(*out, *caches, case.cu, starts, table, **scales)
+    assert int(status.item()) == kda.DEV_BAD_PAGE
+    assert all(bool((o[3:7] == 0).all()) and bool((o[7:] != 0).any()) for o in out)
+    starts[0] = case.max_pages * 16 - 2                # its third row is past the table's end
+    status = kda.kda_cache_read(*out, *caches, case.cu, starts, case.table, **scales)
+    assert int(status.item()) == kda.DEV_BAD_SEQLEN and all(bool((o[:3] == 0).all()) for o in out)
+
+
+def test_offsets_beyond_32_bits():
+    """A cache of 2.4e9 entries: the last page's rows lie past 2^31 elements and 2^32 bytes."""
+    pages, HKV, D, page = 18400, 8, 128, 128
+    k = torch.zeros(pages, HKV, page, D, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    table = torch.tensor([[pages - 1, 0]], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 130], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([130], dtype=torch.int32, device="cuda")
+    x = torch.randn(130, HKV, D, device="cuda").to(torch.bfloat16)
+    assert int(kda.kda_cache_append(k, v, x, -x, cu, lens, table).item()) == 0
+    assert torch.equal(k[-1], x[:128].transpose(0, 1)) and torch.equal(v[0, :, :2], -x[128:].transpose(0, 1))
+    assert int((k != 0).any(-1).sum()) == 130 * HKV
+    out = [torch.empty_like(x) for _ in range(2)]
+    assert int(kda.kda_cache_read(*out, k, v, cu, None, table).item()) == 0
+    assert torch.equal(out[0], x) and torch.equal(out[1], -x)
+
+
+def test_table_of_code_values():
+    codes = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    assert np.array_equal(codes.float().numpy().astype(np.float64), E4M3_TABLE, equal_nan=True)
