@@ -307,8 +307,9 @@ size_t kda_block_tkg_workspace_size(int B, int n, int Hd, int nh, int K, int V, 
  * A cache is two tensors [num_pages, HKV, page_size, D], K and V.  cache_dtype:
  *   KDA_CACHE_BF16   bf16 rows; k_scale and v_scale are NULL.
  *   KDA_CACHE_E4M3   e4m3 codes (8 bits) and fp32 scales [num_pages, HKV,
- *                    page_size], one per row: the row is code * scale.
- * D is 64 or 128, page_size 16, 32, 64 or 128.
+ *                    page_size], one per row: the row is code * scale.  The
+ *                    codes 0x7f and 0xff stand for no value and are not stored.
+ * D is 64 or 128, page_size 16, 32, 64 or 128; caches and scales are aligned to 16 B.
  *   page_table  [B, max_pages] int32: the page that holds request b's positions
  *               i * page_size .. (i + 1) * page_size - 1.  Entries that no
  *               position in use needs are not read.
@@ -317,7 +318,7 @@ size_t kda_block_tkg_workspace_size(int B, int n, int Hd, int nh, int K, int V, 
  *   seq_lens    [B] int32: positions in use, the new tokens' included: token i of
  *               request b is at position seq_lens[b] - n_b + i.  A token at a
  *               negative position is padding: it is not written to the cache and
- *               attends to nothing.  0 <= seq_lens[b] <= max_pages * page_size.
+ *               attends to nothing.  0 <= seq_lens[b] <= max_pages * page_size <= 2^30.
  * A request that breaks one of these sets KDA_DEV_BAD_SEQLEN and is skipped.
  * A position whose page_table entry is outside 0..num_pages-1 sets
  * KDA_DEV_BAD_PAGE: it is not written, reads back as zeros, and takes part in

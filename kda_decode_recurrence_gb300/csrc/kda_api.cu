@@ -217,14 +217,14 @@ kda_status check_cache(kda::PagedCache& c, const void* k, const void* v, const f
       (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128))
     return KDA_ERR_UNSUPPORTED;
   // Positions are 32-bit, and so are row numbers of the cache (a copy's coordinate).
-  if ((long long)max_pages * page_size > 0x7fffffffLL - 128 ||
+  if ((long long)max_pages * page_size > 0x40000000LL ||
       (long long)num_pages * HKV > (0x7fffffffLL - 128) / page_size || (long long)T * HKV > 0x3fffffffLL)
     return KDA_ERR_UNSUPPORTED;
   if (B == 0 || T == 0) return KDA_OK;
   const bool e4m3 = cache_dtype == KDA_CACHE_E4M3;
   if (!k || !v || !page_table || (e4m3 && (!k_scale || !v_scale))) return KDA_ERR_NULL;
-  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(page_table, 4) || !aligned(k_scale, 4) ||
-      !aligned(v_scale, 4))
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(page_table, 4) || !aligned(k_scale, 16) ||
+      !aligned(v_scale, 16))
     return KDA_ERR_ALIGN;
   c.k = const_cast<void*>(k);
   c.v = const_cast<void*>(v);
@@ -333,7 +333,7 @@ kda_status kda_paged_attention(kda_bf16* out, float* lse, const kda_bf16* q, con
   a.lens = seq_lens;
   a.scale = scale;
   a.causal = causal;
-  a.window = window;
+  a.window = window < 0x40000000 ? window : 0x40000000;  // longer than any sequence
   a.B = B;
   a.T = T;
   a.max_tokens = max_tokens;

@@ -1,0 +1,761 @@
+// kda_attn_window.cu -- attention of single tokens and drafted windows: the requests
+// with at most 64 rows (new tokens x query heads per key head).
+//
+// Such a request reads every cached row for 4 G n_b operations a byte at most, so HBM
+// bounds it and the kernel is built to keep copies in flight: two CTAs per SM,
+// each with a ring of key tiles (64 positions of K and V) filled by one
+// warp through TMA, one box per page and 128-byte panel.  Key tiles of all
+// requests are divided evenly over the CTAs (kda_attn.cuh), whatever their lengths.
+//
+// Per key tile the four computing warps split first the positions, then the
+// head dimension:
+//   S[rows, 16 w .. 16 w + 15] = Q K^T        warp w's 16 positions
+//   the rows' maxima are exchanged through shared memory, P = 2^(S - m) goes
+//   there as bf16
+//   O[rows, D/4 w ..] = O 2^(m_old - m) + P V  warp w's quarter of D
+// so that each entry of K and V is read from shared memory (and, for e4m3,
+// widened) once, and no warp's output has to be joined with another's.
+// mma.sync (m16n8k16) is the instruction for it: 16 rows are its native
+// size, where tcgen05 would spend 128 lanes on them.
+#include <cuda.h>
+
+#include "kda_attn.cuh"
+#include "kda_launch.h"
+#include "kda_tcgen05.cuh"
+#include "kda_tmap.h"
+
+namespace kda {
+namespace {
+
+constexpr int kTile = 64;             // positions per key tile
+constexpr int kComputeWarps = 4;
+constexpr int kThreads = 32 * (kComputeWarps + 2);  // + one warp for K and V, one for Q
+
+struct StageNote {
+  int t0, n, L, h;   // the item
+  int start;         // first position of the key tile
+  int flags;         // kFirst, kLast of this CTA's part of the item; kBegins, kEnds the item
+  int pieces;        // CTAs that share the item (flags has kBegins and not kEnds)
+  int pad;
+};
+constexpr int kFirst = 1, kLast = 2, kBegins = 4, kEnds = 8;
+
+template <int D, int kRows, bool kE4m3>
+struct Shape {
+  static constexpr int kElem = kE4m3 ? 1 : 2;
+  static constexpr int kRowBytes = D * kElem;              // 64, 128 or 256
+  static constexpr int kPanelBytes = kRowBytes < 128 ? kRowBytes : 128;
+  static constexpr int kPanels = kRowBytes / kPanelBytes;
+  static constexpr int kTileBytes = kTile * kRowBytes;     // K or V
+  // the ring: as deep as lets two CTAs share an SM
+  static constexpr int kOther = 2 * kRows * D * 2 + kRows * kTile * 2 + 4096;
+  static constexpr int kStageBytes = 2 * kTileBytes + (kE4m3 ? 2 * kTile * 4 : 0);
+  static constexpr int kFit = (113 * 1024 - kOther) / kStageBytes;
+  static constexpr int kStages = kFit < 8 ? kFit : 8;
+};
+
+template <int D, int kRows, bool kE4m3>
+struct Smem {
+  using S = Shape<D, kRows, kE4m3>;
+  unsigned char kv[S::kStages][2][S::kTileBytes];  // 1024-aligned, swizzled panels
+  unsigned char q[2][kRows * D * 2];               // rows of 128-byte swizzled panels
+  unsigned char pw[kRows * kTile * 2];             // P, bf16, 128-byte swizzled rows
+  float scales[kE4m3 ? S::kStages : 1][2][kTile];
+  float4 top[kRows];                               // the warps' row maxima
+  StageNote note[S::kStages];
+  uint64_t full[S::kStages], empty[S::kStages], qfull[2], qempty[2];
+  long long part[32];
+  int start_b;
+  long long start_unit;
+};
+
+// Byte offset of 16-byte chunk c of row r in a panel of kPanelBytes rows under TMA's
+// 128- or 64-byte swizzle.
+template <int kPanelBytes>
+__device__ __forceinline__ int swizzled(int r, int c) {
+  return kPanelBytes == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ void ldsm(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two e4m3 codes, one in the high byte of each half of x (low bytes 0), as bf16 values:
+// s eeee mmm becomes a bf16 of exponent field eeee, 2^-120 too small (subnormal
+// codes and bf16 subnormals alike), and one exact product puts that right.
+__device__ __forceinline__ uint32_t widen(uint32_t x) {
+  const uint32_t y = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x7b807b80u));  // 2^120, twice
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Barriers of the computing warps; the second also says whether all of them go on.
+__device__ __forceinline__ void compute_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kComputeWarps) : "memory");
+}
+__device__ __forceinline__ bool compute_sync_and(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.and.pred p, 1, %2, q;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(all) : "r"((uint32_t)ok), "n"(32 * kComputeWarps) : "memory");
+  return all != 0;
+}
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Units of a request: 0 if it is not this kernel's, else HKV x its key tiles
+// (at least one each: rows that see nothing are written too).
+__device__ __forceinline__ int first_tile(const AttentionArgs& p, const Request& r) {
+  return seen_lo(p, max(0, r.L - r.n)) / kTile;
+}
+__device__ __forceinline__ int key_tiles(const AttentionArgs& p, const Request& r) {
+  return max(1, (r.L + kTile - 1) / kTile - first_tile(p, r));
+}
+__device__ __forceinline__ long long units_of(const AttentionArgs& p, const Request& r) {
+  return r.n > 0 && r.n * p.G <= kWindowRows ? (long long)p.c.HKV * key_tiles(p, r) : 0;
+}
+
+// The items of one CTA's share in order, walked by a whole warp: 32 requests
+// are looked up at a time.
+struct Walk {
+  int base;          // the request that lane 0 holds
+  Request mine;      // this lane's request
+  int b, h;          // the current item
+  Request r;
+  int tile, tiles;   // next key tile of the item (0 .. tiles - 1)
+  long long left;    // units left in this CTA's share
+
+  __device__ __forceinline__ void fetch(const AttentionArgs& p, int from, int lane) {
+    base = from;
+    mine = Request{0, 0, 0};
+    if (from + lane < p.B) mine = load_request(p, from + lane, false);
+    if (units_of(p, mine) == 0) mine.n = 0;
+  }
+  __device__ __forceinline__ void take(const AttentionArgs& p, int lane) {
+    // the first request at b or after it with units
+    while (true) {
+      if (b >= base + 32) fetch(p, b, lane);
+      const unsigned some = __ballot_sync(0xffffffffu, mine.n > 0) & (0xffffffffu << (b - base));
+      if (some) {
+        const int src = __ffs(some) - 1;
+        b = base + src;
+        r.t0 = __shfl_sync(0xffffffffu, mine.t0, src);
+        r.n = __shfl_sync(0xffffffffu, mine.n, src);
+        r.L = __shfl_sync(0xffffffffu, mine.L, src);
+        tiles = key_tiles(p, r);
+        return;
+      }
+      b = base + 32;
+      if (b >= p.B) {  // cannot happen while units are left
+        left = 0;
+        return;
+      }
+    }
+  }
+  // Start at unit `skip` of request b's.
+  __device__ __forceinline__ void start(const AttentionArgs& p, int b0, long long skip, long long units, int lane) {
+    b = b0;
+    left = units;
+    fetch(p, b, lane);
+    take(p, lane);
+    h = (int)(skip / tiles);
+    tile = (int)(skip % tiles);
+  }
+  // Units of the current item that this CTA takes, from `tile` on.
+  __device__ __forceinline__ int count() const { return (int)min((long long)(tiles - tile), left); }
+  __device__ __forceinline__ void next(const AttentionArgs& p, int lane) {
+    left -= count();
+    if (left <= 0) return;
+    tile = 0;
+    if (++h == p.c.HKV) {
+      h = 0;
+      ++b;
+      take(p, lane);
+    }
+  }
+};
+
+template <int D, int kRows, bool kE4m3>
+__global__ void __launch_bounds__(kThreads, 2)
+    window_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                  const AttentionArgs p, const Pieces pieces) {
+  using S = Shape<D, kRows, kE4m3>;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  Smem<D, kRows, kE4m3>& sm = *reinterpret_cast<Smem<D, kRows, kE4m3>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x, ctas = gridDim.x;
+
+  if (tid == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], kComputeWarps);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.qfull[s], 1);
+      mbar_init(&sm.qempty[s], kComputeWarps);
+    }
+    mbar_fence_init();
+  }
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- this CTA's share: each thread counts a run of requests
+  const int run = (p.B + kThreads - 1) / kThreads;
+  const int b_lo = min(p.B, tid * run), b_hi = min(p.B, b_lo + run);
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += units_of(p, load_request(p, b, cta == 0));
+  long long scan = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += y;
+  }
+  if (lane == 31) sm.part[warp] = scan;
+  __syncthreads();
+  long long before = 0, units = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sm.part[w];
+    units += sm.part[w];
+  }
+  const long long from = before + scan - mine;
+  const int used = (int)min((long long)ctas, units);
+  if (tid == 0) pieces.notes[cta].tokens = 0;
+  if (cta >= used) return;
+  const long long u0 = share_begin(units, used, cta), u1 = share_begin(units, used, cta + 1);
+  if (u0 >= from && u0 < from + mine) {
+    long long at = from;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const long long u = units_of(p, load_request(p, b, false));
+      if (u0 < at + u) {
+        sm.start_b = b;
+        sm.start_unit = u0 - at;
+        break;
+      }
+      at += u;
+    }
+  }
+  __syncthreads();
+
+  if (warp == kComputeWarps) {
+    // ---- K and V of every key tile into the ring
+    Walk w;
+    w.start(p, sm.start_b, sm.start_unit, u1 - u0, lane);
+    const int rows_per_box = min(p.c.page_size, kTile);
+    const int boxes = kTile / rows_per_box;
+    int it = 0;
+    long long unit = u0;
+    bool ok = true;
+    while (w.left > 0 && ok) {
+      const int count = w.count();
+      const int lo = seen_lo(p, max(0, w.r.L - w.r.n));
+      const int t_first = first_tile(p, w.r);
+      const int32_t* table = p.c.page_table + (size_t)w.b * p.c.max_pages;
+      const int box_first = (t_first + w.tile) * boxes;  // box i of the segment is box_first + i
+      int page = 0;
+      for (int i = 0; i < count; ++i, ++it) {
+        // lanes hold the pages of the next 32 boxes
+        const int in = (i * boxes) & 31;
+        if (in == 0) {
+          const int pos = (box_first + i * boxes + lane) * rows_per_box;
+          page = -2;  // no position in use: zeros, no report
+          if (pos < w.r.L && pos + rows_per_box > lo) {
+            page = __ldg(table + pos / p.c.page_size);
+            if (page < 0 || page >= p.c.num_pages) {
+              if ((long long)pos < (long long)(t_first + w.tile + count) * kTile)
+                raise_status(p.dev_status, KDA_DEV_BAD_PAGE);
+              page = -1;
+            }
+          }
+        }
+        const int s = it % S::kStages;
+        if (it >= S::kStages) ok = mbar_wait(&sm.empty[s], (it / S::kStages - 1) & 1);
+        if (!ok) break;
+        const int start = (t_first + w.tile + i) * kTile;
+        if (lane == 0) {
+          StageNote& note = sm.note[s];
+          note.t0 = w.r.t0;
+          note.n = w.r.n;
+          note.L = w.r.L;
+          note.h = w.h;
+          note.start = start;
+          const bool begins = w.tile == 0, ends = w.tile + count == w.tiles;
+          note.flags = (i == 0 ? kFirst : 0) | (i + 1 == count ? kLast : 0) | (begins ? kBegins : 0) |
+                       (ends ? kEnds : 0);
+          note.pieces = begins && !ends ? share_of(units, used, unit + w.tiles - 1) - cta + 1 : 1;
+        }
+        if (kE4m3) {
+          // scales of boxes without a page are zeros; written before the barrier's arrival
+          for (int j = lane; j < kTile; j += 32) {
+            const int pg = __shfl_sync(0xffffffffu, page, in + j / rows_per_box);
+            if (pg < 0) sm.scales[s][0][j] = sm.scales[s][1][j] = 0.f;
+          }
+          fence_proxy_async_smem();  // a later copy to the same place comes after
+        }
+        __syncwarp();
+        const int mine_page = __shfl_sync(0xffffffffu, page, in + min(lane, boxes - 1));
+        const unsigned real = __ballot_sync(0xffffffffu, lane < boxes && mine_page >= 0);
+        if (lane == 0)
+          mbar_expect_tx(&sm.full[s], 2 * S::kTileBytes + (kE4m3 ? __popc(real) * 2 * rows_per_box * 4 : 0));
+        __syncwarp();
+        if (lane < boxes) {
+          const int off = (start + lane * rows_per_box) % p.c.page_size;
+          const int row = mine_page >= 0 ? (mine_page * p.c.HKV + w.h) * p.c.page_size + off
+                                         : p.c.num_pages * p.c.HKV * p.c.page_size;  // past the end: zeros
+#pragma unroll
+          for (int pn = 0; pn < S::kPanels; ++pn) {
+            const int at = pn * kTile * S::kPanelBytes + lane * rows_per_box * S::kPanelBytes;
+            tma_load_2d(sm.kv[s][0] + at, &k_map, &sm.full[s], pn * (S::kPanelBytes / S::kElem), row);
+            tma_load_2d(sm.kv[s][1] + at, &v_map, &sm.full[s], pn * (S::kPanelBytes / S::kElem), row);
+          }
+          if (kE4m3 && mine_page >= 0) {
+            bulk_load(&sm.scales[s][0][lane * rows_per_box], p.c.k_scale + row, rows_per_box * 4, &sm.full[s]);
+            bulk_load(&sm.scales[s][1][lane * rows_per_box], p.c.v_scale + row, rows_per_box * 4, &sm.full[s]);
+          }
+        }
+      }
+      unit += count;
+      w.next(p, lane);
+    }
+    if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
+    // Every copy lands before the CTA's memory is released, also when a wait gave up.
+    for (int i = max(0, it - S::kStages); i < it; ++i)
+      mbar_wait(&sm.full[i % S::kStages], (i / S::kStages) & 1);
+  } else if (warp == kComputeWarps + 1) {
+    // ---- the items' queries into two buffers: row i G + g is token i, head h G + g
+    Walk w;
+    w.start(p, sm.start_b, sm.start_unit, u1 - u0, lane);
+    bool ok = true;
+    for (int it = 0; w.left > 0 && ok; ++it) {
+      const int s = it & 1;
+      if (it >= 2) ok = mbar_wait(&sm.qempty[s], (it / 2 - 1) & 1);
+      if (!ok) break;
+      constexpr int kChunks = D / 8;  // 16-byte chunks of a row
+      const int rows = w.r.n * p.G;
+#pragma unroll 4
+      for (int i = lane; i < kRows * kChunks; i += 32) {
+        const int row = i / kChunks, c = i % kChunks;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (row < rows)
+          x = __ldg(reinterpret_cast<const uint4*>(
+              p.q + (w.r.t0 + row / p.G) * p.q_stride + (size_t)(w.h * p.G + row % p.G) * D + c * 8));
+        if (kE4m3) {
+          // Four consecutive entries of K sit in one register of the tensor core's
+          // operand, pairs (0 1) (2 3) as k = 2 j .. and 2 j + 8 ..: the same order here.
+          // Entries 4 j .. 4 j + 3 of each 16 go to 2 j, 2 j + 1, 2 j + 8, 2 j + 9.
+          unsigned char* to = sm.q[s] + (c / 8) * kRows * 128;
+          const int j = (c & 1) * 2;  // this chunk's first group of four
+          const int c0 = (c & 7) & ~1;
+          *reinterpret_cast<uint32_t*>(to + swizzled<128>(row, c0) + j * 4) = x.x;
+          *reinterpret_cast<uint32_t*>(to + swizzled<128>(row, c0 + 1) + j * 4) = x.y;
+          *reinterpret_cast<uint32_t*>(to + swizzled<128>(row, c0) + j * 4 + 4) = x.z;
+          *reinterpret_cast<uint32_t*>(to + swizzled<128>(row, c0 + 1) + j * 4 + 4) = x.w;
+        } else {
+          *reinterpret_cast<uint4*>(sm.q[s] + (c / 8) * kRows * 128 + swizzled<128>(row, c & 7)) = x;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) arrive(&sm.qfull[s]);
+      w.next(p, lane);
+    }
+    if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
+  } else {
+    // ---- the four computing warps
+    constexpr int kR = kRows / 16;        // row blocks of 16
+    constexpr int kN = D / kComputeWarps / 8;  // blocks of 8 columns of O per warp
+    const int quad = lane >> 2, j2 = (lane & 3) * 2;
+    const float xscale = p.scale * kLog2E;
+    float o[kR][kN][4], m[kR][2], l[kR][2];
+    long long left = u1 - u0;
+    int item = -1;
+    bool ok = true;
+    for (int it = 0; left > 0; ++it, --left) {
+      const int s = it % S::kStages;
+      // A wait that gives up in any of the warps ends all four at the next barrier.
+      ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[s], (it / S::kStages) & 1));
+      StageNote note = {};
+      if (ok) note = sm.note[s];
+      if (note.flags & kFirst) {
+        ++item;
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.qfull[item & 1], (item / 2) & 1));
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+          m[r][0] = m[r][1] = -INFINITY;
+          l[r][0] = l[r][1] = 0.f;
+#pragma unroll
+          for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[r][n][i] = 0.f;
+        }
+      }
+      const uint32_t k_addr = smem_u32(sm.kv[s][0]), v_addr = smem_u32(sm.kv[s][1]);
+      const uint32_t q_addr = smem_u32(sm.q[item & 1]), p_addr = smem_u32(sm.pw);
+
+      // S: this warp's 16 positions x all rows
+      float x[kR][2][4];
+#pragma unroll
+      for (int r = 0; r < kR; ++r)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[r][n][i] = 0.f;
+      const int my_pos = 16 * warp;
+      auto dot16 = [&](int kb, uint32_t b00, uint32_t b01, uint32_t b10, uint32_t b11) {
+        // entries 16 kb .. 16 kb + 15 of the head dimension
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+          uint32_t a[4];
+          const int row = 16 * r + (lane & 15), c = 2 * kb + (lane >> 4);
+          ldsm(q_addr + (c / 8) * kRows * 128 + swizzled<128>(row, c & 7), a);
+          mma(x[r][0], a, b00, b01);
+          mma(x[r][1], a, b10, b11);
+        }
+      };
+      if constexpr (!kE4m3) {
+#pragma unroll
+        for (int kb = 0; kb < D / 16; ++kb) {
+          uint32_t b[4];
+          const int row = my_pos + (lane >> 4) * 8 + (lane & 7), c = 2 * kb + ((lane >> 3) & 1);
+          ldsm(k_addr + (c / 8) * kTile * 128 + swizzled<128>(row, c & 7), b);
+          dot16(kb, b[0], b[1], b[2], b[3]);
+        }
+      } else {
+#pragma unroll
+        for (int kb = 0; kb < D / 32; ++kb) {
+          uint32_t b[4];
+          const int row = my_pos + (lane >> 4) * 8 + (lane & 7), c = 2 * kb + ((lane >> 3) & 1);
+          ldsm(k_addr + swizzled<S::kPanelBytes>(row, c), b);
+          uint32_t w[4][2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w[i][0] = widen(__byte_perm(b[i], 0, 0x1404));
+            w[i][1] = widen(__byte_perm(b[i], 0, 0x3424));
+          }
+          dot16(2 * kb, w[0][0], w[0][1], w[2][0], w[2][1]);
+          dot16(2 * kb + 1, w[1][0], w[1][1], w[3][0], w[3][1]);
+        }
+      }
+      // scores in units of log 2, and what a row does not see
+      const int pos0 = note.L - note.n;   // position of token 0
+      const int lo_all = seen_lo(p, max(0, pos0));
+      const bool whole = note.start >= seen_lo(p, note.L - 1) && note.start + kTile <= seen_hi(p, pos0, note.L);
+      float k_scale[2][2] = {{1.f, 1.f}, {1.f, 1.f}};
+      if constexpr (kE4m3) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float2 f = *reinterpret_cast<const float2*>(&sm.scales[s][0][my_pos + 8 * n + j2]);
+          k_scale[n][0] = f.x;
+          k_scale[n][1] = f.y;
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kR; ++r)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          int lo = 0, hi = 0x7fffffff;
+          if (!whole) {
+            const int pos = pos0 + (16 * r + 8 * half + quad) / p.G;
+            lo = seen_lo(p, pos) - note.start;
+            hi = min(seen_hi(p, pos, note.L), note.L) - note.start;
+          }
+          float top = -INFINITY;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float y = x[r][n][2 * half + i] * xscale;
+              if (kE4m3) y *= k_scale[n][i];
+              const int at = my_pos + 8 * n + j2 + i;
+              if (!whole && (at < lo || at >= hi)) y = -INFINITY;
+              x[r][n][2 * half + i] = y;
+              top = fmaxf(top, y);
+            }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          if ((lane & 3) == 0) reinterpret_cast<float*>(&sm.top[16 * r + 8 * half + quad])[warp] = top;
+        }
+      ok = compute_sync_and(ok);
+      if (!ok) break;
+      float v_scale[2][2] = {{1.f, 1.f}, {1.f, 1.f}};
+      if constexpr (kE4m3) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float2 f = *reinterpret_cast<const float2*>(&sm.scales[s][1][my_pos + 8 * n + j2]);
+          v_scale[n][0] = f.x;
+          v_scale[n][1] = f.y;
+        }
+      }
+      float keep[kR][2];
+      bool moved = false;
+#pragma unroll
+      for (int r = 0; r < kR; ++r)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const float4 t = sm.top[16 * r + 8 * half + quad];
+          const float now = fmaxf(fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)), m[r][half]);
+          const float ref = now == -INFINITY ? 0.f : now;
+          keep[r][half] = exp2_approx(m[r][half] - ref);
+          moved |= now != m[r][half];
+          m[r][half] = now;
+          l[r][half] *= keep[r][half];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const float w0 = exp2_approx(x[r][n][2 * half] - ref), w1 = exp2_approx(x[r][n][2 * half + 1] - ref);
+            l[r][half] += w0 + w1;
+            float y0 = w0, y1 = w1;
+            if (kE4m3) {
+              // a weight of 0 stays 0 whatever the scale of a place it does not see
+              y0 = x[r][n][2 * half] == -INFINITY ? 0.f : w0 * v_scale[n][0];
+              y1 = x[r][n][2 * half + 1] == -INFINITY ? 0.f : w1 * v_scale[n][1];
+            }
+            const int row = 16 * r + 8 * half + quad;
+            *reinterpret_cast<uint32_t*>(sm.pw + swizzled<128>(row, 2 * warp + n) + j2 * 2) = pack(y0, y1);
+          }
+        }
+      compute_sync();
+      // O: this warp's columns; the exponent's argument moves little, so most tiles keep
+      // every maximum and skip the rescaling
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int r = 0; r < kR; ++r)
+#pragma unroll
+          for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[r][n][i] *= keep[r][i >> 1];
+      }
+      // rows of V that no token of the request sees count as zeros
+      const bool v_whole = note.start >= lo_all && note.start + kTile <= note.L;
+      auto v_mask = [&](int pos) {  // positions pos, pos + 1 of the tile, as a mask of two halves
+        const int g = note.start + pos;
+        return (g >= lo_all && g < note.L ? 0x0000ffffu : 0u) |
+               (g + 1 >= lo_all && g + 1 < note.L ? 0xffff0000u : 0u);
+      };
+#pragma unroll
+      for (int kb = 0; kb < kTile / 16; ++kb) {
+        uint32_t a[kR][4];
+#pragma unroll
+        for (int r = 0; r < kR; ++r)
+          ldsm(p_addr + swizzled<128>(16 * r + (lane & 15), 2 * kb + (lane >> 4)), a[r]);
+        const int row = 16 * kb + (lane & 15);
+        if constexpr (!kE4m3) {
+#pragma unroll
+          for (int n = 0; n < kN; n += 2) {
+            uint32_t b[4];
+            const int c = warp * kN + n + (lane >> 4);
+            ldsm_t(v_addr + (c / 8) * kTile * 128 + swizzled<128>(row, c & 7), b);
+            if (!v_whole) {
+              const uint32_t lo = v_mask(16 * kb + j2), hi = v_mask(16 * kb + 8 + j2);
+              b[0] &= lo; b[1] &= hi; b[2] &= lo; b[3] &= hi;
+            }
+            if (!whole) {
+              // A value that is not finite reaches the rows that see its position only:
+              // it is taken out here and counted with the rows' visibility as weights.
+              bool bad = false;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                bad |= (b[i] & 0x7f80u) == 0x7f80u || (b[i] & 0x7f800000u) == 0x7f800000u;
+              if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll 1
+                for (int kind = 0; kind < 3; ++kind) {  // +infinity, -infinity, not a number
+                  uint32_t is[4];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    is[i] = 0;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                      const uint32_t v = (b[i] >> (16 * e)) & 0xffffu;
+                      const bool yes = kind == 0 ? v == 0x7f80u : kind == 1 ? v == 0xff80u : (v & 0x7fffu) > 0x7f80u;
+                      if (yes) is[i] |= 0x3f80u << (16 * e);  // 1
+                    }
+                  }
+                  const float add = kind == 0 ? INFINITY : kind == 1 ? -INFINITY : __uint_as_float(0x7fffffffu);
+#pragma unroll
+                  for (int r = 0; r < kR; ++r) {
+                    uint32_t see[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                      const int pos = pos0 + (16 * r + 8 * (i & 1) + quad) / p.G;
+                      const int g = note.start + 16 * kb + 8 * (i >> 1) + j2;
+                      const int lo = seen_lo(p, pos), hi = min(seen_hi(p, pos, note.L), note.L);
+                      see[i] = (g >= lo && g < hi ? 0x3f80u : 0u) | (g + 1 >= lo && g + 1 < hi ? 0x3f800000u : 0u);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                      float c4[4] = {0.f, 0.f, 0.f, 0.f};
+                      mma(c4, see, is[2 * e], is[2 * e + 1]);
+#pragma unroll
+                      for (int i = 0; i < 4; ++i)
+                        if (c4[i] > 0.f) o[r][n + e][i] += add;
+                    }
+                  }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  if ((b[i] & 0x7f80u) == 0x7f80u) b[i] &= 0xffff0000u;
+                  if ((b[i] & 0x7f800000u) == 0x7f800000u) b[i] &= 0x0000ffffu;
+                }
+              }
+            }
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+              mma(o[r][n], a[r], b[0], b[1]);
+              mma(o[r][n + 1], a[r], b[2], b[3]);
+            }
+          }
+        } else {
+          // 16 columns per 16-byte chunk: the even ones, then the odd ones.  Codes have no
+          // bad values (a bad row has a bad scale, which is in P of the rows that see it).
+          constexpr int kChunks = D / kComputeWarps / 16;  // 2 (D = 128) or 1
+          uint32_t b[4];
+          const int c = warp * kChunks + (kChunks == 2 ? lane >> 4 : 0);
+          ldsm_t(v_addr + swizzled<S::kPanelBytes>(row, c), b);
+#pragma unroll
+          for (int ch = 0; ch < kChunks; ++ch) {
+            const uint32_t e0 = widen((b[2 * ch] & 0x00ff00ffu) << 8), e1 = widen((b[2 * ch + 1] & 0x00ff00ffu) << 8);
+            const uint32_t d0 = widen(b[2 * ch] & 0xff00ff00u), d1 = widen(b[2 * ch + 1] & 0xff00ff00u);
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+              mma(o[r][2 * ch], a[r], e0, e1);
+              mma(o[r][2 * ch + 1], a[r], d0, d1);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) {
+        arrive(&sm.empty[s]);
+        if (note.flags & kLast) arrive(&sm.qempty[item & 1]);
+      }
+      if (!(note.flags & kLast)) continue;
+
+      // ---- the end of this CTA's part of the item: the sums of the four warps' positions
+      const bool done = (note.flags & kBegins) && (note.flags & kEnds);
+#pragma unroll
+      for (int r = 0; r < kR; ++r)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float t = l[r][half];
+          t += __shfl_xor_sync(0xffffffffu, t, 1);
+          t += __shfl_xor_sync(0xffffffffu, t, 2);
+          if ((lane & 3) == 0) reinterpret_cast<float*>(&sm.top[16 * r + 8 * half + quad])[warp] = t;
+        }
+      compute_sync();
+      const int place = (note.flags & kBegins) ? 1 : 0;
+      const int rows = note.n * p.G;
+      if (!done && place == 1 && tid == 0)
+        pieces.notes[cta] = PieceNote{note.t0 * p.H + note.h * p.G, note.n, note.pieces, 0};
+#pragma unroll
+      for (int r = 0; r < kR; ++r)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int row = 16 * r + 8 * half + quad;
+          const float4 t = sm.top[row];
+          const float sum = (t.x + t.y) + (t.z + t.w);
+          if (row >= rows) continue;
+          const int tok = row / p.G;
+          const size_t out_row = (size_t)(note.t0 + tok) * p.H + note.h * p.G + (row - tok * p.G);
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          const size_t piece = ((size_t)cta * 2 + place) * kRows + row;
+          if (warp == 0 && (lane & 3) == 0) {
+            if (!done) pieces.ml[piece] = make_float2(m[r][half], sum);
+            else if (p.lse) p.lse[out_row] = (m[r][half] + log2f(sum)) * kLn2;
+          }
+          if constexpr (!kE4m3) {
+#pragma unroll
+            for (int n = 0; n < kN; ++n) {
+              const int col = warp * (D / kComputeWarps) + 8 * n + j2;
+              const float y0 = o[r][n][2 * half], y1 = o[r][n][2 * half + 1];
+              if (done) *reinterpret_cast<uint32_t*>(p.out + out_row * D + col) = pack(y0 * inv, y1 * inv);
+              else *reinterpret_cast<float2*>(pieces.o + piece * D + col) = make_float2(y0, y1);
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < kN; n += 2) {  // even and odd columns: four in a row
+              const int col = warp * (D / kComputeWarps) + 8 * n + 2 * j2;
+              const float y0 = o[r][n][2 * half], y1 = o[r][n + 1][2 * half];
+              const float y2 = o[r][n][2 * half + 1], y3 = o[r][n + 1][2 * half + 1];
+              if (done)
+                *reinterpret_cast<uint2*>(p.out + out_row * D + col) =
+                    make_uint2(pack(y0 * inv, y1 * inv), pack(y2 * inv, y3 * inv));
+              else
+                *reinterpret_cast<float4*>(pieces.o + piece * D + col) = make_float4(y0, y1, y2, y3);
+            }
+          }
+        }
+      compute_sync();  // the sums have been read: the next tile's maxima may come
+    }
+    if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
+  }
+}
+
+template <int D, int kRows, bool kE4m3>
+cudaError_t launch_window(const AttentionArgs& a, cudaStream_t stream) {
+  using Sm = Smem<D, kRows, kE4m3>;
+  using S = Shape<D, kRows, kE4m3>;
+  static_assert(2 * (sizeof(Sm) + 1024 + 1024) <= 228 * 1024, "two window CTAs fit an SM");
+  static_assert(S::kStages >= 2, "the ring holds two key tiles");
+  CUtensorMap maps[2];
+  const uint64_t rows = (uint64_t)a.c.num_pages * a.c.HKV * a.c.page_size;
+  for (int i = 0; i < 2; ++i)
+    if (!make_map_2d(&maps[i], kE4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                     S::kElem, i ? a.c.v : a.c.k, D, rows, S::kPanelBytes / S::kElem,
+                     a.c.page_size < kTile ? a.c.page_size : kTile,
+                     S::kPanelBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+      return cudaErrorInvalidValue;
+  const size_t smem = sizeof(Sm) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(window_kernel<D, kRows, kE4m3>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const Pieces pieces = pieces_at(a.workspace, kRows);
+  e = launch(window_kernel<D, kRows, kE4m3>, dim3(kMaxAttnCtas), dim3(kThreads), smem, stream, true,
+             maps[0], maps[1], a, pieces);
+  if (e != cudaSuccess) return e;
+  return launch_join_pieces(a, pieces, kRows, kMaxAttnCtas, stream);
+}
+
+template <int D, bool kE4m3>
+cudaError_t by_rows(const AttentionArgs& a, cudaStream_t stream) {
+  switch (window_rows(a.max_tokens, a.G)) {
+    case 16: return launch_window<D, 16, kE4m3>(a, stream);
+    case 32: return launch_window<D, 32, kE4m3>(a, stream);
+    default: return launch_window<D, 64, kE4m3>(a, stream);
+  }
+}
+
+}  // namespace
+
+// The fewest rows that hold every window of at most max_tokens tokens (64: some may
+// not fit, and are not this kernel's).
+int window_rows(int max_tokens, int G) {
+  const long long rows = (long long)max_tokens * G;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+cudaError_t launch_window_attention(const AttentionArgs& a, cudaStream_t stream) {
+  if (a.c.D == 128)
+    return a.c.e4m3 ? by_rows<128, true>(a, stream) : by_rows<128, false>(a, stream);
+  return a.c.e4m3 ? by_rows<64, true>(a, stream) : by_rows<64, false>(a, stream);
+}
+
+}  // namespace kda

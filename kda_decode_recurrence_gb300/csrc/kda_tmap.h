@@ -26,12 +26,13 @@ inline EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 2-D row-major tensor map with 128-byte swizzle: inner extent `inner`
-// elements (contiguous), `outer` rows, box box_inner x box_rows (box_inner *
-// element size must be <= 128 bytes), out-of-range reads as zero.
+// 2-D row-major tensor map with a swizzle (128 bytes by default): inner extent
+// `inner` elements (contiguous), `outer` rows, box box_inner x box_rows (box_inner
+// * element size at most the swizzle's bytes), out-of-range reads as zero.
 inline bool make_map_2d(CUtensorMap* map, CUtensorMapDataType type, uint32_t elem_bytes,
                         const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,
-                        uint32_t box_rows) {
+                        uint32_t box_rows,
+                        CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[2] = {inner, outer};
@@ -39,7 +40,7 @@ inline bool make_map_2d(CUtensorMap* map, CUtensorMapDataType type, uint32_t ele
   const cuuint32_t box[2] = {box_inner, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
