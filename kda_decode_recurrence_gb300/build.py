@@ -43,7 +43,7 @@ VARIANTS = {
 
 SOURCES = ["kda_api.cu", "kda_decode.cu", "kda_block.cu", "kda_tc_gemm.cu", "kda_block_static.cu", "kda_prefill.cu",
            "kda_cache.cu", "kda_attention.cu", "kda_attn_window.cu",
-           "kda_verify.cu"]
+           "kda_attn_chunk.cu", "kda_verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
               "--expt-relaxed-constexpr"]

@@ -17,7 +17,8 @@
 
 namespace kda {
 
-constexpr int kMaxAttnCtas = 304;  // two per SM of a GB300
+constexpr int kWindowCtas = 304;  // two per SM of a GB300
+constexpr int kChunkCtas = 152;   // one per SM
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -79,20 +80,68 @@ struct Pieces {
   float* o;     // [ctas][2][rows][D]
 };
 
-__host__ __device__ inline size_t pieces_bytes(int rows, int D) {
-  return kMaxAttnCtas * (sizeof(PieceNote) + 2 * (size_t)rows * (sizeof(float2) + D * sizeof(float)));
+inline size_t pieces_bytes(int ctas, int rows, int D) {
+  return ctas * (sizeof(PieceNote) + 2 * (size_t)rows * (sizeof(float2) + D * sizeof(float)));
 }
-__host__ __device__ inline Pieces pieces_at(void* base, int rows) {
+inline Pieces pieces_at(void* base, int ctas, int rows) {
   Pieces s;
   s.notes = static_cast<PieceNote*>(base);
-  s.ml = reinterpret_cast<float2*>(s.notes + kMaxAttnCtas);
-  s.o = reinterpret_cast<float*>(s.ml + (size_t)kMaxAttnCtas * 2 * rows);
+  s.ml = reinterpret_cast<float2*>(s.notes + ctas);
+  s.o = reinterpret_cast<float*>(s.ml + (size_t)ctas * 2 * rows);
   return s;
+}
+
+// Byte offset of 16-byte chunk c of row r in a panel of kPanelBytes rows under TMA's
+// 128- or 64-byte swizzle.
+template <int kPanelBytes>
+__device__ __forceinline__ int swizzled(int r, int c) {
+  return kPanelBytes == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// Two e4m3 codes, one in the high byte of each half of x (low bytes 0), as bf16 values:
+// s eeee mmm becomes a bf16 of exponent field eeee, 2^-120 too small (subnormal
+// codes and bf16 subnormals alike), and one exact product puts that right.
+__device__ __forceinline__ uint32_t widen(uint32_t x) {
+  const uint32_t y = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x7b807b80u));  // 2^120, twice
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Sum of x over the CTA's threads before this one, and over all; kWarps warps, `part`
+// in shared memory (one entry a warp).
+template <int kWarps>
+__device__ __forceinline__ long long scan_before(long long x, long long* part, long long& all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long scan = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += y;
+  }
+  if (lane == 31) part[warp] = scan;
+  __syncthreads();
+  long long before = scan - x;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += part[w];
+    all += part[w];
+  }
+  return before;
 }
 
 constexpr int kWindowRows = 64;  // rows (tokens x G) of a request that the window kernel takes
 int window_rows(int max_tokens, int G);
 cudaError_t launch_window_attention(const AttentionArgs& a, cudaStream_t stream);
+
+constexpr int kChunkRows = 256;  // rows of an item of the chunk kernel, which takes the other requests
+cudaError_t launch_chunk_attention(const AttentionArgs& a, cudaStream_t stream);
 
 cudaError_t launch_join_pieces(const AttentionArgs& a, const Pieces& pieces, int rows, int ctas,
                                cudaStream_t stream);

@@ -1,0 +1,804 @@
+// kda_attn_chunk.cu -- attention of chunks: the requests with more than 64 rows (new
+// tokens x query heads per key head).
+//
+// Such a request does 4 D operations per row and cached position on 4 D bytes per
+// position: with hundreds of rows the tensor cores bound it.  One CTA per SM
+// works on items of two row tiles of 128 (row i G + g: token i, head g of the
+// group) of one (request, key head), and key tiles of 128 positions:
+//   S_t = Q_t K^T    128 x 128, TMEM; K-major operands from shared memory
+//   P_t = 2^(S_t - m) in bf16, back to TMEM over S_t by the 128 threads that own
+//                    one row each (four warps per row tile)
+//   O_t += P_t V     TMEM; A = P from TMEM, B = V from shared memory (N-major)
+// The two row tiles alternate: while one's softmax runs, the other's products do.
+// One thread issues every product, in the order PV_0 S_0 PV_1 S_1 per key tile, and
+// runs on into the next item.  For D = 128, S and P share columns: the tensor cores
+// take products in order, so the next S_t starts when PV_t has read P_t.
+// O is rescaled only when a row's maximum has grown by more than 2^8: weights up to
+// 256 lose nothing in bf16, and after the first key tiles that hardly ever happens.
+//
+// K and V come through TMA, one box per page and 128-byte panel.  An e4m3 cache's
+// codes are widened to bf16 by four more warps on the way; a key's scale
+// multiplies its column of S, a value's scale its column of P.
+//
+// A key tile that some row sees in part (the diagonal, the window's edge, the
+// sequence's end) is masked in the softmax, and entries of V that are outside the
+// request's range, or not finite, are taken out of shared memory first (0 x NaN
+// would reach the rows that do not see them); an item that had live entries of
+// that kind adds them, for the rows that see them, at its end.
+#include <cuda.h>
+
+#include "kda_attn.cuh"
+#include "kda_launch.h"
+#include "kda_tcgen05.cuh"
+#include "kda_tmap.h"
+
+namespace kda {
+namespace {
+
+constexpr int kTile = 128;          // positions per key tile
+constexpr int kM = 128;             // rows per row tile
+constexpr int kMmaWarp = 8, kKvWarp = 9, kQWarp = 10, kFixWarp = 11;  // after 8 of the softmax; fix: 4 for e4m3
+constexpr int kSteps = 8;           // steps whose notes, scales and barriers are kept: more than the rings hold
+constexpr float kGrow = 8.f;        // growth of a maximum (log 2) that rescales O
+
+// What the product and the copying warps need to know of a step (one key tile of
+// one item); the copying warp for K and V writes it before K.
+struct StepNote {
+  int flags;
+  int start;             // first position of the key tile
+  int begin, end;        // positions of the request that any of its tokens sees
+  int item;              // running number in this CTA
+  int row[8];            // rows of the key tile's boxes in the cache, -1: none (e4m3)
+};
+constexpr int kFirst = 1, kLast = 2;  // of this CTA's part of the item
+constexpr int kSecond = 4;            // the item has a second row tile
+constexpr int kWhole = 8;             // every row sees every position
+constexpr int kMore = 16;             // another step follows
+
+template <int D, bool kE4m3>
+struct Shape {
+  static constexpr int kPanels = D / 64;
+  static constexpr int kUnitBytes = kTile * D * 2;       // K or V of one key tile, bf16
+  static constexpr int kRawBytes = kTile * D;
+  // units alternate K, V, K, V ..
+  static constexpr int kUnits = D == 128 ? (kE4m3 ? 3 : 5) : (kE4m3 ? 6 : 8);
+  static constexpr int kRawUnits = kE4m3 ? (D == 128 ? 3 : 4) : 1;
+  static constexpr int kWarps = kE4m3 ? 15 : 12;
+  static constexpr int kThreads = 32 * kWarps;
+  // TMEM: S of both row tiles in columns 0 .. 255, O of both from kColO on; P in the second
+  // half of its S (D = 128, where S and PV have one shape and so complete in the order
+  // of issue), or in columns of its own
+  static constexpr uint32_t kColO = 256;
+  __host__ __device__ static constexpr uint32_t col_p(int t) { return D == 128 ? t * kTile + 64 : 384 + 64 * t; }
+};
+constexpr uint32_t kTmemCols = 512;
+
+template <int D, bool kE4m3>
+struct Smem {
+  using S = Shape<D, kE4m3>;
+  unsigned char q[2][kM * D * 2];                  // 1024-aligned, swizzled panels
+  unsigned char unit[S::kUnits][S::kUnitBytes];
+  unsigned char raw[kE4m3 ? S::kRawUnits : 1][kE4m3 ? S::kRawBytes : 16];
+  float scale[kE4m3 ? kSteps : 1][2][kE4m3 ? kTile : 1];  // by step: K's (times the score scale), V's
+  StepNote note[kSteps];
+  int bad[kSteps];                                  // by item: live entries of V were taken out
+  uint64_t full[S::kUnits], empty[S::kUnits], fixed[kSteps];
+  uint64_t raw_full[4], raw_empty[4];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], done;
+  long long part[S::kWarps];
+  long long start_unit;
+  int start_b;
+  uint32_t tmem;
+};
+
+// The item's key tiles: from tile `first`, `tiles` of them (at least one: rows that
+// see nothing are written too).
+struct Span {
+  int first, tiles;
+};
+__device__ __forceinline__ Span span_of(const AttentionArgs& p, const Request& r, int token0, int tokens) {
+  const int pos0 = r.L - r.n;
+  const int last = pos0 + min(r.n, token0 + tokens) - 1;
+  const int lo = seen_lo(p, max(0, pos0 + token0)), hi = min(seen_hi(p, last, r.L), r.L);
+  const int first = lo / kTile;
+  return Span{first, max(1, (hi + kTile - 1) / kTile - first)};
+}
+// Units of one key head of a request (0: not this kernel's), `pair` tokens to an item.
+__device__ __forceinline__ long long head_units(const AttentionArgs& p, const Request& r, int pair) {
+  if (r.n * p.G <= kWindowRows) return 0;
+  long long sum = 0;
+  for (int t = 0; t < r.n; t += pair) sum += span_of(p, r, t, pair).tiles;
+  return sum;
+}
+
+// The items of one CTA's share in order (request, key head, row tiles), walked by a
+// whole warp: 32 requests are looked up at a time.
+struct Walk {
+  int base;
+  Request mine;
+  int b, h, token0;
+  Request r;
+  Span span;
+  int tile;         // next key tile of the item, 0 .. span.tiles - 1
+  long long left;
+
+  __device__ __forceinline__ void fetch(const AttentionArgs& p, int lane) {
+    base = b;
+    mine = Request{0, 0, 0};
+    if (b + lane < p.B) mine = load_request(p, b + lane, false);
+    if (mine.n * p.G <= kWindowRows) mine.n = 0;
+  }
+  __device__ __forceinline__ void take(const AttentionArgs& p, int pair, int lane) {
+    while (b < p.B) {
+      if (b >= base + 32) fetch(p, lane);
+      const unsigned some = __ballot_sync(0xffffffffu, mine.n > 0) & (0xffffffffu << (b - base));
+      if (some) {
+        const int src = __ffs(some) - 1;
+        b = base + src;
+        r.t0 = __shfl_sync(0xffffffffu, mine.t0, src);
+        r.n = __shfl_sync(0xffffffffu, mine.n, src);
+        r.L = __shfl_sync(0xffffffffu, mine.L, src);
+        token0 = 0;
+        span = span_of(p, r, 0, pair);
+        return;
+      }
+      b = base + 32;
+    }
+    left = 0;  // cannot happen while units are left
+  }
+  __device__ __forceinline__ void start(const AttentionArgs& p, int pair, int b0, long long skip,
+                                        long long units, int lane) {
+    b = b0;
+    left = units;
+    h = 0;
+    fetch(p, lane);
+    take(p, pair, lane);
+    const long long head = head_units(p, r, pair);
+    h = (int)(skip / head);
+    skip -= h * head;
+    while (skip >= span.tiles) {
+      skip -= span.tiles;
+      token0 += pair;
+      span = span_of(p, r, token0, pair);
+    }
+    tile = (int)skip;
+  }
+  __device__ __forceinline__ int count() const { return (int)min((long long)(span.tiles - tile), left); }
+  __device__ __forceinline__ void next(const AttentionArgs& p, int pair, int lane) {
+    left -= count();
+    if (left <= 0) return;
+    tile = 0;
+    token0 += pair;
+    if (token0 >= r.n) {
+      token0 = 0;
+      if (++h == p.c.HKV) {
+        h = 0;
+        ++b;
+        take(p, pair, lane);
+        return;
+      }
+    }
+    span = span_of(p, r, token0, pair);
+  }
+};
+
+// All steps of 16 along the contraction: S = Q K^T, and O (+)= P V.
+template <int D>
+__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t q_addr, uint32_t k_addr) {
+  const uint32_t idesc = idesc_bf16(kTile, kM, false, false);
+  const uint64_t a = smem_desc_sw128(q_addr, 16, 1024), b = smem_desc_sw128(k_addr, 16, 1024);
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) {
+    const uint64_t off = ((j >> 2) * (kM * 128) + (j & 3) * 32) >> 4;
+    mma_bf16(d, a + off, b + off, idesc, j > 0 ? 1u : 0u);
+  }
+}
+template <int D>
+__device__ __forceinline__ void issue_output(uint32_t d, uint32_t p_col, uint32_t v_addr, bool add) {
+  const uint32_t idesc = idesc_bf16(D, kM, false, true);
+  const uint64_t b = smem_desc_sw128(v_addr, kTile * 128, 1024);
+#pragma unroll
+  for (int j = 0; j < kTile / 16; ++j)
+    mma_bf16_tmem_a(d, p_col + 8 * j, b + ((j * 16 * 128) >> 4), idesc, (add || j > 0) ? 1u : 0u);
+}
+
+// The halves of v (two bf16) that are not finite, as a mask.
+__device__ __forceinline__ uint32_t not_finite(uint32_t v) {
+  return ((v & 0x7f80u) == 0x7f80u ? 0x0000ffffu : 0u) | ((v & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+}
+
+// Whether rows with positions first .. last all see every position of the key tile.
+__device__ __forceinline__ bool sees_whole(const AttentionArgs& p, int L, int first, int last, int start) {
+  return start >= seen_lo(p, last) && start + kTile <= min(seen_hi(p, first, L), L);
+}
+
+// Adds the live entries of V that were taken out of an item's partly seen key tiles
+// (`steps` of them from position start0 on; its rows are at positions first .. last)
+// to columns col .. col + 31 of one row's output: the weight of each is found
+// again from Q and K in memory.  (Rare: values that are not finite.)
+template <int D>
+__device__ __noinline__ void add_bad_values(const AttentionArgs& p, int b, int h, int L, int pos, int first, int last,
+                                            int start0, int steps, const kda_bf16* q, float m, int col, float* o) {
+  const int lo = seen_lo(p, pos), hi = min(seen_hi(p, pos, L), L);
+  const kda_bf16* kc = static_cast<const kda_bf16*>(p.c.k);
+  const kda_bf16* vc = static_cast<const kda_bf16*>(p.c.v);
+  const int32_t* table = p.c.page_table + (size_t)b * p.c.max_pages;
+  for (int s = 0; s < steps; ++s) {
+    const int start = start0 + s * kTile;
+    if (sees_whole(p, L, first, last, start)) continue;
+    for (int j = max(lo, start); j < min(hi, start + kTile); ++j) {
+      const int page = table[j / p.c.page_size];
+      if (page < 0 || page >= p.c.num_pages) continue;
+      const size_t row = ((size_t)page * p.c.HKV + h) * p.c.page_size + j % p.c.page_size;
+      float w = -1.f;
+      for (int d = 0; d < 32; ++d) {
+        const uint32_t v = vc[row * D + col + d];
+        if ((v & 0x7f80u) != 0x7f80u) continue;
+        if (w < 0.f) {
+          float x = 0.f;
+          for (int e = 0; e < D; ++e)
+            x = fmaf(__uint_as_float((uint32_t)q[e] << 16), __uint_as_float((uint32_t)kc[row * D + e] << 16), x);
+          w = exp2_approx(x * (p.scale * kLog2E) - m);
+        }
+        o[d] = fmaf(w, __uint_as_float(v << 16), o[d]);
+      }
+    }
+  }
+}
+
+// The bits of columns lo .. hi - 1 among columns 0 .. 31.
+__device__ __forceinline__ uint32_t below(int k) { return k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u; }
+__device__ __forceinline__ uint32_t columns(int lo, int hi) { return below(hi) & ~below(lo); }
+
+template <int D, bool kE4m3>
+__global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                 const __grid_constant__ CUtensorMap v_map, const AttentionArgs p, const Pieces pieces) {
+  using S = Shape<D, kE4m3>;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  Smem<D, kE4m3>& sm = *reinterpret_cast<Smem<D, kE4m3>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x, ctas = gridDim.x;
+  const int per_tile = kM / p.G;     // tokens of a row tile
+  const int pair = 2 * per_tile;     // of an item
+
+  if (tid == 0) {
+    for (int s = 0; s < S::kUnits; ++s) {
+      mbar_init(&sm.full[s], kE4m3 ? 4 : 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int s = 0; s < kSteps; ++s) mbar_init(&sm.fixed[s], 1);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&sm.raw_full[s], 1);
+      mbar_init(&sm.raw_empty[s], 4);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sm.q_full[t], 1);
+      mbar_init(&sm.q_empty[t], 1);
+      mbar_init(&sm.s_full[t], 1);
+      mbar_init(&sm.p_full[t], 4);
+      mbar_init(&sm.o_done[t], 1);
+    }
+    mbar_init(&sm.done, 1);
+    mbar_fence_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc(&sm.tmem, kTmemCols);
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- this CTA's share: each thread counts a run of requests
+  const int run = (p.B + S::kThreads - 1) / S::kThreads;
+  const int b_lo = min(p.B, tid * run), b_hi = min(p.B, b_lo + run);
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b)
+    mine += p.c.HKV * head_units(p, load_request(p, b, cta == 0), pair);
+  long long units;
+  const long long from = scan_before<S::kWarps>(mine, sm.part, units);
+  const int used = (int)min((long long)ctas, units);
+  if (tid == 0) pieces.notes[cta].tokens = 0;
+  const long long u0 = cta < used ? share_begin(units, used, cta) : 0;
+  const long long u1 = cta < used ? share_begin(units, used, cta + 1) : 0;
+  if (u1 > u0 && u0 >= from && u0 < from + mine) {
+    long long at = from;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const long long u = p.c.HKV * head_units(p, load_request(p, b, false), pair);
+      if (u0 < at + u) {
+        sm.start_b = b;
+        sm.start_unit = u0 - at;
+        break;
+      }
+      at += u;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  const int steps = (int)(u1 - u0);
+  bool ok = true;
+
+  if (steps == 0) {
+    // nothing to do
+  } else if (warp == kKvWarp) {
+    // ---- notes, and K and V of every step into the ring
+    Walk w;
+    w.start(p, pair, sm.start_b, sm.start_unit, u1 - u0, lane);
+    const int rows_per_box = min(p.c.page_size, kTile);
+    const int boxes = kTile / rows_per_box;
+    constexpr int kRing = kE4m3 ? S::kRawUnits : S::kUnits;
+    uint64_t* full = kE4m3 ? sm.raw_full : sm.full;
+    uint64_t* empty = kE4m3 ? sm.raw_empty : sm.empty;
+    int step = 0, item = 0;
+    while (w.left > 0 && ok) {
+      const int count = w.count();
+      const int pos0 = w.r.L - w.r.n;
+      const int begin = seen_lo(p, max(0, pos0));                       // of the request
+      const int lo = seen_lo(p, max(0, pos0 + w.token0));               // of the item
+      const int last_pos = pos0 + min(w.r.n, w.token0 + pair) - 1;
+      const int hi = min(seen_hi(p, last_pos, w.r.L), w.r.L);
+      const int32_t* table = p.c.page_table + (size_t)w.b * p.c.max_pages;
+      const int box_first = (w.span.first + w.tile) * boxes;
+      int page = 0;
+      for (int i = 0; i < count && ok; ++i, ++step) {
+        const int in = (i * boxes) & 31;
+        if (in == 0) {
+          const int pos = (box_first + i * boxes + lane) * rows_per_box;
+          page = -1;
+          if (pos < hi && pos + rows_per_box > lo) {
+            page = __ldg(table + pos / p.c.page_size);
+            if (page < 0 || page >= p.c.num_pages) {
+              if (pos < (w.span.first + w.tile + count) * kTile) raise_status(p.dev_status, KDA_DEV_BAD_PAGE);
+              page = -1;
+            }
+          }
+        }
+        const int start = (w.span.first + w.tile + i) * kTile;
+        const int box_page = __shfl_sync(0xffffffffu, page, in + min(lane, boxes - 1));
+        StepNote& note = sm.note[step % kSteps];
+        const int off = (start + lane * rows_per_box) % p.c.page_size;
+        const int row = box_page >= 0 ? (box_page * p.c.HKV + w.h) * p.c.page_size + off
+                                      : p.c.num_pages * p.c.HKV * p.c.page_size;  // past the end: zeros
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int u = 2 * step + kv, s = u % kRing;
+          if (u >= kRing) ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], (u / kRing - 1) & 1));
+          if (!ok) break;
+          if (kv == 0) {
+            if (lane < boxes) note.row[lane] = box_page >= 0 ? row : -1;
+            if (lane == 0) {
+              note.flags = (i == 0 ? kFirst : 0) | (i + 1 == count ? kLast : 0) |
+                           (w.token0 + per_tile < w.r.n ? kSecond : 0) |
+                           (sees_whole(p, w.r.L, pos0 + w.token0, last_pos, start) ? kWhole : 0) |
+                           (step + 1 < steps ? kMore : 0);
+              note.start = start;
+              note.begin = begin;
+              note.end = w.r.L;
+              note.item = item;
+            }
+            __syncwarp();
+          }
+          if (lane == 0) mbar_expect_tx(&full[s], kE4m3 ? S::kRawBytes : S::kUnitBytes);
+          __syncwarp();
+          if (lane < boxes) {
+            const CUtensorMap* map = kv ? &v_map : &k_map;
+            if (kE4m3) {
+              tma_load_2d(sm.raw[s] + lane * rows_per_box * D, map, &full[s], 0, row);
+            } else {
+#pragma unroll
+              for (int pn = 0; pn < S::kPanels; ++pn)
+                tma_load_2d(sm.unit[s] + pn * kTile * 128 + lane * rows_per_box * 128, map, &full[s], pn * 64, row);
+            }
+          }
+        }
+      }
+      ++item;
+      w.next(p, pair, lane);
+    }
+    if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
+    // Every copy lands before the CTA's memory is released, also when a wait gave up.
+    for (int u = max(0, 2 * step - kRing); u < 2 * step; ++u) mbar_wait(&full[u % kRing], (u / kRing) & 1);
+  } else if (warp == kQWarp) {
+    // ---- each item's queries: token rows of a row tile are rows tok G + g of its panels
+    Walk w;
+    w.start(p, pair, sm.start_b, sm.start_unit, u1 - u0, lane);
+    int items[2] = {0, 0};
+    while (w.left > 0 && ok) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (t == 1 && w.token0 + per_tile >= w.r.n) break;
+        if (items[t] > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait(&sm.q_empty[t], (items[t] - 1) & 1));
+        if (!ok) break;
+        ++items[t];
+        if (lane == 0) {
+          mbar_expect_tx(&sm.q_full[t], S::kPanels * per_tile * p.G * 128);
+#pragma unroll
+          for (int pn = 0; pn < S::kPanels; ++pn)
+            tma_load_3d(sm.q[t] + pn * kM * 128, &q_map, &sm.q_full[t], pn * 64, w.h * p.G,
+                        w.r.t0 + w.token0 + t * per_tile);
+        }
+      }
+      __syncwarp();
+      if (ok) w.next(p, pair, lane);
+    }
+    if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      if (items[t] > 0) mbar_wait(&sm.q_full[t], (items[t] - 1) & 1);
+  } else if (warp == kMmaWarp) {
+    // ---- every product, by one thread
+    if (lane == 0) {
+      int q_items[2] = {0, 0}, p_count[2] = {0, 0};
+      // S of step g for row tile t; `last`: the last row tile of the step
+      auto scores = [&](int g, int t, int n_flags, bool last) {
+        if (n_flags & kFirst) {
+          ok = ok && mbar_wait(&sm.q_full[t], q_items[t] & 1);
+          ++q_items[t];
+        }
+        if (!ok) return;
+        tc_fence_after();
+        issue_scores<D>(tmem + t * kTile, smem_u32(sm.q[t]), smem_u32(sm.unit[(2 * g) % S::kUnits]));
+        mma_commit(&sm.s_full[t]);
+        if (last) mma_commit(&sm.empty[(2 * g) % S::kUnits]);
+        if (n_flags & kLast) mma_commit(&sm.q_empty[t]);
+      };
+      auto k_ready = [&](int g) {
+        ok = ok && mbar_wait(&sm.full[(2 * g) % S::kUnits], ((2 * g) / S::kUnits) & 1);
+      };
+      int flags = 0;
+      k_ready(0);
+      if (ok) {
+        flags = sm.note[0].flags;
+        scores(0, 0, flags, !(flags & kSecond));
+        if (flags & kSecond) scores(0, 1, flags, true);
+      }
+      for (int g = 0; g < steps && ok; ++g) {
+        const int v = (2 * g + 1) % S::kUnits, v_phase = ((2 * g + 1) / S::kUnits) & 1;
+        ok = mbar_wait(&sm.full[v], v_phase);
+        if (!kE4m3) ok = ok && mbar_wait(&sm.fixed[g % kSteps], (g / kSteps) & 1);
+        const bool second = (flags & kSecond) != 0, first = (flags & kFirst) != 0;
+        const bool more = (flags & kMore) != 0;
+        int next_flags = 0;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t == 0 || second) {
+            ok = ok && mbar_wait(&sm.p_full[t], p_count[t] & 1);
+            if (!ok) break;
+            ++p_count[t];
+            tc_fence_after();
+            issue_output<D>(tmem + S::kColO + t * D, tmem + S::col_p(t), smem_u32(sm.unit[v]), !first);
+            mma_commit(&sm.o_done[t]);
+            if (t == 1 || !second) mma_commit(&sm.empty[v]);
+          }
+          if (more) {
+            if (t == 0) {
+              k_ready(g + 1);
+              if (!ok) break;
+              next_flags = sm.note[(g + 1) % kSteps].flags;
+            }
+            if (t == 0) scores(g + 1, 0, next_flags, !(next_flags & kSecond));
+            else if (next_flags & kSecond) scores(g + 1, 1, next_flags, true);
+            if (!ok) break;
+          }
+        }
+        flags = next_flags;
+      }
+      if (!ok) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
+      mma_commit(&sm.done);  // arrives when every product issued has completed
+      mbar_wait(&sm.done, 0);
+    }
+    __syncwarp();
+  } else if (warp >= kFixWarp) {
+    if constexpr (!kE4m3) {
+      // ---- entries of V that are not part of the request or not finite, in key tiles
+      // that some row sees in part
+      for (int g = 0; g < steps && ok; ++g) {
+        const int u = 2 * g + 1, s = u % S::kUnits;
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[s], (u / S::kUnits) & 1));
+        if (!ok) break;
+        const StepNote& n = sm.note[g % kSteps];
+        if ((n.flags & kFirst) && lane == 0) sm.bad[n.item % kSteps] = 0;
+        __syncwarp();
+        if (!(n.flags & kWhole)) {
+          bool any = false;
+#pragma unroll 4
+          for (int i = lane; i < S::kPanels * kTile * 8; i += 32) {  // 16-byte chunks, eight to a panel's row
+            const int row = (i >> 3) & (kTile - 1);
+            const bool in = n.start + row >= n.begin && n.start + row < n.end;
+            uint4* at = reinterpret_cast<uint4*>(sm.unit[s] + (i / (8 * kTile)) * kTile * 128 +
+                                                 swizzled<128>(row, i & 7));
+            uint4 x = *at;
+            const uint4 out = make_uint4(not_finite(x.x), not_finite(x.y), not_finite(x.z), not_finite(x.w));
+            const bool bad = (out.x | out.y | out.z | out.w) != 0;
+            any |= bad && in;
+            if (bad || !in)
+              *at = in ? make_uint4(x.x & ~out.x, x.y & ~out.y, x.z & ~out.z, x.w & ~out.w) : make_uint4(0, 0, 0, 0);
+          }
+          if (any) sm.bad[n.item % kSteps] = 1;
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.fixed[g % kSteps]);
+      }
+    } else {
+      // ---- codes to bf16, four warps
+      const int at = tid - 32 * kFixWarp;
+      for (int u = 0; u < 2 * steps && ok; ++u) {
+        const int r = u % S::kRawUnits, s = u % S::kUnits, g = u >> 1, kv = u & 1;
+        ok = mbar_wait(&sm.raw_full[r], (u / S::kRawUnits) & 1);
+        if (u >= S::kUnits) ok = ok && mbar_wait(&sm.empty[s], (u / S::kUnits - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const StepNote& n = sm.note[g % kSteps];
+        {
+          const int row = n.row[at / min(p.c.page_size, kTile)];
+          const float* scales = kv ? p.c.v_scale : p.c.k_scale;
+          float f = 0.f;
+          if (row >= 0) f = __ldg(scales + row + at % min(p.c.page_size, kTile));
+          sm.scale[g % kSteps][kv][at] = kv ? f : f * (p.scale * kLog2E);
+        }
+        constexpr int kPieces = D / 16;  // 16-code pieces of a row
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int idx = i * 128 + at, row = idx / kPieces, c = idx % kPieces;
+          const uint4 x = *reinterpret_cast<const uint4*>(sm.raw[r] + row * D + c * 16);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          uint32_t y[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[2 * e] = widen(__byte_perm(w[e], 0, 0x1404));
+            y[2 * e + 1] = widen(__byte_perm(w[e], 0, 0x3424));
+          }
+          unsigned char* to = sm.unit[s] + ((2 * c) >> 3) * kTile * 128;
+          *reinterpret_cast<uint4*>(to + swizzled<128>(row, (2 * c) & 7)) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(to + swizzled<128>(row, (2 * c + 1) & 7)) = make_uint4(y[4], y[5], y[6], y[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.full[s]);
+          mbar_arrive(&sm.raw_empty[r]);
+        }
+      }
+    }
+    if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
+  } else {
+    // ---- the softmax: one row per thread
+    const int t = warp >> 2, r = tid & (kM - 1);
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t s_col = lanes + t * kTile, o_col = lanes + S::kColO + t * D, p_col = lanes + S::col_p(t);
+    const float c = p.scale * kLog2E;
+    const int tok_in = r / p.G, g_in = r - tok_in * p.G;
+    const float2 c2 = make_float2(c, c);
+    Walk w;
+    w.start(p, pair, sm.start_b, sm.start_unit, u1 - u0, lane);
+    int g = 0, done_steps = 0;  // steps so far: of the CTA, of this row tile
+    long long unit = u0;
+    for (int item = 0; w.left > 0 && ok; ++item, unit += w.count(), w.next(p, pair, lane)) {
+      const int count = w.count(), L = w.r.L, n = w.r.n;
+      const int token0 = w.token0 + t * per_tile;
+      if (token0 >= n) {  // the item has no second row tile
+        g += count;
+        continue;
+      }
+      const int token = token0 + tok_in, pos = L - n + token;
+      const int row_lo = seen_lo(p, pos), row_hi = min(seen_hi(p, pos, L), L);
+      const int tile_first = L - n + token0, tile_last = L - n + min(n, token0 + per_tile) - 1;
+      const int start0 = (w.span.first + w.tile) * kTile;
+      float m = -INFINITY;
+      float2 l2 = make_float2(0.f, 0.f);
+      for (int i = 0; i < count; ++i, ++g, ++done_steps) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[t], done_steps & 1));
+        if (!ok) break;
+        tc_fence_after();
+        const int start = start0 + i * kTile;
+        // whole key tiles of a bf16 cache take x = c S in one product with the subtraction
+        const bool whole = sees_whole(p, L, tile_first, tile_last, start);
+        const bool plain = !kE4m3 && whole && c >= 0.f;
+        const float* k_scale = sm.scale[kE4m3 ? g % kSteps : 0][0];
+        const float* v_scale = sm.scale[kE4m3 ? g % kSteps : 0][1];
+        // scores in units of log 2 of columns col .. col + 31; what is not seen: -infinity
+        auto scored = [&](float(&x)[32], int col) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float2 a = make_float2(x[e], x[e + 1]), b = make_float2(x[e + 2], x[e + 3]);
+            if constexpr (kE4m3) {
+              const float4 f = *reinterpret_cast<const float4*>(k_scale + col + e);
+              a = __fmul2_rn(a, make_float2(f.x, f.y));
+              b = __fmul2_rn(b, make_float2(f.z, f.w));
+            } else {
+              a = __fmul2_rn(a, c2);
+              b = __fmul2_rn(b, c2);
+            }
+            x[e] = a.x;
+            x[e + 1] = a.y;
+            x[e + 2] = b.x;
+            x[e + 3] = b.y;
+          }
+          if (!whole) {
+            const uint32_t see = columns(row_lo - start - col, row_hi - start - col);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(see >> e & 1)) x[e] = -INFINITY;
+          }
+        };
+        auto highest = [](const float(&x)[32]) {
+          float y[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int e = 4; e < 32; ++e) y[e & 3] = fmaxf(y[e & 3], x[e]);
+          return fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+        };
+        float x0[32], x1[32];
+        tmem_ld_32cols(s_col, x0);
+        tmem_ld_32cols(s_col + 32, x1);
+        tmem_ld_wait();
+        if (!plain) {
+          scored(x0, 0);
+          scored(x1, 32);
+        }
+        float top = fmaxf(highest(x0), highest(x1));
+        tmem_ld_32cols(s_col + 64, x0);
+        tmem_ld_32cols(s_col + 96, x1);
+        tmem_ld_wait();
+        if (!plain) {
+          scored(x0, 64);
+          scored(x1, 96);
+        }
+        top = fmaxf(top, fmaxf(highest(x0), highest(x1)));
+        if (plain) top *= c;
+
+        const float now = fmaxf(m, top);
+        if (__any_sync(0xffffffffu, now > m + kGrow)) {
+          const float keep = exp2_approx(m - (now == -INFINITY ? 0.f : now));
+          l2.x *= keep;
+          l2.y *= keep;
+          // this S came after the product before it, so O is at rest
+          if (i > 0) {
+#pragma unroll
+            for (int cc = 0; cc < D; cc += 32) {
+              float o[32];
+              tmem_ld_32cols(o_col + cc, o);
+              tmem_ld_wait();
+              uint32_t ob[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ob[e] = __float_as_uint(o[e] * keep);
+              tmem_st_32cols(o_col + cc, ob);
+            }
+          }
+          m = now;
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        const float2 nref = make_float2(-ref, -ref);
+        // weights of two times 32 columns, as bf16 pairs
+        auto weigh = [&](const float(&x)[32], int col, uint32_t* out) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 xx = make_float2(x[e], x[e + 1]);
+            const float2 y = plain ? __ffma2_rn(xx, c2, nref) : __fadd2_rn(xx, nref);
+            float2 v = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+            l2 = __fadd2_rn(l2, v);
+            if constexpr (kE4m3) {
+              // a weight of 0 stays 0 whatever the scale of a place that is not seen
+              const float2 f = *reinterpret_cast<const float2*>(v_scale + col + e);
+              v.x = xx.x == -INFINITY ? 0.f : v.x * f.x;
+              v.y = xx.y == -INFINITY ? 0.f : v.y * f.y;
+            }
+            out[e / 2] = pack_bf16(v.x, v.y);
+          }
+        };
+        if constexpr (kE4m3) {  // V's scales are written with V
+          const int u = 2 * g + 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[u % S::kUnits], (u / S::kUnits) & 1));
+          if (!ok) break;
+        }
+        uint32_t pw[32];
+        weigh(x0, 64, pw);
+        weigh(x1, 96, pw + 16);
+        tmem_st_32cols(p_col + 32, pw);
+        tmem_ld_32cols(s_col, x0);
+        tmem_ld_32cols(s_col + 32, x1);
+        tmem_ld_wait();
+        if (!plain) {
+          scored(x0, 0);
+          scored(x1, 32);
+        }
+        weigh(x0, 0, pw);
+        weigh(x1, 32, pw + 16);
+        tmem_st_32cols(p_col, pw);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[t]);
+      }
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_done[t], (done_steps - 1) & 1));
+      if (!ok) break;
+      // ---- the end of this CTA's part of the item
+      tc_fence_after();
+      const float l = l2.x + l2.y;
+      const bool begins = w.tile == 0, ends = w.tile + count == w.span.tiles;
+      const bool done = begins && ends;
+      const bool live = tok_in < per_tile && token < n;
+      const size_t out_row = (size_t)(w.r.t0 + token) * p.H + w.h * p.G + g_in;
+      const size_t piece = ((size_t)cta * 2 + (begins ? 1 : 0)) * kChunkRows + t * per_tile * p.G + r;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const bool bad = !kE4m3 && sm.bad[item % kSteps] != 0;
+      if (live) {
+        if (!done) pieces.ml[piece] = make_float2(m, l);
+        else if (p.lse) p.lse[out_row] = (m + log2f(l)) * kLn2;
+      }
+      if (tid == 0 && begins && !ends)
+        pieces.notes[cta] = PieceNote{(w.r.t0 + w.token0) * p.H + w.h * p.G, min(pair, n - w.token0),
+                                      share_of(units, used, unit + w.span.tiles - 1) - cta + 1, 0};
+#pragma unroll 1
+      for (int cc = 0; cc < D; cc += 32) {
+        float o[32];
+        tmem_ld_32cols(o_col + cc, o);
+        tmem_ld_wait();
+        if (live && bad) {
+          float x[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = o[e];
+          add_bad_values<D>(p, w.b, w.h, L, pos, L - n + w.token0, L - n + min(n, w.token0 + pair) - 1, start0, count,
+                          p.q + (w.r.t0 + token) * p.q_stride + (size_t)(w.h * p.G + g_in) * D,
+                          m == -INFINITY ? 0.f : m, cc, x);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = x[e];
+        }
+        if (live && done) {
+          uint4* to = reinterpret_cast<uint4*>(p.out + out_row * D + cc);
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            to[e / 8] = make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                                   pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+        } else if (live) {
+          float4* to = reinterpret_cast<float4*>(pieces.o + piece * D + cc);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) to[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+        __syncwarp();  // the next load is the whole warp's
+      }
+    }
+    if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, bool kE4m3>
+cudaError_t launch_chunk(const AttentionArgs& a, cudaStream_t stream) {
+  using Sm = Smem<D, kE4m3>;
+  using S = Shape<D, kE4m3>;
+  static_assert(sizeof(Sm) + 1024 <= 227 * 1024, "a chunk CTA fits an SM");
+  CUtensorMap q_map, maps[2];
+  const int per_tile = kM / a.G;
+  if (!make_map_3d_bf16(&q_map, a.q, D, a.H, a.T, D * 2, (uint64_t)a.q_stride * 2, 64, a.G, per_tile))
+    return cudaErrorInvalidValue;
+  const uint64_t rows = (uint64_t)a.c.num_pages * a.c.HKV * a.c.page_size;
+  for (int i = 0; i < 2; ++i)
+    if (!make_map_2d(&maps[i], kE4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                     kE4m3 ? 1 : 2, i ? a.c.v : a.c.k, D, rows, kE4m3 ? D : 64, a.c.page_size,
+                     kE4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  const size_t smem = sizeof(Sm) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<D, kE4m3>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const Pieces pieces = pieces_at(a.workspace, kChunkCtas, kChunkRows);
+  e = launch(chunk_kernel<D, kE4m3>, dim3(kChunkCtas), dim3(S::kThreads), smem, stream, true, q_map, maps[0],
+             maps[1], a, pieces);
+  if (e != cudaSuccess) return e;
+  return launch_join_pieces(a, pieces, kChunkRows, kChunkCtas, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_attention(const AttentionArgs& a, cudaStream_t stream) {
+  if (a.c.D == 128)
+    return a.c.e4m3 ? launch_chunk<128, true>(a, stream) : launch_chunk<128, false>(a, stream);
+  return a.c.e4m3 ? launch_chunk<64, true>(a, stream) : launch_chunk<64, false>(a, stream);
+}
+
+}  // namespace kda

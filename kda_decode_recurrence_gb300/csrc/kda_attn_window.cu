@@ -64,17 +64,10 @@ struct Smem {
   float4 top[kRows];                               // the warps' row maxima
   StageNote note[S::kStages];
   uint64_t full[S::kStages], empty[S::kStages], qfull[2], qempty[2];
-  long long part[32];
+  long long part[kThreads / 32];
   int start_b;
   long long start_unit;
 };
-
-// Byte offset of 16-byte chunk c of row r in a panel of kPanelBytes rows under TMA's
-// 128- or 64-byte swizzle.
-template <int kPanelBytes>
-__device__ __forceinline__ int swizzled(int r, int c) {
-  return kPanelBytes == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-}
 
 __device__ __forceinline__ void ldsm(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -92,21 +85,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two e4m3 codes, one in the high byte of each half of x (low bytes 0), as bf16 values:
-// s eeee mmm becomes a bf16 of exponent field eeee, 2^-120 too small (subnormal
-// codes and bf16 subnormals alike), and one exact product puts that right.
-__device__ __forceinline__ uint32_t widen(uint32_t x) {
-  const uint32_t y = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x7b807b80u));  // 2^120, twice
-  return r;
-}
-
-__device__ __forceinline__ uint32_t pack(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // Barriers of the computing warps; the second also says whether all of them go on.
 __device__ __forceinline__ void compute_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kComputeWarps) : "memory");
@@ -119,10 +97,6 @@ __device__ __forceinline__ bool compute_sync_and(bool ok) {
       : "=r"(all) : "r"((uint32_t)ok), "n"(32 * kComputeWarps) : "memory");
   return all != 0;
 }
-__device__ __forceinline__ void arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
 // Units of a request: 0 if it is not this kernel's, else HKV x its key tiles
 // (at least one each: rows that see nothing are written too).
 __device__ __forceinline__ int first_tile(const AttentionArgs& p, const Request& r) {
@@ -225,21 +199,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int b_lo = min(p.B, tid * run), b_hi = min(p.B, b_lo + run);
   long long mine = 0;
   for (int b = b_lo; b < b_hi; ++b) mine += units_of(p, load_request(p, b, cta == 0));
-  long long scan = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, scan, o);
-    if (lane >= o) scan += y;
-  }
-  if (lane == 31) sm.part[warp] = scan;
-  __syncthreads();
-  long long before = 0, units = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += sm.part[w];
-    units += sm.part[w];
-  }
-  const long long from = before + scan - mine;
+  long long units;
+  const long long from = scan_before<kThreads / 32>(mine, sm.part, units);
   const int used = (int)min((long long)ctas, units);
   if (tid == 0) pieces.notes[cta].tokens = 0;
   if (cta >= used) return;
@@ -290,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
         const int s = it % S::kStages;
-        if (it >= S::kStages) ok = mbar_wait(&sm.empty[s], (it / S::kStages - 1) & 1);
+        if (it >= S::kStages) ok = __all_sync(0xffffffffu, mbar_wait(&sm.empty[s], (it / S::kStages - 1) & 1));
         if (!ok) break;
         const int start = (t_first + w.tile + i) * kTile;
         if (lane == 0) {
@@ -349,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     bool ok = true;
     for (int it = 0; w.left > 0 && ok; ++it) {
       const int s = it & 1;
-      if (it >= 2) ok = mbar_wait(&sm.qempty[s], (it / 2 - 1) & 1);
+      if (it >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&sm.qempty[s], (it / 2 - 1) & 1));
       if (!ok) break;
       constexpr int kChunks = D / 8;  // 16-byte chunks of a row
       const int rows = w.r.n * p.G;
@@ -376,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       __syncwarp();
-      if (lane == 0) arrive(&sm.qfull[s]);
+      if (lane == 0) mbar_arrive(&sm.qfull[s]);
       w.next(p, lane);
     }
     if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
@@ -530,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               y1 = x[r][n][2 * half + 1] == -INFINITY ? 0.f : w1 * v_scale[n][1];
             }
             const int row = 16 * r + 8 * half + quad;
-            *reinterpret_cast<uint32_t*>(sm.pw + swizzled<128>(row, 2 * warp + n) + j2 * 2) = pack(y0, y1);
+            *reinterpret_cast<uint32_t*>(sm.pw + swizzled<128>(row, 2 * warp + n) + j2 * 2) = pack_bf16(y0, y1);
           }
         }
       compute_sync();
@@ -644,8 +605,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       __syncwarp();
       if (lane == 0) {
-        arrive(&sm.empty[s]);
-        if (note.flags & kLast) arrive(&sm.qempty[item & 1]);
+        mbar_arrive(&sm.empty[s]);
+        if (note.flags & kLast) mbar_arrive(&sm.qempty[item & 1]);
       }
       if (!(note.flags & kLast)) continue;
 
@@ -686,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int n = 0; n < kN; ++n) {
               const int col = warp * (D / kComputeWarps) + 8 * n + j2;
               const float y0 = o[r][n][2 * half], y1 = o[r][n][2 * half + 1];
-              if (done) *reinterpret_cast<uint32_t*>(p.out + out_row * D + col) = pack(y0 * inv, y1 * inv);
+              if (done) *reinterpret_cast<uint32_t*>(p.out + out_row * D + col) = pack_bf16(y0 * inv, y1 * inv);
               else *reinterpret_cast<float2*>(pieces.o + piece * D + col) = make_float2(y0, y1);
             }
           } else {
@@ -697,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               const float y2 = o[r][n][2 * half + 1], y3 = o[r][n + 1][2 * half + 1];
               if (done)
                 *reinterpret_cast<uint2*>(p.out + out_row * D + col) =
-                    make_uint2(pack(y0 * inv, y1 * inv), pack(y2 * inv, y3 * inv));
+                    make_uint2(pack_bf16(y0 * inv, y1 * inv), pack_bf16(y2 * inv, y3 * inv));
               else
                 *reinterpret_cast<float4*>(pieces.o + piece * D + col) = make_float4(y0, y1, y2, y3);
             }
@@ -727,11 +688,11 @@ cudaError_t launch_window(const AttentionArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(window_kernel<D, kRows, kE4m3>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const Pieces pieces = pieces_at(a.workspace, kRows);
-  e = launch(window_kernel<D, kRows, kE4m3>, dim3(kMaxAttnCtas), dim3(kThreads), smem, stream, true,
+  const Pieces pieces = pieces_at(a.workspace, kWindowCtas, kRows);
+  e = launch(window_kernel<D, kRows, kE4m3>, dim3(kWindowCtas), dim3(kThreads), smem, stream, true,
              maps[0], maps[1], a, pieces);
   if (e != cudaSuccess) return e;
-  return launch_join_pieces(a, pieces, kRows, kMaxAttnCtas, stream);
+  return launch_join_pieces(a, pieces, kRows, kWindowCtas, stream);
 }
 
 template <int D, bool kE4m3>

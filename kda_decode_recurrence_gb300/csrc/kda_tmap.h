@@ -44,4 +44,20 @@ inline bool make_map_2d(CUtensorMap* map, CUtensorMapDataType type, uint32_t ele
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3-D map with the 128-byte swizzle: `inner` contiguous bf16 elements, then extents y
+// and z with their strides in bytes (multiples of 16).
+inline bool make_map_3d_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t y,
+                             uint64_t z, uint64_t y_bytes, uint64_t z_bytes, uint32_t box_inner,
+                             uint32_t box_y, uint32_t box_z) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {inner, y, z};
+  const cuuint64_t strides[2] = {y_bytes, z_bytes};
+  const cuuint32_t box[3] = {box_inner, box_y, box_z};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace kda
