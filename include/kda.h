@@ -309,7 +309,7 @@ size_t kda_block_tkg_workspace_size(int B, int n, int Hd, int nh, int K, int V, 
  *   KDA_CACHE_E4M3   e4m3 codes (8 bits) and fp32 scales [num_pages, HKV,
  *                    page_size], one per row: the row is code * scale.  The
  *                    codes 0x7f and 0xff stand for no value and are not stored.
- * D is 64 or 128, page_size 16, 32, 64 or 128; caches and scales are aligned to 16 B.
+ * D is 64 or 128, page_size 16, 32, 64 or 128, HKV at most 4096; caches and scales are aligned to 16 B.
  *   page_table  [B, max_pages] int32: the page that holds request b's positions
  *               i * page_size .. (i + 1) * page_size - 1.  Entries that no
  *               position in use needs are not read.

@@ -217,7 +217,7 @@ kda_status check_cache(kda::PagedCache& c, const void* k, const void* v, const f
       (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128))
     return KDA_ERR_UNSUPPORTED;
   // Positions are 32-bit, and so are row numbers of the cache (a copy's coordinate).
-  if ((long long)max_pages * page_size > 0x40000000LL ||
+  if (HKV > 4096 || (long long)max_pages * page_size > 0x40000000LL ||
       (long long)num_pages * HKV > (0x7fffffffLL - 128) / page_size || (long long)T * HKV > 0x3fffffffLL)
     return KDA_ERR_UNSUPPORTED;
   if (B == 0 || T == 0) return KDA_OK;

@@ -36,9 +36,9 @@ struct Request {
 // `report`: raise the status bit of a malformed request (one CTA does).
 __device__ __forceinline__ Request load_request(const AttentionArgs& p, int b, bool report) {
   Request r;
-  r.t0 = __ldg(p.cu + b);
-  r.n = __ldg(p.cu + b + 1) - r.t0;
-  r.L = __ldg(p.lens + b);
+  r.t0 = fresh(p.cu + b);
+  r.n = fresh(p.cu + b + 1) - r.t0;
+  r.L = fresh(p.lens + b);
   const bool good = r.t0 >= 0 && r.n >= 0 && r.t0 + (long long)r.n <= p.T && r.n <= p.max_tokens &&
                     r.L >= 0 && r.L <= (long long)p.c.max_pages * p.c.page_size;
   if (!good) {

@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
           const int pos = (box_first + i * boxes + lane) * rows_per_box;
           page = -1;
           if (pos < hi && pos + rows_per_box > lo) {
-            page = __ldg(table + pos / p.c.page_size);
+            page = fresh(table + pos / p.c.page_size);
             if (page < 0 || page >= p.c.num_pages) {
               if (pos < (w.span.first + w.tile + count) * kTile) raise_status(p.dev_status, KDA_DEV_BAD_PAGE);
               page = -1;
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
           const int row = n.row[at / min(p.c.page_size, kTile)];
           const float* scales = kv ? p.c.v_scale : p.c.k_scale;
           float f = 0.f;
-          if (row >= 0) f = __ldg(scales + row + at % min(p.c.page_size, kTile));
+          if (row >= 0) f = fresh(scales + row + at % min(p.c.page_size, kTile));
           sm.scale[g % kSteps][kv][at] = kv ? f : f * (p.scale * kLog2E);
         }
         constexpr int kPieces = D / 16;  // 16-code pieces of a row

@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           const int pos = (box_first + i * boxes + lane) * rows_per_box;
           page = -2;  // no position in use: zeros, no report
           if (pos < w.r.L && pos + rows_per_box > lo) {
-            page = __ldg(table + pos / p.c.page_size);
+            page = fresh(table + pos / p.c.page_size);
             if (page < 0 || page >= p.c.num_pages) {
               if ((long long)pos < (long long)(t_first + w.tile + count) * kTile)
                 raise_status(p.dev_status, KDA_DEV_BAD_PAGE);
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int row = i / kChunks, c = i % kChunks;
         uint4 x = make_uint4(0, 0, 0, 0);
         if (row < rows)
-          x = __ldg(reinterpret_cast<const uint4*>(
+          x = fresh(reinterpret_cast<const uint4*>(
               p.q + (w.r.t0 + row / p.G) * p.q_stride + (size_t)(w.h * p.G + row % p.G) * D + c * 8));
         if (kE4m3) {
           // Four consecutive entries of K sit in one register of the tensor core's

@@ -10,6 +10,7 @@
 #include <cuda_fp8.h>
 
 #include "kda_common.cuh"
+#include "kda_launch.h"
 #include "kda_paged.h"
 
 namespace kda {
@@ -24,7 +25,7 @@ __device__ __forceinline__ int find_request(const int32_t* cu, int B, int t) {
   int lo = 0, hi = B - 1;  // the answer lies in lo..hi
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(cu + mid + 1) > t) hi = mid; else lo = mid + 1;
+    if (fresh(cu + mid + 1) > t) hi = mid; else lo = mid + 1;
   }
   return lo;
 }
@@ -34,12 +35,12 @@ template <bool kAppend>
 __device__ __forceinline__ int2 find_place(const CacheRowsArgs& p, int t) {
   const int2 none = make_int2(-1, 0);
   const int b = find_request(p.cu, p.B, t);
-  const int t0 = __ldg(p.cu + b), t1 = __ldg(p.cu + b + 1);
+  const int t0 = fresh(p.cu + b), t1 = fresh(p.cu + b + 1);
   if (t < t0 || t >= t1 || t0 < 0 || t1 > p.T) {
     raise_status(p.dev_status, KDA_DEV_BAD_SEQLEN);
     return none;
   }
-  const long long at = p.at ? __ldg(p.at + b) : 0;
+  const long long at = p.at ? fresh(p.at + b) : 0;
   const long long capacity = (long long)p.c.max_pages * p.c.page_size;
   if (at < 0 || (kAppend ? at : at + (t1 - t0)) > capacity) {
     raise_status(p.dev_status, KDA_DEV_BAD_SEQLEN);
@@ -47,7 +48,7 @@ __device__ __forceinline__ int2 find_place(const CacheRowsArgs& p, int t) {
   }
   const long long pos = kAppend ? at - (t1 - t) : at + (t - t0);
   if (pos < 0) return none;  // padding before the sequence's first position
-  const int page = __ldg(p.c.page_table + (size_t)b * p.c.max_pages + pos / p.c.page_size);
+  const int page = fresh(p.c.page_table + (size_t)b * p.c.max_pages + pos / p.c.page_size);
   if (page < 0 || page >= p.c.num_pages) {
     raise_status(p.dev_status, KDA_DEV_BAD_PAGE);
     return none;
@@ -55,95 +56,193 @@ __device__ __forceinline__ int2 find_place(const CacheRowsArgs& p, int t) {
   return make_int2(page, (int)(pos % p.c.page_size));
 }
 
-template <int D, bool kE4m3>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const CacheRowsArgs p) {
-  constexpr int kLanes = D / 8;  // lanes per row, 8 elements each
-  constexpr int kRows = kThreads / kLanes;
-  const int sub = threadIdx.x % kLanes;
-  const long long rows = 2ll * p.T * p.c.HKV;
-  const long long row = (long long)blockIdx.x * kRows + threadIdx.x / kLanes;
-  const bool live = row < rows;
-  const long long r = live ? row : 0;
-  const int h = (int)(r % p.c.HKV);
-  const bool is_v = (r / p.c.HKV) & 1;
-  const int t = (int)(r / (2 * p.c.HKV));
-  const int2 place = find_place<true>(p, t);
-  const kda_bf16* src = is_v ? p.v_rows + t * p.v_stride : p.k_rows + t * p.k_stride;
-  const uint4 x = *reinterpret_cast<const uint4*>(src + (size_t)h * D + sub * 8);
-  const size_t dst = ((size_t)max(place.x, 0) * p.c.HKV + h) * p.c.page_size + place.y;
-  void* cache = is_v ? p.c.v : p.c.k;
-  if (!kE4m3) {
-    if (live && place.x >= 0)
-      *reinterpret_cast<uint4*>(static_cast<kda_bf16*>(cache) + dst * D + sub * 8) = x;
-    return;
+// A warp takes `tokens` consecutive tokens: each lane looks up the place of one, then
+// all their rows follow, kLanes lanes (8 entries each) to a row and kUnroll rows per
+// lane in flight.
+struct Split {
+  int tokens;      // per warp, at most 32
+  uint32_t inv;    // ceil(2^32 / (2 HKV)): r / (2 HKV) = umulhi(r, inv) for the warp's rows r
+};
+constexpr int kUnroll = 4;
+
+template <int D>
+struct Rows {
+  static constexpr int kLanes = D / 8;
+  static constexpr int kPerWarp = 32 / kLanes;
+
+  int t0, rows, sub, mine;
+  int2 place;  // this lane's token's
+
+  template <bool kAppend>
+  __device__ __forceinline__ bool start(const CacheRowsArgs& p, const Split& s) {
+    const int lane = threadIdx.x & 31;
+    const long long first = ((long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * s.tokens;
+    if (first >= p.T) return false;
+    t0 = (int)first;
+    const int tokens = min(s.tokens, p.T - t0);
+    rows = tokens * 2 * p.c.HKV;
+    sub = lane % kLanes;
+    mine = lane / kLanes;
+    place = lane < tokens ? find_place<kAppend>(p, t0 + lane) : make_int2(-1, 0);
+    return true;
   }
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const bool finite = top < 0x7f80u;
-  const float s = !finite ? __uint_as_float(0x7fffffffu)
-                  : top == 0 ? 1.0f : __fdiv_rn(__uint_as_float(top << 16), kE4m3Max);
-  uint32_t code[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 y = make_float2(__fdiv_rn(bf16_lo(w[i]), s), __fdiv_rn(bf16_hi(w[i]), s));
-    code[i >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << (16 * (i & 1));
+  struct Row {
+    int t, h, page;    // token, key head, page (-1: none)
+    bool is_v;
+    size_t at;         // row of the cache
+  };
+  __device__ __forceinline__ Row row(const CacheRowsArgs& p, const Split& s, int r) const {
+    Row x;
+    const int i = min((int)__umulhi((uint32_t)r, s.inv), 31);
+    const int in = r - i * 2 * p.c.HKV;
+    x.is_v = in >= p.c.HKV;
+    x.h = x.is_v ? in - p.c.HKV : in;
+    x.t = t0 + i;
+    x.page = __shfl_sync(0xffffffffu, place.x, i);
+    const int off = __shfl_sync(0xffffffffu, place.y, i);
+    x.at = ((size_t)max(x.page, 0) * p.c.HKV + x.h) * p.c.page_size + off;
+    return x;
   }
-  if (live && place.x >= 0) {
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + dst * D + sub * 8) =
-        make_uint2(code[0], code[1]);
-    if (sub == 0) (is_v ? p.c.v_scale : p.c.k_scale)[dst] = s;
-  }
+};
+
+// x / s rounded to nearest, r = 1 / s rounded to nearest: one correction by the exact
+// remainder (Markstein), for s > 0 far from the ends of fp32's range.
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+  const float y = x * r;
+  return copysignf(fmaf(fmaf(-s, y, x), r, y), x);  // a zero keeps its sign
 }
 
 template <int D, bool kE4m3>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheRowsArgs p) {
-  constexpr int kLanes = D / 8;
-  constexpr int kRows = kThreads / kLanes;
-  const int sub = threadIdx.x % kLanes;
-  const long long rows = 2ll * p.T * p.c.HKV;
-  const long long row = (long long)blockIdx.x * kRows + threadIdx.x / kLanes;
-  if (row >= rows) return;
-  const int h = (int)(row % p.c.HKV);
-  const bool is_v = (row / p.c.HKV) & 1;
-  const int t = (int)(row / (2 * p.c.HKV));
-  const int2 place = find_place<false>(p, t);
-  uint4 x = make_uint4(0, 0, 0, 0);
-  if (place.x >= 0) {
-    const size_t src = ((size_t)place.x * p.c.HKV + h) * p.c.page_size + place.y;
-    const void* cache = is_v ? p.c.v : p.c.k;
-    if (kE4m3) {
-      const uint2 code = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(cache) + src * D + sub * 8);
-      const float s = (is_v ? p.c.v_scale : p.c.k_scale)[src];
-      uint32_t o[4];
+__global__ void __launch_bounds__(kThreads) cache_append_kernel(const CacheRowsArgs p, const Split split) {
+  using R = Rows<D>;
+  R rows;
+  pdl_wait();
+  pdl_trigger();
+  if (!rows.template start<true>(p, split)) return;
+  for (int base = 0; base < rows.rows; base += R::kPerWarp * kUnroll) {
+    uint4 x[kUnroll];
+    typename R::Row row[kUnroll];
+    bool live[kUnroll];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t pair = ((i < 2 ? code.x : code.y) >> (16 * (i & 1))) & 0xffffu;
-        const __half2 y(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)pair, __NV_E4M3));
-        const float2 f = __half22float2(y);
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
-        o[i] = *reinterpret_cast<const uint32_t*>(&b);
+    for (int u = 0; u < kUnroll; ++u) {
+      const int r = base + u * R::kPerWarp + rows.mine;
+      live[u] = r < rows.rows;
+      row[u] = rows.row(p, split, live[u] ? r : 0);
+      const kda_bf16* src = row[u].is_v ? p.v_rows + row[u].t * p.v_stride : p.k_rows + row[u].t * p.k_stride;
+      x[u] = fresh(reinterpret_cast<const uint4*>(src + (size_t)row[u].h * D + rows.sub * 8));
+      live[u] = live[u] && row[u].page >= 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      void* cache = row[u].is_v ? p.c.v : p.c.k;
+      if constexpr (!kE4m3) {
+        if (live[u]) *reinterpret_cast<uint4*>(static_cast<kda_bf16*>(cache) + row[u].at * D + rows.sub * 8) = x[u];
+      } else {
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+#pragma unroll
+        for (int o = R::kLanes / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = max(top & 0xffffu, top >> 16);
+        const bool finite = top < 0x7f80u;
+        const float s = !finite ? __uint_as_float(0x7fffffffu)
+                        : top == 0 ? 1.0f : __fdiv_rn(__uint_as_float(top << 16), kE4m3Max);
+        float y[8];
+        if (s > 0x1p-60f && s < 0x1p60f) {
+          const float r = __frcp_rn(s);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y[2 * i] = quotient(bf16_lo(w[i]), s, r);
+            y[2 * i + 1] = quotient(bf16_hi(w[i]), s, r);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y[2 * i] = __fdiv_rn(bf16_lo(w[i]), s);
+            y[2 * i + 1] = __fdiv_rn(bf16_hi(w[i]), s);
+          }
+        }
+        uint32_t code[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          code[i >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y[2 * i], y[2 * i + 1]), __NV_SATFINITE,
+                                                             __NV_E4M3) << (16 * (i & 1));
+        if (live[u]) {
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + row[u].at * D + rows.sub * 8) =
+              make_uint2(code[0], code[1]);
+          if (rows.sub == 0) (row[u].is_v ? p.c.v_scale : p.c.k_scale)[row[u].at] = s;
+        }
       }
-      x = make_uint4(o[0], o[1], o[2], o[3]);
-    } else {
-      x = *reinterpret_cast<const uint4*>(static_cast<const kda_bf16*>(cache) + src * D + sub * 8);
     }
   }
-  kda_bf16* out = is_v ? p.v_rows + t * p.v_stride : p.k_rows + t * p.k_stride;
-  *reinterpret_cast<uint4*>(out + (size_t)h * D + sub * 8) = x;
 }
 
+template <int D, bool kE4m3>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheRowsArgs p, const Split split) {
+  using R = Rows<D>;
+  R rows;
+  pdl_wait();
+  pdl_trigger();
+  if (!rows.template start<false>(p, split)) return;
+  for (int base = 0; base < rows.rows; base += R::kPerWarp * kUnroll) {
+    uint4 x[kUnroll];
+    float s[kUnroll];
+    typename R::Row row[kUnroll];
+    bool live[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int r = base + u * R::kPerWarp + rows.mine;
+      live[u] = r < rows.rows;
+      row[u] = rows.row(p, split, live[u] ? r : 0);
+      x[u] = make_uint4(0, 0, 0, 0);
+      s[u] = 0.f;
+      const void* cache = row[u].is_v ? p.c.v : p.c.k;
+      if (live[u] && row[u].page >= 0) {
+        if constexpr (kE4m3) {
+          const uint2 c = fresh(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(cache) +
+                                                               row[u].at * D + rows.sub * 8));
+          x[u].x = c.x;
+          x[u].y = c.y;
+          s[u] = fresh((row[u].is_v ? p.c.v_scale : p.c.k_scale) + row[u].at);
+        } else {
+          x[u] = fresh(reinterpret_cast<const uint4*>(static_cast<const kda_bf16*>(cache) +
+                                                      row[u].at * D + rows.sub * 8));
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if constexpr (kE4m3) {
+        const uint32_t c[2] = {x[u].x, x[u].y};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t pair = (c[i >> 1] >> (16 * (i & 1))) & 0xffffu;
+          const __half2 y(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)pair, __NV_E4M3));
+          const float2 f = __half22float2(y);
+          const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s[u], f.y * s[u]);
+          o[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        x[u] = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      kda_bf16* out = row[u].is_v ? p.v_rows + row[u].t * p.v_stride : p.k_rows + row[u].t * p.k_stride;
+      if (live[u]) *reinterpret_cast<uint4*>(out + (size_t)row[u].h * D + rows.sub * 8) = x[u];
+    }
+  }
+}
+
+// As many tokens to a warp as leave every SM's 64 warps something to do (one look-up
+// then serves several rows in flight), eight at most.
 template <typename Kernel>
 cudaError_t run(Kernel kernel, const CacheRowsArgs& a, cudaStream_t stream) {
-  const long long rows = 2ll * a.T * a.c.HKV;
-  const int per_cta = kThreads / (a.c.D / 8);
-  const long long grid = (rows + per_cta - 1) / per_cta;
-  if (grid == 0) return cudaSuccess;
-  kernel<<<(unsigned)grid, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  if (a.T == 0) return cudaSuccess;
+  constexpr int kAllWarps = 152 * 64;
+  Split s;
+  s.tokens = a.T / kAllWarps < 1 ? 1 : a.T / kAllWarps > 8 ? 8 : a.T / kAllWarps;
+  s.inv = (uint32_t)(((1ull << 32) + 2 * a.c.HKV - 1) / (2 * a.c.HKV));
+  const long long per_cta = (long long)(kThreads / 32) * s.tokens;
+  return launch(kernel, dim3((unsigned)((a.T + per_cta - 1) / per_cta)), dim3(kThreads), 0, stream, true, a, s);
 }
 
 }  // namespace

@@ -37,6 +37,11 @@ __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// A load that stays behind pdl_wait() (the read-only path's loads may be moved): what
+// an earlier kernel of the stream may have written.
+template <typename T>
+__device__ __forceinline__ T fresh(const T* p) { return *p; }
+
 __device__ __forceinline__ void raise_status(int32_t* status, int32_t bit) {
   if (status != nullptr) atomicOr(status, bit);
 }

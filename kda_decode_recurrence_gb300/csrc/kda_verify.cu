@@ -9,9 +9,14 @@
 // A draw reads two rows of V probabilities (one if all drafts were accepted) and
 // does about 13 operations per entry: HBM bounds it.  fp64 adds cannot keep
 // up (152 SMs x 2 per clock = 0.6 T/s against 0.8 T entries/s from HBM), so
-// sums are pairs of fp32 (hi + lo, about 48 bits) per lane and fp64 only where
-// lanes are joined: the drawn token has to be the same for any order of
+// sums are pairs of fp32 (hi + lo, about 48 bits) within a warp and fp64 only
+// where warps are joined: the drawn token has to be the same for any order of
 // summation, and neighbours in a large vocabulary lie 1e-6 of the sum apart.
+//
+// A cluster of CTAs serves a request, its warps a segment of the row each; the
+// segments' sums meet through distributed shared memory, so that one launch does
+// it all.  The cluster has as many CTAs (8, 4, 2 or 1) as let all requests run at
+// once: a second wave would find few CTAs left to keep HBM busy.
 #include <cooperative_groups.h>
 
 #include "kda_common.cuh"
@@ -24,8 +29,9 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCluster = 8;                  // CTAs per request
-constexpr int kSegments = kWarps * kCluster;  // a row is cut into one segment per warp
+constexpr int kMaxCluster = 8;               // CTAs per request
+constexpr int kCtasPerSm = 8;
+constexpr int kSms = 152;
 constexpr int kBlocks = 8;                   // blocks a segment is searched by
 
 struct Pair {
@@ -40,10 +46,13 @@ __device__ __forceinline__ void add(Pair& s, float d, float e) {
   s.hi = t;
 }
 
-__device__ __forceinline__ double warp_total(double x) {
+__device__ __forceinline__ double warp_total(Pair s) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+  for (int o = 16; o > 0; o >>= 1) {
+    const float hi = __shfl_xor_sync(0xffffffffu, s.hi, o), lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
+    add(s, hi, lo);
+  }
+  return (double)s.hi + (double)s.lo;
 }
 
 __device__ __forceinline__ double warp_scan(double x, int lane) {
@@ -76,7 +85,7 @@ struct Weights {
 // This lane's share of the weights lo..hi-1 (entries lo + lane, + 32, ...).
 template <bool kHasQ>
 __device__ __forceinline__ Pair lane_sum(const Weights& w, int lo, int hi, int lane) {
-  constexpr int kUnroll = 8;
+  constexpr int kUnroll = 4;
   Pair s = {0.f, 0.f};
   int v = lo + lane;
   for (; v + 32 * (kUnroll - 1) < hi; v += 32 * kUnroll) {
@@ -100,8 +109,6 @@ __device__ __forceinline__ Pair lane_sum(const Weights& w, int lo, int hi, int l
   return s;
 }
 
-__device__ __forceinline__ double total(const Pair& s) { return (double)s.hi + (double)s.lo; }
-
 // The first lane with a weight x whose inclusive running sum c passes `target`;
 // if rounding lets none pass, the last lane with a weight (0: no weight at all).
 __device__ __forceinline__ int first_past(double c, double x, double target) {
@@ -110,14 +117,13 @@ __device__ __forceinline__ int first_past(double c, double x, double target) {
   return past ? __ffs(past) - 1 : some ? 31 - __clz(some) : 0;
 }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
-    verify_kernel(const VerifyArgs a) {
-  __shared__ int s_taken;
-  __shared__ double s_own[kWarps];
-  __shared__ double s_all[kSegments];
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const VerifyArgs a, const int size) {
+  __shared__ int s_taken, s_found;
+  __shared__ double s_own[kWarps], s_base, s_target;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
-  const int b = blockIdx.x / kCluster;
+  const int segments = kWarps * size;  // of a row, one per warp
+  const int b = blockIdx.x / size;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int d0 = a.cu[b], d1 = a.cu[b + 1];
   // The whole cluster sees the same range and leaves together.
@@ -165,47 +171,49 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
   w.skip = taken < n && !a.draft ? a.draft_tokens[d0 + taken] : -1;
 
   // ---- the sum of this warp's segment
-  const int seg = (a.V + kSegments - 1) / kSegments;
+  const int seg = (a.V + segments - 1) / segments;
   const int segment = rank * kWarps + warp;
-  const int lo = min((long long)a.V, (long long)segment * seg), hi = min(a.V, lo + seg);
-  const Pair mine = w.q ? lane_sum<true>(w, lo, hi, lane) : lane_sum<false>(w, lo, hi, lane);
-  const double sum = warp_total(total(mine));
+  const int lo = (int)min((long long)a.V, (long long)segment * seg), hi = min(a.V, lo + seg);
+  const double sum = warp_total(w.q ? lane_sum<true>(w, lo, hi, lane) : lane_sum<false>(w, lo, hi, lane));
   if (lane == 0) s_own[warp] = sum;
   cluster.sync();
-  if (tid < kSegments) s_all[tid] = cluster.map_shared_rank(s_own, tid / kWarps)[tid % kWarps];
-  cluster.sync();  // (also: every s_own has been read, so a CTA may leave)
-
-  // ---- the segment that holds the drawn token: two per lane, scanned
-  const double x0 = s_all[2 * lane], x1 = s_all[2 * lane + 1];
-  const double c1 = warp_scan(x0 + x1, lane), c0 = c1 - x1;
-  const double all = __shfl_sync(0xffffffffu, c1, 31);
-  if (!(all > 0.0) || all > 1e300) {  // nothing to draw from, or an infinity
-    if (rank == 0 && tid == 0) {
-      a.tokens[row0 + taken] = -1;
-      raise_status(a.dev_status, KDA_DEV_BAD_PROB);
+  // ---- the segment that holds the drawn token: two per lane, scanned by every CTA's
+  // first warp
+  if (warp == 0) {
+    const int i0 = 2 * lane, i1 = 2 * lane + 1;
+    const double x0 = i0 < segments ? cluster.map_shared_rank(s_own, i0 / kWarps)[i0 % kWarps] : 0.0;
+    const double x1 = i1 < segments ? cluster.map_shared_rank(s_own, i1 / kWarps)[i1 % kWarps] : 0.0;
+    const double c1 = warp_scan(x0 + x1, lane), c0 = c1 - x1;
+    const double all = __shfl_sync(0xffffffffu, c1, 31);
+    const bool some = all > 0.0 && all <= 1e300;  // else nothing to draw from, or an infinity
+    const double target = (double)a.sample_u[b] * all;
+    const int l = first_past(c1, x0 + x1, target);
+    if (lane == l) {
+      const bool second = x1 > 0.0 && !(x0 > 0.0 && c0 > target);
+      s_found = some ? 2 * l + (second ? 1 : 0) : -1;
+      s_base = second ? c1 - x1 : c0 - x0;  // the running sum before the segment
+      s_target = target;
     }
-    return;
   }
-  const double target = (double)a.sample_u[b] * all;
-  int l = first_past(c1, x0 + x1, target);
-  // the two halves of that lane
-  const double b1 = __shfl_sync(0xffffffffu, c1, l), b0 = __shfl_sync(0xffffffffu, c0, l);
-  const double h0 = __shfl_sync(0xffffffffu, x0, l), h1 = __shfl_sync(0xffffffffu, x1, l);
-  const bool second = h1 > 0.0 && !(h0 > 0.0 && b0 > target);
-  const int found = 2 * l + (second ? 1 : 0);
-  if (found != segment) return;
-  double base = second ? b1 - h1 : b0 - h0;  // the running sum before the segment
+  cluster.sync();  // (also: every s_own has been read, so a CTA may leave)
+  if (s_found < 0 && rank == 0 && tid == 0) {
+    a.tokens[row0 + taken] = -1;
+    raise_status(a.dev_status, KDA_DEV_BAD_PROB);
+  }
+  if (s_found != segment) return;
+  const double target = s_target;
+  double base = s_base;
 
   // ---- within the segment (one warp per request): the block, then the entry
   const int step = (((hi - lo) + kBlocks - 1) / kBlocks + 31) & ~31;
   double part = 0.0;
   for (int i = 0; i < kBlocks; ++i) {
     const int from = min(hi, lo + i * step), to = min(hi, from + step);
-    const double x = warp_total(total(w.q ? lane_sum<true>(w, from, to, lane) : lane_sum<false>(w, from, to, lane)));
+    const double x = warp_total(w.q ? lane_sum<true>(w, from, to, lane) : lane_sum<false>(w, from, to, lane));
     if (lane == i) part = x;
   }
   double c = base + warp_scan(part, lane);
-  l = first_past(c, part, target);
+  const int l = first_past(c, part, target);
   base = __shfl_sync(0xffffffffu, c - part, l);
   const int from = lo + l * step, to = min(hi, from + step);
   int drawn = -1;
@@ -229,8 +237,19 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 }  // namespace
 
 cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t stream) {
-  verify_kernel<<<(unsigned)a.B * kCluster, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  int size = kMaxCluster;
+  while (size > 1 && (long long)a.B * size > kSms * kCtasPerSm) size /= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.B * size);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, verify_kernel, a, size);
 }
 
 }  // namespace kda

@@ -116,6 +116,29 @@ def test_read(shape, cache, from_start):
         assert bool((off <= (U_BF16 + 2 * U_F32) * want.abs() if cache == "e4m3" else off == 0).all())
 
 
+def test_every_quotient_of_two_bf16_fractions():
+    """Codes depend on the fractions of an entry and of its row's largest and on how far
+    apart their exponents are: all 128 x 128 x 20 of them, compared for equality."""
+    most = torch.arange(128) * 2.0 ** -7 + 1                       # the row's largest entry
+    part = (torch.arange(128) * 2.0 ** -7 + 1)[None] * torch.exp2(-torch.arange(20.0))[:, None]
+    part = part.flatten()
+    x = torch.zeros(128, 21, 128)                                   # 20 rows of 127 entries and some
+    entries = torch.minimum(part[None].expand(128, -1), most[:, None])
+    x.view(128, -1)[:, :entries.shape[1]] = entries
+    x[:, :, 127] = most[:, None]
+    x.view(128, -1)[:, entries.shape[1]:entries.shape[1] + 20] = entries[:, 127::128]   # those that 127 took
+    x = x.reshape(-1, 1, 128).to(torch.bfloat16)
+    case = Case(n=[len(x)], lens=[len(x)], HKV=1, D=128, page=128, cache="e4m3", junk=0.0)
+    held, status = append(case, x.cuda(), -x.cuda())
+    assert status == 0
+    codes, scales = quantise(x.float().numpy())
+    pages = case.table[0, :-(-len(x) // 128)].long()
+    for name, sign in (("k", 0), ("v", 0x80)):
+        got = bits(held[name].t[pages])[:, 0].reshape(-1, 128)[:len(x)]
+        assert np.array_equal(got, codes[:, 0] ^ sign)
+        assert np.array_equal(held[name + "_scale"].t[pages].cpu().numpy()[:, 0].reshape(-1)[:len(x)], scales[:, 0])
+
+
 def test_round_trip_is_within_half_a_step():
     case = Case(n=[500], lens=[500], HKV=4, D=128, page=64, cache="e4m3", seed=6)
     k, v = rows(case, 7)
