@@ -1,18 +1,21 @@
-// kda_attn_chunk.cu -- attention of chunks: the requests with more than 64 rows (new
-// tokens x query heads per key head).
+// kda_attn_chunk.cu -- attention of chunks: the requests with more rows (new tokens x
+// query heads per key head) than the window kernel takes.
 //
 // Such a request does 4 D operations per row and cached position on 4 D bytes per
 // position: with hundreds of rows the tensor cores bound it.  One CTA per SM
-// works on items of two row tiles of 128 (row i G + g: token i, head g of the
-// group) of one (request, key head), and key tiles of 128 positions:
-//   S_t = Q_t K^T    128 x 128, TMEM; K-major operands from shared memory
-//   P_t = 2^(S_t - m) in bf16, back to TMEM over S_t by the 128 threads that own
-//                    one row each (four warps per row tile)
-//   O_t += P_t V     TMEM; A = P from TMEM, B = V from shared memory (N-major)
-// The two row tiles alternate: while one's softmax runs, the other's products do.
-// One thread issues every product, in the order PV_0 S_0 PV_1 S_1 per key tile, and
-// runs on into the next item.  For D = 128, S and P share columns: the tensor cores
-// take products in order, so the next S_t starts when PV_t has read P_t.
+// works on items of one or two row tiles of 128 (row i G + g: token i, head g of the
+// group) of one (request, key head), and key tiles of 128 positions.  A task is a
+// (row tile, key tile):
+//   S = Q K^T        128 x 128, TMEM; K-major operands from shared memory
+//   P = 2^(S - m)    in bf16, back to TMEM by the 128 threads that own one row each
+//   O += P V         TMEM; A = P from TMEM, B = V from shared memory (N-major)
+// Tasks take two slots (S, P, O and four softmax warps each) in turn: while one
+// slot's softmax runs, the other's products do.  An item of two row tiles has one in
+// each slot; an item of one row tile deals its key tiles to both, and their two
+// outputs are joined at its end.  One thread issues every product, PV of task k and
+// then S of task k + 2, and runs on into the next item.  For D = 128, a slot's S
+// and P share columns: the tensor cores take products in order, so the next S
+// starts when PV has read P.  P is handed over in halves.
 // O is rescaled only when a row's maximum has grown by more than 2^8: weights up to
 // 256 lose nothing in bf16, and after the first key tiles that hardly ever happens.
 //
@@ -27,6 +30,8 @@
 // that kind adds them, for the rows that see them, at its end.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "kda_attn.cuh"
 #include "kda_launch.h"
 #include "kda_tcgen05.cuh"
@@ -37,35 +42,45 @@ namespace {
 
 constexpr int kTile = 128;          // positions per key tile
 constexpr int kM = 128;             // rows per row tile
-constexpr int kMmaWarp = 8, kKvWarp = 9, kQWarp = 10, kFixWarp = 11;  // after 8 of the softmax; fix: 4 for e4m3
-constexpr int kSteps = 8;           // steps whose notes, scales and barriers are kept: more than the rings hold
+// Warps: 0-3 and 4-7 the slots' softmax, then one each for the products, K and V, Q and
+// V's entries that are not finite; for e4m3 four more that widen the codes.
+constexpr int kMmaWarp = 8, kKvWarp = 9, kQWarp = 10, kWidenWarp = 12;
+constexpr int kSteps = 8;           // steps whose notes and barriers are kept: more than the rings hold
 constexpr float kGrow = 8.f;        // growth of a maximum (log 2) that rescales O
 
-// What the product and the copying warps need to know of a step (one key tile of
+// What the product and the fixing warps need to know of a step (one key tile of
 // one item); the copying warp for K and V writes it before K.
 struct StepNote {
   int flags;
   int start;             // first position of the key tile
   int begin, end;        // positions of the request that any of its tokens sees
   int item;              // running number in this CTA
-  int row[8];            // rows of the key tile's boxes in the cache, -1: none (e4m3)
+  int index;             // of the step in this CTA's part of the item
 };
 constexpr int kFirst = 1, kLast = 2;  // of this CTA's part of the item
-constexpr int kSecond = 4;            // the item has a second row tile
-constexpr int kWhole = 8;             // every row sees every position
-constexpr int kMore = 16;             // another step follows
+constexpr int kSecond = 8;            // the item has a second row tile
+constexpr int kWhole = 16;            // every row sees every position
 
 template <int D, bool kE4m3>
 struct Shape {
   static constexpr int kPanels = D / 64;
   static constexpr int kUnitBytes = kTile * D * 2;       // K or V of one key tile, bf16
-  static constexpr int kRawBytes = kTile * D;
-  // units alternate K, V, K, V ..
-  static constexpr int kUnits = D == 128 ? (kE4m3 ? 3 : 5) : (kE4m3 ? 6 : 8);
-  static constexpr int kRawUnits = kE4m3 ? (D == 128 ? 3 : 4) : 1;
-  static constexpr int kWarps = kE4m3 ? 15 : 12;
+  // units alternate K, V, K, V ..; four are the least that S two tasks ahead needs
+  static constexpr int kUnits = D == 128 ? (kE4m3 ? 4 : 5) : 8;
+  static constexpr int kPart = kE4m3 ? 64 : 128;         // positions copied at a time
+  static constexpr int kRawUnits = kE4m3 ? (D == 128 ? 3 : 6) : 1;  // parts of codes
+  static constexpr int kRawBytes = kPart * D;
+  static constexpr int kScaleSteps = D == 128 ? 4 : 8;   // steps whose scales are kept
+  static constexpr int kWarps = kE4m3 ? 16 : 12;
   static constexpr int kThreads = 32 * kWarps;
-  // TMEM: S of both row tiles in columns 0 .. 255, O of both from kColO on; P in the second
+  // Registers per thread: 65536 (e4m3) or 64512 at launch, then dealt by role to no more
+  static constexpr int kSoftmaxRegs = kE4m3 ? 184 : 208;
+  static constexpr int kOtherRegs = kE4m3 ? 56 : 88;
+  [[maybe_unused]] static constexpr int kWidenRegs = 80;
+  static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs + (kE4m3 ? 128 * kWidenRegs : 0) <=
+                    kThreads * (65536 / kThreads & ~7),
+                "the roles' registers fit in the launch's");
+  // TMEM: S of both slots in columns 0 .. 255, O of both from kColO on; P in the second
   // half of its S (D = 128, where S and PV have one shape and so complete in the order
   // of issue), or in columns of its own
   static constexpr uint32_t kColO = 256;
@@ -73,18 +88,29 @@ struct Shape {
 };
 constexpr uint32_t kTmemCols = 512;
 
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 template <int D, bool kE4m3>
 struct Smem {
   using S = Shape<D, kE4m3>;
   unsigned char q[2][kM * D * 2];                  // 1024-aligned, swizzled panels
   unsigned char unit[S::kUnits][S::kUnitBytes];
   unsigned char raw[kE4m3 ? S::kRawUnits : 1][kE4m3 ? S::kRawBytes : 16];
-  float scale[kE4m3 ? kSteps : 1][2][kE4m3 ? kTile : 1];  // by step: K's (times the score scale), V's
+  float raw_scale[kE4m3 ? S::kRawUnits : 1][kE4m3 ? S::kPart : 4];
+  float scale[kE4m3 ? S::kScaleSteps : 1][2][kE4m3 ? kTile : 4];  // by step: K's (times the score scale), V's
+  float2 other[kM];                                // the second slot's maxima and sums, to be joined
   StepNote note[kSteps];
-  int bad[kSteps];                                  // by item: live entries of V were taken out
+  int bad[kSteps];                                 // by item: live entries of V were taken out
   uint64_t full[S::kUnits], empty[S::kUnits], fixed[kSteps];
-  uint64_t raw_full[4], raw_empty[4];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], done;
+  uint64_t raw_full[S::kRawUnits], raw_empty[S::kRawUnits];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_done[2], done, join_ready, join_done;
   long long part[S::kWarps];
   long long start_unit;
   int start_b;
@@ -182,7 +208,7 @@ struct Walk {
   }
 };
 
-// All steps of 16 along the contraction: S = Q K^T, and O (+)= P V.
+// All steps of 16 along the contraction of S = Q K^T.
 template <int D>
 __device__ __forceinline__ void issue_scores(uint32_t d, uint32_t q_addr, uint32_t k_addr) {
   const uint32_t idesc = idesc_bf16(kTile, kM, false, false);
@@ -193,13 +219,20 @@ __device__ __forceinline__ void issue_scores(uint32_t d, uint32_t q_addr, uint32
     mma_bf16(d, a + off, b + off, idesc, j > 0 ? 1u : 0u);
   }
 }
-template <int D>
+// Half of the steps of O (+)= P V.
+template <int D, int kHalf>
 __device__ __forceinline__ void issue_output(uint32_t d, uint32_t p_col, uint32_t v_addr, bool add) {
   const uint32_t idesc = idesc_bf16(D, kM, false, true);
   const uint64_t b = smem_desc_sw128(v_addr, kTile * 128, 1024);
 #pragma unroll
-  for (int j = 0; j < kTile / 16; ++j)
+  for (int j = 4 * kHalf; j < 4 * kHalf + 4; ++j)
     mma_bf16_tmem_a(d, p_col + 8 * j, b + ((j * 16 * 128) >> 4), idesc, (add || j > 0) ? 1u : 0u);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // The halves of v (two bf16) that are not finite, as a mask.
@@ -269,7 +302,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
       mbar_init(&sm.empty[s], 1);
     }
     for (int s = 0; s < kSteps; ++s) mbar_init(&sm.fixed[s], 1);
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < S::kRawUnits; ++s) {
       mbar_init(&sm.raw_full[s], 1);
       mbar_init(&sm.raw_empty[s], 4);
     }
@@ -277,9 +310,12 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
       mbar_init(&sm.q_full[t], 1);
       mbar_init(&sm.q_empty[t], 1);
       mbar_init(&sm.s_full[t], 1);
+      mbar_init(&sm.p_half[t], 4);
       mbar_init(&sm.p_full[t], 4);
       mbar_init(&sm.o_done[t], 1);
     }
+    mbar_init(&sm.join_ready, 4);
+    mbar_init(&sm.join_done, 4);
     mbar_init(&sm.done, 1);
     mbar_fence_init();
   }
@@ -318,178 +354,231 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
   const int steps = (int)(u1 - u0);
   bool ok = true;
 
-  if (steps == 0) {
-    // nothing to do
-  } else if (warp == kKvWarp) {
-    // ---- notes, and K and V of every step into the ring
-    Walk w;
-    w.start(p, pair, sm.start_b, sm.start_unit, u1 - u0, lane);
-    const int rows_per_box = min(p.c.page_size, kTile);
-    const int boxes = kTile / rows_per_box;
-    constexpr int kRing = kE4m3 ? S::kRawUnits : S::kUnits;
-    uint64_t* full = kE4m3 ? sm.raw_full : sm.full;
-    uint64_t* empty = kE4m3 ? sm.raw_empty : sm.empty;
-    int step = 0, item = 0;
-    while (w.left > 0 && ok) {
-      const int count = w.count();
-      const int pos0 = w.r.L - w.r.n;
-      const int begin = seen_lo(p, max(0, pos0));                       // of the request
-      const int lo = seen_lo(p, max(0, pos0 + w.token0));               // of the item
-      const int last_pos = pos0 + min(w.r.n, w.token0 + pair) - 1;
-      const int hi = min(seen_hi(p, last_pos, w.r.L), w.r.L);
-      const int32_t* table = p.c.page_table + (size_t)w.b * p.c.max_pages;
-      const int box_first = (w.span.first + w.tile) * boxes;
-      int page = 0;
-      for (int i = 0; i < count && ok; ++i, ++step) {
-        const int in = (i * boxes) & 31;
-        if (in == 0) {
-          const int pos = (box_first + i * boxes + lane) * rows_per_box;
-          page = -1;
-          if (pos < hi && pos + rows_per_box > lo) {
-            page = fresh(table + pos / p.c.page_size);
-            if (page < 0 || page >= p.c.num_pages) {
-              if (pos < (w.span.first + w.tile + count) * kTile) raise_status(p.dev_status, KDA_DEV_BAD_PAGE);
-              page = -1;
+  if (warp >= kWidenWarp) {
+    if constexpr (kE4m3) {
+      // ---- codes to bf16, four warps
+      fewer_registers<S::kWidenRegs>();
+      const int at = tid - 32 * kWidenWarp;
+      for (int r = 0; r < 4 * steps && ok; ++r) {  // parts: two of K, two of V
+        const int u = r >> 1, s = u % S::kUnits, g = u >> 1, kv = u & 1, part = r & 1, rs = r % S::kRawUnits;
+        ok = mbar_wait(&sm.raw_full[rs], (r / S::kRawUnits) & 1);
+        if (part == 0 && u >= S::kUnits) ok = ok && mbar_wait(&sm.empty[s], (u / S::kUnits - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (at < S::kPart) {
+          const float f = sm.raw_scale[rs][at];
+          sm.scale[g % S::kScaleSteps][kv][part * S::kPart + at] = kv ? f : f * (p.scale * kLog2E);
+        }
+        constexpr int kPieces = D / 16;  // 16-code pieces of a row
+#pragma unroll
+        for (int i = 0; i < S::kPart * kPieces / 128; ++i) {
+          const int idx = i * 128 + at, row = idx / kPieces, c = idx % kPieces, to_row = part * S::kPart + row;
+          const uint4 x = *reinterpret_cast<const uint4*>(sm.raw[rs] + row * D + c * 16);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          uint32_t y[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[2 * e] = widen(__byte_perm(w[e], 0, 0x1404));
+            y[2 * e + 1] = widen(__byte_perm(w[e], 0, 0x3424));
+          }
+          unsigned char* to = sm.unit[s] + ((2 * c) >> 3) * kTile * 128;
+          *reinterpret_cast<uint4*>(to + swizzled<128>(to_row, (2 * c) & 7)) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(to + swizzled<128>(to_row, (2 * c + 1) & 7)) = make_uint4(y[4], y[5], y[6], y[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.raw_empty[rs]);
+          if (part == 1) mbar_arrive(&sm.full[s]);
+        }
+      }
+      if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
+    }
+  } else if (warp >= kMmaWarp) {
+    fewer_registers<S::kOtherRegs>();
+    if (steps == 0) {
+      // nothing to do
+    } else if (warp == kKvWarp) {
+      // ---- notes, and K and V of every step into the ring
+      Walk w;
+      w.start(p, pair, sm.start_b, sm.start_unit, u1 - u0, lane);
+      const int rows_per_box = min(p.c.page_size, S::kPart);
+      const int boxes = kTile / rows_per_box;        // of a key tile, and of a part of it:
+      const int part_boxes = S::kPart / rows_per_box;
+      constexpr int kParts = kTile / S::kPart;
+      constexpr int kRing = kE4m3 ? S::kRawUnits : S::kUnits;
+      uint64_t* full = kE4m3 ? sm.raw_full : sm.full;
+      uint64_t* empty = kE4m3 ? sm.raw_empty : sm.empty;
+      int step = 0, item = 0, put = 0;               // put: parts requested
+      while (w.left > 0 && ok) {
+        const int count = w.count();
+        const int pos0 = w.r.L - w.r.n;
+        const int begin = seen_lo(p, max(0, pos0));                       // of the request
+        const int lo = seen_lo(p, max(0, pos0 + w.token0));               // of the item
+        const int last_pos = pos0 + min(w.r.n, w.token0 + pair) - 1;
+        const int hi = min(seen_hi(p, last_pos, w.r.L), w.r.L);
+        const int32_t* table = p.c.page_table + (size_t)w.b * p.c.max_pages;
+        const int box_first = (w.span.first + w.tile) * boxes;
+        int page = 0;
+        for (int i = 0; i < count && ok; ++i, ++step) {
+          const int in = (i * boxes) & 31;
+          if (in == 0) {  // lanes hold the pages of the next 32 boxes
+            const int pos = (box_first + i * boxes + lane) * rows_per_box;
+            page = -1;
+            if (pos < hi && pos + rows_per_box > lo) {
+              page = fresh(table + pos / p.c.page_size);
+              if (page < 0 || page >= p.c.num_pages) {
+                if (pos < (w.span.first + w.tile + count) * kTile) raise_status(p.dev_status, KDA_DEV_BAD_PAGE);
+                page = -1;
+              }
             }
           }
-        }
-        const int start = (w.span.first + w.tile + i) * kTile;
-        const int box_page = __shfl_sync(0xffffffffu, page, in + min(lane, boxes - 1));
-        StepNote& note = sm.note[step % kSteps];
-        const int off = (start + lane * rows_per_box) % p.c.page_size;
-        const int row = box_page >= 0 ? (box_page * p.c.HKV + w.h) * p.c.page_size + off
-                                      : p.c.num_pages * p.c.HKV * p.c.page_size;  // past the end: zeros
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const int u = 2 * step + kv, s = u % kRing;
-          if (u >= kRing) ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], (u / kRing - 1) & 1));
-          if (!ok) break;
-          if (kv == 0) {
-            if (lane < boxes) note.row[lane] = box_page >= 0 ? row : -1;
-            if (lane == 0) {
+          const int start = (w.span.first + w.tile + i) * kTile;
+          StepNote& note = sm.note[step % kSteps];
+#pragma unroll 1
+          for (int q = 0; q < 2 * kParts; ++q, ++put) {
+            const int kv = q / kParts, part = q % kParts, s = put % kRing;
+            if (put >= kRing) ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], (put / kRing - 1) & 1));
+            if (!ok) break;
+            if (q == 0 && lane == 0) {
               note.flags = (i == 0 ? kFirst : 0) | (i + 1 == count ? kLast : 0) |
                            (w.token0 + per_tile < w.r.n ? kSecond : 0) |
-                           (sees_whole(p, w.r.L, pos0 + w.token0, last_pos, start) ? kWhole : 0) |
-                           (step + 1 < steps ? kMore : 0);
+                           (sees_whole(p, w.r.L, pos0 + w.token0, last_pos, start) ? kWhole : 0);
               note.start = start;
               note.begin = begin;
               note.end = w.r.L;
               note.item = item;
+              note.index = i;
+            }
+            const int box = part * part_boxes + min(lane, part_boxes - 1);
+            const int box_page = __shfl_sync(0xffffffffu, page, in + box);
+            const int off = (start + box * rows_per_box) % p.c.page_size;
+            const int row = box_page >= 0 ? (box_page * p.c.HKV + w.h) * p.c.page_size + off
+                                          : p.c.num_pages * p.c.HKV * p.c.page_size;  // past the end: zeros
+            uint32_t bytes = kE4m3 ? S::kRawBytes : S::kUnitBytes;
+            if (kE4m3) {
+              const unsigned real = __ballot_sync(0xffffffffu, lane < part_boxes && box_page >= 0);
+              bytes += __popc(real) * rows_per_box * 4;
+              if (lane < part_boxes && box_page < 0) {  // scales of positions without a page are zeros
+                for (int j = 0; j < rows_per_box; ++j) sm.raw_scale[s][lane * rows_per_box + j] = 0.f;
+                fence_proxy_async_smem();
+              }
             }
             __syncwarp();
-          }
-          if (lane == 0) mbar_expect_tx(&full[s], kE4m3 ? S::kRawBytes : S::kUnitBytes);
-          __syncwarp();
-          if (lane < boxes) {
-            const CUtensorMap* map = kv ? &v_map : &k_map;
-            if (kE4m3) {
-              tma_load_2d(sm.raw[s] + lane * rows_per_box * D, map, &full[s], 0, row);
-            } else {
+            if (lane == 0) mbar_expect_tx(&full[s], bytes);
+            __syncwarp();
+            if (lane < part_boxes) {
+              const CUtensorMap* map = kv ? &v_map : &k_map;
+              if (kE4m3) {
+                tma_load_2d(sm.raw[s] + lane * rows_per_box * D, map, &full[s], 0, row);
+                if (box_page >= 0)
+                  bulk_load(&sm.raw_scale[s][lane * rows_per_box], (kv ? p.c.v_scale : p.c.k_scale) + row,
+                            rows_per_box * 4, &full[s]);
+              } else {
 #pragma unroll
-              for (int pn = 0; pn < S::kPanels; ++pn)
-                tma_load_2d(sm.unit[s] + pn * kTile * 128 + lane * rows_per_box * 128, map, &full[s], pn * 64, row);
+                for (int pn = 0; pn < S::kPanels; ++pn)
+                  tma_load_2d(sm.unit[s] + pn * kTile * 128 + lane * rows_per_box * 128, map, &full[s], pn * 64, row);
+              }
             }
           }
         }
+        ++item;
+        w.next(p, pair, lane);
       }
-      ++item;
-      w.next(p, pair, lane);
-    }
-    if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
-    // Every copy lands before the CTA's memory is released, also when a wait gave up.
-    for (int u = max(0, 2 * step - kRing); u < 2 * step; ++u) mbar_wait(&full[u % kRing], (u / kRing) & 1);
-  } else if (warp == kQWarp) {
-    // ---- each item's queries: token rows of a row tile are rows tok G + g of its panels
-    Walk w;
-    w.start(p, pair, sm.start_b, sm.start_unit, u1 - u0, lane);
-    int items[2] = {0, 0};
-    while (w.left > 0 && ok) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (t == 1 && w.token0 + per_tile >= w.r.n) break;
-        if (items[t] > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait(&sm.q_empty[t], (items[t] - 1) & 1));
-        if (!ok) break;
-        ++items[t];
-        if (lane == 0) {
-          mbar_expect_tx(&sm.q_full[t], S::kPanels * per_tile * p.G * 128);
-#pragma unroll
-          for (int pn = 0; pn < S::kPanels; ++pn)
-            tma_load_3d(sm.q[t] + pn * kM * 128, &q_map, &sm.q_full[t], pn * 64, w.h * p.G,
-                        w.r.t0 + w.token0 + t * per_tile);
-        }
-      }
-      __syncwarp();
-      if (ok) w.next(p, pair, lane);
-    }
-    if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-      if (items[t] > 0) mbar_wait(&sm.q_full[t], (items[t] - 1) & 1);
-  } else if (warp == kMmaWarp) {
-    // ---- every product, by one thread
-    if (lane == 0) {
-      int q_items[2] = {0, 0}, p_count[2] = {0, 0};
-      // S of step g for row tile t; `last`: the last row tile of the step
-      auto scores = [&](int g, int t, int n_flags, bool last) {
-        if (n_flags & kFirst) {
-          ok = ok && mbar_wait(&sm.q_full[t], q_items[t] & 1);
-          ++q_items[t];
-        }
-        if (!ok) return;
-        tc_fence_after();
-        issue_scores<D>(tmem + t * kTile, smem_u32(sm.q[t]), smem_u32(sm.unit[(2 * g) % S::kUnits]));
-        mma_commit(&sm.s_full[t]);
-        if (last) mma_commit(&sm.empty[(2 * g) % S::kUnits]);
-        if (n_flags & kLast) mma_commit(&sm.q_empty[t]);
-      };
-      auto k_ready = [&](int g) {
-        ok = ok && mbar_wait(&sm.full[(2 * g) % S::kUnits], ((2 * g) / S::kUnits) & 1);
-      };
-      int flags = 0;
-      k_ready(0);
-      if (ok) {
-        flags = sm.note[0].flags;
-        scores(0, 0, flags, !(flags & kSecond));
-        if (flags & kSecond) scores(0, 1, flags, true);
-      }
-      for (int g = 0; g < steps && ok; ++g) {
-        const int v = (2 * g + 1) % S::kUnits, v_phase = ((2 * g + 1) / S::kUnits) & 1;
-        ok = mbar_wait(&sm.full[v], v_phase);
-        if (!kE4m3) ok = ok && mbar_wait(&sm.fixed[g % kSteps], (g / kSteps) & 1);
-        const bool second = (flags & kSecond) != 0, first = (flags & kFirst) != 0;
-        const bool more = (flags & kMore) != 0;
-        int next_flags = 0;
+      if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
+      // Every copy lands before the CTA's memory is released, also when a wait gave up.
+      for (int u = max(0, put - kRing); u < put; ++u) mbar_wait(&full[u % kRing], (u / kRing) & 1);
+    } else if (warp == kQWarp) {
+      // ---- each item's queries: token rows of a row tile are rows tok G + g of its panels
+      Walk w;
+      w.start(p, pair, sm.start_b, sm.start_unit, u1 - u0, lane);
+      int items[2] = {0, 0};
+      while (w.left > 0 && ok) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (t == 0 || second) {
-            ok = ok && mbar_wait(&sm.p_full[t], p_count[t] & 1);
-            if (!ok) break;
-            ++p_count[t];
-            tc_fence_after();
-            issue_output<D>(tmem + S::kColO + t * D, tmem + S::col_p(t), smem_u32(sm.unit[v]), !first);
-            mma_commit(&sm.o_done[t]);
-            if (t == 1 || !second) mma_commit(&sm.empty[v]);
-          }
-          if (more) {
-            if (t == 0) {
-              k_ready(g + 1);
-              if (!ok) break;
-              next_flags = sm.note[(g + 1) % kSteps].flags;
-            }
-            if (t == 0) scores(g + 1, 0, next_flags, !(next_flags & kSecond));
-            else if (next_flags & kSecond) scores(g + 1, 1, next_flags, true);
-            if (!ok) break;
+          if (t == 1 && w.token0 + per_tile >= w.r.n) break;
+          if (items[t] > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait(&sm.q_empty[t], (items[t] - 1) & 1));
+          if (!ok) break;
+          ++items[t];
+          if (lane == 0) {
+            mbar_expect_tx(&sm.q_full[t], S::kPanels * per_tile * p.G * 128);
+#pragma unroll
+            for (int pn = 0; pn < S::kPanels; ++pn)
+              tma_load_3d(sm.q[t] + pn * kM * 128, &q_map, &sm.q_full[t], pn * 64, w.h * p.G,
+                          w.r.t0 + w.token0 + t * per_tile);
           }
         }
-        flags = next_flags;
+        __syncwarp();
+        if (ok) w.next(p, pair, lane);
       }
-      if (!ok) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
-      mma_commit(&sm.done);  // arrives when every product issued has completed
-      mbar_wait(&sm.done, 0);
-    }
-    __syncwarp();
-  } else if (warp >= kFixWarp) {
-    if constexpr (!kE4m3) {
+      if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (items[t] > 0) mbar_wait(&sm.q_full[t], (items[t] - 1) & 1);
+    } else if (warp == kMmaWarp) {
+      // ---- every product, by one thread
+      if (lane == 0) {
+        // S: next task, its step, row tile, the step's flags, queries taken
+        int s_task = 0, sg = 0, s_tile = 0, s_flags = 0, q_items[2] = {0, 0};
+        auto next_scores = [&]() {
+          if (sg >= steps || !ok) return;
+          const int u = (2 * sg) % S::kUnits;
+          if (s_tile == 0) {
+            ok = mbar_wait(&sm.full[u], ((2 * sg) / S::kUnits) & 1);
+            if (!ok) return;
+            s_flags = sm.note[sg % kSteps].flags;
+          }
+          if (s_flags & kFirst) {
+            ok = mbar_wait(&sm.q_full[s_tile], q_items[s_tile] & 1);
+            ++q_items[s_tile];
+            if (!ok) return;
+          }
+          tc_fence_after();
+          const int slot = s_task & 1;
+          issue_scores<D>(tmem + slot * kTile, smem_u32(sm.q[s_tile]), smem_u32(sm.unit[u]));
+          mma_commit(&sm.s_full[slot]);
+          const bool last = s_tile == 1 || !(s_flags & kSecond);
+          if (last) mma_commit(&sm.empty[u]);
+          if (s_flags & kLast) mma_commit(&sm.q_empty[s_tile]);
+          ++s_task;
+          s_tile = last ? 0 : 1;
+          if (last) ++sg;
+        };
+        next_scores();
+        next_scores();
+        int task = 0, tile = 0;
+        for (int g = 0; g < steps && ok;) {
+          const int u = 2 * g + 1, v = u % S::kUnits;
+          if (tile == 0) {
+            ok = mbar_wait(&sm.full[v], (u / S::kUnits) & 1);
+            if (!kE4m3) ok = ok && mbar_wait(&sm.fixed[g % kSteps], (g / kSteps) & 1);
+          }
+          const int slot = task & 1, flags = sm.note[g % kSteps].flags;
+          const bool two = (flags & kSecond) != 0;
+          const bool add = sm.note[g % kSteps].index > (two ? 0 : 1);  // the slot's first task of the item starts O
+          const uint32_t o = tmem + S::kColO + slot * D, pc = tmem + S::col_p(slot), va = smem_u32(sm.unit[v]);
+          ok = ok && mbar_wait(&sm.p_half[slot], (task >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          issue_output<D, 0>(o, pc, va, add);
+          ok = mbar_wait(&sm.p_full[slot], (task >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          issue_output<D, 1>(o, pc, va, true);
+          mma_commit(&sm.o_done[slot]);
+          const bool last = tile == 1 || !two;
+          if (last) mma_commit(&sm.empty[v]);
+          next_scores();
+          ++task;
+          tile = last ? 0 : 1;
+          if (last) ++g;
+        }
+        if (!ok) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
+        mma_commit(&sm.done);  // arrives when every product issued has completed
+        mbar_wait(&sm.done, 0);
+      }
+      __syncwarp();
+    } else if (!kE4m3) {
       // ---- entries of V that are not part of the request or not finite, in key tiles
       // that some row sees in part
       for (int g = 0; g < steps && ok; ++g) {
@@ -520,50 +609,11 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.fixed[g % kSteps]);
       }
-    } else {
-      // ---- codes to bf16, four warps
-      const int at = tid - 32 * kFixWarp;
-      for (int u = 0; u < 2 * steps && ok; ++u) {
-        const int r = u % S::kRawUnits, s = u % S::kUnits, g = u >> 1, kv = u & 1;
-        ok = mbar_wait(&sm.raw_full[r], (u / S::kRawUnits) & 1);
-        if (u >= S::kUnits) ok = ok && mbar_wait(&sm.empty[s], (u / S::kUnits - 1) & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const StepNote& n = sm.note[g % kSteps];
-        {
-          const int row = n.row[at / min(p.c.page_size, kTile)];
-          const float* scales = kv ? p.c.v_scale : p.c.k_scale;
-          float f = 0.f;
-          if (row >= 0) f = fresh(scales + row + at % min(p.c.page_size, kTile));
-          sm.scale[g % kSteps][kv][at] = kv ? f : f * (p.scale * kLog2E);
-        }
-        constexpr int kPieces = D / 16;  // 16-code pieces of a row
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int idx = i * 128 + at, row = idx / kPieces, c = idx % kPieces;
-          const uint4 x = *reinterpret_cast<const uint4*>(sm.raw[r] + row * D + c * 16);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-          uint32_t y[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            y[2 * e] = widen(__byte_perm(w[e], 0, 0x1404));
-            y[2 * e + 1] = widen(__byte_perm(w[e], 0, 0x3424));
-          }
-          unsigned char* to = sm.unit[s] + ((2 * c) >> 3) * kTile * 128;
-          *reinterpret_cast<uint4*>(to + swizzled<128>(row, (2 * c) & 7)) = make_uint4(y[0], y[1], y[2], y[3]);
-          *reinterpret_cast<uint4*>(to + swizzled<128>(row, (2 * c + 1) & 7)) = make_uint4(y[4], y[5], y[6], y[7]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sm.full[s]);
-          mbar_arrive(&sm.raw_empty[r]);
-        }
-      }
+      if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
     }
-    if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
   } else {
     // ---- the softmax: one row per thread
+    more_registers<S::kSoftmaxRegs>();
     const int t = warp >> 2, r = tid & (kM - 1);
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t s_col = lanes + t * kTile, o_col = lanes + S::kColO + t * D, p_col = lanes + S::col_p(t);
@@ -571,162 +621,192 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
     const int tok_in = r / p.G, g_in = r - tok_in * p.G;
     const float2 c2 = make_float2(c, c);
     Walk w;
-    w.start(p, pair, sm.start_b, sm.start_unit, u1 - u0, lane);
-    int g = 0, done_steps = 0;  // steps so far: of the CTA, of this row tile
+    if (steps > 0) w.start(p, pair, sm.start_b, sm.start_unit, u1 - u0, lane);
+    else w.left = 0;
+    int g0 = 0, task0 = 0;   // steps and tasks of the CTA before the item
+    int mine = 0, joins = 0; // tasks of this slot so far, items joined so far
     long long unit = u0;
     for (int item = 0; w.left > 0 && ok; ++item, unit += w.count(), w.next(p, pair, lane)) {
       const int count = w.count(), L = w.r.L, n = w.r.n;
-      const int token0 = w.token0 + t * per_tile;
-      if (token0 >= n) {  // the item has no second row tile
-        g += count;
-        continue;
-      }
+      const bool two = w.token0 + per_tile < n;
+      const int slot0 = task0 & 1;              // the slot of the item's first task
+      // two row tiles: this slot has one of them, all steps; one: every other step
+      const int tile = two ? t ^ slot0 : 0;
+      const int step1 = two ? 0 : t ^ slot0, step_by = two ? 1 : 2;
+      const int token0 = w.token0 + tile * per_tile;
       const int token = token0 + tok_in, pos = L - n + token;
       const int row_lo = seen_lo(p, pos), row_hi = min(seen_hi(p, pos, L), L);
       const int tile_first = L - n + token0, tile_last = L - n + min(n, token0 + per_tile) - 1;
       const int start0 = (w.span.first + w.tile) * kTile;
       float m = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
-      for (int i = 0; i < count; ++i, ++g, ++done_steps) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[t], done_steps & 1));
+      bool begun = false;
+      for (int i = step1; i < count; i += step_by, ++mine) {
+        const int g = g0 + i;
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[t], mine & 1));
         if (!ok) break;
         tc_fence_after();
         const int start = start0 + i * kTile;
         // whole key tiles of a bf16 cache take x = c S in one product with the subtraction
         const bool whole = sees_whole(p, L, tile_first, tile_last, start);
         const bool plain = !kE4m3 && whole && c >= 0.f;
-        const float* k_scale = sm.scale[kE4m3 ? g % kSteps : 0][0];
-        const float* v_scale = sm.scale[kE4m3 ? g % kSteps : 0][1];
-        // scores in units of log 2 of columns col .. col + 31; what is not seen: -infinity
-        auto scored = [&](float(&x)[32], int col) {
+        float x[4][32];
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            float2 a = make_float2(x[e], x[e + 1]), b = make_float2(x[e + 2], x[e + 3]);
-            if constexpr (kE4m3) {
-              const float4 f = *reinterpret_cast<const float4*>(k_scale + col + e);
-              a = __fmul2_rn(a, make_float2(f.x, f.y));
-              b = __fmul2_rn(b, make_float2(f.z, f.w));
-            } else {
-              a = __fmul2_rn(a, c2);
-              b = __fmul2_rn(b, c2);
+        for (int q = 0; q < 4; ++q) tmem_ld_32cols(s_col + 32 * q, x[q]);
+        tmem_ld_wait();
+        if (!plain) {
+          // scores in units of log 2; what is not seen: -infinity
+          const float* k_scale = sm.scale[kE4m3 ? g % S::kScaleSteps : 0][0];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              float4 f = make_float4(c, c, c, c);
+              if constexpr (kE4m3) f = *reinterpret_cast<const float4*>(k_scale + 32 * q + e);
+              const float2 a = __fmul2_rn(make_float2(x[q][e], x[q][e + 1]), make_float2(f.x, f.y));
+              const float2 b = __fmul2_rn(make_float2(x[q][e + 2], x[q][e + 3]), make_float2(f.z, f.w));
+              x[q][e] = a.x;
+              x[q][e + 1] = a.y;
+              x[q][e + 2] = b.x;
+              x[q][e + 3] = b.y;
             }
-            x[e] = a.x;
-            x[e + 1] = a.y;
-            x[e + 2] = b.x;
-            x[e + 3] = b.y;
           }
           if (!whole) {
-            const uint32_t see = columns(row_lo - start - col, row_hi - start - col);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(see >> e & 1)) x[e] = -INFINITY;
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t see = columns(row_lo - start - 32 * q, row_hi - start - 32 * q);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((see >> e) & 1)) x[q][e] = -INFINITY;
+            }
           }
-        };
-        auto highest = [](const float(&x)[32]) {
-          float y[4] = {x[0], x[1], x[2], x[3]};
+        }
+        float top;
+        {
+          float y[4];
 #pragma unroll
-          for (int e = 4; e < 32; ++e) y[e & 3] = fmaxf(y[e & 3], x[e]);
-          return fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-        };
-        float x0[32], x1[32];
-        tmem_ld_32cols(s_col, x0);
-        tmem_ld_32cols(s_col + 32, x1);
-        tmem_ld_wait();
-        if (!plain) {
-          scored(x0, 0);
-          scored(x1, 32);
+          for (int q = 0; q < 4; ++q) {
+            y[q] = fmaxf(x[q][0], x[q][1]);
+#pragma unroll
+            for (int e = 2; e < 32; e += 2) y[q] = max3(y[q], x[q][e], x[q][e + 1]);
+          }
+          top = fmaxf(max3(y[0], y[1], y[2]), y[3]);
         }
-        float top = fmaxf(highest(x0), highest(x1));
-        tmem_ld_32cols(s_col + 64, x0);
-        tmem_ld_32cols(s_col + 96, x1);
-        tmem_ld_wait();
-        if (!plain) {
-          scored(x0, 64);
-          scored(x1, 96);
-        }
-        top = fmaxf(top, fmaxf(highest(x0), highest(x1)));
         if (plain) top *= c;
-
         const float now = fmaxf(m, top);
         if (__any_sync(0xffffffffu, now > m + kGrow)) {
           const float keep = exp2_approx(m - (now == -INFINITY ? 0.f : now));
           l2.x *= keep;
           l2.y *= keep;
-          // this S came after the product before it, so O is at rest
-          if (i > 0) {
-#pragma unroll
-            for (int cc = 0; cc < D; cc += 32) {
-              float o[32];
-              tmem_ld_32cols(o_col + cc, o);
+          // S came after the product before it, so O is at rest
+          if (begun) {
+#pragma unroll 1
+            for (int cc = 0; cc < D; cc += 16) {
+              float o[16];
+              tmem_ld_16cols(o_col + cc, o);
               tmem_ld_wait();
-              uint32_t ob[32];
+              uint32_t ob[16];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) ob[e] = __float_as_uint(o[e] * keep);
-              tmem_st_32cols(o_col + cc, ob);
+              for (int e = 0; e < 16; ++e) ob[e] = __float_as_uint(o[e] * keep);
+              tmem_st_16cols(o_col + cc, ob);
             }
           }
           m = now;
         }
+        begun = true;
         const float ref = m == -INFINITY ? 0.f : m;
         const float2 nref = make_float2(-ref, -ref);
-        // weights of two times 32 columns, as bf16 pairs
-        auto weigh = [&](const float(&x)[32], int col, uint32_t* out) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 xx = make_float2(x[e], x[e + 1]);
-            const float2 y = plain ? __ffma2_rn(xx, c2, nref) : __fadd2_rn(xx, nref);
-            float2 v = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-            l2 = __fadd2_rn(l2, v);
-            if constexpr (kE4m3) {
-              // a weight of 0 stays 0 whatever the scale of a place that is not seen
-              const float2 f = *reinterpret_cast<const float2*>(v_scale + col + e);
-              v.x = xx.x == -INFINITY ? 0.f : v.x * f.x;
-              v.y = xx.y == -INFINITY ? 0.f : v.y * f.y;
-            }
-            out[e / 2] = pack_bf16(v.x, v.y);
-          }
-        };
         if constexpr (kE4m3) {  // V's scales are written with V
           const int u = 2 * g + 1;
           ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[u % S::kUnits], (u / S::kUnits) & 1));
           if (!ok) break;
         }
-        uint32_t pw[32];
-        weigh(x0, 64, pw);
-        weigh(x1, 96, pw + 16);
-        tmem_st_32cols(p_col + 32, pw);
-        tmem_ld_32cols(s_col, x0);
-        tmem_ld_32cols(s_col + 32, x1);
-        tmem_ld_wait();
-        if (!plain) {
-          scored(x0, 0);
-          scored(x1, 32);
-        }
-        weigh(x0, 0, pw);
-        weigh(x1, 32, pw + 16);
-        tmem_st_32cols(p_col, pw);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[t]);
+        const float* v_scale = sm.scale[kE4m3 ? g % S::kScaleSteps : 0][1];
+        // the weights, as bf16 pairs, 32 columns at a time; handed over by halves
+        auto weigh = [&](auto is_plain, auto is_whole) {
+          float2 sum[2] = {l2, make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t pw[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 xx = make_float2(x[q][e], x[q][e + 1]);
+              const float2 y = decltype(is_plain)::value ? __ffma2_rn(xx, c2, nref) : __fadd2_rn(xx, nref);
+              float2 v = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+              sum[(e >> 1) & 1] = __fadd2_rn(sum[(e >> 1) & 1], v);
+              if constexpr (kE4m3) {
+                const float2 f = *reinterpret_cast<const float2*>(v_scale + 32 * q + e);
+                v = __fmul2_rn(v, f);
+                if (!decltype(is_whole)::value) {
+                  // a weight of 0 stays 0 whatever the scale of a place that is not seen
+                  if (xx.x == -INFINITY) v.x = 0.f;
+                  if (xx.y == -INFINITY) v.y = 0.f;
+                }
+              }
+              pw[e / 2] = pack_bf16(v.x, v.y);
+            }
+            tmem_st_16cols(p_col + 16 * q, pw);
+            if (q & 1) {
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(q == 1 ? &sm.p_half[t] : &sm.p_full[t]);
+            }
+          }
+          l2 = __fadd2_rn(sum[0], sum[1]);
+        };
+        if (!kE4m3 && plain) weigh(std::true_type{}, std::true_type{});
+        else if (kE4m3 && whole) weigh(std::false_type{}, std::true_type{});
+        else weigh(std::false_type{}, std::false_type{});
       }
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_done[t], (done_steps - 1) & 1));
+      const int first_join = joins;
+      if (!two && count > 1) ++joins;
+      g0 += count;
+      task0 += two ? 2 * count : count;
+      if (!ok) break;
+      if (!begun) continue;  // the only step was the other slot's
+      ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_done[t], (mine - 1) & 1));
       if (!ok) break;
       // ---- the end of this CTA's part of the item
       tc_fence_after();
-      const float l = l2.x + l2.y;
+      float l = l2.x + l2.y;
+      float keep = 1.f, keep2 = 0.f;
+      const bool join = !two && count > 1;
+      if (join) {
+        if (t != slot0) {
+          // the second slot hands its sums over, and keeps its O until it has been read
+          sm.other[r] = make_float2(m, l);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.join_ready);
+          ok = __all_sync(0xffffffffu, mbar_wait(&sm.join_done, first_join & 1));
+          if (!ok) break;
+          tc_fence_after();
+          continue;
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.join_ready, first_join & 1));
+        if (!ok) break;
+        tc_fence_after();
+        const float2 ml = sm.other[r];
+        const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.f : top;
+        keep = exp2_approx(m - ref);
+        keep2 = exp2_approx(ml.x - ref);
+        l = l * keep + ml.y * keep2;
+        m = top;
+      }
+      const uint32_t o_other = lanes + S::kColO + (t ^ 1) * D;
       const bool begins = w.tile == 0, ends = w.tile + count == w.span.tiles;
       const bool done = begins && ends;
       const bool live = tok_in < per_tile && token < n;
       const size_t out_row = (size_t)(w.r.t0 + token) * p.H + w.h * p.G + g_in;
-      const size_t piece = ((size_t)cta * 2 + (begins ? 1 : 0)) * kChunkRows + t * per_tile * p.G + r;
+      const size_t piece = ((size_t)cta * 2 + (begins ? 1 : 0)) * kChunkRows + tile * per_tile * p.G + r;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const bool bad = !kE4m3 && sm.bad[item % kSteps] != 0;
       if (live) {
         if (!done) pieces.ml[piece] = make_float2(m, l);
         else if (p.lse) p.lse[out_row] = (m + log2f(l)) * kLn2;
       }
-      if (tid == 0 && begins && !ends)
+      if (r == 0 && t == slot0 && begins && !ends)
         pieces.notes[cta] = PieceNote{(w.r.t0 + w.token0) * p.H + w.h * p.G, min(pair, n - w.token0),
                                       share_of(units, used, unit + w.span.tiles - 1) - cta + 1, 0};
 #pragma unroll 1
@@ -734,15 +814,22 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
         float o[32];
         tmem_ld_32cols(o_col + cc, o);
         tmem_ld_wait();
+        if (join) {
+          float o2[32];
+          tmem_ld_32cols(o_other + cc, o2);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = fmaf(o[e], keep, o2[e] * keep2);
+        }
         if (live && bad) {
-          float x[32];
+          float y[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = o[e];
+          for (int e = 0; e < 32; ++e) y[e] = o[e];
           add_bad_values<D>(p, w.b, w.h, L, pos, L - n + w.token0, L - n + min(n, w.token0 + pair) - 1, start0, count,
-                          p.q + (w.r.t0 + token) * p.q_stride + (size_t)(w.h * p.G + g_in) * D,
-                          m == -INFINITY ? 0.f : m, cc, x);
+                            p.q + (w.r.t0 + token) * p.q_stride + (size_t)(w.h * p.G + g_in) * D,
+                            m == -INFINITY ? 0.f : m, cc, y);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = x[e];
+          for (int e = 0; e < 32; ++e) o[e] = y[e];
         }
         if (live && done) {
           uint4* to = reinterpret_cast<uint4*>(p.out + out_row * D + cc);
@@ -756,6 +843,11 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
           for (int e = 0; e < 32; e += 4) to[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
         __syncwarp();  // the next load is the whole warp's
+      }
+      if (join) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.join_done);
       }
     }
     if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
@@ -780,7 +872,8 @@ cudaError_t launch_chunk(const AttentionArgs& a, cudaStream_t stream) {
   const uint64_t rows = (uint64_t)a.c.num_pages * a.c.HKV * a.c.page_size;
   for (int i = 0; i < 2; ++i)
     if (!make_map_2d(&maps[i], kE4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                     kE4m3 ? 1 : 2, i ? a.c.v : a.c.k, D, rows, kE4m3 ? D : 64, a.c.page_size,
+                     kE4m3 ? 1 : 2, i ? a.c.v : a.c.k, D, rows, kE4m3 ? D : 64,
+                     a.c.page_size < S::kPart ? a.c.page_size : S::kPart,
                      kE4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   const size_t smem = sizeof(Sm) + 1024;

@@ -27,10 +27,10 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;               // CTAs per request
-constexpr int kCtasPerSm = 8;
+constexpr int kCtasPerSm = 16;
 constexpr int kSms = 152;
 constexpr int kBlocks = 8;                   // blocks a segment is searched by
 
@@ -82,31 +82,57 @@ struct Weights {
   }
 };
 
-// This lane's share of the weights lo..hi-1 (entries lo + lane, + 32, ...).
-template <bool kHasQ>
+// This lane's share of the weights lo..hi-1 (both multiples of 4, or hi = V): by
+// 16-byte loads where the rows allow it (kVec), else one entry at a time.
+template <bool kHasQ, bool kVec>
 __device__ __forceinline__ Pair lane_sum(const Weights& w, int lo, int hi, int lane) {
-  constexpr int kUnroll = 4;
+  constexpr int kEach = kVec ? 4 : 1;
+  constexpr int kUnroll = kVec ? 2 : 4;
+  constexpr int kStep = 32 * kEach;
   Pair s = {0.f, 0.f};
-  int v = lo + lane;
-  for (; v + 32 * (kUnroll - 1) < hi; v += 32 * kUnroll) {
-    float pv[kUnroll], qv[kUnroll];
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) pv[i] = __ldg(w.p + v + 32 * i);
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) qv[i] = kHasQ ? __ldg(w.q + v + 32 * i) : 0.f;
+  int v = lo + lane * kEach;
+  for (; v + kStep * (kUnroll - 1) + kEach <= hi; v += kStep * kUnroll) {
+    float pv[kUnroll * kEach], qv[kUnroll * kEach];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
+      if constexpr (kVec) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(w.p + v + kStep * i));
+        pv[4 * i] = x.x; pv[4 * i + 1] = x.y; pv[4 * i + 2] = x.z; pv[4 * i + 3] = x.w;
+      } else {
+        pv[i] = __ldg(w.p + v + kStep * i);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      if constexpr (kHasQ && kVec) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(w.q + v + kStep * i));
+        qv[4 * i] = x.x; qv[4 * i + 1] = x.y; qv[4 * i + 2] = x.z; qv[4 * i + 3] = x.w;
+      } else if constexpr (kVec) {
+        qv[4 * i] = qv[4 * i + 1] = qv[4 * i + 2] = qv[4 * i + 3] = 0.f;
+      } else {
+        qv[i] = kHasQ ? __ldg(w.q + v + kStep * i) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll * kEach; ++i) {
       float d, e;
-      w.get(pv[i], qv[i], v + 32 * i, d, e);
+      w.get(pv[i], qv[i], v + kStep * (i / kEach) + i % kEach, d, e);
       add(s, d, e);
     }
   }
-  for (; v < hi; v += 32) {
-    float d, e;
-    w.get(__ldg(w.p + v), kHasQ ? __ldg(w.q + v) : 0.f, v, d, e);
-    add(s, d, e);
-  }
+  for (; v < hi; v += kStep)
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (v + i >= hi) break;
+      float d, e;
+      w.get(__ldg(w.p + v + i), kHasQ ? __ldg(w.q + v + i) : 0.f, v + i, d, e);
+      add(s, d, e);
+    }
   return s;
+}
+template <bool kVec>
+__device__ __forceinline__ Pair lane_sum(const Weights& w, int lo, int hi, int lane) {
+  return w.q ? lane_sum<true, kVec>(w, lo, hi, lane) : lane_sum<false, kVec>(w, lo, hi, lane);
 }
 
 // The first lane with a weight x whose inclusive running sum c passes `target`;
@@ -117,6 +143,7 @@ __device__ __forceinline__ int first_past(double c, double x, double target) {
   return past ? __ffs(past) - 1 : some ? 31 - __clz(some) : 0;
 }
 
+template <bool kVec>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const VerifyArgs a, const int size) {
   __shared__ int s_taken, s_found;
   __shared__ double s_own[kWarps], s_base, s_target;
@@ -171,10 +198,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
   w.skip = taken < n && !a.draft ? a.draft_tokens[d0 + taken] : -1;
 
   // ---- the sum of this warp's segment
-  const int seg = (a.V + segments - 1) / segments;
+  const int seg = ((a.V + segments - 1) / segments + 3) & ~3;
   const int segment = rank * kWarps + warp;
-  const int lo = (int)min((long long)a.V, (long long)segment * seg), hi = min(a.V, lo + seg);
-  const double sum = warp_total(w.q ? lane_sum<true>(w, lo, hi, lane) : lane_sum<false>(w, lo, hi, lane));
+  const int lo = (int)min((long long)a.V, (long long)segment * seg), hi = (int)min((long long)a.V, (long long)lo + seg);
+  const double sum = warp_total(lane_sum<kVec>(w, lo, hi, lane));
   if (lane == 0) s_own[warp] = sum;
   cluster.sync();
   // ---- the segment that holds the drawn token: two per lane, scanned by every CTA's
@@ -209,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
   double part = 0.0;
   for (int i = 0; i < kBlocks; ++i) {
     const int from = min(hi, lo + i * step), to = min(hi, from + step);
-    const double x = warp_total(w.q ? lane_sum<true>(w, from, to, lane) : lane_sum<false>(w, from, to, lane));
+    const double x = warp_total(lane_sum<kVec>(w, from, to, lane));
     if (lane == i) part = x;
   }
   double c = base + warp_scan(part, lane);
@@ -239,9 +266,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
 cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t stream) {
   int size = kMaxCluster;
   while (size > 1 && (long long)a.B * size > kSms * kCtasPerSm) size /= 2;
+  const bool vec = ((reinterpret_cast<uintptr_t>(a.target) | reinterpret_cast<uintptr_t>(a.draft)) & 15) == 0 &&
+                   a.target_stride % 4 == 0 && (!a.draft || a.draft_stride % 4 == 0);
+  // CTAs of a cluster are placed together, so an SM fills up before the next one gets
+  // any: shared memory that nobody uses holds each SM to its share.
+  const long long ctas = (long long)a.B * size;
+  const long long each = (ctas + kSms - 1) / kSms;
+  size_t smem = 0;
+  if (ctas > kSms && each < kCtasPerSm) smem = (size_t)(227 * 1024) / each - 2048;
+  void (*kernel)(VerifyArgs, int) = vec ? verify_kernel<true> : verify_kernel<false>;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.B * size);
+  cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -249,7 +290,7 @@ cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t stream) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, verify_kernel, a, size);
+  return cudaLaunchKernelEx(&cfg, kernel, a, size);
 }
 
 }  // namespace kda
