@@ -516,67 +516,91 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
       for (int t = 0; t < 2; ++t)
         if (items[t] > 0) mbar_wait(&sm.q_full[t], (items[t] - 1) & 1);
     } else if (warp == kMmaWarp) {
-      // ---- every product, by one thread
-      if (lane == 0) {
-        // S: next task, its step, row tile, the step's flags, queries taken
-        int s_task = 0, sg = 0, s_tile = 0, s_flags = 0, q_items[2] = {0, 0};
-        auto next_scores = [&]() {
-          if (sg >= steps || !ok) return;
-          const int u = (2 * sg) % S::kUnits;
-          if (s_tile == 0) {
-            ok = mbar_wait(&sm.full[u], ((2 * sg) / S::kUnits) & 1);
-            if (!ok) return;
-            s_flags = sm.note[sg % kSteps].flags;
-          }
-          if (s_flags & kFirst) {
-            ok = mbar_wait(&sm.q_full[s_tile], q_items[s_tile] & 1);
-            ++q_items[s_tile];
-            if (!ok) return;
-          }
-          tc_fence_after();
-          const int slot = s_task & 1;
-          issue_scores<D>(tmem + slot * kTile, smem_u32(sm.q[s_tile]), smem_u32(sm.unit[u]));
-          mma_commit(&sm.s_full[slot]);
-          const bool last = s_tile == 1 || !(s_flags & kSecond);
-          if (last) mma_commit(&sm.empty[u]);
-          if (s_flags & kLast) mma_commit(&sm.q_empty[s_tile]);
-          ++s_task;
-          s_tile = last ? 0 : 1;
-          if (last) ++sg;
-        };
-        next_scores();
-        next_scores();
-        int task = 0, tile = 0;
-        for (int g = 0; g < steps && ok;) {
-          const int u = 2 * g + 1, v = u % S::kUnits;
-          if (tile == 0) {
-            ok = mbar_wait(&sm.full[v], (u / S::kUnits) & 1);
-            if (!kE4m3) ok = ok && mbar_wait(&sm.fixed[g % kSteps], (g / kSteps) & 1);
-          }
-          const int slot = task & 1, flags = sm.note[g % kSteps].flags;
-          const bool two = (flags & kSecond) != 0;
-          const bool add = sm.note[g % kSteps].index > (two ? 0 : 1);  // the slot's first task of the item starts O
-          const uint32_t o = tmem + S::kColO + slot * D, pc = tmem + S::col_p(slot), va = smem_u32(sm.unit[v]);
-          ok = ok && mbar_wait(&sm.p_half[slot], (task >> 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          issue_output<D, 0>(o, pc, va, add);
-          ok = mbar_wait(&sm.p_full[slot], (task >> 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          issue_output<D, 1>(o, pc, va, true);
-          mma_commit(&sm.o_done[slot]);
-          const bool last = tile == 1 || !two;
-          if (last) mma_commit(&sm.empty[v]);
-          next_scores();
-          ++task;
-          tile = last ? 0 : 1;
-          if (last) ++g;
+      // ---- every product: the warp waits together, one elected lane issues
+      const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
+      const int all = __shfl_sync(0xffffffffu, steps, 0);
+      auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
+      // S: next task, its step and ring place, row tile, the step's flags, queries taken
+      int s_task = 0, sg = 0, su = 0, su_phase = 0, s_tile = 0, s_flags = 0, q_items[2] = {0, 0};
+      auto next_scores = [&]() {
+        if (sg >= all || !ok) return;
+        if (s_tile == 0) {
+          ok = wait(&sm.full[su], su_phase);
+          if (!ok) return;
+          s_flags = __shfl_sync(0xffffffffu, sm.note[sg % kSteps].flags, 0);
         }
-        if (!ok) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
-        mma_commit(&sm.done);  // arrives when every product issued has completed
-        mbar_wait(&sm.done, 0);
+        if (s_flags & kFirst) {
+          ok = wait(&sm.q_full[s_tile], (s_tile ? q_items[1]++ : q_items[0]++) & 1);
+          if (!ok) return;
+        }
+        tc_fence_after();
+        const int slot = s_task & 1;
+        const bool last = s_tile == 1 || !(s_flags & kSecond);
+        const uint32_t q_addr = smem_u32(sm.q[0]) + s_tile * (kM * D * 2);
+        const uint32_t k_addr = smem_u32(sm.unit[0]) + su * S::kUnitBytes;
+        if (elect_one()) {
+          issue_scores<D>(base + slot * kTile, q_addr, k_addr);
+          mma_commit(&sm.s_full[slot]);
+          if (last) mma_commit(&sm.empty[su]);
+          if (s_flags & kLast) mma_commit(&sm.q_empty[s_tile]);
+        }
+        __syncwarp();
+        ++s_task;
+        s_tile = last ? 0 : 1;
+        if (last) {
+          ++sg;
+          su += 2;
+          if (su >= S::kUnits) {
+            su -= S::kUnits;
+            su_phase ^= 1;
+          }
+        }
+      };
+      next_scores();
+      next_scores();
+      int task = 0, tile = 0, v = 1, v_phase = 0;
+      for (int g = 0; g < all && ok;) {
+        if (tile == 0) {
+          ok = wait(&sm.full[v], v_phase);
+          if (!kE4m3) ok = ok && wait(&sm.fixed[g % kSteps], (g / kSteps) & 1);
+        }
+        const int slot = task & 1;
+        const bool two = (__shfl_sync(0xffffffffu, sm.note[g % kSteps].flags, 0) & kSecond) != 0;
+        // the slot's first task of the item starts O
+        const bool add = __shfl_sync(0xffffffffu, sm.note[g % kSteps].index, 0) > (two ? 0 : 1);
+        const uint32_t o = base + S::kColO + slot * D, pc = base + (slot ? S::col_p(1) : S::col_p(0));
+        const uint32_t v_addr = smem_u32(sm.unit[0]) + v * S::kUnitBytes;
+        ok = ok && wait(&sm.p_half[slot], (task >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) issue_output<D, 0>(o, pc, v_addr, add);
+        __syncwarp();
+        ok = wait(&sm.p_full[slot], (task >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const bool last = tile == 1 || !two;
+        if (elect_one()) {
+          issue_output<D, 1>(o, pc, v_addr, true);
+          mma_commit(&sm.o_done[slot]);
+          if (last) mma_commit(&sm.empty[v]);
+        }
+        __syncwarp();
+        next_scores();
+        ++task;
+        tile = last ? 0 : 1;
+        if (last) {
+          ++g;
+          v += 2;
+          if (v >= S::kUnits) {
+            v -= S::kUnits;
+            v_phase ^= 1;
+          }
+        }
       }
+      if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
+      if (elect_one()) mma_commit(&sm.done);  // arrives when every product issued has completed
+      __syncwarp();
+      mbar_wait(&sm.done, 0);
       __syncwarp();
     } else if (!kE4m3) {
       // ---- entries of V that are not part of the request or not finite, in key tiles

@@ -37,6 +37,17 @@ __device__ __forceinline__ uint32_t idesc_bf16(int n, int m, bool a_mn_major, bo
          ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
+// True in one lane of a converged warp, always the same one.  The tensor-core
+// instructions take their descriptors from uniform registers: issued by an elected
+// lane of a warp that runs its loop together they follow each other freely, while
+// inside a branch on the lane number each costs some 90 cycles.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(yes));
+  return yes != 0;
+}
+
 // D (TMEM) (+)= A (shared memory) x B (shared memory).
 __device__ __forceinline__ void mma_bf16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
                                          uint32_t idesc, uint32_t accumulate) {
