@@ -12,10 +12,12 @@
 // Tasks take two slots (S, P, O and four softmax warps each) in turn: while one
 // slot's softmax runs, the other's products do.  An item of two row tiles has one in
 // each slot; an item of one row tile deals its key tiles to both, and their two
-// outputs are joined at its end.  One thread issues every product, PV of task k and
-// then S of task k + 2, and runs on into the next item.  For D = 128, a slot's S
-// and P share columns: the tensor cores take products in order, so the next S
-// starts when PV has read P.  P is handed over in halves.
+// outputs are joined at its end.  A warp per slot issues its products, PV of task k
+// and then S of task k + 2, and runs on into the next item; the two warps take
+// turns, since products of both slots mixed would end together, and then both
+// slots' softmax would run at once and the tensor cores wait.  For D = 128, a slot's
+// S and P share columns: the tensor cores take one thread's products in order, so
+// the next S starts when PV has read P.  P is handed over in halves.
 // O is rescaled only when a row's maximum has grown by more than 2^8: weights up to
 // 256 lose nothing in bf16, and after the first key tiles that hardly ever happens.
 //
@@ -42,9 +44,10 @@ namespace {
 
 constexpr int kTile = 128;          // positions per key tile
 constexpr int kM = 128;             // rows per row tile
-// Warps: 0-3 and 4-7 the slots' softmax, then one each for the products, K and V, Q and
-// V's entries that are not finite; for e4m3 four more that widen the codes.
-constexpr int kMmaWarp = 8, kKvWarp = 9, kQWarp = 10, kWidenWarp = 12;
+// Warps: 0-3 and 4-7 the slots' softmax, 8 and 9 their products, then one each for
+// what is copied and for V's entries that are not finite; for e4m3 four more that
+// widen the codes.
+constexpr int kMmaWarp = 8, kCopyWarp = 10, kWidenWarp = 12;
 constexpr int kSteps = 8;           // steps whose notes and barriers are kept: more than the rings hold
 constexpr float kGrow = 8.f;        // growth of a maximum (log 2) that rescales O
 
@@ -74,9 +77,9 @@ struct Shape {
   static constexpr int kWarps = kE4m3 ? 16 : 12;
   static constexpr int kThreads = 32 * kWarps;
   // Registers per thread: 65536 (e4m3) or 64512 at launch, then dealt by role to no more
-  static constexpr int kSoftmaxRegs = kE4m3 ? 184 : 208;
-  static constexpr int kOtherRegs = kE4m3 ? 56 : 88;
-  [[maybe_unused]] static constexpr int kWidenRegs = 80;
+  static constexpr int kSoftmaxRegs = kE4m3 ? 152 : 208;
+  static constexpr int kOtherRegs = kE4m3 ? 72 : 88;
+  [[maybe_unused]] static constexpr int kWidenRegs = 120;
   static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs + (kE4m3 ? 128 * kWidenRegs : 0) <=
                     kThreads * (65536 / kThreads & ~7),
                 "the roles' registers fit in the launch's");
@@ -110,7 +113,7 @@ struct Smem {
   int bad[kSteps];                                 // by item: live entries of V were taken out
   uint64_t full[S::kUnits], empty[S::kUnits], fixed[kSteps];
   uint64_t raw_full[S::kRawUnits], raw_empty[S::kRawUnits];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_done[2], done, join_ready, join_done;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_done[2], turn[2], done, join_ready, join_done;
   long long part[S::kWarps];
   long long start_unit;
   int start_b;
@@ -219,14 +222,14 @@ __device__ __forceinline__ void issue_scores(uint32_t d, uint32_t q_addr, uint32
     mma_bf16(d, a + off, b + off, idesc, j > 0 ? 1u : 0u);
   }
 }
-// Half of the steps of O (+)= P V.
+// The steps of O (+)= P V over one half of the key tile.
 template <int D, int kHalf>
 __device__ __forceinline__ void issue_output(uint32_t d, uint32_t p_col, uint32_t v_addr, bool add) {
   const uint32_t idesc = idesc_bf16(D, kM, false, true);
   const uint64_t b = smem_desc_sw128(v_addr, kTile * 128, 1024);
 #pragma unroll
   for (int j = 4 * kHalf; j < 4 * kHalf + 4; ++j)
-    mma_bf16_tmem_a(d, p_col + 8 * j, b + ((j * 16 * 128) >> 4), idesc, (add || j > 0) ? 1u : 0u);
+    mma_bf16_tmem_a(d, p_col + 8 * j, b + ((j * 16 * 128) >> 4), idesc, (add || j > 4 * kHalf) ? 1u : 0u);
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < S::kUnits; ++s) {
       mbar_init(&sm.full[s], kE4m3 ? 4 : 1);
-      mbar_init(&sm.empty[s], 1);
+      mbar_init(&sm.empty[s], 2);
     }
     for (int s = 0; s < kSteps; ++s) mbar_init(&sm.fixed[s], 1);
     for (int s = 0; s < S::kRawUnits; ++s) {
@@ -308,15 +311,16 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sm.q_full[t], 1);
-      mbar_init(&sm.q_empty[t], 1);
+      mbar_init(&sm.q_empty[t], 2);
       mbar_init(&sm.s_full[t], 1);
       mbar_init(&sm.p_half[t], 4);
       mbar_init(&sm.p_full[t], 4);
       mbar_init(&sm.o_done[t], 1);
+      mbar_init(&sm.turn[t], 1);
     }
     mbar_init(&sm.join_ready, 4);
     mbar_init(&sm.join_done, 4);
-    mbar_init(&sm.done, 1);
+    mbar_init(&sm.done, 2);
     mbar_fence_init();
   }
   if (warp == kMmaWarp) tmem_alloc(&sm.tmem, kTmemCols);
@@ -370,11 +374,15 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
           sm.scale[g % S::kScaleSteps][kv][part * S::kPart + at] = kv ? f : f * (p.scale * kLog2E);
         }
         constexpr int kPieces = D / 16;  // 16-code pieces of a row
+        constexpr int kEach = S::kPart * kPieces / 128;
+        uint4 x[kEach];
 #pragma unroll
-        for (int i = 0; i < S::kPart * kPieces / 128; ++i) {
-          const int idx = i * 128 + at, row = idx / kPieces, c = idx % kPieces, to_row = part * S::kPart + row;
-          const uint4 x = *reinterpret_cast<const uint4*>(sm.raw[rs] + row * D + c * 16);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        for (int i = 0; i < kEach; ++i)
+          x[i] = *reinterpret_cast<const uint4*>(sm.raw[rs] + (i * 128 + at) * 16);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const int idx = i * 128 + at, to_row = part * S::kPart + idx / kPieces, c = idx % kPieces;
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
           uint32_t y[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -398,8 +406,8 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
     fewer_registers<S::kOtherRegs>();
     if (steps == 0) {
       // nothing to do
-    } else if (warp == kKvWarp) {
-      // ---- notes, and K and V of every step into the ring
+    } else if (warp == kCopyWarp) {
+      // ---- notes, the items' queries, and K and V of every step into the ring
       Walk w;
       w.start(p, pair, sm.start_b, sm.start_unit, u1 - u0, lane);
       const int rows_per_box = min(p.c.page_size, S::kPart);
@@ -410,7 +418,24 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
       uint64_t* full = kE4m3 ? sm.raw_full : sm.full;
       uint64_t* empty = kE4m3 ? sm.raw_empty : sm.empty;
       int step = 0, item = 0, put = 0;               // put: parts requested
+      int queries[2] = {0, 0};                       // row tiles requested
       while (w.left > 0 && ok) {
+        // token rows of a row tile are rows tok G + g of its panels
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t == 1 && w.token0 + per_tile >= w.r.n) break;
+          if (queries[t] > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait(&sm.q_empty[t], (queries[t] - 1) & 1));
+          if (!ok) break;
+          ++queries[t];
+          if (lane == 0) {
+            mbar_expect_tx(&sm.q_full[t], S::kPanels * per_tile * p.G * 128);
+#pragma unroll
+            for (int pn = 0; pn < S::kPanels; ++pn)
+              tma_load_3d(sm.q[t] + pn * kM * 128, &q_map, &sm.q_full[t], pn * 64, w.h * p.G,
+                          w.r.t0 + w.token0 + t * per_tile);
+          }
+          __syncwarp();
+        }
         const int count = w.count();
         const int pos0 = w.r.L - w.r.n;
         const int begin = seen_lo(p, max(0, pos0));                       // of the request
@@ -488,66 +513,56 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
       if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
       // Every copy lands before the CTA's memory is released, also when a wait gave up.
       for (int u = max(0, put - kRing); u < put; ++u) mbar_wait(&full[u % kRing], (u / kRing) & 1);
-    } else if (warp == kQWarp) {
-      // ---- each item's queries: token rows of a row tile are rows tok G + g of its panels
-      Walk w;
-      w.start(p, pair, sm.start_b, sm.start_unit, u1 - u0, lane);
-      int items[2] = {0, 0};
-      while (w.left > 0 && ok) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (t == 1 && w.token0 + per_tile >= w.r.n) break;
-          if (items[t] > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait(&sm.q_empty[t], (items[t] - 1) & 1));
-          if (!ok) break;
-          ++items[t];
-          if (lane == 0) {
-            mbar_expect_tx(&sm.q_full[t], S::kPanels * per_tile * p.G * 128);
-#pragma unroll
-            for (int pn = 0; pn < S::kPanels; ++pn)
-              tma_load_3d(sm.q[t] + pn * kM * 128, &q_map, &sm.q_full[t], pn * 64, w.h * p.G,
-                          w.r.t0 + w.token0 + t * per_tile);
-          }
-        }
-        __syncwarp();
-        if (ok) w.next(p, pair, lane);
-      }
-      if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
-        if (items[t] > 0) mbar_wait(&sm.q_full[t], (items[t] - 1) & 1);
-    } else if (warp == kMmaWarp) {
-      // ---- every product: the warp waits together, one elected lane issues
+        if (queries[t] > 0) mbar_wait(&sm.q_full[t], (queries[t] - 1) & 1);
+    } else if (warp < kMmaWarp + 2) {
+      // ---- the products of a slot: the warp waits together, one elected lane issues.
+      // Both warps pass every step, and say of every K, V and Q when they are done with it.
       const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
       const int all = __shfl_sync(0xffffffffu, steps, 0);
+      const int slot = __shfl_sync(0xffffffffu, warp, 0) - kMmaWarp;
+      const uint32_t s_col = base + slot * kTile, o_col = base + S::kColO + slot * D;
+      const uint32_t p_col = base + (slot ? S::col_p(1) : S::col_p(0));
+      const uint32_t q0 = smem_u32(sm.q[0]), unit0 = smem_u32(sm.unit[0]);
       auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
-      // S: next task, its step and ring place, row tile, the step's flags, queries taken
-      int s_task = 0, sg = 0, su = 0, su_phase = 0, s_tile = 0, s_flags = 0, q_items[2] = {0, 0};
+      // S: next step and its ring place, the tasks before it, items' row tiles so far
+      int sg = 0, su = 0, su_phase = 0, s_task = 0, q_items[2] = {0, 0};
+      bool q_due = false;   // the item's queries have not been waited for
       auto next_scores = [&]() {
-        if (sg >= all || !ok) return;
-        if (s_tile == 0) {
+        for (bool found = false; sg < all && !found;) {
           ok = wait(&sm.full[su], su_phase);
           if (!ok) return;
-          s_flags = __shfl_sync(0xffffffffu, sm.note[sg % kSteps].flags, 0);
-        }
-        if (s_flags & kFirst) {
-          ok = wait(&sm.q_full[s_tile], (s_tile ? q_items[1]++ : q_items[0]++) & 1);
-          if (!ok) return;
-        }
-        tc_fence_after();
-        const int slot = s_task & 1;
-        const bool last = s_tile == 1 || !(s_flags & kSecond);
-        const uint32_t q_addr = smem_u32(sm.q[0]) + s_tile * (kM * D * 2);
-        const uint32_t k_addr = smem_u32(sm.unit[0]) + su * S::kUnitBytes;
-        if (elect_one()) {
-          issue_scores<D>(base + slot * kTile, q_addr, k_addr);
-          mma_commit(&sm.s_full[slot]);
-          if (last) mma_commit(&sm.empty[su]);
-          if (s_flags & kLast) mma_commit(&sm.q_empty[s_tile]);
-        }
-        __syncwarp();
-        ++s_task;
-        s_tile = last ? 0 : 1;
-        if (last) {
+          const int flags = __shfl_sync(0xffffffffu, sm.note[sg % kSteps].flags, 0);
+          const bool two = (flags & kSecond) != 0;
+          if (flags & kFirst) {
+            q_due = true;
+            ++q_items[0];
+            if (two) ++q_items[1];
+          }
+          const int tile = two ? slot ^ (s_task & 1) : 0;
+          found = two || (s_task & 1) == slot;
+          if (found && q_due) {
+            ok = wait(&sm.q_full[tile], ((tile ? q_items[1] : q_items[0]) - 1) & 1);
+            if (!ok) return;
+            q_due = false;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            if (found) {
+              issue_scores<D>(s_col, q0 + tile * (kM * D * 2), unit0 + su * S::kUnitBytes);
+              mma_commit(&sm.s_full[slot]);
+              mma_commit(&sm.empty[su]);
+            } else {
+              mbar_arrive(&sm.empty[su]);
+            }
+            if (flags & kLast) {
+              mma_commit(&sm.q_empty[0]);
+              if (two) mma_commit(&sm.q_empty[1]);
+            }
+          }
+          __syncwarp();
+          s_task += two ? 2 : 1;
           ++sg;
           su += 2;
           if (su >= S::kUnits) {
@@ -557,44 +572,46 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
         }
       };
       next_scores();
-      next_scores();
-      int task = 0, tile = 0, v = 1, v_phase = 0;
-      for (int g = 0; g < all && ok;) {
-        if (tile == 0) {
-          ok = wait(&sm.full[v], v_phase);
-          if (!kE4m3) ok = ok && wait(&sm.fixed[g % kSteps], (g / kSteps) & 1);
-        }
-        const int slot = task & 1;
+      int task = 0, mine = 0, v = 1, v_phase = 0;
+      for (int g = 0; g < all && ok; ++g) {
+        // (the fixing warp waits for V)
+        ok = kE4m3 ? wait(&sm.full[v], v_phase) : wait(&sm.fixed[g % kSteps], (g / kSteps) & 1);
+        if (!ok) break;
         const bool two = (__shfl_sync(0xffffffffu, sm.note[g % kSteps].flags, 0) & kSecond) != 0;
         // the slot's first task of the item starts O
         const bool add = __shfl_sync(0xffffffffu, sm.note[g % kSteps].index, 0) > (two ? 0 : 1);
-        const uint32_t o = base + S::kColO + slot * D, pc = base + (slot ? S::col_p(1) : S::col_p(0));
-        const uint32_t v_addr = smem_u32(sm.unit[0]) + v * S::kUnitBytes;
-        ok = ok && wait(&sm.p_half[slot], (task >> 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) issue_output<D, 0>(o, pc, v_addr, add);
-        __syncwarp();
-        ok = wait(&sm.p_full[slot], (task >> 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        const bool last = tile == 1 || !two;
-        if (elect_one()) {
-          issue_output<D, 1>(o, pc, v_addr, true);
-          mma_commit(&sm.o_done[slot]);
-          if (last) mma_commit(&sm.empty[v]);
+        if (two || (task & 1) == slot) {
+          const uint32_t v_addr = unit0 + v * S::kUnitBytes;
+          // task 0 has the first turn; every other one follows the task before it
+          const int first_turn = slot == 0 ? 1 : 0;
+          if (mine >= first_turn) ok = wait(&sm.turn[slot], (mine - first_turn) & 1);
+          ok = ok && wait(&sm.p_half[slot], mine & 1);
+          if (!ok) break;
+          tc_fence_after();
+          // (e4m3 hands the second half over first)
+          if (elect_one()) issue_output<D, kE4m3 ? 1 : 0>(o_col, p_col, v_addr, add);
+          __syncwarp();
+          ok = wait(&sm.p_full[slot], mine & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            issue_output<D, kE4m3 ? 0 : 1>(o_col, p_col, v_addr, true);
+            mma_commit(&sm.o_done[slot]);
+            mma_commit(&sm.empty[v]);
+          }
+          __syncwarp();
+          ++mine;
+          next_scores();
+          if (elect_one()) mbar_arrive(&sm.turn[slot ^ 1]);
+        } else if (elect_one()) {
+          mbar_arrive(&sm.empty[v]);
         }
         __syncwarp();
-        next_scores();
-        ++task;
-        tile = last ? 0 : 1;
-        if (last) {
-          ++g;
-          v += 2;
-          if (v >= S::kUnits) {
-            v -= S::kUnits;
-            v_phase ^= 1;
-          }
+        task += two ? 2 : 1;
+        v += 2;
+        if (v >= S::kUnits) {
+          v -= S::kUnits;
+          v_phase ^= 1;
         }
       }
       if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
@@ -674,114 +691,144 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
         // whole key tiles of a bf16 cache take x = c S in one product with the subtraction
         const bool whole = sees_whole(p, L, tile_first, tile_last, start);
         const bool plain = !kE4m3 && whole && c >= 0.f;
-        float x[4][32];
+        // Scores of 32 columns from col on in units of log 2; what is not seen: -infinity.
+        const float* k_scale = sm.scale[kE4m3 ? g % S::kScaleSteps : 0][0];
+        const float* v_scale = sm.scale[kE4m3 ? g % S::kScaleSteps : 0][1];
+        auto scored = [&](float(&x)[32], int col) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld_32cols(s_col + 32 * q, x[q]);
-        tmem_ld_wait();
-        if (!plain) {
-          // scores in units of log 2; what is not seen: -infinity
-          const float* k_scale = sm.scale[kE4m3 ? g % S::kScaleSteps : 0][0];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              float4 f = make_float4(c, c, c, c);
-              if constexpr (kE4m3) f = *reinterpret_cast<const float4*>(k_scale + 32 * q + e);
-              const float2 a = __fmul2_rn(make_float2(x[q][e], x[q][e + 1]), make_float2(f.x, f.y));
-              const float2 b = __fmul2_rn(make_float2(x[q][e + 2], x[q][e + 3]), make_float2(f.z, f.w));
-              x[q][e] = a.x;
-              x[q][e + 1] = a.y;
-              x[q][e + 2] = b.x;
-              x[q][e + 3] = b.y;
-            }
+          for (int e = 0; e < 32; e += 4) {
+            float4 f = make_float4(c, c, c, c);
+            if constexpr (kE4m3) f = *reinterpret_cast<const float4*>(k_scale + col + e);
+            const float2 a = __fmul2_rn(make_float2(x[e], x[e + 1]), make_float2(f.x, f.y));
+            const float2 b = __fmul2_rn(make_float2(x[e + 2], x[e + 3]), make_float2(f.z, f.w));
+            x[e] = a.x;
+            x[e + 1] = a.y;
+            x[e + 2] = b.x;
+            x[e + 3] = b.y;
           }
           if (!whole) {
+            const uint32_t see = columns(row_lo - start - col, row_hi - start - col);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t see = columns(row_lo - start - 32 * q, row_hi - start - 32 * q);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((see >> e) & 1)) x[q][e] = -INFINITY;
-            }
+            for (int e = 0; e < 32; ++e)
+              if (!((see >> e) & 1)) x[e] = -INFINITY;
           }
-        }
-        float top;
-        {
-          float y[4];
+        };
+        auto highest = [](const float(&x)[32]) {
+          float y = fmaxf(x[0], x[1]), z = fmaxf(x[2], x[3]);
+#pragma unroll
+          for (int e = 4; e < 32; e += 4) {
+            y = max3(y, x[e], x[e + 1]);
+            z = max3(z, x[e + 2], x[e + 3]);
+          }
+          return fmaxf(y, z);
+        };
+        // A larger maximum moves the sum and O; S came after the product before it, so O is
+        // at rest.
+        auto move = [&](float top) {
+          const float now = fmaxf(m, top);
+          if (__any_sync(0xffffffffu, now > m + kGrow)) {
+            const float keep = exp2_approx(m - (now == -INFINITY ? 0.f : now));
+            l2.x *= keep;
+            l2.y *= keep;
+            if (begun) {
+#pragma unroll 1
+              for (int cc = 0; cc < D; cc += 16) {
+                float o[16];
+                tmem_ld_16cols(o_col + cc, o);
+                tmem_ld_wait();
+                uint32_t ob[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) ob[e] = __float_as_uint(o[e] * keep);
+                tmem_st_16cols(o_col + cc, ob);
+              }
+            }
+            m = now;
+          }
+          begun = true;
+        };
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+        // The weights of 32 columns as bf16 pairs, to TMEM.
+        auto weigh = [&](const float(&x)[32], int col, auto is_plain) {
+          const float ref = m == -INFINITY ? 0.f : m;
+          const float2 nref = make_float2(-ref, -ref);
+          uint32_t pw[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float2 xa = make_float2(x[e], x[e + 1]), xb = make_float2(x[e + 2], x[e + 3]);
+            const float2 ya = decltype(is_plain)::value ? __ffma2_rn(xa, c2, nref) : __fadd2_rn(xa, nref);
+            const float2 yb = decltype(is_plain)::value ? __ffma2_rn(xb, c2, nref) : __fadd2_rn(xb, nref);
+            float2 va = make_float2(exp2_approx(ya.x), exp2_approx(ya.y));
+            float2 vb = make_float2(exp2_approx(yb.x), exp2_approx(yb.y));
+            sum0 = __fadd2_rn(sum0, va);
+            sum1 = __fadd2_rn(sum1, vb);
+            if constexpr (kE4m3) {
+              float4 f = *reinterpret_cast<const float4*>(v_scale + col + e);
+              if (!whole) {
+                // a weight of 0 stays 0 whatever the scale of a place that is not seen
+                f.x = xa.x == -INFINITY ? 0.f : f.x;
+                f.y = xa.y == -INFINITY ? 0.f : f.y;
+                f.z = xb.x == -INFINITY ? 0.f : f.z;
+                f.w = xb.y == -INFINITY ? 0.f : f.w;
+              }
+              va = __fmul2_rn(va, make_float2(f.x, f.y));
+              vb = __fmul2_rn(vb, make_float2(f.z, f.w));
+            }
+            pw[e / 2] = pack_bf16(va.x, va.y);
+            pw[e / 2 + 1] = pack_bf16(vb.x, vb.y);
+          }
+          tmem_st_16cols(p_col + col / 2, pw);
+        };
+        auto hand_over = [&](uint64_t* bar) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar);
+        };
+        if constexpr (!kE4m3) {
+          // all of S in registers
+          float x[4][32];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld_32cols(s_col + 32 * q, x[q]);
+          tmem_ld_wait();
+          if (!plain)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) scored(x[q], 32 * q);
+          const float top = fmaxf(max3(highest(x[0]), highest(x[1]), highest(x[2])), highest(x[3]));
+          move(plain ? top * c : top);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            y[q] = fmaxf(x[q][0], x[q][1]);
-#pragma unroll
-            for (int e = 2; e < 32; e += 2) y[q] = max3(y[q], x[q][e], x[q][e + 1]);
+            if (plain) weigh(x[q], 32 * q, std::true_type{});
+            else weigh(x[q], 32 * q, std::false_type{});
+            if (q == 1) hand_over(&sm.p_half[t]);
           }
-          top = fmaxf(max3(y[0], y[1], y[2]), y[3]);
-        }
-        if (plain) top *= c;
-        const float now = fmaxf(m, top);
-        if (__any_sync(0xffffffffu, now > m + kGrow)) {
-          const float keep = exp2_approx(m - (now == -INFINITY ? 0.f : now));
-          l2.x *= keep;
-          l2.y *= keep;
-          // S came after the product before it, so O is at rest
-          if (begun) {
-#pragma unroll 1
-            for (int cc = 0; cc < D; cc += 16) {
-              float o[16];
-              tmem_ld_16cols(o_col + cc, o);
-              tmem_ld_wait();
-              uint32_t ob[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) ob[e] = __float_as_uint(o[e] * keep);
-              tmem_st_16cols(o_col + cc, ob);
-            }
-          }
-          m = now;
-        }
-        begun = true;
-        const float ref = m == -INFINITY ? 0.f : m;
-        const float2 nref = make_float2(-ref, -ref);
-        if constexpr (kE4m3) {  // V's scales are written with V
-          const int u = 2 * g + 1;
+          hand_over(&sm.p_full[t]);
+        } else {
+          // half of S in registers (the scales and the widening warps want their share of
+          // them): the first half is read again after the second
+          float x[2][32];
+          auto load = [&](int col) {
+            tmem_ld_32cols(s_col + col, x[0]);
+            tmem_ld_32cols(s_col + col + 32, x[1]);
+            tmem_ld_wait();
+            scored(x[0], col);
+            scored(x[1], col + 32);
+          };
+          load(0);
+          const float top = fmaxf(highest(x[0]), highest(x[1]));
+          load(64);
+          move(max3(top, highest(x[0]), highest(x[1])));
+          const int u = 2 * g + 1;  // V's scales are written with V
           ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[u % S::kUnits], (u / S::kUnits) & 1));
           if (!ok) break;
+          weigh(x[0], 64, std::false_type{});
+          weigh(x[1], 96, std::false_type{});
+          hand_over(&sm.p_half[t]);
+          load(0);
+          weigh(x[0], 0, std::false_type{});
+          weigh(x[1], 32, std::false_type{});
+          hand_over(&sm.p_full[t]);
         }
-        const float* v_scale = sm.scale[kE4m3 ? g % S::kScaleSteps : 0][1];
-        // the weights, as bf16 pairs, 32 columns at a time; handed over by halves
-        auto weigh = [&](auto is_plain, auto is_whole) {
-          float2 sum[2] = {l2, make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t pw[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 xx = make_float2(x[q][e], x[q][e + 1]);
-              const float2 y = decltype(is_plain)::value ? __ffma2_rn(xx, c2, nref) : __fadd2_rn(xx, nref);
-              float2 v = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-              sum[(e >> 1) & 1] = __fadd2_rn(sum[(e >> 1) & 1], v);
-              if constexpr (kE4m3) {
-                const float2 f = *reinterpret_cast<const float2*>(v_scale + 32 * q + e);
-                v = __fmul2_rn(v, f);
-                if (!decltype(is_whole)::value) {
-                  // a weight of 0 stays 0 whatever the scale of a place that is not seen
-                  if (xx.x == -INFINITY) v.x = 0.f;
-                  if (xx.y == -INFINITY) v.y = 0.f;
-                }
-              }
-              pw[e / 2] = pack_bf16(v.x, v.y);
-            }
-            tmem_st_16cols(p_col + 16 * q, pw);
-            if (q & 1) {
-              tmem_st_wait();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(q == 1 ? &sm.p_half[t] : &sm.p_full[t]);
-            }
-          }
-          l2 = __fadd2_rn(sum[0], sum[1]);
-        };
-        if (!kE4m3 && plain) weigh(std::true_type{}, std::true_type{});
-        else if (kE4m3 && whole) weigh(std::false_type{}, std::true_type{});
-        else weigh(std::false_type{}, std::false_type{});
+        l2 = __fadd2_rn(l2, __fadd2_rn(sum0, sum1));
       }
       const int first_join = joins;
       if (!two && count > 1) ++joins;
