@@ -211,15 +211,20 @@ struct Walk {
   }
 };
 
-// All steps of 16 along the contraction of S = Q K^T.
+// All steps of 16 along the contraction of S = Q K^T.  `turn` goes to the other slot's
+// warp before the last two: what is queued by then covers its waking up.  (Loops, not
+// unrolled: the softmax's code leaves little of the instruction cache to this.)
 template <int D>
-__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t q_addr, uint32_t k_addr) {
+__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t q_addr, uint32_t k_addr, uint64_t* turn) {
   const uint32_t idesc = idesc_bf16(kTile, kM, false, false);
-  const uint64_t a = smem_desc_sw128(q_addr, 16, 1024), b = smem_desc_sw128(k_addr, 16, 1024);
-#pragma unroll
+  uint64_t a = smem_desc_sw128(q_addr, 16, 1024), b = smem_desc_sw128(k_addr, 16, 1024);
+#pragma unroll 1
   for (int j = 0; j < D / 16; ++j) {
-    const uint64_t off = ((j >> 2) * (kM * 128) + (j & 3) * 32) >> 4;
-    mma_bf16(d, a + off, b + off, idesc, j > 0 ? 1u : 0u);
+    if (j == D / 16 - 2 && turn) mbar_arrive(turn);
+    mma_bf16(d, a, b, idesc, j > 0 ? 1u : 0u);
+    const uint32_t step = (j & 3) == 3 ? kM * 128 / 16 - 6 : 2;  // 32 bytes on, or the next panel
+    a += step;
+    b += step;
   }
 }
 // The steps of O (+)= P V over one half of the key tile.
@@ -227,7 +232,7 @@ template <int D, int kHalf>
 __device__ __forceinline__ void issue_output(uint32_t d, uint32_t p_col, uint32_t v_addr, bool add) {
   const uint32_t idesc = idesc_bf16(D, kM, false, true);
   const uint64_t b = smem_desc_sw128(v_addr, kTile * 128, 1024);
-#pragma unroll
+#pragma unroll 1
   for (int j = 4 * kHalf; j < 4 * kHalf + 4; ++j)
     mma_bf16_tmem_a(d, p_col + 8 * j, b + ((j * 16 * 128) >> 4), idesc, (add || j > 4 * kHalf) ? 1u : 0u);
 }
@@ -285,6 +290,21 @@ __device__ __noinline__ void add_bad_values(const AttentionArgs& p, int b, int h
 // The bits of columns lo .. hi - 1 among columns 0 .. 31.
 __device__ __forceinline__ uint32_t below(int k) { return k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u; }
 __device__ __forceinline__ uint32_t columns(int lo, int hi) { return below(hi) & ~below(lo); }
+
+// A wait of a whole warp; what follows when the phase is not there at once is out of
+// line, so that the product warps' waits take little room in the instruction cache.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity) {
+  const unsigned long long t0 = global_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, global_ns() - t0 > kWaitLimitNs)) return false;
+  }
+}
+__device__ __forceinline__ bool wait_together(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_try(bar, parity)) || wait_on(bar, parity);
+}
 
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
@@ -525,41 +545,40 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
       const uint32_t s_col = base + slot * kTile, o_col = base + S::kColO + slot * D;
       const uint32_t p_col = base + (slot ? S::col_p(1) : S::col_p(0));
       const uint32_t q0 = smem_u32(sm.q[0]), unit0 = smem_u32(sm.unit[0]);
-      auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
-      // S: next step and its ring place, the tasks before it, items' row tiles so far
+      auto wait = [&](uint64_t* bar, int parity) { return wait_together(smem_u32(bar), parity); };
+      // The slot's next S, found and waited for before the turn in which it is issued: its
+      // ring place, the step's flags and the addresses of its operands.
       int sg = 0, su = 0, su_phase = 0, s_task = 0, q_items[2] = {0, 0};
       bool q_due = false;   // the item's queries have not been waited for
-      auto next_scores = [&]() {
-        for (bool found = false; sg < all && !found;) {
+      bool found = false;
+      int f_unit = 0, f_flags = 0;
+      uint32_t f_q = 0, f_k = 0;
+      auto find_scores = [&]() {
+        found = false;
+        while (sg < all && !found) {
           ok = wait(&sm.full[su], su_phase);
           if (!ok) return;
-          const int flags = __shfl_sync(0xffffffffu, sm.note[sg % kSteps].flags, 0);
-          const bool two = (flags & kSecond) != 0;
-          if (flags & kFirst) {
+          f_flags = __shfl_sync(0xffffffffu, sm.note[sg % kSteps].flags, 0);
+          const bool two = (f_flags & kSecond) != 0;
+          if (f_flags & kFirst) {
             q_due = true;
             ++q_items[0];
             if (two) ++q_items[1];
           }
-          const int tile = two ? slot ^ (s_task & 1) : 0;
           found = two || (s_task & 1) == slot;
-          if (found && q_due) {
-            ok = wait(&sm.q_full[tile], ((tile ? q_items[1] : q_items[0]) - 1) & 1);
-            if (!ok) return;
-            q_due = false;
-          }
-          tc_fence_after();
-          if (elect_one()) {
-            if (found) {
-              issue_scores<D>(s_col, q0 + tile * (kM * D * 2), unit0 + su * S::kUnitBytes);
-              mma_commit(&sm.s_full[slot]);
-              mma_commit(&sm.empty[su]);
-            } else {
-              mbar_arrive(&sm.empty[su]);
+          if (found) {
+            const int tile = two ? slot ^ (s_task & 1) : 0;
+            if (q_due) {
+              ok = wait(&sm.q_full[tile], ((tile ? q_items[1] : q_items[0]) - 1) & 1);
+              if (!ok) return;
+              q_due = false;
             }
-            if (flags & kLast) {
-              mma_commit(&sm.q_empty[0]);
-              if (two) mma_commit(&sm.q_empty[1]);
-            }
+            f_unit = su;
+            f_q = q0 + tile * (kM * D * 2);
+            f_k = unit0 + su * S::kUnitBytes;
+          } else if (elect_one()) {
+            mbar_arrive(&sm.empty[su]);
+            if (f_flags & kLast) mma_commit(&sm.q_empty[0]);
           }
           __syncwarp();
           s_task += two ? 2 : 1;
@@ -571,7 +590,22 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
           }
         }
       };
-      next_scores();
+      // by the elected lane
+      auto issue_found = [&](uint64_t* turn) {
+        issue_scores<D>(s_col, f_q, f_k, turn);
+        mma_commit(&sm.s_full[slot]);
+        mma_commit(&sm.empty[f_unit]);
+        if (f_flags & kLast) {
+          mma_commit(&sm.q_empty[0]);
+          if (f_flags & kSecond) mma_commit(&sm.q_empty[1]);
+        }
+      };
+      find_scores();
+      if (ok && found) {
+        tc_fence_after();
+        if (elect_one()) issue_found(nullptr);
+        __syncwarp();
+      }
       int task = 0, mine = 0, v = 1, v_phase = 0;
       for (int g = 0; g < all && ok; ++g) {
         // (the fixing warp waits for V)
@@ -583,9 +617,10 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
         if (two || (task & 1) == slot) {
           const uint32_t v_addr = unit0 + v * S::kUnitBytes;
           // task 0 has the first turn; every other one follows the task before it
-          const int first_turn = slot == 0 ? 1 : 0;
-          if (mine >= first_turn) ok = wait(&sm.turn[slot], (mine - first_turn) & 1);
+          find_scores();
           ok = ok && wait(&sm.p_half[slot], mine & 1);
+          const int first_turn = slot == 0 ? 1 : 0;
+          if (ok && mine >= first_turn) ok = wait(&sm.turn[slot], (mine - first_turn) & 1);
           if (!ok) break;
           tc_fence_after();
           // (e4m3 hands the second half over first)
@@ -598,11 +633,11 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
             issue_output<D, kE4m3 ? 0 : 1>(o_col, p_col, v_addr, true);
             mma_commit(&sm.o_done[slot]);
             mma_commit(&sm.empty[v]);
+            if (found) issue_found(&sm.turn[slot ^ 1]);
+            else mbar_arrive(&sm.turn[slot ^ 1]);
           }
           __syncwarp();
           ++mine;
-          next_scores();
-          if (elect_one()) mbar_arrive(&sm.turn[slot ^ 1]);
         } else if (elect_one()) {
           mbar_arrive(&sm.empty[v]);
         }
