@@ -90,6 +90,14 @@ def _stream_handle(stream) -> int:
     return int(stream.cuda_stream)
 
 
+def _stream_of(stream, device) -> int:
+    """The handle of the caller's stream, or of the current one of ``device`` (by the raw
+    handle: the small calls take less time than building a Stream object)."""
+    if stream is not None:
+        return int(stream.cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _status_word(dev_status, device, stream) -> torch.Tensor:
     """The caller's status word, or a new zeroed one, ordered on the call's
     stream (so the zeroing precedes the kernels that OR into it)."""
@@ -268,11 +276,10 @@ def _check_rows(t: torch.Tensor, name: str, heads: int, D: int, device) -> int:
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
         raise ValueError(f"{name} shape {tuple(t.shape)} != [T, {heads}, {D}]")
-    T = t.shape[0]
     s = t.stride()
-    if (D > 1 and s[2] != 1) or (heads > 1 and s[1] != D):
+    if s[2] != 1 or (heads > 1 and s[1] != D):
         raise ValueError(f"{name}: a token's rows must be contiguous (strides {s})")
-    return s[0] if T > 1 else heads * D
+    return s[0] if t.shape[0] > 1 else heads * D
 
 
 def _check_cache(k_cache, v_cache, k_scale, v_scale, page_table, cu, what):
@@ -332,7 +339,7 @@ def kda_cache_append(k_cache, v_cache, k, v, cu_seqlens, seq_lens, page_table, k
     rc = _lib.load().kda_cache_append(
         k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale), k.data_ptr(),
         v.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), dtype, B,
-        k.shape[0], HKV, D, page, N, max_pages, ks, vs, status.data_ptr(), _stream_handle(stream))
+        k.shape[0], HKV, D, page, N, max_pages, ks, vs, status.data_ptr(), _stream_of(stream, dev))
     return _finish(rc, status, "kda_cache_append", check, check_device, stream)
 
 
@@ -357,7 +364,7 @@ def kda_cache_read(k_rows, v_rows, k_cache, v_cache, cu_rows, starts, page_table
         k_rows.data_ptr(), v_rows.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         _ptr(k_scale), _ptr(v_scale), cu_rows.data_ptr(), _ptr(starts), page_table.data_ptr(),
         dtype, B, k_rows.shape[0], HKV, D, page, N, max_pages, status.data_ptr(),
-        _stream_handle(stream))
+        _stream_of(stream, dev))
     return _finish(rc, status, "kda_cache_read", check, check_device, stream)
 
 
@@ -405,7 +412,7 @@ def kda_paged_attention(out, q, k_cache, v_cache, cu_seqlens, seq_lens, page_tab
         _ptr(k_scale), _ptr(v_scale), cu_seqlens.data_ptr(), seq_lens.data_ptr(),
         page_table.data_ptr(), float(D ** -0.5 if scale is None else scale), int(causal),
         int(window), dtype, B, T, int(max_tokens), H, HKV, D, page, N, max_pages, qs,
-        workspace.data_ptr(), workspace.numel(), status.data_ptr(), _stream_handle(stream))
+        workspace.data_ptr(), workspace.numel(), status.data_ptr(), _stream_of(stream, dev))
     return _finish(rc, status, "kda_paged_attention", check, check_device, stream)
 
 
@@ -448,7 +455,7 @@ def kda_verify_draft(tokens, accepted, target_probs, draft_probs, draft_tokens, 
     rc = _lib.load().kda_verify_draft(
         tokens.data_ptr(), accepted.data_ptr(), target_probs.data_ptr(), _ptr(draft_probs),
         draft_tokens.data_ptr(), accept_u.data_ptr(), sample_u.data_ptr(), cu_drafts.data_ptr(),
-        B, N, V, strides[0], strides[1], status.data_ptr(), _stream_handle(stream))
+        B, N, V, strides[0], strides[1], status.data_ptr(), _stream_of(stream, dev))
     return _finish(rc, status, "kda_verify_draft", check, check_device, stream)
 
 

@@ -22,7 +22,6 @@ namespace {
 // row, or all four to a row (each every fourth piece, in order) where an item is in
 // many pieces.
 constexpr int kJoinWarps = 4;
-constexpr int kJoinY = 16;
 constexpr int kManyPieces = 8;
 
 template <int D>
@@ -36,7 +35,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttentionAr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool many = note.pieces > kManyPieces;
   const int row0 = many ? blockIdx.y : blockIdx.y * kJoinWarps + warp;
-  const int row_step = many ? kJoinY : kJoinY * kJoinWarps;
+  const int row_step = many ? gridDim.y : gridDim.y * kJoinWarps;
   const int first = many ? warp : 0, step = many ? kJoinWarps : 1;
   for (int row = row0; row < note.tokens * p.G; row += row_step) {
     auto at = [&](int i) { return ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * rows + row; };
@@ -90,7 +89,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttentionAr
 
 cudaError_t launch_join_pieces(const AttentionArgs& a, const Pieces& pieces, int rows, int ctas,
                                cudaStream_t stream) {
-  const dim3 grid(ctas, kJoinY);
+  const dim3 grid(ctas, rows <= 64 ? rows / 4 : 32);
   if (a.c.D == 128)
     return launch(join_kernel<128>, grid, dim3(kJoinWarps * 32), 0, stream, true, a, pieces, rows);
   return launch(join_kernel<64>, grid, dim3(kJoinWarps * 32), 0, stream, true, a, pieces, rows);

@@ -685,8 +685,8 @@ cudaError_t launch_window(const AttentionArgs& a, cudaStream_t stream) {
                      S::kPanelBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
   const size_t smem = sizeof(Sm) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(window_kernel<D, kRows, kE4m3>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static SmemSet set;
+  cudaError_t e = allow_smem(window_kernel<D, kRows, kE4m3>, smem, set);
   if (e != cudaSuccess) return e;
   const Pieces pieces = pieces_at(a.workspace, kWindowCtas, kRows);
   e = launch(window_kernel<D, kRows, kE4m3>, dim3(kWindowCtas), dim3(kThreads), smem, stream, true,

@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <utility>
 
 namespace kda {
@@ -24,6 +25,24 @@ cudaError_t launch(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem
   cfg.attrs = pdl ? attr : nullptr;
   cfg.numAttrs = pdl ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Let `kernel` use `smem` bytes of dynamic shared memory on the current device.  The
+// attribute lasts, so each (kernel, device) sets it once (`done`: the kernel's own
+// record, by device ordinal).
+struct SmemSet {
+  std::atomic<unsigned long long> devices{0};
+};
+template <typename... Params>
+cudaError_t allow_smem(void (*kernel)(Params...), size_t smem, SmemSet& done) {
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = device < 64 ? 1ull << device : 0;
+  if (done.devices.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess) done.devices.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 }  // namespace kda

@@ -146,6 +146,7 @@ __device__ __forceinline__ int first_past(double c, double x, double target) {
 template <bool kVec>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const VerifyArgs a, const int size) {
   __shared__ int s_taken, s_found;
+  __shared__ Pair s_lane[kBlocks][kThreads];  // every lane's sum of each block of its segment
   __shared__ double s_own[kWarps], s_base, s_target;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
@@ -201,7 +202,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
   const int seg = ((a.V + segments - 1) / segments + 3) & ~3;
   const int segment = rank * kWarps + warp;
   const int lo = (int)min((long long)a.V, (long long)segment * seg), hi = (int)min((long long)a.V, (long long)lo + seg);
-  const double sum = warp_total(lane_sum<kVec>(w, lo, hi, lane));
+  const int step = (((hi - lo) + kBlocks - 1) / kBlocks + 127) & ~127;
+  Pair mine = {0.f, 0.f};
+#pragma unroll 1
+  for (int i = 0; i < kBlocks; ++i) {
+    const int from = min(hi, lo + i * step), to = min(hi, from + step);
+    const Pair x = lane_sum<kVec>(w, from, to, lane);
+    s_lane[i][tid] = x;
+    add(mine, x.hi, x.lo);
+  }
+  const double sum = warp_total(mine);
   if (lane == 0) s_own[warp] = sum;
   cluster.sync();
   // ---- the segment that holds the drawn token: two per lane, scanned by every CTA's
@@ -231,34 +241,42 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
   const double target = s_target;
   double base = s_base;
 
-  // ---- within the segment (one warp per request): the block, then the entry
-  const int step = (((hi - lo) + kBlocks - 1) / kBlocks + 31) & ~31;
+  // ---- within the segment (one warp per request): the block, the lane's run of
+  // entries, the entry
   double part = 0.0;
+#pragma unroll
   for (int i = 0; i < kBlocks; ++i) {
-    const int from = min(hi, lo + i * step), to = min(hi, from + step);
-    const double x = warp_total(lane_sum<kVec>(w, from, to, lane));
+    const double x = warp_total(s_lane[i][tid]);
     if (lane == i) part = x;
   }
   double c = base + warp_scan(part, lane);
-  const int l = first_past(c, part, target);
+  int l = first_past(c, part, target);
   base = __shfl_sync(0xffffffffu, c - part, l);
-  const int from = lo + l * step, to = min(hi, from + step);
-  int drawn = -1;
-  for (int v0 = from; v0 < to; v0 += 32) {
-    float dh = 0.f, dl = 0.f;
-    if (v0 + lane < to) w.load(v0 + lane, dh, dl);
-    const double x = (double)dh + (double)dl;
-    c = base + warp_scan(x, lane);
-    const unsigned past = __ballot_sync(0xffffffffu, c > target);
-    const unsigned some = __ballot_sync(0xffffffffu, x > 0.0);
-    if (past & some) {
-      drawn = v0 + __ffs(past & some) - 1;
-      break;
-    }
-    if (some) drawn = v0 + 31 - __clz(some);  // the last with a weight so far
-    base = __shfl_sync(0xffffffffu, c, 31);
+  const int from = min(hi, lo + l * step), to = min(hi, from + step);
+  const int each = (to - from + 31) / 32;
+  const int v0 = min(to, from + lane * each), v1 = min(to, v0 + each);
+  part = 0.0;
+#pragma unroll 8
+  for (int v = v0; v < v1; ++v) {
+    float dh, dl;
+    w.load(v, dh, dl);
+    part += (double)dh + (double)dl;
   }
-  if (lane == 0) a.tokens[row0 + taken] = drawn;
+  c = base + warp_scan(part, lane);
+  l = first_past(c, part, target);
+  if (lane != l) return;
+  c -= part;
+  int drawn = -1;
+  for (int v = v0; v < v1; ++v) {
+    float dh, dl;
+    w.load(v, dh, dl);
+    const double x = (double)dh + (double)dl;
+    if (!(x > 0.0)) continue;
+    c += x;
+    drawn = v;  // the last with a weight, should rounding let none pass
+    if (c > target) break;
+  }
+  a.tokens[row0 + taken] = drawn;
 }
 
 }  // namespace
@@ -268,21 +286,11 @@ cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t stream) {
   while (size > 1 && (long long)a.B * size > kSms * kCtasPerSm) size /= 2;
   const bool vec = ((reinterpret_cast<uintptr_t>(a.target) | reinterpret_cast<uintptr_t>(a.draft)) & 15) == 0 &&
                    a.target_stride % 4 == 0 && (!a.draft || a.draft_stride % 4 == 0);
-  // CTAs of a cluster are placed together, so an SM fills up before the next one gets
-  // any: shared memory that nobody uses holds each SM to its share.
   const long long ctas = (long long)a.B * size;
-  const long long each = (ctas + kSms - 1) / kSms;
-  size_t smem = 0;
-  if (ctas > kSms && each < kCtasPerSm) smem = (size_t)(227 * 1024) / each - 2048;
   void (*kernel)(VerifyArgs, int) = vec ? verify_kernel<true> : verify_kernel<false>;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
