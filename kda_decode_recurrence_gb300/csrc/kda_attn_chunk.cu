@@ -109,6 +109,7 @@ struct Smem {
   float raw_scale[kE4m3 ? S::kRawUnits : 1][kE4m3 ? S::kPart : 4];
   float scale[kE4m3 ? S::kScaleSteps : 1][2][kE4m3 ? kTile : 4];  // by step: K's (times the score scale), V's
   float2 other[kM];                                // the second slot's maxima and sums, to be joined
+  float2 rows[kE4m3 ? 2 : 1][kE4m3 ? kM : 1];     // maxima and sums on their way between layouts
   StepNote note[kSteps];
   int bad[kSteps];                                 // by item: live entries of V were taken out
   uint64_t full[S::kUnits], empty[S::kUnits], fixed[kSteps];
@@ -396,13 +397,19 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
         }
         constexpr int kPieces = D / 16;  // 16-code pieces of a row
         constexpr int kEach = S::kPart * kPieces / 128;
+        // Eight lanes write two rows by four pieces, whose chunks lie in different banks.
+        auto piece = [&](int i) {  // row, piece
+          const int n = i * 128 + at;
+          return kPieces == 8 ? make_int2((n >> 4) * 2 + ((n >> 2) & 1), (n & 3) + ((n >> 3) & 1) * 4)
+                              : make_int2(n >> 2, n & 3);
+        };
         uint4 x[kEach];
 #pragma unroll
         for (int i = 0; i < kEach; ++i)
-          x[i] = *reinterpret_cast<const uint4*>(sm.raw[rs] + (i * 128 + at) * 16);
+          x[i] = *reinterpret_cast<const uint4*>(sm.raw[rs] + piece(i).x * D + piece(i).y * 16);
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-          const int idx = i * 128 + at, to_row = part * S::kPart + idx / kPieces, c = idx % kPieces;
+          const int to_row = part * S::kPart + piece(i).x, c = piece(i).y;
           const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
           uint32_t y[8];
 #pragma unroll
@@ -718,6 +725,19 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
       float m = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       bool begun = false;
+      // e4m3: the four rows of the fragment layout, 8 k + lane / 4 of the warp's 32
+      [[maybe_unused]] float m4[4], l4[4];
+      [[maybe_unused]] int lo4[4], hi4[4];
+      if constexpr (kE4m3) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int at = L - n + token0 + (32 * (warp & 3) + 8 * k + (lane >> 2)) / p.G;
+          lo4[k] = seen_lo(p, at);
+          hi4[k] = min(seen_hi(p, at, L), L);
+          m4[k] = -INFINITY;
+          l4[k] = 0.f;
+        }
+      }
       for (int i = step1; i < count; i += step_by, ++mine) {
         const int g = g0 + i;
         ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[t], mine & 1));
@@ -728,15 +748,11 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
         const bool whole = sees_whole(p, L, tile_first, tile_last, start);
         const bool plain = !kE4m3 && whole && c >= 0.f;
         // Scores of 32 columns from col on in units of log 2; what is not seen: -infinity.
-        const float* k_scale = sm.scale[kE4m3 ? g % S::kScaleSteps : 0][0];
-        const float* v_scale = sm.scale[kE4m3 ? g % S::kScaleSteps : 0][1];
         auto scored = [&](float(&x)[32], int col) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            float4 f = make_float4(c, c, c, c);
-            if constexpr (kE4m3) f = *reinterpret_cast<const float4*>(k_scale + col + e);
-            const float2 a = __fmul2_rn(make_float2(x[e], x[e + 1]), make_float2(f.x, f.y));
-            const float2 b = __fmul2_rn(make_float2(x[e + 2], x[e + 3]), make_float2(f.z, f.w));
+            const float2 a = __fmul2_rn(make_float2(x[e], x[e + 1]), c2);
+            const float2 b = __fmul2_rn(make_float2(x[e + 2], x[e + 3]), c2);
             x[e] = a.x;
             x[e + 1] = a.y;
             x[e + 2] = b.x;
@@ -793,22 +809,10 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
             const float2 xa = make_float2(x[e], x[e + 1]), xb = make_float2(x[e + 2], x[e + 3]);
             const float2 ya = decltype(is_plain)::value ? __ffma2_rn(xa, c2, nref) : __fadd2_rn(xa, nref);
             const float2 yb = decltype(is_plain)::value ? __ffma2_rn(xb, c2, nref) : __fadd2_rn(xb, nref);
-            float2 va = make_float2(exp2_approx(ya.x), exp2_approx(ya.y));
-            float2 vb = make_float2(exp2_approx(yb.x), exp2_approx(yb.y));
+            const float2 va = make_float2(exp2_approx(ya.x), exp2_approx(ya.y));
+            const float2 vb = make_float2(exp2_approx(yb.x), exp2_approx(yb.y));
             sum0 = __fadd2_rn(sum0, va);
             sum1 = __fadd2_rn(sum1, vb);
-            if constexpr (kE4m3) {
-              float4 f = *reinterpret_cast<const float4*>(v_scale + col + e);
-              if (!whole) {
-                // a weight of 0 stays 0 whatever the scale of a place that is not seen
-                f.x = xa.x == -INFINITY ? 0.f : f.x;
-                f.y = xa.y == -INFINITY ? 0.f : f.y;
-                f.z = xb.x == -INFINITY ? 0.f : f.z;
-                f.w = xb.y == -INFINITY ? 0.f : f.w;
-              }
-              va = __fmul2_rn(va, make_float2(f.x, f.y));
-              vb = __fmul2_rn(vb, make_float2(f.z, f.w));
-            }
             pw[e / 2] = pack_bf16(va.x, va.y);
             pw[e / 2 + 1] = pack_bf16(vb.x, vb.y);
           }
@@ -839,32 +843,123 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
           }
           hand_over(&sm.p_full[t]);
         } else {
-          // half of S in registers (the scales and the widening warps want their share of
-          // them): the first half is read again after the second
+          // A key's and a value's scale belong to a column, so the fragment layout is taken, in
+          // which a thread has a quarter of the columns of four rows: a quarter of the loads
+          // of scales (with a row to a thread they took 5000 cycles a task).  Half of S in
+          // registers; the first half is read again after the second.
+          const float* k_scale = sm.scale[g % S::kScaleSteps][0] + 2 * (lane & 3);
+          const float* v_scale = sm.scale[g % S::kScaleSteps][1] + 2 * (lane & 3);
           float x[2][32];
           auto load = [&](int col) {
-            tmem_ld_32cols(s_col + col, x[0]);
-            tmem_ld_32cols(s_col + col + 32, x[1]);
+            tmem_ld_fragments_64cols(s_col + col, x[0]);
+            tmem_ld_fragments_64cols(s_col + col + (16u << 16), x[1]);
             tmem_ld_wait();
-            scored(x[0], col);
-            scored(x[1], col + 32);
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+              const float2 f = *reinterpret_cast<const float2*>(k_scale + col + 8 * b);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                float* y = &x[k >> 1][4 * b + 2 * (k & 1)];
+                const float2 z = __fmul2_rn(make_float2(y[0], y[1]), f);
+                y[0] = z.x;
+                y[1] = z.y;
+              }
+            }
+            if (!whole) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int at = start + col + 2 * (lane & 3);
+                const int from = lo4[k] - at, to = hi4[k] - at;  // seen: from <= 8 b + e < to
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    if (8 * b + e < from || 8 * b + e >= to) x[k >> 1][4 * b + 2 * (k & 1) + e] = -INFINITY;
+              }
+            }
+          };
+          float now[4] = {m4[0], m4[1], m4[2], m4[3]};
+          auto raise = [&]() {
+#pragma unroll
+            for (int b = 0; b < 8; ++b)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                now[k] = max3(now[k], x[k >> 1][4 * b + 2 * (k & 1)], x[k >> 1][4 * b + 2 * (k & 1) + 1]);
           };
           load(0);
-          const float top = fmaxf(highest(x[0]), highest(x[1]));
+          raise();
           load(64);
-          move(max3(top, highest(x[0]), highest(x[1])));
+          raise();
+          bool grown = false;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            now[k] = fmaxf(now[k], __shfl_xor_sync(0xffffffffu, now[k], 1));
+            now[k] = fmaxf(now[k], __shfl_xor_sync(0xffffffffu, now[k], 2));
+            grown |= now[k] > m4[k] + kGrow;
+          }
+          if (__any_sync(0xffffffffu, grown)) {
+            float keep[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              keep[k] = exp2_approx(m4[k] - (now[k] == -INFINITY ? 0.f : now[k]));
+              l4[k] *= keep[k];
+              m4[k] = now[k];
+            }
+            if (begun) {
+#pragma unroll 1
+              for (int cc = 0; cc < 2 * D; cc += 32) {  // 16 lanes, then the others
+                const uint32_t at = o_col + cc % D + (cc >= D ? 16u << 16 : 0u);
+                float o[16];
+                tmem_ld_fragments_32cols(at, o);
+                tmem_ld_wait();
+                uint32_t ob[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  ob[e] = __float_as_uint(o[e] * ((e >> 1) & 1 ? (cc >= D ? keep[3] : keep[1])
+                                                               : (cc >= D ? keep[2] : keep[0])));
+                tmem_st_fragments_32cols(at, ob);
+              }
+            }
+          }
+          begun = true;
+          float nref[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) nref[k] = m4[k] == -INFINITY ? 0.f : -m4[k];
+          auto weigh4 = [&](int col, auto is_whole) {
+            uint32_t pw[2][16];
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+              const float2 f = *reinterpret_cast<const float2*>(v_scale + col + 8 * b);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float* y = &x[k >> 1][4 * b + 2 * (k & 1)];
+                const float2 z = __fadd2_rn(make_float2(y[0], y[1]), make_float2(nref[k], nref[k]));
+                float2 v = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+                l4[k] += v.x + v.y;
+                v = __fmul2_rn(v, f);
+                if constexpr (!decltype(is_whole)::value) {
+                  // a weight of 0 stays 0 whatever the scale of a place that is not seen
+                  if (y[0] == -INFINITY) v.x = 0.f;
+                  if (y[1] == -INFINITY) v.y = 0.f;
+                }
+                pw[k >> 1][2 * b + (k & 1)] = pack_bf16(v.x, v.y);
+              }
+            }
+            tmem_st_packed_fragments_32cols(p_col + col / 2, pw[0]);
+            tmem_st_packed_fragments_32cols(p_col + col / 2 + (16u << 16), pw[1]);
+          };
           const int u = 2 * g + 1;  // V's scales are written with V
           ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[u % S::kUnits], (u / S::kUnits) & 1));
           if (!ok) break;
-          weigh(x[0], 64, std::false_type{});
-          weigh(x[1], 96, std::false_type{});
+          if (whole) weigh4(64, std::true_type{});
+          else weigh4(64, std::false_type{});
           hand_over(&sm.p_half[t]);
           load(0);
-          weigh(x[0], 0, std::false_type{});
-          weigh(x[1], 32, std::false_type{});
+          if (whole) weigh4(0, std::true_type{});
+          else weigh4(0, std::false_type{});
           hand_over(&sm.p_full[t]);
         }
-        l2 = __fadd2_rn(l2, __fadd2_rn(sum0, sum1));
+        if constexpr (!kE4m3) l2 = __fadd2_rn(l2, __fadd2_rn(sum0, sum1));
       }
       const int first_join = joins;
       if (!two && count > 1) ++joins;
@@ -877,6 +972,18 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
       // ---- the end of this CTA's part of the item
       tc_fence_after();
       float l = l2.x + l2.y;
+      if constexpr (kE4m3) {  // to a row per thread (the warp's own 32)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          l4[k] += __shfl_xor_sync(0xffffffffu, l4[k], 1);
+          l4[k] += __shfl_xor_sync(0xffffffffu, l4[k], 2);
+          if ((lane & 3) == 0) sm.rows[t][32 * (warp & 3) + 8 * k + (lane >> 2)] = make_float2(m4[k], l4[k]);
+        }
+        __syncwarp();
+        m = sm.rows[t][r].x;
+        l = sm.rows[t][r].y;
+        __syncwarp();
+      }
       float keep = 1.f, keep2 = 0.f;
       const bool join = !two && count > 1;
       if (join) {

@@ -105,11 +105,21 @@ struct Rows {
   }
 };
 
-// x / s rounded to nearest, r = 1 / s rounded to nearest: one correction by the exact
-// remainder (Markstein), for s > 0 far from the ends of fp32's range.
-__device__ __forceinline__ float quotient(float x, float s, float r) {
-  const float y = x * r;
-  return copysignf(fmaf(fmaf(-s, y, x), r, y), x);  // a zero keeps its sign
+// 1 / s within two roundings, for s far from the ends of fp32's range.
+__device__ __forceinline__ float reciprocal(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return fmaf(fmaf(-s, r, 1.f), r, r);
+}
+// x / s rounded to nearest, nr = -1 / s: one correction by the exact remainder
+// (Markstein), the remainder with the sign that lets a zero keep its own.
+__device__ __forceinline__ float quotient(float x, float s, float nr) {
+  const float y = x * -nr;
+  return fmaf(fmaf(s, y, -x), nr, y);
+}
+__device__ __forceinline__ float2 quotient2(float2 x, float2 s, float2 r, float2 nr) {
+  const float2 y = __fmul2_rn(x, r);
+  return __ffma2_rn(__ffma2_rn(s, y, make_float2(-x.x, -x.y)), nr, y);
 }
 
 template <int D, bool kE4m3>
@@ -146,17 +156,21 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const CacheRowsA
         for (int o = R::kLanes / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
         top = max(top & 0xffffu, top >> 16);
         const bool finite = top < 0x7f80u;
-        const float s = !finite ? __uint_as_float(0x7fffffffu)
-                        : top == 0 ? 1.0f : __fdiv_rn(__uint_as_float(top << 16), kE4m3Max);
-        float y[8];
-        if (s > 0x1p-60f && s < 0x1p60f) {
-          const float r = __frcp_rn(s);
+        // (the largest entry from 2^-50 to 2^69: everything in fp32's normal range)
+        const bool usual = top - 0x2680u < 0x6200u - 0x2680u;
+        float s, y[8];
+        if (usual) {
+          s = quotient(__uint_as_float(top << 16), kE4m3Max, -1.f / kE4m3Max);
+          const float r = reciprocal(s);
+          const float2 s2 = make_float2(s, s), r2 = make_float2(r, r), nr2 = make_float2(-r, -r);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            y[2 * i] = quotient(bf16_lo(w[i]), s, r);
-            y[2 * i + 1] = quotient(bf16_hi(w[i]), s, r);
+            const float2 z = quotient2(make_float2(bf16_lo(w[i]), bf16_hi(w[i])), s2, r2, nr2);
+            y[2 * i] = z.x;
+            y[2 * i + 1] = z.y;
           }
         } else {
+          s = !finite ? __uint_as_float(0x7fffffffu) : top == 0 ? 1.0f : __fdiv_rn(__uint_as_float(top << 16), kE4m3Max);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             y[2 * i] = __fdiv_rn(bf16_lo(w[i]), s);
