@@ -17,7 +17,7 @@
 
 namespace kda {
 
-constexpr int kWindowCtas = 304;  // two per SM of a GB300
+constexpr int kWindowCtas = 456;  // three per SM of a GB300 at most
 constexpr int kChunkCtas = 152;   // one per SM
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;

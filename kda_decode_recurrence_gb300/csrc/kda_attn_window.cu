@@ -15,9 +15,17 @@
 //   O[rows, D/4 w ..] = O 2^(m_old - m) + P V  warp w's quarter of D
 // so that each entry of K and V is read from shared memory (and, for e4m3,
 // widened) once, and no warp's output has to be joined with another's.
+// e4m3 codes are widened to f16 (one conversion for two; bf16 takes five operations on
+// the pipe that is busiest), so Q and P are f16 there too, each scaled so that it
+// loses nothing: Q by a power of two per item (its largest entry becomes 2^8 .. 2^9),
+// P by the row's largest product of a weight and a value's scale:
+//   r = max_j (x_j + log2 vs_j),  w_j = 2^(x_j - r),  P_j = 2^15 w_j vs_j <= 2^15
+// (11 bits down to 2^-29 of the largest contribution, where bf16 would keep 8), the
+// sum being that of w_j.
 // mma.sync (m16n8k16) is the instruction for it: 16 rows are its native
 // size, where tcgen05 would spend 128 lanes on them.
 #include <cuda.h>
+#include <cuda_fp16.h>
 
 #include "kda_attn.cuh"
 #include "kda_launch.h"
@@ -47,10 +55,13 @@ struct Shape {
   static constexpr int kPanelBytes = kRowBytes < 128 ? kRowBytes : 128;
   static constexpr int kPanels = kRowBytes / kPanelBytes;
   static constexpr int kTileBytes = kTile * kRowBytes;     // K or V
-  // the ring: as deep as lets two CTAs share an SM
+  // CTAs per SM: e4m3 has twice the tiles for its bytes, and what a warp does per tile is a
+  // chain of dependent steps, so a third CTA fills issue slots where the registers allow it
+  static constexpr int kCtas = kE4m3 && kRows == 16 ? 3 : 2;
+  // the ring: as deep as lets them share the SM
   static constexpr int kOther = 2 * kRows * D * 2 + kRows * kTile * 2 + 4096;
   static constexpr int kStageBytes = 2 * kTileBytes + (kE4m3 ? 2 * kTile * 4 : 0);
-  static constexpr int kFit = (113 * 1024 - kOther) / kStageBytes;
+  static constexpr int kFit = ((227 * 1024) / kCtas - 1024 - kOther) / kStageBytes;
   static constexpr int kStages = kFit < 8 ? kFit : 8;
 };
 
@@ -62,6 +73,7 @@ struct Smem {
   unsigned char pw[kRows * kTile * 2];             // P, bf16, 128-byte swizzled rows
   float scales[kE4m3 ? S::kStages : 1][2][kTile];
   float4 top[kRows];                               // the warps' row maxima
+  float qinv[2];                                   // e4m3: what undoes Q's scaling
   StageNote note[S::kStages];
   uint64_t full[S::kStages], empty[S::kStages], qfull[2], qempty[2];
   long long part[kThreads / 32];
@@ -76,6 +88,28 @@ __device__ __forceinline__ void ldsm(uint32_t addr, uint32_t (&r)[4]) {
 __device__ __forceinline__ void ldsm_t(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two e4m3 codes (the low half of x) as f16 values.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t x) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float log2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -170,7 +204,7 @@ struct Walk {
 };
 
 template <int D, int kRows, bool kE4m3>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
     window_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                   const AttentionArgs p, const Pieces pieces) {
   using S = Shape<D, kRows, kE4m3>;
@@ -314,27 +348,62 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!ok) break;
       constexpr int kChunks = D / 8;  // 16-byte chunks of a row
       const int rows = w.r.n * p.G;
-#pragma unroll 4
-      for (int i = lane; i < kRows * kChunks; i += 32) {
+      auto load = [&](int i) {
         const int row = i / kChunks, c = i % kChunks;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (row < rows)
-          x = fresh(reinterpret_cast<const uint4*>(
-              p.q + (w.r.t0 + row / p.G) * p.q_stride + (size_t)(w.h * p.G + row % p.G) * D + c * 8));
-        if (kE4m3) {
+        if (row >= rows) return make_uint4(0, 0, 0, 0);
+        return *reinterpret_cast<const uint4*>(
+            p.q + (w.r.t0 + row / p.G) * p.q_stride + (size_t)(w.h * p.G + row % p.G) * D + c * 8);
+      };
+      auto store = [&](int i, uint4 x, float factor) {
+        const int row = i / kChunks, c = i % kChunks;
+        unsigned char* to = sm.q[s] + (c / 8) * kRows * 128;
+        if constexpr (kE4m3) {
           // Four consecutive entries of K sit in one register of the tensor core's
           // operand, pairs (0 1) (2 3) as k = 2 j .. and 2 j + 8 ..: the same order here.
           // Entries 4 j .. 4 j + 3 of each 16 go to 2 j, 2 j + 1, 2 j + 8, 2 j + 9.
-          unsigned char* to = sm.q[s] + (c / 8) * kRows * 128;
           const int j = (c & 1) * 2;  // this chunk's first group of four
           const int c0 = (c & 7) & ~1;
-          *reinterpret_cast<uint32_t*>(to + swizzled<128>(row, c0) + j * 4) = x.x;
-          *reinterpret_cast<uint32_t*>(to + swizzled<128>(row, c0 + 1) + j * 4) = x.y;
-          *reinterpret_cast<uint32_t*>(to + swizzled<128>(row, c0) + j * 4 + 4) = x.z;
-          *reinterpret_cast<uint32_t*>(to + swizzled<128>(row, c0 + 1) + j * 4 + 4) = x.w;
+          const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint32_t*>(to + swizzled<128>(row, c0 + (e & 1)) + j * 4 + (e >> 1) * 4) =
+                pack_f16(bf16_lo(v[e]) * factor, bf16_hi(v[e]) * factor);
         } else {
-          *reinterpret_cast<uint4*>(sm.q[s] + (c / 8) * kRows * 128 + swizzled<128>(row, c & 7)) = x;
+          *reinterpret_cast<uint4*>(to + swizzled<128>(row, c & 7)) = x;
         }
+      };
+      constexpr int kLoads = kRows * kChunks / 32;
+      if constexpr (kE4m3) {
+        // the largest finite entry's exponent e: factor 2^(135 - e)
+        uint32_t top = 0;
+        auto raise = [&](const uint4& x) {
+          const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = v[e] & 0x7fffu, hi = (v[e] >> 16) & 0x7fffu;
+            top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+          }
+        };
+        constexpr int kHeld = kLoads < 16 ? kLoads : 16;  // (64 rows of 128 entries are read twice)
+        uint4 held[kHeld];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) held[i] = load(i * 32 + lane);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) raise(held[i]);
+#pragma unroll 4
+        for (int i = kHeld; i < kLoads; ++i) raise(load(i * 32 + lane));
+#pragma unroll
+        for (int e = 16; e > 0; e >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, e));
+        const int field = min(253, 262 - (int)(top >> 7));  // its inverse is a normal number too
+        const float factor = __uint_as_float((uint32_t)field << 23);
+        if (lane == 0) sm.qinv[s] = __uint_as_float((uint32_t)(254 - field) << 23);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) store(i * 32 + lane, held[i], factor);
+#pragma unroll 4
+        for (int i = kHeld; i < kLoads; ++i) store(i * 32 + lane, load(i * 32 + lane), factor);
+      } else {
+#pragma unroll 8
+        for (int i = 0; i < kLoads; ++i) store(i * 32 + lane, load(i * 32 + lane), 1.f);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.qfull[s]);
@@ -346,7 +415,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     constexpr int kR = kRows / 16;        // row blocks of 16
     constexpr int kN = D / kComputeWarps / 8;  // blocks of 8 columns of O per warp
     const int quad = lane >> 2, j2 = (lane & 3) * 2;
-    const float xscale = p.scale * kLog2E;
+    float xscale = p.scale * kLog2E;
+    constexpr float kPScale = kE4m3 ? 32768.f : 1.f;  // of P, and so of O
     float o[kR][kN][4], m[kR][2], l[kR][2];
     long long left = u1 - u0;
     int item = -1;
@@ -360,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (note.flags & kFirst) {
         ++item;
         ok = __all_sync(0xffffffffu, mbar_wait(&sm.qfull[item & 1], (item / 2) & 1));
+        if (kE4m3) xscale = p.scale * kLog2E * sm.qinv[item & 1];
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
           m[r][0] = m[r][1] = -INFINITY;
@@ -389,8 +460,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           uint32_t a[4];
           const int row = 16 * r + (lane & 15), c = 2 * kb + (lane >> 4);
           ldsm(q_addr + (c / 8) * kRows * 128 + swizzled<128>(row, c & 7), a);
-          mma(x[r][0], a, b00, b01);
-          mma(x[r][1], a, b10, b11);
+          if constexpr (kE4m3) {
+            mma_f16(x[r][0], a, b00, b01);
+            mma_f16(x[r][1], a, b10, b11);
+          } else {
+            mma(x[r][0], a, b00, b01);
+            mma(x[r][1], a, b10, b11);
+          }
         }
       };
       if constexpr (!kE4m3) {
@@ -410,8 +486,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           uint32_t w[4][2];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            w[i][0] = widen(__byte_perm(b[i], 0, 0x1404));
-            w[i][1] = widen(__byte_perm(b[i], 0, 0x3424));
+            w[i][0] = codes_f16(b[i]);
+            w[i][1] = codes_f16(b[i] >> 16);
           }
           dot16(2 * kb, w[0][0], w[0][1], w[2][0], w[2][1]);
           dot16(2 * kb + 1, w[1][0], w[1][1], w[3][0], w[3][1]);
@@ -421,13 +497,22 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int pos0 = note.L - note.n;   // position of token 0
       const int lo_all = seen_lo(p, max(0, pos0));
       const bool whole = note.start >= seen_lo(p, note.L - 1) && note.start + kTile <= seen_hi(p, pos0, note.L);
-      float k_scale[2][2] = {{1.f, 1.f}, {1.f, 1.f}};
-      if constexpr (kE4m3) {
+      float k_scale[2][2], v_scale[2][2], v_log[2][2];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+      for (int n = 0; n < 2; ++n) {
+        k_scale[n][0] = k_scale[n][1] = xscale;
+        v_scale[n][0] = v_scale[n][1] = 1.f;
+        v_log[n][0] = v_log[n][1] = 0.f;
+        if constexpr (kE4m3) {
           const float2 f = *reinterpret_cast<const float2*>(&sm.scales[s][0][my_pos + 8 * n + j2]);
-          k_scale[n][0] = f.x;
-          k_scale[n][1] = f.y;
+          const float2 v = *reinterpret_cast<const float2*>(&sm.scales[s][1][my_pos + 8 * n + j2]);
+          k_scale[n][0] *= f.x;
+          k_scale[n][1] *= f.y;
+          v_scale[n][0] = v.x * kPScale;
+          v_scale[n][1] = v.y * kPScale;
+          // (a scale of 0: the value is 0, and r takes the score itself)
+          v_log[n][0] = v.x > 0.f ? log2_approx(v.x) : 0.f;
+          v_log[n][1] = v.y > 0.f ? log2_approx(v.y) : 0.f;
         }
       }
 #pragma unroll
@@ -445,12 +530,11 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float y = x[r][n][2 * half + i] * xscale;
-              if (kE4m3) y *= k_scale[n][i];
+              float y = x[r][n][2 * half + i] * k_scale[n][i];
               const int at = my_pos + 8 * n + j2 + i;
               if (!whole && (at < lo || at >= hi)) y = -INFINITY;
               x[r][n][2 * half + i] = y;
-              top = fmaxf(top, y);
+              top = fmaxf(top, kE4m3 ? y + v_log[n][i] : y);
             }
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -458,15 +542,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       ok = compute_sync_and(ok);
       if (!ok) break;
-      float v_scale[2][2] = {{1.f, 1.f}, {1.f, 1.f}};
-      if constexpr (kE4m3) {
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float2 f = *reinterpret_cast<const float2*>(&sm.scales[s][1][my_pos + 8 * n + j2]);
-          v_scale[n][0] = f.x;
-          v_scale[n][1] = f.y;
-        }
-      }
       float keep[kR][2];
       bool moved = false;
 #pragma unroll
@@ -491,7 +566,8 @@ __global__ void __launch_bounds__(kThreads, 2)
               y1 = x[r][n][2 * half + 1] == -INFINITY ? 0.f : w1 * v_scale[n][1];
             }
             const int row = 16 * r + 8 * half + quad;
-            *reinterpret_cast<uint32_t*>(sm.pw + swizzled<128>(row, 2 * warp + n) + j2 * 2) = pack_bf16(y0, y1);
+            *reinterpret_cast<uint32_t*>(sm.pw + swizzled<128>(row, 2 * warp + n) + j2 * 2) =
+                kE4m3 ? pack_f16(y0, y1) : pack_bf16(y0, y1);
           }
         }
       compute_sync();
@@ -585,20 +661,26 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
           }
         } else {
-          // 16 columns per 16-byte chunk: the even ones, then the odd ones.  Codes have no
-          // bad values (a bad row has a bad scale, which is in P of the rows that see it).
+          // 16 columns per 16-byte chunk: the even ones, then the odd ones.  Codes in use have
+          // no bad values (a bad row has a bad scale, which is in P of the rows that see it).
           constexpr int kChunks = D / kComputeWarps / 16;  // 2 (D = 128) or 1
           uint32_t b[4];
           const int c = warp * kChunks + (kChunks == 2 ? lane >> 4 : 0);
           ldsm_t(v_addr + swizzled<S::kPanelBytes>(row, c), b);
+          if (!v_whole) {
+            const uint32_t lo = v_mask(16 * kb + j2), hi = v_mask(16 * kb + 8 + j2);
+            b[0] &= lo; b[1] &= hi; b[2] &= lo; b[3] &= hi;
+          }
 #pragma unroll
           for (int ch = 0; ch < kChunks; ++ch) {
-            const uint32_t e0 = widen((b[2 * ch] & 0x00ff00ffu) << 8), e1 = widen((b[2 * ch + 1] & 0x00ff00ffu) << 8);
-            const uint32_t d0 = widen(b[2 * ch] & 0xff00ff00u), d1 = widen(b[2 * ch + 1] & 0xff00ff00u);
+            // columns of two positions: (0 1 | 0 1) to (0 | 0), (1 | 1)
+            const uint32_t b0 = __byte_perm(b[2 * ch], 0, 0x3120), b1 = __byte_perm(b[2 * ch + 1], 0, 0x3120);
+            const uint32_t e0 = codes_f16(b0), e1 = codes_f16(b1);
+            const uint32_t d0 = codes_f16(b0 >> 16), d1 = codes_f16(b1 >> 16);
 #pragma unroll
             for (int r = 0; r < kR; ++r) {
-              mma(o[r][2 * ch], a[r], e0, e1);
-              mma(o[r][2 * ch + 1], a[r], d0, d1);
+              mma_f16(o[r][2 * ch], a[r], e0, e1);
+              mma_f16(o[r][2 * ch + 1], a[r], d0, d1);
             }
           }
         }
@@ -636,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (row >= rows) continue;
           const int tok = row / p.G;
           const size_t out_row = (size_t)(note.t0 + tok) * p.H + note.h * p.G + (row - tok * p.G);
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          const float inv = (sum == 0.f ? 0.f : 1.f / sum) * (1.f / kPScale);
           const size_t piece = ((size_t)cta * 2 + place) * kRows + row;
           if (warp == 0 && (lane & 3) == 0) {
             if (!done) pieces.ml[piece] = make_float2(m[r][half], sum);
@@ -660,7 +742,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 *reinterpret_cast<uint2*>(p.out + out_row * D + col) =
                     make_uint2(pack_bf16(y0 * inv, y1 * inv), pack_bf16(y2 * inv, y3 * inv));
               else
-                *reinterpret_cast<float4*>(pieces.o + piece * D + col) = make_float4(y0, y1, y2, y3);
+                *reinterpret_cast<float4*>(pieces.o + piece * D + col) =
+                    make_float4(y0 / kPScale, y1 / kPScale, y2 / kPScale, y3 / kPScale);
             }
           }
         }
@@ -674,7 +757,7 @@ template <int D, int kRows, bool kE4m3>
 cudaError_t launch_window(const AttentionArgs& a, cudaStream_t stream) {
   using Sm = Smem<D, kRows, kE4m3>;
   using S = Shape<D, kRows, kE4m3>;
-  static_assert(2 * (sizeof(Sm) + 1024 + 1024) <= 228 * 1024, "two window CTAs fit an SM");
+  static_assert(S::kCtas * (sizeof(Sm) + 1024 + 1024) <= 228 * 1024, "the window CTAs fit an SM");
   static_assert(S::kStages >= 2, "the ring holds two key tiles");
   CUtensorMap maps[2];
   const uint64_t rows = (uint64_t)a.c.num_pages * a.c.HKV * a.c.page_size;
@@ -688,11 +771,11 @@ cudaError_t launch_window(const AttentionArgs& a, cudaStream_t stream) {
   static SmemSet set;
   cudaError_t e = allow_smem(window_kernel<D, kRows, kE4m3>, smem, set);
   if (e != cudaSuccess) return e;
-  const Pieces pieces = pieces_at(a.workspace, kWindowCtas, kRows);
-  e = launch(window_kernel<D, kRows, kE4m3>, dim3(kWindowCtas), dim3(kThreads), smem, stream, true,
+  const Pieces pieces = pieces_at(a.workspace, 152 * S::kCtas, kRows);
+  e = launch(window_kernel<D, kRows, kE4m3>, dim3(152 * S::kCtas), dim3(kThreads), smem, stream, true,
              maps[0], maps[1], a, pieces);
   if (e != cudaSuccess) return e;
-  return launch_join_pieces(a, pieces, kRows, kWindowCtas, stream);
+  return launch_join_pieces(a, pieces, kRows, 152 * S::kCtas, stream);
 }
 
 template <int D, bool kE4m3>

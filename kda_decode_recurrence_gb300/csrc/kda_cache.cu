@@ -123,7 +123,7 @@ __device__ __forceinline__ float2 quotient2(float2 x, float2 s, float2 r, float2
 }
 
 template <int D, bool kE4m3>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const CacheRowsArgs p, const Split split) {
+__global__ void __launch_bounds__(kThreads, 4) cache_append_kernel(const CacheRowsArgs p, const Split split) {
   using R = Rows<D>;
   R rows;
   pdl_wait();
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const CacheRowsA
 }
 
 template <int D, bool kE4m3>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheRowsArgs p, const Split split) {
+__global__ void __launch_bounds__(kThreads, 6) cache_read_kernel(const CacheRowsArgs p, const Split split) {
   using R = Rows<D>;
   R rows;
   pdl_wait();
@@ -246,12 +246,12 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheRowsArg
   }
 }
 
-// As many tokens to a warp as leave every SM's 64 warps something to do (one look-up
-// then serves several rows in flight), eight at most.
+// As many tokens to a warp as leave every SM 128 of them (one look-up then serves
+// several rows in flight; fewer warps leave a tail), eight at most.
 template <typename Kernel>
 cudaError_t run(Kernel kernel, const CacheRowsArgs& a, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
-  constexpr int kAllWarps = 152 * 64;
+  constexpr int kAllWarps = 152 * 128;
   Split s;
   s.tokens = a.T / kAllWarps < 1 ? 1 : a.T / kAllWarps > 8 ? 8 : a.T / kAllWarps;
   s.inv = (uint32_t)(((1ull << 32) + 2 * a.c.HKV - 1) / (2 * a.c.HKV));
