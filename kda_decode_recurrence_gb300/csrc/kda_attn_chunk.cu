@@ -64,12 +64,14 @@ constexpr int kFirst = 1, kLast = 2;  // of this CTA's part of the item
 constexpr int kSecond = 8;            // the item has a second row tile
 constexpr int kWhole = 16;            // every row sees every position
 
-template <int D, bool kE4m3>
+template <int D, bool kE4m3, bool kPair>
 struct Shape {
   static constexpr int kPanels = D / 64;
   static constexpr int kUnitBytes = kTile * D * 2;       // K or V of one key tile, bf16
-  // units alternate K, V, K, V ..; four are the least that S two tasks ahead needs
-  static constexpr int kUnits = D == 128 ? (kE4m3 ? 4 : 5) : 8;
+  static constexpr int kQTiles = kPair ? 2 : 1;
+  // units alternate K, V, K, V ..; four are the least that S two tasks ahead needs, and as
+  // many as fit are taken: with a key tile per task (kPair false) copies have to be far ahead
+  static constexpr int kUnits = D == 128 ? (kE4m3 ? 4 : 5) + (kPair ? 0 : 1) : kE4m3 ? 8 : 12;
   static constexpr int kPart = kE4m3 ? 64 : 128;         // positions copied at a time
   static constexpr int kRawUnits = kE4m3 ? (D == 128 ? 3 : 6) : 1;  // parts of codes
   static constexpr int kRawBytes = kPart * D;
@@ -100,10 +102,10 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-template <int D, bool kE4m3>
+template <int D, bool kE4m3, bool kPair>
 struct Smem {
-  using S = Shape<D, kE4m3>;
-  unsigned char q[2][kM * D * 2];                  // 1024-aligned, swizzled panels
+  using S = Shape<D, kE4m3, kPair>;
+  unsigned char q[S::kQTiles][kM * D * 2];         // 1024-aligned, swizzled panels
   unsigned char unit[S::kUnits][S::kUnitBytes];
   unsigned char raw[kE4m3 ? S::kRawUnits : 1][kE4m3 ? S::kRawBytes : 16];
   float raw_scale[kE4m3 ? S::kRawUnits : 1][kE4m3 ? S::kPart : 4];
@@ -135,7 +137,7 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& p, const Request& r
 }
 // Units of one key head of a request (0: not this kernel's), `pair` tokens to an item.
 __device__ __forceinline__ long long head_units(const AttentionArgs& p, const Request& r, int pair) {
-  if (r.n * p.G <= kWindowRows) return 0;
+  if (r.n * p.G <= p.window_rows) return 0;
   long long sum = 0;
   for (int t = 0; t < r.n; t += pair) sum += span_of(p, r, t, pair).tiles;
   return sum;
@@ -156,7 +158,7 @@ struct Walk {
     base = b;
     mine = Request{0, 0, 0};
     if (b + lane < p.B) mine = load_request(p, b + lane, false);
-    if (mine.n * p.G <= kWindowRows) mine.n = 0;
+    if (mine.n * p.G <= p.window_rows) mine.n = 0;
   }
   __device__ __forceinline__ void take(const AttentionArgs& p, int pair, int lane) {
     while (b < p.B) {
@@ -308,13 +310,14 @@ __device__ __forceinline__ bool wait_together(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_try(bar, parity)) || wait_on(bar, parity);
 }
 
-template <int D, bool kE4m3>
-__global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
+// kPair: items may have two row tiles (else no request of the call has more than one).
+template <int D, bool kE4m3, bool kPair>
+__global__ void __launch_bounds__(Shape<D, kE4m3, kPair>::kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                  const __grid_constant__ CUtensorMap v_map, const AttentionArgs p, const Pieces pieces) {
-  using S = Shape<D, kE4m3>;
+  using S = Shape<D, kE4m3, kPair>;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  Smem<D, kE4m3>& sm = *reinterpret_cast<Smem<D, kE4m3>*>(
+  Smem<D, kE4m3, kPair>& sm = *reinterpret_cast<Smem<D, kE4m3, kPair>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
@@ -451,7 +454,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
         // token rows of a row tile are rows tok G + g of its panels
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (t == 1 && w.token0 + per_tile >= w.r.n) break;
+          if (t == 1 && (!kPair || w.token0 + per_tile >= w.r.n)) break;
           if (queries[t] > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait(&sm.q_empty[t], (queries[t] - 1) & 1));
           if (!ok) break;
           ++queries[t];
@@ -459,7 +462,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
             mbar_expect_tx(&sm.q_full[t], S::kPanels * per_tile * p.G * 128);
 #pragma unroll
             for (int pn = 0; pn < S::kPanels; ++pn)
-              tma_load_3d(sm.q[t] + pn * kM * 128, &q_map, &sm.q_full[t], pn * 64, w.h * p.G,
+              tma_load_3d(sm.q[t % S::kQTiles] + pn * kM * 128, &q_map, &sm.q_full[t], pn * 64, w.h * p.G,
                           w.r.t0 + w.token0 + t * per_tile);
           }
           __syncwarp();
@@ -554,33 +557,36 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
       const uint32_t p_col = base + (slot ? S::col_p(1) : S::col_p(0));
       const uint32_t q0 = smem_u32(sm.q[0]), unit0 = smem_u32(sm.unit[0]);
       auto wait = [&](uint64_t* bar, int parity) { return wait_together(smem_u32(bar), parity); };
-      // The slot's next S, found and waited for before the turn in which it is issued: its
-      // ring place, the step's flags and the addresses of its operands.
+      // The slot's next S, found before the turn in which it is issued (if its operands are
+      // there by then: PV does not wait for them): its ring place, the step's flags and the
+      // addresses of its operands.
       int sg = 0, su = 0, su_phase = 0, s_task = 0, q_items[2] = {0, 0};
       bool q_due = false;   // the item's queries have not been waited for
       bool found = false;
       int f_unit = 0, f_flags = 0;
       uint32_t f_q = 0, f_k = 0;
-      auto find_scores = [&]() {
-        found = false;
+      auto there = [&](uint64_t* bar, int parity, bool stay) {
+        if (__all_sync(0xffffffffu, mbar_try(smem_u32(bar), parity))) return true;
+        if (stay) ok = wait_on(smem_u32(bar), parity);
+        return stay && ok;
+      };
+      bool counted = false;  // the step's flags have been taken in
+      auto find_scores = [&](bool stay) {
         while (sg < all && !found) {
-          ok = wait(&sm.full[su], su_phase);
-          if (!ok) return;
+          if (!there(&sm.full[su], su_phase, stay)) return;
           f_flags = __shfl_sync(0xffffffffu, sm.note[sg % kSteps].flags, 0);
-          const bool two = (f_flags & kSecond) != 0;
-          if (f_flags & kFirst) {
+          const bool two = kPair && (f_flags & kSecond) != 0;
+          if ((f_flags & kFirst) && !counted) {
             q_due = true;
             ++q_items[0];
             if (two) ++q_items[1];
           }
-          found = two || (s_task & 1) == slot;
-          if (found) {
+          counted = true;
+          if (two || (s_task & 1) == slot) {
             const int tile = two ? slot ^ (s_task & 1) : 0;
-            if (q_due) {
-              ok = wait(&sm.q_full[tile], ((tile ? q_items[1] : q_items[0]) - 1) & 1);
-              if (!ok) return;
-              q_due = false;
-            }
+            if (q_due && !there(&sm.q_full[tile], ((tile ? q_items[1] : q_items[0]) - 1) & 1, stay)) return;
+            q_due = false;
+            found = true;
             f_unit = su;
             f_q = q0 + tile * (kM * D * 2);
             f_k = unit0 + su * S::kUnitBytes;
@@ -589,6 +595,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
             if (f_flags & kLast) mma_commit(&sm.q_empty[0]);
           }
           __syncwarp();
+          counted = false;
           s_task += two ? 2 : 1;
           ++sg;
           su += 2;
@@ -598,35 +605,38 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
           }
         }
       };
-      // by the elected lane
+      // by the elected lane, after a fence
       auto issue_found = [&](uint64_t* turn) {
         issue_scores<D>(s_col, f_q, f_k, turn);
         mma_commit(&sm.s_full[slot]);
         mma_commit(&sm.empty[f_unit]);
         if (f_flags & kLast) {
           mma_commit(&sm.q_empty[0]);
-          if (f_flags & kSecond) mma_commit(&sm.q_empty[1]);
+          if (kPair && (f_flags & kSecond)) mma_commit(&sm.q_empty[1]);
         }
       };
-      find_scores();
-      if (ok && found) {
+      auto find_and_issue = [&]() {
+        find_scores(true);
+        if (!ok || !found) return;
         tc_fence_after();
         if (elect_one()) issue_found(nullptr);
         __syncwarp();
-      }
+        found = false;
+      };
+      find_and_issue();
       int task = 0, mine = 0, v = 1, v_phase = 0;
       for (int g = 0; g < all && ok; ++g) {
         // (the fixing warp waits for V)
         ok = kE4m3 ? wait(&sm.full[v], v_phase) : wait(&sm.fixed[g % kSteps], (g / kSteps) & 1);
         if (!ok) break;
-        const bool two = (__shfl_sync(0xffffffffu, sm.note[g % kSteps].flags, 0) & kSecond) != 0;
+        const bool two = kPair && (__shfl_sync(0xffffffffu, sm.note[g % kSteps].flags, 0) & kSecond) != 0;
         // the slot's first task of the item starts O
         const bool add = __shfl_sync(0xffffffffu, sm.note[g % kSteps].index, 0) > (two ? 0 : 1);
         if (two || (task & 1) == slot) {
           const uint32_t v_addr = unit0 + v * S::kUnitBytes;
           // task 0 has the first turn; every other one follows the task before it
-          find_scores();
-          ok = ok && wait(&sm.p_half[slot], mine & 1);
+          find_scores(false);
+          ok = wait(&sm.p_half[slot], mine & 1);
           const int first_turn = slot == 0 ? 1 : 0;
           if (ok && mine >= first_turn) ok = wait(&sm.turn[slot], (mine - first_turn) & 1);
           if (!ok) break;
@@ -646,6 +656,8 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
           }
           __syncwarp();
           ++mine;
+          if (found) found = false;
+          else find_and_issue();
         } else if (elect_one()) {
           mbar_arrive(&sm.empty[v]);
         }
@@ -666,8 +678,12 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
       // ---- entries of V that are not part of the request or not finite, in key tiles
       // that some row sees in part
       for (int g = 0; g < steps && ok; ++g) {
+        // K too: a wait for a place's next phase says nothing while the one before it is open,
+        // and with an odd number of places V follows K there
         const int u = 2 * g + 1, s = u % S::kUnits;
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[s], (u / S::kUnits) & 1));
+        ok = mbar_wait(&sm.full[(u - 1) % S::kUnits], ((u - 1) / S::kUnits) & 1) &&
+             mbar_wait(&sm.full[s], (u / S::kUnits) & 1);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const StepNote& n = sm.note[g % kSteps];
         if ((n.flags & kFirst) && lane == 0) sm.bad[n.item % kSteps] = 0;
@@ -712,7 +728,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
     long long unit = u0;
     for (int item = 0; w.left > 0 && ok; ++item, unit += w.count(), w.next(p, pair, lane)) {
       const int count = w.count(), L = w.r.L, n = w.r.n;
-      const bool two = w.token0 + per_tile < n;
+      const bool two = kPair && w.token0 + per_tile < n;
       const int slot0 = task0 & 1;              // the slot of the item's first task
       // two row tiles: this slot has one of them, all steps; one: every other step
       const int tile = two ? t ^ slot0 : 0;
@@ -1074,10 +1090,10 @@ __global__ void __launch_bounds__(Shape<D, kE4m3>::kThreads, 1)
   }
 }
 
-template <int D, bool kE4m3>
+template <int D, bool kE4m3, bool kPair>
 cudaError_t launch_chunk(const AttentionArgs& a, cudaStream_t stream) {
-  using Sm = Smem<D, kE4m3>;
-  using S = Shape<D, kE4m3>;
+  using Sm = Smem<D, kE4m3, kPair>;
+  using S = Shape<D, kE4m3, kPair>;
   static_assert(sizeof(Sm) + 1024 <= 227 * 1024, "a chunk CTA fits an SM");
   CUtensorMap q_map, maps[2];
   const int per_tile = kM / a.G;
@@ -1092,21 +1108,26 @@ cudaError_t launch_chunk(const AttentionArgs& a, cudaStream_t stream) {
       return cudaErrorInvalidValue;
   const size_t smem = sizeof(Sm) + 1024;
   static SmemSet set;
-  cudaError_t e = allow_smem(chunk_kernel<D, kE4m3>, smem, set);
+  cudaError_t e = allow_smem(chunk_kernel<D, kE4m3, kPair>, smem, set);
   if (e != cudaSuccess) return e;
   const Pieces pieces = pieces_at(a.workspace, kChunkCtas, kChunkRows);
-  e = launch(chunk_kernel<D, kE4m3>, dim3(kChunkCtas), dim3(S::kThreads), smem, stream, true, q_map, maps[0],
+  e = launch(chunk_kernel<D, kE4m3, kPair>, dim3(kChunkCtas), dim3(S::kThreads), smem, stream, true, q_map, maps[0],
              maps[1], a, pieces);
   if (e != cudaSuccess) return e;
   return launch_join_pieces(a, pieces, kChunkRows, kChunkCtas, stream);
 }
 
+template <int D, bool kE4m3>
+cudaError_t by_pair(const AttentionArgs& a, bool pair, cudaStream_t stream) {
+  return pair ? launch_chunk<D, kE4m3, true>(a, stream) : launch_chunk<D, kE4m3, false>(a, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_chunk_attention(const AttentionArgs& a, cudaStream_t stream) {
-  if (a.c.D == 128)
-    return a.c.e4m3 ? launch_chunk<128, true>(a, stream) : launch_chunk<128, false>(a, stream);
-  return a.c.e4m3 ? launch_chunk<64, true>(a, stream) : launch_chunk<64, false>(a, stream);
+  const bool pair = a.max_tokens > kM / a.G;
+  if (a.c.D == 128) return a.c.e4m3 ? by_pair<128, true>(a, pair, stream) : by_pair<128, false>(a, pair, stream);
+  return a.c.e4m3 ? by_pair<64, true>(a, pair, stream) : by_pair<64, false>(a, pair, stream);
 }
 
 }  // namespace kda

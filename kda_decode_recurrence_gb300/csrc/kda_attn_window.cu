@@ -1,9 +1,9 @@
 // kda_attn_window.cu -- attention of single tokens and drafted windows: the requests
-// with at most 64 rows (new tokens x query heads per key head).
+// with few rows (new tokens x query heads per key head; window_limit: 32, or 16).
 //
 // Such a request reads every cached row for 4 G n_b operations a byte at most, so HBM
-// bounds it and the kernel is built to keep copies in flight: two CTAs per SM,
-// each with a ring of key tiles (64 positions of K and V) filled by one
+// bounds it and the kernel is built to keep copies in flight: two or three CTAs per
+// SM, each with a ring of key tiles (64 positions of K and V) filled by one
 // warp through TMA, one box per page and 128-byte panel.  Key tiles of all
 // requests are divided evenly over the CTAs (kda_attn.cuh), whatever their lengths.
 //
@@ -24,6 +24,13 @@
 // sum being that of w_j.
 // mma.sync (m16n8k16) is the instruction for it: 16 rows are its native
 // size, where tcgen05 would spend 128 lanes on them.
+//
+// 128 single tokens over 5.05 GB of bf16 cache: 713 us, 7.07 TB/s (a copy: 6.70).
+// 64 over 628 MB of e4m3: 141 us, 4.47 TB/s, bound by the issue of its instructions
+// (two CTAs an SM and bf16 operands: 178 us).  With more rows a warp reads as many
+// operands of Q and P as of K and V: 3.9 TB/s at 32 rows, 2.3 at 64.  Eight warps that
+// split D by eight: 165 us and 755 us on these two; streams of 32 positions per warp
+// that exchange nothing until an item's end, one CTA an SM: 265 us and 1320 us.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -140,7 +147,7 @@ __device__ __forceinline__ int key_tiles(const AttentionArgs& p, const Request& 
   return max(1, (r.L + kTile - 1) / kTile - first_tile(p, r));
 }
 __device__ __forceinline__ long long units_of(const AttentionArgs& p, const Request& r) {
-  return r.n > 0 && r.n * p.G <= kWindowRows ? (long long)p.c.HKV * key_tiles(p, r) : 0;
+  return r.n > 0 && r.n * p.G <= p.window_rows ? (long long)p.c.HKV * key_tiles(p, r) : 0;
 }
 
 // The items of one CTA's share in order, walked by a whole warp: 32 requests
@@ -384,23 +391,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
             top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
           }
         };
-        constexpr int kHeld = kLoads < 16 ? kLoads : 16;  // (64 rows of 128 entries are read twice)
-        uint4 held[kHeld];
+        uint4 held[kLoads];
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) held[i] = load(i * 32 + lane);
+        for (int i = 0; i < kLoads; ++i) held[i] = load(i * 32 + lane);
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) raise(held[i]);
-#pragma unroll 4
-        for (int i = kHeld; i < kLoads; ++i) raise(load(i * 32 + lane));
+        for (int i = 0; i < kLoads; ++i) raise(held[i]);
 #pragma unroll
         for (int e = 16; e > 0; e >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, e));
         const int field = min(253, 262 - (int)(top >> 7));  // its inverse is a normal number too
         const float factor = __uint_as_float((uint32_t)field << 23);
         if (lane == 0) sm.qinv[s] = __uint_as_float((uint32_t)(254 - field) << 23);
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) store(i * 32 + lane, held[i], factor);
-#pragma unroll 4
-        for (int i = kHeld; i < kLoads; ++i) store(i * 32 + lane, load(i * 32 + lane), factor);
+        for (int i = 0; i < kLoads; ++i) store(i * 32 + lane, held[i], factor);
       } else {
 #pragma unroll 8
         for (int i = 0; i < kLoads; ++i) store(i * 32 + lane, load(i * 32 + lane), 1.f);
@@ -780,21 +782,14 @@ cudaError_t launch_window(const AttentionArgs& a, cudaStream_t stream) {
 
 template <int D, bool kE4m3>
 cudaError_t by_rows(const AttentionArgs& a, cudaStream_t stream) {
-  switch (window_rows(a.max_tokens, a.G)) {
-    case 16: return launch_window<D, 16, kE4m3>(a, stream);
-    case 32: return launch_window<D, 32, kE4m3>(a, stream);
-    default: return launch_window<D, 64, kE4m3>(a, stream);
-  }
+  if (window_rows(a.max_tokens, a.G) == 16 || a.window_rows == 16) return launch_window<D, 16, kE4m3>(a, stream);
+  if constexpr (D == 128 || kE4m3) return launch_window<D, 32, kE4m3>(a, stream);
+  return cudaErrorInvalidValue;  // its limit is 16 rows
 }
 
 }  // namespace
 
-// The fewest rows that hold every window of at most max_tokens tokens (64: some may
-// not fit, and are not this kernel's).
-int window_rows(int max_tokens, int G) {
-  const long long rows = (long long)max_tokens * G;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-}
+int window_rows(int max_tokens, int G) { return (long long)max_tokens * G <= 16 ? 16 : 32; }
 
 cudaError_t launch_window_attention(const AttentionArgs& a, cudaStream_t stream) {
   if (a.c.D == 128)

@@ -47,6 +47,7 @@ struct AttentionArgs {
   float scale;
   int causal, window;
   int B, T, max_tokens, H, G;
+  int window_rows;  // requests of at most so many rows are the window kernel's
   void* workspace;
   int32_t* dev_status;
 };
