@@ -48,9 +48,9 @@ FALLBACK_HBM_GBS = 6800.0
 # requests, one eighth of the grouped workload: `bench.py --profile decode`)
 # and scaled to the full launch: reads x 8; writes x 8 less what is still
 # dirty in L2 when the kernel ends (the reduced case's algorithmic writes
-# minus its measured ones, 55.2 MB), which does not grow with the workload.
-NCU_REDUCED = {"read": 204660992, "write": 147660544, "algorithmic_write": 202899456, "scale": 8}
-NCU_TRAFFIC = {"sources_sha256": "ad45e14dfdb5a47ad6fe947108b664dbad52393d5635ff7dbb9604994e466120",
+# minus its measured ones, 54.7 MB), which does not grow with the workload.
+NCU_REDUCED = {"read": 204670208, "write": 148156672, "algorithmic_write": 202899456, "scale": 8}
+NCU_TRAFFIC = {"sources_sha256": "4a1892a66c64bd204059030c7efe99fc13d20aad0c04998ddd6bbd06fe344886",
                "bytes_per_launch": (NCU_REDUCED["read"] * NCU_REDUCED["scale"]
                                     + NCU_REDUCED["algorithmic_write"] * NCU_REDUCED["scale"]
                                     - (NCU_REDUCED["algorithmic_write"] - NCU_REDUCED["write"]))}
