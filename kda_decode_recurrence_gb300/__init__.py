@@ -76,6 +76,8 @@ class KdaDeviceError(RuntimeError):
 
 
 def _check(t: torch.Tensor, name: str, dtype, device) -> None:
+    if t.dtype is dtype and t.device == device and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != device:
@@ -270,46 +272,49 @@ def kda_block_tkg(out, hidden, gamma_in, W_in, W_fb, W_gb, conv_w, A_log, dt_bia
 def _check_rows(t: torch.Tensor, name: str, heads: int, D: int, device) -> int:
     """A [T, heads, D] bf16 tensor whose tokens may be strided (a view of a fused
     projection's output); returns the elements between two tokens."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
-        raise ValueError(f"{name} shape {tuple(t.shape)} != [T, {heads}, {D}]")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D:
+        raise ValueError(f"{name} shape {tuple(shape)} != [T, {heads}, {D}]")
     s = t.stride()
     if s[2] != 1 or (heads > 1 and s[1] != D):
         raise ValueError(f"{name}: a token's rows must be contiguous (strides {s})")
-    return s[0] if t.shape[0] > 1 else heads * D
+    return s[0] if shape[0] > 1 else heads * D
 
 
 def _check_cache(k_cache, v_cache, k_scale, v_scale, page_table, cu, what):
     """The tensors every call on a paged cache takes; returns (cache_dtype, B, HKV,
     D, page_size, num_pages, max_pages)."""
-    dev = k_cache.device
-    if k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
-        raise TypeError(f"k_cache: expected bfloat16 or float8_e4m3fn, got {k_cache.dtype}")
-    e4m3 = k_cache.dtype == torch.float8_e4m3fn
-    _check(k_cache, "k_cache", k_cache.dtype, dev)
-    _check(v_cache, "v_cache", k_cache.dtype, dev)
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
-        raise ValueError(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} must be "
+    dev, dtype, shape = k_cache.device, k_cache.dtype, k_cache.shape
+    e4m3 = dtype is torch.float8_e4m3fn
+    if not e4m3 and dtype is not torch.bfloat16:
+        raise TypeError(f"k_cache: expected bfloat16 or float8_e4m3fn, got {dtype}")
+    _check(k_cache, "k_cache", dtype, dev)
+    _check(v_cache, "v_cache", dtype, dev)
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError(f"k_cache {tuple(shape)} and v_cache {tuple(v_cache.shape)} must be "
                          "the same [num_pages, HKV, page_size, D]")
+    N, HKV, page, D = shape
     if e4m3:
         if k_scale is None or v_scale is None:
             raise ValueError("an e4m3 cache needs k_scale and v_scale")
+        rows = (N, HKV, page)
         for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             _check(t, n, torch.float32, dev)
-            if t.shape != k_cache.shape[:3]:
-                raise ValueError(f"{n} shape {tuple(t.shape)} != {tuple(k_cache.shape[:3])}")
+            if t.shape != rows:
+                raise ValueError(f"{n} shape {tuple(t.shape)} != {rows}")
     elif k_scale is not None or v_scale is not None:
         raise ValueError("a bf16 cache takes no scales")
     _check(page_table, "page_table", torch.int32, dev)
     _check(cu, what, torch.int32, dev)
-    B = page_table.shape[0]
-    if page_table.dim() != 2 or cu.numel() != B + 1:
+    table = page_table.shape
+    B = table[0]
+    if len(table) != 2 or cu.numel() != B + 1:
         raise ValueError(f"page_table must be [B, max_pages] and {what} have B + 1 entries")
-    N, HKV, page, D = k_cache.shape
-    return (CACHE_E4M3 if e4m3 else CACHE_BF16), B, HKV, D, page, N, page_table.shape[1]
+    return (CACHE_E4M3 if e4m3 else CACHE_BF16), B, HKV, D, page, N, table[1]
 
 
 def _ptr(t):
@@ -388,17 +393,18 @@ def kda_paged_attention(out, q, k_cache, v_cache, cu_seqlens, seq_lens, page_tab
     dev = k_cache.device
     dtype, B, HKV, D, page, N, max_pages = _check_cache(k_cache, v_cache, k_scale, v_scale,
                                                         page_table, cu_seqlens, "cu_seqlens")
-    T, H = out.shape[0], out.shape[1]
+    shape = out.shape
+    T, H = shape[0], shape[1]
     _check(out, "out", torch.bfloat16, dev)
     qs = _check_rows(q, "q", H, D, dev)
-    if tuple(out.shape) != (q.shape[0], H, D):
-        raise ValueError(f"out shape {tuple(out.shape)} != {tuple(q.shape)}")
+    if shape != q.shape:
+        raise ValueError(f"out shape {tuple(shape)} != {tuple(q.shape)}")
     _check(seq_lens, "seq_lens", torch.int32, dev)
     if seq_lens.numel() != B:
         raise ValueError("seq_lens must have B entries")
     if lse is not None:
         _check(lse, "lse", torch.float32, dev)
-        if tuple(lse.shape) != (T, H):
+        if lse.shape != (T, H):
             raise ValueError(f"lse shape {tuple(lse.shape)} != [{T}, {H}]")
     if workspace is None:
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
@@ -448,7 +454,7 @@ def kda_verify_draft(tokens, accepted, target_probs, draft_probs, draft_tokens, 
             raise TypeError(f"{n}: expected {torch.float32}, got {t.dtype}")
         if t.device != dev:
             raise ValueError(f"{n}: expected device {dev}, got {t.device}")
-        if tuple(t.shape) != (rows, V) or (V > 1 and t.stride(1) != 1):
+        if t.shape != (rows, V) or (V > 1 and t.stride(1) != 1):
             raise ValueError(f"{n}: expected [{rows}, {V}] with contiguous rows, got {tuple(t.shape)}")
         strides.append(t.stride(0) if rows > 1 else V)
     status = _status_word(dev_status, dev, stream)
