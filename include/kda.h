@@ -308,7 +308,8 @@ size_t kda_block_tkg_workspace_size(int B, int n, int Hd, int nh, int K, int V, 
  *   KDA_CACHE_BF16   bf16 rows; k_scale and v_scale are NULL.
  *   KDA_CACHE_E4M3   e4m3 codes (8 bits) and fp32 scales [num_pages, HKV,
  *                    page_size], one per row: the row is code * scale.  The
- *                    codes 0x7f and 0xff stand for no value and are not stored.
+ *                    codes 0x7f and 0xff stand for no value and are not
+ *                    stored; a row that is not finite has a NaN for its scale.
  * D is 64 or 128, page_size 16, 32, 64 or 128, HKV at most 4096; caches and scales are aligned to 16 B.
  *   page_table  [B, max_pages] int32: the page that holds request b's positions
  *               i * page_size .. (i + 1) * page_size - 1.  Entries that no
@@ -380,8 +381,8 @@ kda_status kda_cache_read(kda_bf16* k_rows, kda_bf16* v_rows, const void* k_cach
  *   out = sum_j e^(x_j - m) v_j / sum_j e^(x_j - m),  m = max_j x_j
  *   lse = ln sum_j e^(x_j)
  * A token that sees nothing gets out = 0, lse = -inf.  Scores, sums and outputs
- * are accumulated in fp32; the weights e^(x_j - m) are rounded to bf16 for the
- * product with V.  What a position beyond seq_lens[b] or outside every token's
+ * are accumulated in fp32; the weights are rounded for the product with V: to bf16,
+ * or, by requests with few rows over an e4m3 cache, times v's scale to f16.  What a position beyond seq_lens[b] or outside every token's
  * window holds (not a number, an infinity) has no influence.
  *
  *   out          [T, H, D] bf16, written.  Alignment 16 B.

@@ -173,8 +173,10 @@ __global__ void __launch_bounds__(kThreads, 4) cache_append_kernel(const CacheRo
           s = !finite ? __uint_as_float(0x7fffffffu) : top == 0 ? 1.0f : __fdiv_rn(__uint_as_float(top << 16), kE4m3Max);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            y[2 * i] = __fdiv_rn(bf16_lo(w[i]), s);
-            y[2 * i + 1] = __fdiv_rn(bf16_hi(w[i]), s);
+            // (zeros where the scale says it all: a code that is no number would reach tokens
+            // that do not see the row, 0 x NaN)
+            y[2 * i] = finite ? __fdiv_rn(bf16_lo(w[i]), s) : 0.f;
+            y[2 * i + 1] = finite ? __fdiv_rn(bf16_hi(w[i]), s) : 0.f;
           }
         }
         uint32_t code[2] = {0, 0};

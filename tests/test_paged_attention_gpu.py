@@ -286,3 +286,34 @@ def test_many_requests():
     lens = torch.randint(0, 60, (700,), generator=g).tolist()
     case, q = make(dict(n=[min(1, x) for x in lens], lens=lens, H=2, HKV=1, D=64, page=16), seed=24)
     check(case, q)
+
+
+# n, lens and query heads of single tokens, windows and chunks (of one and two row tiles)
+KERNELS = [(1, 300, 4), (5, 200, 4), (60, 300, 4), (150, 150, 2), (300, 300, 1)]
+
+
+@pytest.mark.parametrize("n,lens,G", KERNELS[1:])
+def test_a_row_that_is_not_finite_reaches_only_the_tokens_that_see_it(n, lens, G):
+    """A later token's V row with a NaN, appended to an e4m3 cache: earlier tokens are as
+    before, and the ones that see it are not numbers."""
+    case, q = make(dict(n=[n], lens=[lens], H=2 * G, HKV=2, D=128, page=16), cache="e4m3", seed=32)
+    i = (2 * n) // 3
+    k, v = (torch.randn(n, 2, 128, device="cuda", generator=torch.Generator("cuda").manual_seed(s)).to(torch.bfloat16)
+            for s in (1, 2))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    (kc, vc), scales = case.args()
+
+    def append():
+        kda.kda_cache_append(kc, vc, k, v, case.cu, case.seq_lens, case.table, dev_status=status, **scales)
+
+    append()
+    want, wlse, _ = attend(case, q)
+    v[i, 1, 7] = float("nan")
+    append()
+    out, lse, bits = attend(case, q)
+    assert bits == 0 and int(status) == 0
+    pos = lens - n + i
+    assert not bool(vc[int(case.table[0, pos // 16]), 1, pos % 16].view(torch.uint8).any())  # codes of 0
+    assert torch.equal(out[:i], want[:i]) and torch.equal(lse[:i], wlse[:i])
+    assert torch.equal(out[:, :G], want[:, :G])
+    assert bool(torch.isnan(out[i:, G:]).all())
