@@ -19,7 +19,7 @@
 // the pipe that is busiest), so Q and P are f16 there too, each scaled so that it
 // loses nothing: Q by a power of two per item (its largest entry becomes 2^8 .. 2^9),
 // P by the row's largest product of a weight and a value's scale:
-//   r = max_j (x_j + log2 vs_j),  w_j = 2^(x_j - r),  P_j = 2^15 w_j vs_j <= 2^15
+//   r = max_j (x_j + log2 vs_j) - 15,  w_j = 2^(x_j - r),  P_j = w_j vs_j <= 2^15
 // (11 bits down to 2^-29 of the largest contribution, where bf16 would keep 8), the
 // sum being that of w_j.
 // mma.sync (m16n8k16) is the instruction for it: 16 rows are its native
@@ -117,6 +117,14 @@ __device__ __forceinline__ float log2_approx(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// What a value's scale s adds to its score in the reference r of a row's weights
+// w_j = 2^(x_j - r): P_j = w_j s_j, in f16, is at most 2^15.  A scale of 0 makes the value 0,
+// and r takes the score itself; below 2^-90 the sum of w could pass fp32's range (and P has
+// bits left).
+__device__ __forceinline__ float log2_of_scale(float s) {
+  const float a = fabsf(s);
+  return (a > 0.f ? fmaxf(log2_approx(a), -90.f) : 0.f) - 15.f;
 }
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -418,7 +426,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
     constexpr int kN = D / kComputeWarps / 8;  // blocks of 8 columns of O per warp
     const int quad = lane >> 2, j2 = (lane & 3) * 2;
     float xscale = p.scale * kLog2E;
-    constexpr float kPScale = kE4m3 ? 32768.f : 1.f;  // of P, and so of O
     float o[kR][kN][4], m[kR][2], l[kR][2];
     long long left = u1 - u0;
     int item = -1;
@@ -510,11 +517,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
           const float2 v = *reinterpret_cast<const float2*>(&sm.scales[s][1][my_pos + 8 * n + j2]);
           k_scale[n][0] *= f.x;
           k_scale[n][1] *= f.y;
-          v_scale[n][0] = v.x * kPScale;
-          v_scale[n][1] = v.y * kPScale;
-          // (a scale of 0: the value is 0, and r takes the score itself)
-          v_log[n][0] = v.x > 0.f ? log2_approx(v.x) : 0.f;
-          v_log[n][1] = v.y > 0.f ? log2_approx(v.y) : 0.f;
+          v_scale[n][0] = v.x;
+          v_scale[n][1] = v.y;
+          v_log[n][0] = log2_of_scale(v.x);
+          v_log[n][1] = log2_of_scale(v.y);
         }
       }
 #pragma unroll
@@ -720,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
           if (row >= rows) continue;
           const int tok = row / p.G;
           const size_t out_row = (size_t)(note.t0 + tok) * p.H + note.h * p.G + (row - tok * p.G);
-          const float inv = (sum == 0.f ? 0.f : 1.f / sum) * (1.f / kPScale);
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
           const size_t piece = ((size_t)cta * 2 + place) * kRows + row;
           if (warp == 0 && (lane & 3) == 0) {
             if (!done) pieces.ml[piece] = make_float2(m[r][half], sum);
@@ -745,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
                     make_uint2(pack_bf16(y0 * inv, y1 * inv), pack_bf16(y2 * inv, y3 * inv));
               else
                 *reinterpret_cast<float4*>(pieces.o + piece * D + col) =
-                    make_float4(y0 / kPScale, y1 / kPScale, y2 / kPScale, y3 / kPScale);
+                    make_float4(y0, y1, y2, y3);
             }
           }
         }

@@ -292,6 +292,23 @@ def test_many_requests():
 KERNELS = [(1, 300, 4), (5, 200, 4), (60, 300, 4), (150, 150, 2), (300, 300, 1)]
 
 
+@pytest.mark.parametrize("n,lens,G", KERNELS)
+@pytest.mark.parametrize("amplitude", [2.0 ** -115, 2.0 ** -90, 2.0 ** 120])
+def test_value_scales_at_both_ends(n, lens, G, amplitude):
+    """Value scales near the ends of fp32's range (here 2^-10 .. 2^-5 times the amplitude): the
+    sum of the weights keeps within it.  At 2^-115 the weights' product with a scale has few
+    bits left, and only the log-sum is compared."""
+    case, q = make(dict(n=[n], lens=[lens], H=2 * G, HKV=2, D=128, page=16), cache="e4m3", seed=31)
+    case.tensors["v"][1].mul_(amplitude)
+    if amplitude >= 2.0 ** -90:
+        check(case, q)
+        return
+    out, lse, status = attend(case, q)
+    _, want, _, tol = attention(case, q, case.D ** -0.5)
+    assert status == 0 and bool(((lse.double() - want).abs() <= tol).all())
+    assert bool((out.double().abs() <= case.dense("v", 0).abs().max()).all())
+
+
 @pytest.mark.parametrize("n,lens,G", KERNELS[1:])
 def test_a_row_that_is_not_finite_reaches_only_the_tokens_that_see_it(n, lens, G):
     """A later token's V row with a NaN, appended to an e4m3 cache: earlier tokens are as
