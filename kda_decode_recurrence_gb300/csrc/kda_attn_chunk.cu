@@ -310,6 +310,27 @@ __device__ __forceinline__ bool wait_together(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_try(bar, parity)) || wait_on(bar, parity);
 }
 
+// Lanes 4 i .. 4 i + 3: x[e] of lane j becomes x[j] of lane e.
+__device__ __forceinline__ void transpose4(uint4 (&x)[4], int lane) {
+#pragma unroll
+  for (int bit = 1; bit < 4; bit *= 2) {
+    const bool up = (lane & bit) != 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & bit) continue;
+      uint4& lo = x[i];
+      uint4& hi = x[i + bit];
+      uint4 y = up ? lo : hi;
+      y.x = __shfl_xor_sync(0xffffffffu, y.x, bit);
+      y.y = __shfl_xor_sync(0xffffffffu, y.y, bit);
+      y.z = __shfl_xor_sync(0xffffffffu, y.z, bit);
+      y.w = __shfl_xor_sync(0xffffffffu, y.w, bit);
+      if (up) lo = y;
+      else hi = y;
+    }
+  }
+}
+
 // kPair: items may have two row tiles (else no request of the call has more than one).
 template <int D, bool kE4m3, bool kPair>
 __global__ void __launch_bounds__(Shape<D, kE4m3, kPair>::kThreads, 1)
@@ -566,6 +587,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, kPair>::kThreads, 1)
       int f_unit = 0, f_flags = 0;
       uint32_t f_q = 0, f_k = 0;
       auto there = [&](uint64_t* bar, int parity, bool stay) {
+        // (a try_wait may put the warp to sleep, and PV would wait)
         if (__all_sync(0xffffffffu, mbar_try(smem_u32(bar), parity))) return true;
         if (stay) ok = wait_on(smem_u32(bar), parity);
         return stay && ok;
@@ -1028,6 +1050,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, kPair>::kThreads, 1)
       const bool begins = w.tile == 0, ends = w.tile + count == w.span.tiles;
       const bool done = begins && ends;
       const bool live = tok_in < per_tile && token < n;
+      const unsigned live_rows = __ballot_sync(0xffffffffu, live);
       const size_t out_row = (size_t)(w.r.t0 + token) * p.H + w.h * p.G + g_in;
       const size_t piece = ((size_t)cta * 2 + (begins ? 1 : 0)) * kChunkRows + tile * per_tile * p.G + r;
       const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -1061,12 +1084,21 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, kPair>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = y[e];
         }
-        if (live && done) {
-          uint4* to = reinterpret_cast<uint4*>(p.out + out_row * D + cc);
+        if (done) {
+          uint4 y[4];
 #pragma unroll
           for (int e = 0; e < 32; e += 8)
-            to[e / 8] = make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
-                                   pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+            y[e / 8] = make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                                  pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+          // four lanes write 64 bytes of one row together
+          transpose4(y, lane);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int from = (lane & ~3) + e;
+            const int to_row = __shfl_sync(0xffffffffu, (int)out_row, from);
+            if ((live_rows >> from) & 1)
+              *reinterpret_cast<uint4*>(p.out + (size_t)to_row * D + cc + 8 * (lane & 3)) = y[e];
+          }
         } else if (live) {
           float4* to = reinterpret_cast<float4*>(pieces.o + piece * D + cc);
 #pragma unroll
