@@ -64,6 +64,13 @@ constexpr int kFirst = 1, kLast = 2;  // of this CTA's part of the item
 constexpr int kSecond = 8;            // the item has a second row tile
 constexpr int kWhole = 16;            // every row sees every position
 
+// Where a unit of work is: its item, the key tile (0 where the unit stands for none), the item's
+// first unit, and how many units before it stand for no key tile.
+struct Place {
+  int b, h, token0, tile;
+  long long item_unit, idle;
+};
+
 template <int D, bool kE4m3, bool kPair>
 struct Shape {
   static constexpr int kPanels = D / 64;
@@ -76,6 +83,11 @@ struct Shape {
   static constexpr int kRawUnits = kE4m3 ? (D == 128 ? 3 : 6) : 1;  // parts of codes
   static constexpr int kRawBytes = kPart * D;
   static constexpr int kScaleSteps = D == 128 ? 4 : 8;   // steps whose scales are kept
+  // What an item's beginning and end take, in key tiles, for an even division (an item costs
+  // some 9000 cycles beside its steps of 2300, e4m3 4500).  0, 2, 4, 5 tiles: six prompts of
+  // 300 .. 4000 bf16 356, 318, 294, 292 us; 0, 1, 2, 3: four of 1500 .. 6001 e4m3 820, 762,
+  // 732, 742 us.
+  static constexpr int kItemCost = kE4m3 ? 2 : 4;
   static constexpr int kWarps = kE4m3 ? 16 : 12;
   static constexpr int kThreads = 32 * kWarps;
   // Registers per thread: 65536 (e4m3) or 64512 at launch, then dealt by role to no more
@@ -117,9 +129,8 @@ struct Smem {
   uint64_t full[S::kUnits], empty[S::kUnits], fixed[kSteps];
   uint64_t raw_full[S::kRawUnits], raw_empty[S::kRawUnits];
   uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_done[2], turn[2], done, join_ready, join_done;
-  long long part[S::kWarps];
-  long long start_unit;
-  int start_b;
+  long long part[2][S::kWarps];
+  Place edge[2];          // of the first unit of this CTA, of the first one past it
   uint32_t tmem;
 };
 
@@ -135,12 +146,53 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& p, const Request& r
   const int first = lo / kTile;
   return Span{first, max(1, (hi + kTile - 1) / kTile - first)};
 }
-// Units of one key head of a request (0: not this kernel's), `pair` tokens to an item.
-__device__ __forceinline__ long long head_units(const AttentionArgs& p, const Request& r, int pair) {
+// Units of one key head of a request (0: not this kernel's), `pair` tokens to an item: an
+// item's are `cost` for its beginning and end, then one per key tile.
+__device__ __forceinline__ int head_items(const AttentionArgs& p, const Request& r, int pair) {
+  return r.n * p.G <= p.window_rows ? 0 : (r.n + pair - 1) / pair;
+}
+__device__ __forceinline__ long long head_units(const AttentionArgs& p, const Request& r, int pair, int cost) {
   if (r.n * p.G <= p.window_rows) return 0;
   long long sum = 0;
-  for (int t = 0; t < r.n; t += pair) sum += span_of(p, r, t, pair).tiles;
+  for (int t = 0; t < r.n; t += pair) sum += span_of(p, r, t, pair).tiles + cost;
   return sum;
+}
+// The place of unit u in request at.b, whose first unit is at.item_unit, with at.idle items
+// before it; by a whole warp.
+__device__ __forceinline__ Place place_of(const AttentionArgs& p, Place at, long long u, int pair, int cost, int lane) {
+  const Request r = load_request(p, at.b, false);
+  const int items = head_items(p, r, pair);
+  auto units_of = [&](int i) { return i < items ? span_of(p, r, i * pair, pair).tiles + cost : 0; };
+  long long head = 0;
+  for (int i = lane; i < items; i += 32) head += units_of(i);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) head += __shfl_xor_sync(0xffffffffu, head, o);
+  at.h = (int)((u - at.item_unit) / head);
+  long long left = u - at.item_unit - at.h * head;  // less than the head's units
+  int first = 0;
+  while (true) {
+    const int mine = units_of(first + lane);
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, left < upto);
+    if (past || first + 32 >= items) {
+      const int in = past ? __ffs(past) - 1 : 0;
+      left -= __shfl_sync(0xffffffffu, upto - mine, in);
+      first += in;
+      break;
+    }
+    left -= __shfl_sync(0xffffffffu, upto, 31);
+    first += 32;
+  }
+  at.token0 = first * pair;
+  at.tile = max(0, (int)left - cost);
+  at.item_unit = u - left;
+  at.idle = (at.idle + (long long)at.h * items + first) * cost + min(left, (long long)cost);
+  return at;
 }
 
 // The items of one CTA's share in order (request, key head, row tiles), walked by a
@@ -178,22 +230,15 @@ struct Walk {
     }
     left = 0;  // cannot happen while units are left
   }
-  __device__ __forceinline__ void start(const AttentionArgs& p, int pair, int b0, long long skip,
-                                        long long units, int lane) {
-    b = b0;
-    left = units;
-    h = 0;
+  __device__ __forceinline__ void start(const AttentionArgs& p, int pair, const Place& at, long long tiles, int lane) {
+    b = at.b;
+    left = tiles;
     fetch(p, lane);
     take(p, pair, lane);
-    const long long head = head_units(p, r, pair);
-    h = (int)(skip / head);
-    skip -= h * head;
-    while (skip >= span.tiles) {
-      skip -= span.tiles;
-      token0 += pair;
-      span = span_of(p, r, token0, pair);
-    }
-    tile = (int)skip;
+    h = at.h;
+    token0 = at.token0;
+    span = span_of(p, r, token0, pair);
+    tile = at.tile;
   }
   __device__ __forceinline__ int count() const { return (int)min((long long)(span.tiles - tile), left); }
   __device__ __forceinline__ void next(const AttentionArgs& p, int pair, int lane) {
@@ -376,32 +421,46 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, kPair>::kThreads, 1)
   // ---- this CTA's share: each thread counts a run of requests
   const int run = (p.B + S::kThreads - 1) / S::kThreads;
   const int b_lo = min(p.B, tid * run), b_hi = min(p.B, b_lo + run);
-  long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b)
-    mine += p.c.HKV * head_units(p, load_request(p, b, cta == 0), pair);
-  long long units;
-  const long long from = scan_before<S::kWarps>(mine, sm.part, units);
+  long long mine = 0, my_items = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const Request r = load_request(p, b, cta == 0);
+    mine += p.c.HKV * head_units(p, r, pair, S::kItemCost);
+    my_items += p.c.HKV * head_items(p, r, pair);
+  }
+  long long units, items;
+  const long long from = scan_before<S::kWarps>(mine, sm.part[0], units);
+  const long long items_from = scan_before<S::kWarps>(my_items, sm.part[1], items);
   const int used = (int)min((long long)ctas, units);
   if (tid == 0) pieces.notes[cta].tokens = 0;
   const long long u0 = cta < used ? share_begin(units, used, cta) : 0;
   const long long u1 = cta < used ? share_begin(units, used, cta + 1) : 0;
-  if (u1 > u0 && u0 >= from && u0 < from + mine) {
-    long long at = from;
-    for (int b = b_lo; b < b_hi; ++b) {
-      const long long u = p.c.HKV * head_units(p, load_request(p, b, false), pair);
-      if (u0 < at + u) {
-        sm.start_b = b;
-        sm.start_unit = u0 - at;
-        break;
-      }
-      at += u;
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    const long long u = i ? u1 : u0;
+    if (u1 <= u0 || u < from || u >= from + mine) continue;
+    Place at{b_lo, 0, 0, 0, from, items_from};
+    for (; at.b + 1 < b_hi; ++at.b) {
+      const Request r = load_request(p, at.b, false);
+      const long long n = p.c.HKV * head_units(p, r, pair, S::kItemCost);
+      if (u < at.item_unit + n) break;
+      at.item_unit += n;
+      at.idle += p.c.HKV * head_items(p, r, pair);
     }
+    sm.edge[i] = at;
+  }
+  __syncthreads();
+  if (warp < 2) {
+    const long long u = warp ? u1 : u0;
+    Place at{0, 0, 0, 0, 0, items * S::kItemCost};  // past the last unit
+    if (u1 > u0 && u < units) at = place_of(p, sm.edge[warp], u, pair, S::kItemCost, lane);
+    __syncwarp();
+    if (lane == 0) sm.edge[warp] = at;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  const int steps = (int)(u1 - u0);
+  const int steps = u1 > u0 ? (int)((u1 - sm.edge[1].idle) - (u0 - sm.edge[0].idle)) : 0;  // key tiles
   bool ok = true;
 
   if (warp >= kWidenWarp) {
@@ -461,7 +520,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, kPair>::kThreads, 1)
     } else if (warp == kCopyWarp) {
       // ---- notes, the items' queries, and K and V of every step into the ring
       Walk w;
-      w.start(p, pair, sm.start_b, sm.start_unit, u1 - u0, lane);
+      w.start(p, pair, sm.edge[0], steps, lane);
       const int rows_per_box = min(p.c.page_size, S::kPart);
       const int boxes = kTile / rows_per_box;        // of a key tile, and of a part of it:
       const int part_boxes = S::kPart / rows_per_box;
@@ -743,12 +802,12 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, kPair>::kThreads, 1)
     const int tok_in = r / p.G, g_in = r - tok_in * p.G;
     const float2 c2 = make_float2(c, c);
     Walk w;
-    if (steps > 0) w.start(p, pair, sm.start_b, sm.start_unit, u1 - u0, lane);
+    if (steps > 0) w.start(p, pair, sm.edge[0], steps, lane);
     else w.left = 0;
     int g0 = 0, task0 = 0;   // steps and tasks of the CTA before the item
     int mine = 0, joins = 0; // tasks of this slot so far, items joined so far
-    long long unit = u0;
-    for (int item = 0; w.left > 0 && ok; ++item, unit += w.count(), w.next(p, pair, lane)) {
+    long long item_unit = sm.edge[0].item_unit;
+    for (int item = 0; w.left > 0 && ok; ++item, item_unit += S::kItemCost + w.span.tiles, w.next(p, pair, lane)) {
       const int count = w.count(), L = w.r.L, n = w.r.n;
       const bool two = kPair && w.token0 + per_tile < n;
       const int slot0 = task0 & 1;              // the slot of the item's first task
@@ -1061,7 +1120,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, kPair>::kThreads, 1)
       }
       if (r == 0 && t == slot0 && begins && !ends)
         pieces.notes[cta] = PieceNote{(w.r.t0 + w.token0) * p.H + w.h * p.G, min(pair, n - w.token0),
-                                      share_of(units, used, unit + w.span.tiles - 1) - cta + 1, 0};
+                                      share_of(units, used, item_unit + S::kItemCost + w.span.tiles - 1) - cta + 1, 0};
 #pragma unroll 1
       for (int cc = 0; cc < D; cc += 32) {
         float o[32];
