@@ -770,19 +770,47 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, kPair>::kThreads, 1)
         if ((n.flags & kFirst) && lane == 0) sm.bad[n.item % kSteps] = 0;
         __syncwarp();
         if (!(n.flags & kWhole)) {
-          bool any = false;
-#pragma unroll 4
-          for (int i = lane; i < S::kPanels * kTile * 8; i += 32) {  // 16-byte chunks, eight to a panel's row
-            const int row = (i >> 3) & (kTile - 1);
-            const bool in = n.start + row >= n.begin && n.start + row < n.end;
-            uint4* at = reinterpret_cast<uint4*>(sm.unit[s] + (i / (8 * kTile)) * kTile * 128 +
-                                                 swizzled<128>(row, i & 7));
-            uint4 x = *at;
-            const uint4 out = make_uint4(not_finite(x.x), not_finite(x.y), not_finite(x.z), not_finite(x.w));
-            const bool bad = (out.x | out.y | out.z | out.w) != 0;
-            any |= bad && in;
-            if (bad || !in)
-              *at = in ? make_uint4(x.x & ~out.x, x.y & ~out.y, x.z & ~out.z, x.w & ~out.w) : make_uint4(0, 0, 0, 0);
+          constexpr int kChunks = S::kPanels * kTile * 8;  // of 16 bytes, eight to a panel's row
+          const int from = n.begin - n.start, to = n.end - n.start;  // the request's rows
+          auto chunk = [&](int i) {
+            return reinterpret_cast<uint4*>(sm.unit[s] + (i / (8 * kTile)) * kTile * 128 +
+                                            swizzled<128>((i >> 3) & (kTile - 1), i & 7));
+          };
+          if (from > 0 || to < kTile) {
+#pragma unroll 1
+            for (int i = lane; i < kChunks; i += 32) {
+              const int row = (i >> 3) & (kTile - 1);
+              if (row < from || row >= to) *chunk(i) = make_uint4(0, 0, 0, 0);
+            }
+            __syncwarp();
+          }
+          // 0 x is 0 for all that is finite, so that a sum tells: loads and little else (with a
+          // look at every entry's exponent the item's last step waited 9000 cycles for this)
+          const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+          __nv_bfloat162 sum[4] = {zero, zero, zero, zero};
+#pragma unroll 1
+          for (int first = lane; first < kChunks; first += 8 * 32) {
+            uint4 x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = *chunk(first + 32 * i);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              sum[0] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x[i].x), zero, sum[0]);
+              sum[1] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x[i].y), zero, sum[1]);
+              sum[2] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x[i].z), zero, sum[2]);
+              sum[3] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x[i].w), zero, sum[3]);
+            }
+          }
+          const __nv_bfloat162 all = __hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3]));
+          const bool any = __any_sync(0xffffffffu, __hisnan(all.x) || __hisnan(all.y));
+          if (any) {
+#pragma unroll 1
+            for (int i = lane; i < kChunks; i += 32) {
+              uint4 x = *chunk(i);
+              const uint4 out = make_uint4(not_finite(x.x), not_finite(x.y), not_finite(x.z), not_finite(x.w));
+              if (out.x | out.y | out.z | out.w)
+                *chunk(i) = make_uint4(x.x & ~out.x, x.y & ~out.y, x.z & ~out.z, x.w & ~out.w);
+            }
           }
           if (any) sm.bad[n.item % kSteps] = 1;
           fence_proxy_async_smem();
