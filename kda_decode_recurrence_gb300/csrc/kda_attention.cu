@@ -20,7 +20,8 @@ namespace {
 //   o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i,   lse = (m + log2 l) ln 2.
 // CTA (c, y) takes rows of the item that CTA c of the main kernel began: a warp to a
 // row, or all four to a row (each every fourth piece, in order) where an item is in
-// many pieces.
+// many pieces.  Latency bounds it: dependent reads of what the main kernel has just
+// written.
 constexpr int kJoinWarps = 4;
 constexpr int kManyPieces = 8;
 

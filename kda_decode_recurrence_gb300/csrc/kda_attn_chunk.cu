@@ -25,6 +25,17 @@
 // codes are widened to bf16 by four more warps on the way; a key's scale
 // multiplies its column of S, a value's scale its column of P.
 //
+// Items' key tiles are divided evenly over the CTAs, an item's ends counted as some.
+//
+// 2048 new tokens over 28001 cached, 32 / 8 heads, D = 128, bf16: 643 us, 1.51 PFLOP/s
+// (a cuBLAS product: 1.89), the tensor cores busy for two thirds; a softmax task is a
+// chain of some 3000 cycles beside the 1280 of its products, and two of them overlap.  Four
+// prompts of 1500 .. 6001 from an e4m3 cache: 731 us, 0.68 PFLOP/s: the scales are a
+// product and the widening five operations per pair, and the schedulers issue in 54% of their cycles.
+// (e4m3 operands widened to f16 as in the window kernel: 1149 us against 818 then, the
+// conversions run where the exponentials do.  Codes taken to registers one part ahead:
+// 882 against 847.)
+//
 // A key tile that some row sees in part (the diagonal, the window's edge, the
 // sequence's end) is masked in the softmax, and entries of V that are outside the
 // request's range, or not finite, are taken out of shared memory first (0 x NaN
@@ -83,10 +94,9 @@ struct Shape {
   static constexpr int kRawUnits = kE4m3 ? (D == 128 ? 3 : 6) : 1;  // parts of codes
   static constexpr int kRawBytes = kPart * D;
   static constexpr int kScaleSteps = D == 128 ? 4 : 8;   // steps whose scales are kept
-  // What an item's beginning and end take, in key tiles, for an even division (an item costs
-  // some 9000 cycles beside its steps of 2300, e4m3 4500).  0, 2, 4, 5 tiles: six prompts of
-  // 300 .. 4000 bf16 356, 318, 294, 292 us; 0, 1, 2, 3: four of 1500 .. 6001 e4m3 820, 762,
-  // 732, 742 us.
+  // What an item's beginning and end take, in key tiles, so that shares with many short items
+  // end with the others.  1, 2, 3, 4 tiles: six prompts of 300 .. 4000 in bf16 272, 255, 249,
+  // 245 us; 0, 1, 2, 3: four of 1500 .. 6001 in e4m3 820, 762, 732, 742 us.
   static constexpr int kItemCost = kE4m3 ? 2 : 4;
   static constexpr int kWarps = kE4m3 ? 16 : 12;
   static constexpr int kThreads = 32 * kWarps;
@@ -1137,8 +1147,10 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, kPair>::kThreads, 1)
       const bool begins = w.tile == 0, ends = w.tile + count == w.span.tiles;
       const bool done = begins && ends;
       const bool live = tok_in < per_tile && token < n;
-      const unsigned live_rows = __ballot_sync(0xffffffffu, live);
       const size_t out_row = (size_t)(w.r.t0 + token) * p.H + w.h * p.G + g_in;
+      int to_rows[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) to_rows[e] = __shfl_sync(0xffffffffu, live ? (int)out_row : -1, (lane & ~3) + e);
       const size_t piece = ((size_t)cta * 2 + (begins ? 1 : 0)) * kChunkRows + tile * per_tile * p.G + r;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const bool bad = !kE4m3 && sm.bad[item % kSteps] != 0;
@@ -1181,10 +1193,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, kPair>::kThreads, 1)
           transpose4(y, lane);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int from = (lane & ~3) + e;
-            const int to_row = __shfl_sync(0xffffffffu, (int)out_row, from);
-            if ((live_rows >> from) & 1)
-              *reinterpret_cast<uint4*>(p.out + (size_t)to_row * D + cc + 8 * (lane & 3)) = y[e];
+            if (to_rows[e] >= 0) *reinterpret_cast<uint4*>(p.out + (size_t)to_rows[e] * D + cc + 8 * (lane & 3)) = y[e];
           }
         } else if (live) {
           float4* to = reinterpret_cast<float4*>(pieces.o + piece * D + cc);

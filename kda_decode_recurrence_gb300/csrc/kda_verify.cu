@@ -17,6 +17,10 @@
 // segments' sums meet through distributed shared memory, so that one launch does
 // it all.  The cluster has as many CTAs (8, 4, 2 or 1) as let all requests run at
 // once: a second wave would find few CTAs left to keep HBM busy.
+//
+// 256 requests of 1 .. 7 drafts over 131072 tokens: 268 MB in 56 us, 4.8 TB/s (a copy:
+// 6.7): the pair sums take 13 operations an entry, and a cluster's last warp is waited
+// for twice.  Four over 32001: 12.5 us with the host's call.
 #include <cooperative_groups.h>
 
 #include "kda_common.cuh"
