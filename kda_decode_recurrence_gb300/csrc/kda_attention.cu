@@ -108,15 +108,21 @@ size_t attention_workspace_bytes(int B, int T, int max_tokens, int H, int HKV, i
   return (need + 255) & ~(size_t)255;
 }
 
-// Measured with 32 requests over 200 .. 6000 positions, 8 key heads, window kernel
-// against chunk kernel: 32 rows bf16 D = 128 114 us against 131, D = 64 85 against 78,
-// e4m3 101 against 151 and 83 against 128; 64 rows 199 against 136, 141 against 82,
-// 206 against 158, 142 against 131.
-int window_limit(int D, bool e4m3) { return D == 64 && !e4m3 ? 16 : 32; }
+// Rows up to which a request is the window kernel's.  Measured with 32 requests over 200 ..
+// 6000 positions, 8 key heads, window kernel against chunk kernel: 32 rows e4m3 89 us
+// against 116; bf16 118 against 87, 20 rows 99 against 85 (200 requests 722 against 599);
+// 64 rows e4m3 D = 128 206 against 158, D = 64 142 against 131.  Where requests of up to 32
+// rows differ, the two kernels would take turns: 1 to 8 tokens of 4 heads in the window
+// kernel alone 95 us, in both 112 (D = 128; for D = 64 the chunk kernel is faster still).
+int window_limit(const AttentionArgs& a) {
+  if (a.c.e4m3) return 32;
+  const bool alike = (long long)a.T == (long long)a.B * a.max_tokens;
+  return a.c.D == 128 && !alike && (long long)a.max_tokens * a.G <= 32 ? 32 : 16;
+}
 
 cudaError_t launch_paged_attention(const AttentionArgs& in, cudaStream_t stream) {
   AttentionArgs a = in;
-  a.window_rows = window_limit(a.c.D, a.c.e4m3);
+  a.window_rows = window_limit(a);
   const bool chunks = (long long)a.max_tokens * a.G > a.window_rows;
   // No request is a window's where all have max_tokens tokens (T = B max_tokens and
   // none has more).

@@ -136,8 +136,8 @@ __device__ __forceinline__ long long scan_before(long long x, long long* part, l
   return before;
 }
 
-// Rows (tokens x G) up to which a request is the window kernel's.
-int window_limit(int D, bool e4m3);
+// Rows (tokens x G) up to which a request of the call is the window kernel's.
+int window_limit(const AttentionArgs& a);
 // Rows of its variant that holds every such request of at most max_tokens tokens.
 int window_rows(int max_tokens, int G);
 cudaError_t launch_window_attention(const AttentionArgs& a, cudaStream_t stream);

@@ -1,5 +1,5 @@
 // kda_attn_window.cu -- attention of single tokens and drafted windows: the requests
-// with few rows (new tokens x query heads per key head; window_limit: 32, or 16).
+// with few rows (new tokens x query heads per key head: window_limit).
 //
 // Such a request reads every cached row for 4 G n_b operations a byte at most, so HBM
 // bounds it and the kernel is built to keep copies in flight: two or three CTAs per
