@@ -96,37 +96,42 @@ cudaError_t launch_join_pieces(const AttentionArgs& a, const Pieces& pieces, int
   return launch(join_kernel<64>, grid, dim3(kJoinWarps * 32), 0, stream, true, a, pieces, rows);
 }
 
+// Whether a call may launch the chunk kernel; others need no room for its pieces.
+static bool may_chunk(int max_tokens, int G) { return (long long)max_tokens * G > 16; }
+
 size_t attention_workspace_bytes(int B, int T, int max_tokens, int H, int HKV, int D) {
   if (B < 0 || T < 0 || max_tokens < 0 || H < 1 || HKV < 1 || H % HKV != 0 || (D != 64 && D != 128))
     return 0;
   const int G = H / HKV;
   size_t need = pieces_bytes(kWindowCtas, window_rows(max_tokens, G), D);
-  if ((long long)max_tokens * G > 16) {
+  if (may_chunk(max_tokens, G)) {
     const size_t chunk = pieces_bytes(kChunkCtas, kChunkRows, D);
     if (chunk > need) need = chunk;  // the kernels take their turns
   }
   return (need + 255) & ~(size_t)255;
 }
 
-// Rows up to which a request is the window kernel's.  Measured with 32 requests over 200 ..
-// 6000 positions, 8 key heads, window kernel against chunk kernel: 32 rows e4m3 89 us
-// against 116; bf16 118 against 87, 20 rows 99 against 85 (200 requests 722 against 599);
-// 64 rows e4m3 D = 128 206 against 158, D = 64 142 against 131.  Where requests of up to 32
-// rows differ, the two kernels would take turns: 1 to 8 tokens of 4 heads in the window
-// kernel alone 95 us, in both 112 (D = 128; for D = 64 the chunk kernel is faster still).
+// Rows up to which a request is the window kernel's (none: 0).  Measured with 32 requests
+// over 200 .. 6000 positions, 8 key heads of 128, window kernel against chunk kernel: e4m3 32
+// rows 89 us against 116, 64 rows 206 against 158; bf16 20 rows 99 against 85, 32 rows 118
+// against 87.  bf16 windows that differ, the chunk kernel for all against the window kernel
+// for the short ones: 1 to 8 tokens of 4 heads 86 us against 95, 1 to 16 85 against 112 (128
+// requests of up to 16000 positions 664 against 689), 1 to 8 of 8 heads of 64 55 against 73.
+// Longer chunks may come with many single tokens, which are HBM's.
 int window_limit(const AttentionArgs& a) {
   if (a.c.e4m3) return 32;
-  const bool alike = (long long)a.T == (long long)a.B * a.max_tokens;
-  return a.c.D == 128 && !alike && (long long)a.max_tokens * a.G <= 32 ? 32 : 16;
+  const long long most = (long long)a.max_tokens * a.G;
+  return may_chunk(a.max_tokens, a.G) && most <= 128 ? 0 : 16;
 }
 
 cudaError_t launch_paged_attention(const AttentionArgs& in, cudaStream_t stream) {
   AttentionArgs a = in;
   a.window_rows = window_limit(a);
-  const bool chunks = (long long)a.max_tokens * a.G > a.window_rows;
+  // (the workspace holds the chunk kernel's pieces where may_chunk says so)
+  const bool chunks = may_chunk(a.max_tokens, a.G) && (long long)a.max_tokens * a.G > a.window_rows;
   // No request is a window's where all have max_tokens tokens (T = B max_tokens and
   // none has more).
-  if (!chunks || (long long)a.T != (long long)a.B * a.max_tokens) {
+  if (!chunks || (a.window_rows > 0 && (long long)a.T != (long long)a.B * a.max_tokens)) {
     const cudaError_t e = launch_window_attention(a, stream);
     if (e != cudaSuccess || !chunks) return e;
   }

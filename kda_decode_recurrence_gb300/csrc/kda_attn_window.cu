@@ -28,7 +28,8 @@
 // 128 single tokens over 5.05 GB of bf16 cache: 713 us, 7.07 TB/s (a copy: 6.70).
 // 64 over 628 MB of e4m3: 141 us, 4.47 TB/s, bound by the issue of its instructions
 // (two CTAs an SM and bf16 operands: 178 us).  With more rows a warp reads as many
-// operands of Q and P as of K and V: 3.9 TB/s at 32 rows, 2.3 at 64.  Eight warps that
+// operands of Q and P as of K and V: 32 rows are for e4m3 only, where the chunk kernel
+// widens at the same price.  Eight warps that
 // split D by eight: 165 us and 755 us on these two; streams of 32 positions per warp
 // that exchange nothing until an item's end, one CTA an SM: 265 us and 1320 us.
 #include <cuda.h>
@@ -789,7 +790,7 @@ cudaError_t launch_window(const AttentionArgs& a, cudaStream_t stream) {
 template <int D, bool kE4m3>
 cudaError_t by_rows(const AttentionArgs& a, cudaStream_t stream) {
   if (window_rows(a.max_tokens, a.G) == 16 || a.window_rows == 16) return launch_window<D, 16, kE4m3>(a, stream);
-  if constexpr (D == 128 || kE4m3) return launch_window<D, 32, kE4m3>(a, stream);
+  if constexpr (kE4m3) return launch_window<D, 32, kE4m3>(a, stream);
   return cudaErrorInvalidValue;  // its limit is 16 rows
 }
 
