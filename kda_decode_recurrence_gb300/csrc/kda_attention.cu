@@ -129,9 +129,10 @@ cudaError_t launch_paged_attention(const AttentionArgs& in, cudaStream_t stream)
   a.window_rows = window_limit(a);
   // (the workspace holds the chunk kernel's pieces where may_chunk says so)
   const bool chunks = may_chunk(a.max_tokens, a.G) && (long long)a.max_tokens * a.G > a.window_rows;
-  // No request is a window's where all have max_tokens tokens (T = B max_tokens and
-  // none has more).
-  if (!chunks || (a.window_rows > 0 && (long long)a.T != (long long)a.B * a.max_tokens)) {
+  // Where T = B max_tokens every request has max_tokens tokens, or some request or offset
+  // breaks the contract: the chunk kernel then takes all that are well formed, however short.
+  if (chunks && (long long)a.T == (long long)a.B * a.max_tokens) a.window_rows = 0;
+  if (a.window_rows > 0) {
     const cudaError_t e = launch_window_attention(a, stream);
     if (e != cudaSuccess || !chunks) return e;
   }

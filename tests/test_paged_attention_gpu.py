@@ -6,7 +6,7 @@ import torch
 
 import kda_decode_recurrence_gb300 as kda
 
-from _paged import Case, attention
+from _paged import Case, attention, cumulative
 from _parity import Guarded
 
 pytestmark = pytest.mark.gpu
@@ -334,3 +334,23 @@ def test_a_row_that_is_not_finite_reaches_only_the_tokens_that_see_it(n, lens, G
     assert torch.equal(out[:i], want[:i]) and torch.equal(lse[:i], wlse[:i])
     assert torch.equal(out[:, :G], want[:, :G])
     assert bool(torch.isnan(out[i:, G:]).all())
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,most,G", [([197, 3], 100, 4), ([195, 5], 100, 2), ([1, 199, 8, 32], 60, 1)])
+def test_a_request_that_is_too_long_leaves_the_others_served(n, most, G, cache):
+    """T = B max_tokens, yet not every request has max_tokens tokens: one has more (and is
+    skipped), the short ones are as alone."""
+    assert sum(n) == len(n) * most
+    case, q = make(dict(n=n, lens=[x + 150 for x in n], H=2 * G, HKV=2, D=128, page=16), cache=cache, seed=41)
+    out, lse, status = attend(case, q, max_tokens=most)
+    assert status == kda.DEV_BAD_SEQLEN
+    want, wlse, tol, ltol = attention(case, q, q.shape[2] ** -0.5)
+    at = cumulative(n)
+    for b, x in enumerate(n):
+        rows = slice(at[b], at[b + 1])
+        if x > most:
+            assert bool(torch.isnan(out[rows]).all()) and bool(torch.isnan(lse[rows]).all())
+        else:
+            assert bool(((out[rows].double() - want[rows]).abs() <= tol[rows]).all())
+            assert bool(((lse[rows].double() - wlse[rows]).abs() <= ltol[rows]).all())
