@@ -320,7 +320,8 @@ size_t kda_block_tkg_workspace_size(int B, int n, int Hd, int nh, int K, int V, 
  *               request b is at position seq_lens[b] - n_b + i.  A token at a
  *               negative position is padding: it is not written to the cache and
  *               attends to nothing.  0 <= seq_lens[b] <= max_pages * page_size <= 2^30.
- * A request that breaks one of these sets KDA_DEV_BAD_SEQLEN and is skipped.
+ * A request that breaks one of these sets KDA_DEV_BAD_SEQLEN and is skipped; offsets
+ * with cu[0] != 0 or cu[B] != T set it too, and the well-formed requests are served.
  * A position whose page_table entry is outside 0..num_pages-1 sets
  * KDA_DEV_BAD_PAGE: it is not written, reads back as zeros, and takes part in
  * attention as a zero key and a zero value.

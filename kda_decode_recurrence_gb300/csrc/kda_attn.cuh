@@ -48,6 +48,12 @@ __device__ __forceinline__ Request load_request(const AttentionArgs& p, int b, b
   return r;
 }
 
+// By one thread of the call: offsets that do not span the T tokens are reported (rows outside
+// them are nobody's and stay as they are).
+__device__ __forceinline__ void check_offsets(const AttentionArgs& p) {
+  if (fresh(p.cu) != 0 || fresh(p.cu + p.B) != p.T) raise_status(p.dev_status, KDA_DEV_BAD_SEQLEN);
+}
+
 // Positions [lo, hi) that the token at position pos sees (none for padding, pos < 0).
 __device__ __forceinline__ int seen_lo(const AttentionArgs& p, int pos) {
   return p.window > 0 ? max(0, pos - p.window + 1) : 0;

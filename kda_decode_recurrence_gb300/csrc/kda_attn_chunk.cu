@@ -429,6 +429,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, kPair>::kThreads, 1)
   pdl_trigger();
 
   // ---- this CTA's share: each thread counts a run of requests
+  if (cta == 0 && tid == S::kThreads - 1) check_offsets(p);
   const int run = (p.B + S::kThreads - 1) / S::kThreads;
   const int b_lo = min(p.B, tid * run), b_hi = min(p.B, b_lo + run);
   long long mine = 0, my_items = 0;

@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
   pdl_trigger();
 
   // ---- this CTA's share: each thread counts a run of requests
+  if (cta == 0 && tid == kThreads - 1) check_offsets(p);
   const int run = (p.B + kThreads - 1) / kThreads;
   const int b_lo = min(p.B, tid * run), b_hi = min(p.B, b_lo + run);
   long long mine = 0;

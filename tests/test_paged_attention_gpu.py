@@ -354,3 +354,40 @@ def test_a_request_that_is_too_long_leaves_the_others_served(n, most, G, cache):
         else:
             assert bool(((out[rows].double() - want[rows]).abs() <= tol[rows]).all())
             assert bool(((lse[rows].double() - wlse[rows]).abs() <= ltol[rows]).all())
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("full,n,G", [(1, [1, 0, 1], 4), (6, [1, 3, 6], 2), (24, [24, 2, 9], 4), (150, [3, 150, 60], 2)])
+def test_offsets_that_do_not_span_the_tokens_are_reported(full, n, G, cache):
+    """cu[B] < T (a graph captured with full windows, replayed with shorter ones) and cu[0] > 0
+    set the status; the requests are served all the same."""
+    B = len(n)
+    case, q = make(dict(n=n, lens=[x + 100 for x in n], H=2 * G, HKV=2, D=128, page=16), cache=cache, seed=42)
+    want, wlse, tol, ltol = attention(case, q, 128 ** -0.5)
+    caches, scales = case.args()
+    shape = (B * full, 2 * G, 128)
+    wide = torch.randn(shape, device="cuda", generator=torch.Generator("cuda").manual_seed(1)).to(torch.bfloat16)
+    out, lse = torch.full(shape, 7.0, dtype=torch.bfloat16, device="cuda"), torch.full(shape[:2], 7.0, device="cuda")
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda") * full
+    lens = torch.full((B,), full + 50, dtype=torch.int32, device="cuda").clamp_max(case.max_pages * 16)
+    work = torch.empty(kda.paged_attention_workspace_size(B, B * full, full, 2 * G, 2, 128), dtype=torch.uint8, device="cuda")
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kda.kda_paged_attention(out, wide, *caches, cu, lens, case.table, full, **scales, lse=lse, workspace=work,
+                                dev_status=word)
+    lens.copy_(case.seq_lens)
+    for first in (0, 1):                         # cu[0] = 1: a row in front that is nobody's
+        if first + sum(n) > B * full:
+            continue
+        cu.copy_(case.cu + first)
+        rows = slice(first, first + sum(n))
+        wide[rows] = q
+        out.fill_(7.0)
+        word.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(word) == kda.DEV_BAD_SEQLEN
+        assert bool(((out[rows].double() - want).abs() <= tol).all())
+        assert bool(((lse[rows].double() - wlse).abs() <= ltol).all())
+        assert bool((out[:first] == 7).all()) and bool((out[first + sum(n):] == 7).all())
