@@ -35,22 +35,31 @@ __device__ __forceinline__ int find_request(const int32_t* cu, int B, int t) {
   return lo;
 }
 
+// Whether request b with rows t0 .. t1 - 1 and at[b] = `at` is well formed.
+template <bool kAppend>
+__device__ __forceinline__ bool good_request(const CacheRowsArgs& p, int t0, int t1, long long at) {
+  return t0 >= 0 && t1 >= t0 && t1 <= p.T && at >= 0 &&
+         (kAppend ? at : at + (t1 - t0)) <= (long long)p.c.max_pages * p.c.page_size;
+}
+
+// By one more CTA, beside those that take rows: every request that is not well formed is
+// reported, whether or not a row shows it, and so are offsets that do not span the T rows.
+template <bool kAppend>
+__device__ __forceinline__ void check_requests(const CacheRowsArgs& p) {
+  bool bad = threadIdx.x == 0 && (fresh(p.cu) != 0 || fresh(p.cu + p.B) != p.T);
+  for (unsigned b = threadIdx.x; b < (unsigned)p.B; b += kThreads)
+    bad |= !good_request<kAppend>(p, fresh(p.cu + b), fresh(p.cu + b + 1), p.at ? fresh(p.at + b) : 0);
+  if (bad) raise_status(p.dev_status, KDA_DEV_BAD_SEQLEN);
+}
+
 // Page and offset of packed row t; page -1: the row has no place.
 template <bool kAppend>
 __device__ __forceinline__ int2 find_place(const CacheRowsArgs& p, int t) {
   const int2 none = make_int2(-1, 0);
   const int b = find_request(p.cu, p.B, t);
   const int t0 = fresh(p.cu + b), t1 = fresh(p.cu + b + 1);
-  if (t < t0 || t >= t1 || t0 < 0 || t1 > p.T) {
-    raise_status(p.dev_status, KDA_DEV_BAD_SEQLEN);
-    return none;
-  }
   const long long at = p.at ? fresh(p.at + b) : 0;
-  const long long capacity = (long long)p.c.max_pages * p.c.page_size;
-  if (at < 0 || (kAppend ? at : at + (t1 - t0)) > capacity) {
-    raise_status(p.dev_status, KDA_DEV_BAD_SEQLEN);
-    return none;
-  }
+  if (t < t0 || t >= t1 || !good_request<kAppend>(p, t0, t1, at)) return none;
   const long long pos = kAppend ? at - (t1 - t) : at + (t - t0);
   if (pos < 0) return none;  // padding before the sequence's first position
   const int page = fresh(p.c.page_table + (size_t)b * p.c.max_pages + pos / p.c.page_size);
@@ -133,6 +142,7 @@ __global__ void __launch_bounds__(kThreads, 4) cache_append_kernel(const CacheRo
   R rows;
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x == gridDim.x - 1) return check_requests<true>(p);
   if (!rows.template start<true>(p, split)) return;
   for (int base = 0; base < rows.rows; base += R::kPerWarp * kUnroll) {
     uint4 x[kUnroll];
@@ -205,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, 6) cache_read_kernel(const CacheRows
   R rows;
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x == gridDim.x - 1) return check_requests<false>(p);
   if (!rows.template start<false>(p, split)) return;
   for (int base = 0; base < rows.rows; base += R::kPerWarp * kUnroll) {
     uint4 x[kUnroll];
@@ -263,7 +274,8 @@ cudaError_t run(Kernel kernel, const CacheRowsArgs& a, cudaStream_t stream) {
   s.tokens = a.T / kAllWarps < 1 ? 1 : a.T / kAllWarps > 8 ? 8 : a.T / kAllWarps;
   s.inv = (uint32_t)(((1ull << 32) + 2 * a.c.HKV - 1) / (2 * a.c.HKV));
   const long long per_cta = (long long)(kThreads / 32) * s.tokens;
-  return launch(kernel, dim3((unsigned)((a.T + per_cta - 1) / per_cta)), dim3(kThreads), 0, stream, true, a, s);
+  // (the last CTA looks at the requests)
+  return launch(kernel, dim3((unsigned)((a.T + per_cta - 1) / per_cta) + 1), dim3(kThreads), 0, stream, true, a, s);
 }
 
 }  // namespace

@@ -221,3 +221,33 @@ def test_offsets_beyond_32_bits():
 def test_table_of_code_values():
     codes = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn)
     assert np.array_equal(codes.float().numpy().astype(np.float64), E4M3_TABLE, equal_nan=True)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_every_malformed_request_is_reported(cache):
+    """Also where no row of the call shows it: offsets that start past 0 or before it, end
+    before T or past it, or go back; a bad length of a request without new rows."""
+    case = Case(n=[3, 0, 5], lens=[20, 12, 30], HKV=2, D=64, page=16, cache=cache, junk=1.0)
+    k, v = rows(case, 9)
+    good, status = append(case, k, v)
+    assert status == 0
+    caches, scales = case.args()
+    out = [torch.zeros(case.T, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    starts = case.seq_lens - torch.tensor(case.n, **i32)
+    assert int(kda.kda_cache_read(*out, *caches, case.cu, starts, case.table, **scales)) == 0
+    # the last three leave every row of the call in a well-formed request
+    for cu in ([1, 3, 3, 8], [0, 3, 3, 7], [0, 3, 3, 9], [-2, 3, 3, 8], [0, 8, 3, 8], [0, 8, 8, 7], [-1, 0, 0, 8]):
+        cu = torch.tensor(cu, **i32)
+        _, status = append(case, k, v, cu=cu, seq_lens=torch.full((3,), 30, **i32))
+        assert status == kda.DEV_BAD_SEQLEN, cu
+        assert int(kda.kda_cache_read(*out, *caches, cu, None, case.table, **scales)) == kda.DEV_BAD_SEQLEN, cu
+    for bad in (-1, case.max_pages * 16 + 1):
+        lens = case.seq_lens.clone()
+        lens[1] = bad                                       # request 1 has no new rows
+        held, status = append(case, k, v, seq_lens=lens)
+        assert status == kda.DEV_BAD_SEQLEN
+        for name in ("k", "v"):                             # and the others are served
+            assert np.array_equal(bits(held[name].t), bits(good[name].t))
+        starts[1] = bad
+        assert int(kda.kda_cache_read(*out, *caches, case.cu, starts, case.table, **scales)) == kda.DEV_BAD_SEQLEN
