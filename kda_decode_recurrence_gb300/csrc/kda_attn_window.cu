@@ -16,23 +16,31 @@
 // so that each entry of K and V is read from shared memory (and, for e4m3,
 // widened) once, and no warp's output has to be joined with another's.
 // e4m3 codes are widened to f16 (one conversion for two; bf16 takes five operations on
-// the pipe that is busiest), so Q and P are f16 there too, each scaled so that it
-// loses nothing: Q by a power of two per item (its largest entry becomes 2^8 .. 2^9),
-// P by the row's largest product of a weight and a value's scale:
-//   r = max_j (x_j + log2 vs_j) - 15,  w_j = 2^(x_j - r),  P_j = w_j vs_j <= 2^15
-// (11 bits down to 2^-29 of the largest contribution, where bf16 would keep 8), the
-// sum being that of w_j.
+// the pipe that is busiest), so Q and P are f16 there too.  Q is scaled by a power of two
+// per item (its largest entry becomes 2^8 .. 2^9), P by one per CTA's part of an item:
+//   w_j = 2^(x_j - m),  P_j = F w_j vs_j   (vs_j: the value's scale)
+// F takes the first key tile's largest vs to 2^7 .. 2^8; as long as every F vs_j that is not
+// 0 lies in 2^0 .. 2^15, P is within f16 and its error within 2^-11 of it or 2^-25 of the
+// largest weight (bf16: 2^-8).  Scales that do not fit (a row of zeros beside tiny values
+// has the scale 1) end that for the rest of the part: P is then w_j vs_j in bf16, whose range
+// is fp32's, and the codes of V are widened to bf16.  (log2 vs_j in the reference, in place of
+// F, lets scales of rows without weight take bits from the others, and next to scores of 2^24
+// it rounds by octaves.)
 // mma.sync (m16n8k16) is the instruction for it: 16 rows are its native
 // size, where tcgen05 would spend 128 lanes on them.
 //
 // 128 single tokens over 5.05 GB of bf16 cache: 713 us, 7.07 TB/s (a copy: 6.70).
-// 64 over 628 MB of e4m3: 141 us, 4.47 TB/s, bound by the issue of its instructions
-// (two CTAs an SM and bf16 operands: 178 us).  With more rows a warp reads as many
+// 64 over 628 MB of e4m3: 146 us, 4.31 TB/s (of which the look at V's scales 3 and the bf16
+// form beside the f16 one 3; two CTAs an SM and bf16 operands throughout: 178 us).
+// With more rows a warp reads as many
 // operands of Q and P as of K and V: 32 rows are for e4m3 only (89 us
-// against the chunk kernel's 116 for 32 such requests).  Eight warps that split D by eight: 165 us and 755 us on these two; streams of 32 positions per warp
-// that exchange nothing until an item's end, one CTA an SM: 265 us and 1320 us.
+// against the chunk kernel's 116 for 32 such requests).  Eight warps that split D by eight:
+// 165 us and 755 us on these two; streams of 32 positions per warp that exchange nothing until
+// an item's end, one CTA an SM: 265 us and 1320 us.
 #include <cuda.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "kda_attn.cuh"
 #include "kda_launch.h"
@@ -81,6 +89,7 @@ struct Smem {
   float scales[kE4m3 ? S::kStages : 1][2][kTile];
   float4 top[kRows];                               // the warps' row maxima
   float qinv[2];                                   // e4m3: what undoes Q's scaling
+  int4 span[kComputeWarps];                        // e4m3: of the warps' scales of V (see below)
   StageNote note[S::kStages];
   uint64_t full[S::kStages], empty[S::kStages], qfull[2], qempty[2];
   long long part[kThreads / 32];
@@ -113,19 +122,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ float log2_approx(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// What a value's scale s adds to its score in the reference r of a row's weights
-// w_j = 2^(x_j - r): P_j = w_j s_j, in f16, is at most 2^15.  A scale of 0 makes the value 0,
-// and r takes the score itself; below 2^-90 the sum of w could pass fp32's range (and P has
-// bits left).
-__device__ __forceinline__ float log2_of_scale(float s) {
-  const float a = fabsf(s);
-  return (a > 0.f ? fmaxf(log2_approx(a), -90.f) : 0.f) - 15.f;
-}
+// F takes a part's first scales to at most 2^kSpan .. 2^(kSpan + 1) and at least 2^0.  Those
+// that fit then lie in 1 / F .. 2^(2 kSpan + 1) / F, kRoom steps of their bits.  (One that is
+// not finite makes the rows that see it NaN in either type, and must not show in the others.)
+constexpr int kSpan = 7;
+constexpr uint32_t kRoom = (uint32_t)(2 * kSpan + 1) << 23, kUnset = 0x80000000u;
+
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
@@ -428,6 +430,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
     const int quad = lane >> 2, j2 = (lane & 3) * 2;
     float xscale = p.scale * kLog2E;
     float o[kR][kN][4], m[kR][2], l[kR][2];
+    // e4m3: F, the bits of 1 / F (kUnset: no scale has been seen, and F is 1), and whether P is
+    // bf16 (then F is 1 too)
+    [[maybe_unused]] float factor = 1.f;
+    [[maybe_unused]] uint32_t unit = kUnset;
+    [[maybe_unused]] bool v_wide = false;
     long long left = u1 - u0;
     int item = -1;
     bool ok = true;
@@ -441,6 +448,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
         ++item;
         ok = __all_sync(0xffffffffu, mbar_wait(&sm.qfull[item & 1], (item / 2) & 1));
         if (kE4m3) xscale = p.scale * kLog2E * sm.qinv[item & 1];
+        factor = 1.f;
+        unit = kUnset;
+        v_wide = false;
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
           m[r][0] = m[r][1] = -INFINITY;
@@ -454,6 +464,19 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
       const uint32_t k_addr = smem_u32(sm.kv[s][0]), v_addr = smem_u32(sm.kv[s][1]);
       const uint32_t q_addr = smem_u32(sm.q[item & 1]), p_addr = smem_u32(sm.pw);
 
+      const int my_pos = 16 * warp;
+      const int pos0 = note.L - note.n;   // position of token 0
+      const int lo_all = seen_lo(p, max(0, pos0));
+      const bool v_whole = note.start >= lo_all && note.start + kTile <= note.L;  // all seen by some token
+      bool narrow = true;
+      [[maybe_unused]] uint32_t bits = 0;  // of one of the warp's 16 scales of V, each in two lanes
+      if constexpr (kE4m3) {
+        const int at = my_pos + (lane & 15);
+        bits = __float_as_uint(sm.scales[s][1][at]) & 0x7fffffffu;
+        if (!v_whole && (note.start + at < lo_all || note.start + at >= note.L)) bits = 0;
+        narrow = v_wide | (bits == 0) | (bits - unit < kRoom);
+      }
+
       // S: this warp's 16 positions x all rows
       float x[kR][2][4];
 #pragma unroll
@@ -462,7 +485,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) x[r][n][i] = 0.f;
-      const int my_pos = 16 * warp;
       auto dot16 = [&](int kb, uint32_t b00, uint32_t b01, uint32_t b10, uint32_t b11) {
         // entries 16 kb .. 16 kb + 15 of the head dimension
 #pragma unroll
@@ -504,15 +526,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
         }
       }
       // scores in units of log 2, and what a row does not see
-      const int pos0 = note.L - note.n;   // position of token 0
-      const int lo_all = seen_lo(p, max(0, pos0));
       const bool whole = note.start >= seen_lo(p, note.L - 1) && note.start + kTile <= seen_hi(p, pos0, note.L);
-      float k_scale[2][2], v_scale[2][2], v_log[2][2];
+      float k_scale[2][2];
+      [[maybe_unused]] float v_scale[2][2];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         k_scale[n][0] = k_scale[n][1] = xscale;
-        v_scale[n][0] = v_scale[n][1] = 1.f;
-        v_log[n][0] = v_log[n][1] = 0.f;
         if constexpr (kE4m3) {
           const float2 f = *reinterpret_cast<const float2*>(&sm.scales[s][0][my_pos + 8 * n + j2]);
           const float2 v = *reinterpret_cast<const float2*>(&sm.scales[s][1][my_pos + 8 * n + j2]);
@@ -520,8 +539,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
           k_scale[n][1] *= f.y;
           v_scale[n][0] = v.x;
           v_scale[n][1] = v.y;
-          v_log[n][0] = log2_of_scale(v.x);
-          v_log[n][1] = log2_of_scale(v.y);
         }
       }
 #pragma unroll
@@ -543,156 +560,238 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
               const int at = my_pos + 8 * n + j2 + i;
               if (!whole && (at < lo || at >= hi)) y = -INFINITY;
               x[r][n][2 * half + i] = y;
-              top = fmaxf(top, kE4m3 ? y + v_log[n][i] : y);
+              top = fmaxf(top, y);
             }
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
           if ((lane & 3) == 0) reinterpret_cast<float*>(&sm.top[16 * r + 8 * half + quad])[warp] = top;
         }
-      ok = compute_sync_and(ok);
-      if (!ok) break;
-      float keep[kR][2];
-      bool moved = false;
-#pragma unroll
-      for (int r = 0; r < kR; ++r)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const float4 t = sm.top[16 * r + 8 * half + quad];
-          const float now = fmaxf(fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)), m[r][half]);
-          const float ref = now == -INFINITY ? 0.f : now;
-          keep[r][half] = exp2_approx(m[r][half] - ref);
-          moved |= now != m[r][half];
-          m[r][half] = now;
-          l[r][half] *= keep[r][half];
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float w0 = exp2_approx(x[r][n][2 * half] - ref), w1 = exp2_approx(x[r][n][2 * half + 1] - ref);
-            l[r][half] += w0 + w1;
-            float y0 = w0, y1 = w1;
-            if (kE4m3) {
-              // a weight of 0 stays 0 whatever the scale of a place it does not see
-              y0 = x[r][n][2 * half] == -INFINITY ? 0.f : w0 * v_scale[n][0];
-              y1 = x[r][n][2 * half + 1] == -INFINITY ? 0.f : w1 * v_scale[n][1];
-            }
-            const int row = 16 * r + 8 * half + quad;
-            *reinterpret_cast<uint32_t*>(sm.pw + swizzled<128>(row, 2 * warp + n) + j2 * 2) =
-                kE4m3 ? pack_f16(y0, y1) : pack_bf16(y0, y1);
-          }
+      // cold: a scale of a place that some row does not see may be anything (else the key tile's
+      // are finite, and a weight of 0 stays 0), or P is bf16
+      bool cold = v_wide || !v_whole;
+      if (!compute_sync_and(ok && narrow)) {
+        // (out of the way: a part's first scales, ones that do not fit or are not finite)
+        if constexpr (kE4m3) {
+          const bool some = bits != 0, finite = bits < 0x7f800000u;
+          int4 span;  // largest and smallest exponent; whether one does not fit, is not finite
+          span.x = __reduce_max_sync(0xffffffffu, some && finite ? (int)(bits >> 23) : -1);
+          span.y = __reduce_min_sync(0xffffffffu, some && finite ? (int)(bits >> 23) : 255);
+          span.z = __any_sync(0xffffffffu, some && finite && !narrow);
+          span.w = __any_sync(0xffffffffu, !finite);
+          if (lane == 0) sm.span[warp] = span;
         }
-      compute_sync();
-      // O: this warp's columns; the exponent's argument moves little, so most tiles keep
-      // every maximum and skip the rescaling
-      if (__any_sync(0xffffffffu, moved)) {
+        ok = compute_sync_and(ok);
+        if (!ok) break;
+        if constexpr (kE4m3) {
+          int most = -1, least = 255;
+          bool misfit = false;
 #pragma unroll
-        for (int r = 0; r < kR; ++r)
+          for (int w = 0; w < kComputeWarps; ++w) {
+            const int4 span = sm.span[w];
+            most = max(most, span.x);
+            least = min(least, span.y);
+            misfit |= span.z != 0;
+            cold |= span.w != 0;
+          }
+          if (unit == kUnset) {
+            if (most >= 0) {
+              // (F and 1 / F are normal numbers, and what fits is finite)
+              v_wide = most < 8 || most > 247 || least < most - kSpan;
+              unit = v_wide ? 0 : (uint32_t)(most - kSpan) << 23;
+              if (!v_wide) factor = __uint_as_float((254u << 23) - unit);
+            }
+          } else if (misfit) {  // from here on O and P are not scaled
 #pragma unroll
-          for (int n = 0; n < kN; ++n)
+            for (int r = 0; r < kR; ++r)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[r][n][i] *= keep[r][i >> 1];
+              for (int n = 0; n < kN; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[r][n][i] *= __uint_as_float(unit);
+            factor = 1.f;
+            unit = 0;
+            v_wide = true;
+          }
+          cold |= v_wide;
+        }
       }
-      // rows of V that no token of the request sees count as zeros
-      const bool v_whole = note.start >= lo_all && note.start + kTile <= note.L;
-      auto v_mask = [&](int pos) {  // positions pos, pos + 1 of the tile, as a mask of two halves
-        const int g = note.start + pos;
-        return (g >= lo_all && g < note.L ? 0x0000ffffu : 0u) |
-               (g + 1 >= lo_all && g + 1 < note.L ? 0xffff0000u : 0u);
-      };
+      if constexpr (kE4m3) {
 #pragma unroll
-      for (int kb = 0; kb < kTile / 16; ++kb) {
-        uint32_t a[kR][4];
+        for (int n = 0; n < 2; ++n) {
+          v_scale[n][0] *= factor;
+          v_scale[n][1] *= factor;
+        }
+      }
+      // the second half of the key tile: the weights, then O
+      auto weigh = [&](auto is_cold) {
+        constexpr bool kCold = decltype(is_cold)::value;
+        float keep[kR][2];
+        bool moved = false;
 #pragma unroll
         for (int r = 0; r < kR; ++r)
-          ldsm(p_addr + swizzled<128>(16 * r + (lane & 15), 2 * kb + (lane >> 4)), a[r]);
-        const int row = 16 * kb + (lane & 15);
-        if constexpr (!kE4m3) {
 #pragma unroll
-          for (int n = 0; n < kN; n += 2) {
+          for (int half = 0; half < 2; ++half) {
+            const float4 t = sm.top[16 * r + 8 * half + quad];
+            const float now = fmaxf(fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)), m[r][half]);
+            const float ref = now == -INFINITY ? 0.f : now;
+            keep[r][half] = exp2_approx(m[r][half] - ref);
+            moved |= now != m[r][half];
+            m[r][half] = now;
+            l[r][half] *= keep[r][half];
+            const int row = 16 * r + 8 * half + quad;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const float w0 = exp2_approx(x[r][n][2 * half] - ref), w1 = exp2_approx(x[r][n][2 * half + 1] - ref);
+              l[r][half] += w0 + w1;
+              float y0 = w0, y1 = w1;
+              if constexpr (kE4m3) {
+                y0 *= v_scale[n][0];
+                y1 *= v_scale[n][1];
+                if constexpr (kCold) {
+                  // a weight of 0 stays 0 whatever the scale of a place that the row does not see
+                  if (x[r][n][2 * half] == -INFINITY) y0 = 0.f;
+                  if (x[r][n][2 * half + 1] == -INFINITY) y1 = 0.f;
+                }
+              }
+              *reinterpret_cast<uint32_t*>(sm.pw + swizzled<128>(row, 2 * warp + n) + j2 * 2) =
+                  kE4m3 && !(kCold && v_wide) ? pack_f16(y0, y1) : pack_bf16(y0, y1);
+            }
+          }
+        compute_sync();
+        // O: this warp's columns; the exponent's argument moves little, so most tiles keep
+        // every maximum and skip the rescaling
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+          for (int r = 0; r < kR; ++r)
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[r][n][i] *= keep[r][i >> 1];
+        }
+        // rows of V that no token of the request sees count as zeros
+        auto v_mask = [&](int pos) {  // positions pos, pos + 1 of the tile, as a mask of two halves
+          const int g = note.start + pos;
+          return (g >= lo_all && g < note.L ? 0x0000ffffu : 0u) |
+                 (g + 1 >= lo_all && g + 1 < note.L ? 0xffff0000u : 0u);
+        };
+        auto weigh16 = [&](int kb) {  // positions 16 kb .. 16 kb + 15
+          uint32_t a[kR][4];
+#pragma unroll
+          for (int r = 0; r < kR; ++r)
+            ldsm(p_addr + swizzled<128>(16 * r + (lane & 15), 2 * kb + (lane >> 4)), a[r]);
+          const int row = 16 * kb + (lane & 15);
+          if constexpr (!kE4m3) {
+#pragma unroll
+            for (int n = 0; n < kN; n += 2) {
+              uint32_t b[4];
+              const int c = warp * kN + n + (lane >> 4);
+              ldsm_t(v_addr + (c / 8) * kTile * 128 + swizzled<128>(row, c & 7), b);
+              if (!v_whole) {
+                const uint32_t lo = v_mask(16 * kb + j2), hi = v_mask(16 * kb + 8 + j2);
+                b[0] &= lo; b[1] &= hi; b[2] &= lo; b[3] &= hi;
+              }
+              if (!whole) {
+                // A value that is not finite reaches the rows that see its position only:
+                // it is taken out here and counted with the rows' visibility as weights.
+                bool bad = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  bad |= (b[i] & 0x7f80u) == 0x7f80u || (b[i] & 0x7f800000u) == 0x7f800000u;
+                if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll 1
+                  for (int kind = 0; kind < 3; ++kind) {  // +infinity, -infinity, not a number
+                    uint32_t is[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                      is[i] = 0;
+#pragma unroll
+                      for (int e = 0; e < 2; ++e) {
+                        const uint32_t v = (b[i] >> (16 * e)) & 0xffffu;
+                        const bool yes = kind == 0 ? v == 0x7f80u : kind == 1 ? v == 0xff80u : (v & 0x7fffu) > 0x7f80u;
+                        if (yes) is[i] |= 0x3f80u << (16 * e);  // 1
+                      }
+                    }
+                    const float add = kind == 0 ? INFINITY : kind == 1 ? -INFINITY : __uint_as_float(0x7fffffffu);
+#pragma unroll
+                    for (int r = 0; r < kR; ++r) {
+                      uint32_t see[4];
+#pragma unroll
+                      for (int i = 0; i < 4; ++i) {
+                        const int pos = pos0 + (16 * r + 8 * (i & 1) + quad) / p.G;
+                        const int g = note.start + 16 * kb + 8 * (i >> 1) + j2;
+                        const int lo = seen_lo(p, pos), hi = min(seen_hi(p, pos, note.L), note.L);
+                        see[i] = (g >= lo && g < hi ? 0x3f80u : 0u) | (g + 1 >= lo && g + 1 < hi ? 0x3f800000u : 0u);
+                      }
+#pragma unroll
+                      for (int e = 0; e < 2; ++e) {
+                        float c4[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma(c4, see, is[2 * e], is[2 * e + 1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                          if (c4[i] > 0.f) o[r][n + e][i] += add;
+                      }
+                    }
+                  }
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    if ((b[i] & 0x7f80u) == 0x7f80u) b[i] &= 0xffff0000u;
+                    if ((b[i] & 0x7f800000u) == 0x7f800000u) b[i] &= 0x0000ffffu;
+                  }
+                }
+              }
+#pragma unroll
+              for (int r = 0; r < kR; ++r) {
+                mma(o[r][n], a[r], b[0], b[1]);
+                mma(o[r][n + 1], a[r], b[2], b[3]);
+              }
+            }
+          } else {
+            // 16 columns per 16-byte chunk: the even ones, then the odd ones.  Codes in use have
+            // no bad values (a bad row has a bad scale, which is in P of the rows that see it).
+            constexpr int kChunks = D / kComputeWarps / 16;  // 2 (D = 128) or 1
             uint32_t b[4];
-            const int c = warp * kN + n + (lane >> 4);
-            ldsm_t(v_addr + (c / 8) * kTile * 128 + swizzled<128>(row, c & 7), b);
+            const int c = warp * kChunks + (kChunks == 2 ? lane >> 4 : 0);
+            ldsm_t(v_addr + swizzled<S::kPanelBytes>(row, c), b);
             if (!v_whole) {
               const uint32_t lo = v_mask(16 * kb + j2), hi = v_mask(16 * kb + 8 + j2);
               b[0] &= lo; b[1] &= hi; b[2] &= lo; b[3] &= hi;
             }
-            if (!whole) {
-              // A value that is not finite reaches the rows that see its position only:
-              // it is taken out here and counted with the rows' visibility as weights.
-              bool bad = false;
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                bad |= (b[i] & 0x7f80u) == 0x7f80u || (b[i] & 0x7f800000u) == 0x7f800000u;
-              if (__any_sync(0xffffffffu, bad)) {
-#pragma unroll 1
-                for (int kind = 0; kind < 3; ++kind) {  // +infinity, -infinity, not a number
-                  uint32_t is[4];
+            for (int ch = 0; ch < kChunks; ++ch) {
+              if (kCold && v_wide) {
+                const uint32_t e0 = widen(__byte_perm(b[2 * ch], 0, 0x2404)), d0 = widen(b[2 * ch]);
+                const uint32_t e1 = widen(__byte_perm(b[2 * ch + 1], 0, 0x2404)), d1 = widen(b[2 * ch + 1]);
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    is[i] = 0;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                      const uint32_t v = (b[i] >> (16 * e)) & 0xffffu;
-                      const bool yes = kind == 0 ? v == 0x7f80u : kind == 1 ? v == 0xff80u : (v & 0x7fffu) > 0x7f80u;
-                      if (yes) is[i] |= 0x3f80u << (16 * e);  // 1
-                    }
-                  }
-                  const float add = kind == 0 ? INFINITY : kind == 1 ? -INFINITY : __uint_as_float(0x7fffffffu);
-#pragma unroll
-                  for (int r = 0; r < kR; ++r) {
-                    uint32_t see[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                      const int pos = pos0 + (16 * r + 8 * (i & 1) + quad) / p.G;
-                      const int g = note.start + 16 * kb + 8 * (i >> 1) + j2;
-                      const int lo = seen_lo(p, pos), hi = min(seen_hi(p, pos, note.L), note.L);
-                      see[i] = (g >= lo && g < hi ? 0x3f80u : 0u) | (g + 1 >= lo && g + 1 < hi ? 0x3f800000u : 0u);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                      float c4[4] = {0.f, 0.f, 0.f, 0.f};
-                      mma(c4, see, is[2 * e], is[2 * e + 1]);
-#pragma unroll
-                      for (int i = 0; i < 4; ++i)
-                        if (c4[i] > 0.f) o[r][n + e][i] += add;
-                    }
-                  }
+                for (int r = 0; r < kR; ++r) {
+                  mma(o[r][2 * ch], a[r], e0, e1);
+                  mma(o[r][2 * ch + 1], a[r], d0, d1);
                 }
+                continue;
+              }
+              // columns of two positions: (0 1 | 0 1) to (0 | 0), (1 | 1)
+              const uint32_t b0 = __byte_perm(b[2 * ch], 0, 0x3120), b1 = __byte_perm(b[2 * ch + 1], 0, 0x3120);
+              const uint32_t e0 = codes_f16(b0), e1 = codes_f16(b1);
+              const uint32_t d0 = codes_f16(b0 >> 16), d1 = codes_f16(b1 >> 16);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  if ((b[i] & 0x7f80u) == 0x7f80u) b[i] &= 0xffff0000u;
-                  if ((b[i] & 0x7f800000u) == 0x7f800000u) b[i] &= 0x0000ffffu;
-                }
+              for (int r = 0; r < kR; ++r) {
+                mma_f16(o[r][2 * ch], a[r], e0, e1);
+                mma_f16(o[r][2 * ch + 1], a[r], d0, d1);
               }
             }
-#pragma unroll
-            for (int r = 0; r < kR; ++r) {
-              mma(o[r][n], a[r], b[0], b[1]);
-              mma(o[r][n + 1], a[r], b[2], b[3]);
-            }
           }
+        };
+        if constexpr (!kCold) {
+#pragma unroll
+          for (int kb = 0; kb < kTile / 16; ++kb) weigh16(kb);
         } else {
-          // 16 columns per 16-byte chunk: the even ones, then the odd ones.  Codes in use have
-          // no bad values (a bad row has a bad scale, which is in P of the rows that see it).
-          constexpr int kChunks = D / kComputeWarps / 16;  // 2 (D = 128) or 1
-          uint32_t b[4];
-          const int c = warp * kChunks + (kChunks == 2 ? lane >> 4 : 0);
-          ldsm_t(v_addr + swizzled<S::kPanelBytes>(row, c), b);
-          if (!v_whole) {
-            const uint32_t lo = v_mask(16 * kb + j2), hi = v_mask(16 * kb + 8 + j2);
-            b[0] &= lo; b[1] &= hi; b[2] &= lo; b[3] &= hi;
-          }
-#pragma unroll
-          for (int ch = 0; ch < kChunks; ++ch) {
-            // columns of two positions: (0 1 | 0 1) to (0 | 0), (1 | 1)
-            const uint32_t b0 = __byte_perm(b[2 * ch], 0, 0x3120), b1 = __byte_perm(b[2 * ch + 1], 0, 0x3120);
-            const uint32_t e0 = codes_f16(b0), e1 = codes_f16(b1);
-            const uint32_t d0 = codes_f16(b0 >> 16), d1 = codes_f16(b1 >> 16);
-#pragma unroll
-            for (int r = 0; r < kR; ++r) {
-              mma_f16(o[r][2 * ch], a[r], e0, e1);
-              mma_f16(o[r][2 * ch + 1], a[r], d0, d1);
-            }
-          }
+#pragma unroll 1
+          for (int kb = 0; kb < kTile / 16; ++kb) weigh16(kb);
         }
+      };
+      if constexpr (!kE4m3) {
+        weigh(std::false_type{});
+      } else {
+        if (!cold) weigh(std::false_type{});
+        else weigh(std::true_type{});
       }
       __syncwarp();
       if (lane == 0) {
@@ -715,6 +814,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
       compute_sync();
       const int place = (note.flags & kBegins) ? 1 : 0;
       const int rows = note.n * p.G;
+      const float undo = factor == 1.f ? 1.f : __uint_as_float(unit);
       if (!done && place == 1 && tid == 0)
         pieces.notes[cta] = PieceNote{note.t0 * p.H + note.h * p.G, note.n, note.pieces, 0};
 #pragma unroll
@@ -745,14 +845,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
 #pragma unroll
             for (int n = 0; n < kN; n += 2) {  // even and odd columns: four in a row
               const int col = warp * (D / kComputeWarps) + 8 * n + 2 * j2;
-              const float y0 = o[r][n][2 * half], y1 = o[r][n + 1][2 * half];
-              const float y2 = o[r][n][2 * half + 1], y3 = o[r][n + 1][2 * half + 1];
+              // (times 1 / l first where the row ends here: a sum of weights is 1 or more)
+              const float by = done ? inv : 1.f;
+              const float y0 = o[r][n][2 * half] * by * undo, y1 = o[r][n + 1][2 * half] * by * undo;
+              const float y2 = o[r][n][2 * half + 1] * by * undo, y3 = o[r][n + 1][2 * half + 1] * by * undo;
               if (done)
-                *reinterpret_cast<uint2*>(p.out + out_row * D + col) =
-                    make_uint2(pack_bf16(y0 * inv, y1 * inv), pack_bf16(y2 * inv, y3 * inv));
+                *reinterpret_cast<uint2*>(p.out + out_row * D + col) = make_uint2(pack_bf16(y0, y1), pack_bf16(y2, y3));
               else
-                *reinterpret_cast<float4*>(pieces.o + piece * D + col) =
-                    make_float4(y0, y1, y2, y3);
+                *reinterpret_cast<float4*>(pieces.o + piece * D + col) = make_float4(y0, y1, y2, y3);
             }
           }
         }

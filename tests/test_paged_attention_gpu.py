@@ -391,3 +391,86 @@ def test_offsets_that_do_not_span_the_tokens_are_reported(full, n, G, cache):
         assert bool(((out[rows].double() - want).abs() <= tol).all())
         assert bool(((lse[rows].double() - wlse).abs() <= ltol).all())
         assert bool((out[:first] == 7).all()) and bool((out[first + sum(n):] == 7).all())
+
+
+# requests of up to 32 rows over e4m3: the window kernel's
+FEW = [dict(n=[1, 1], lens=[300, 77], H=16, HKV=2, D=128, page=16), dict(n=[4, 4], lens=[200, 70], H=8, HKV=2, D=64, page=32),
+       dict(n=[5, 2], lens=[150, 130], H=10, HKV=2, D=128, page=64), dict(n=[60], lens=[150], H=4, HKV=2, D=128, page=16)]
+FEW_IDS = ["token", "window16", "window32", "chunk"]
+
+
+@pytest.mark.parametrize("amplitude", [1.0, 1e-8, 1e-9, 1e-20, 1e12])
+@pytest.mark.parametrize("shape", FEW, ids=FEW_IDS)
+def test_rows_of_zeros_have_no_say_in_the_weights(shape, amplitude):
+    """An appended V row of zeros has the scale 1, a position without a page 0: neither
+    takes bits from the weights of values that are much smaller, or larger."""
+    for where in ("row", "page"):
+        case, q = make(shape, cache="e4m3", seed=46)
+        code, scale = case.tensors["v"]
+        scale.mul_(amplitude)
+        table = case.table.clone()
+        if where == "page":
+            table[0, 1 if case.lens[0] > case.page else 0] = -7
+            out, lse, status = attend(case, q, table=table)
+            want, wlse, tol, ltol = attention(case, q, case.D ** -0.5, table=table)
+            assert status == kda.DEV_BAD_PAGE
+            assert bool(((out.double() - want).abs() <= tol).all()) and bool(((lse.double() - wlse).abs() <= ltol).all())
+            continue
+        for b in range(case.B):
+            for pos in (0, case.lens[b] // 2, case.lens[b] - 1):
+                code[int(table[b, pos // case.page]), :, pos % case.page] = 0
+                scale[int(table[b, pos // case.page]), :, pos % case.page] = 1.0
+        check(case, q)
+
+
+@pytest.mark.parametrize("factor", [2.0 ** 9, 2.0 ** 40, 2.0 ** -40, 2.0 ** 100])
+@pytest.mark.parametrize("shape", FEW, ids=FEW_IDS)
+def test_value_rows_of_different_size(shape, factor):
+    """Some rows of V far larger or smaller than the others, and 0 in half of their columns:
+    those columns come from the other rows alone."""
+    case, q = make(shape, cache="e4m3", seed=47)
+    code, scale = case.tensors["v"]
+    for b in range(case.B):
+        for pos in range(0, case.lens[b], 11):
+            code.view(torch.uint8)[int(case.table[b, pos // case.page]), :, pos % case.page, ::2] = 0
+            scale[int(case.table[b, pos // case.page]), :, pos % case.page] *= factor
+    check(case, q)
+
+
+@pytest.mark.parametrize("H,D", [(8, 128), (16, 64)])
+@pytest.mark.parametrize("jump", [2.0 ** 5, 2.0 ** -12, 2.0 ** 60, 2.0 ** -60, 0.0])
+def test_value_sizes_that_change_along_the_sequence(H, D, jump):
+    """Shares of several key tiles, in which V's scales jump from one tile to a later one."""
+    n = [1] * 24 + [2] * 8
+    case, q = make(dict(n=n, lens=[2000 + 37 * i for i in range(32)], H=H, HKV=4, D=D, page=64), cache="e4m3", seed=48)
+    scale = case.tensors["v"][1]
+    for b in range(case.B):
+        pages = case.table[b, :-(-case.lens[b] // 64)].long()
+        scale[pages[(b % 7) + 3:]] *= jump
+        scale[pages[(b % 7) + 9:]] *= 2.0 ** 10
+    check(case, q)
+
+
+@pytest.mark.parametrize("amplitude", [1.0, 2.0 ** -60, 2.0 ** 126])
+@pytest.mark.parametrize("n,lens", [(3, 190), (6, 200), (8, 64)])
+def test_a_value_scale_that_is_not_finite_reaches_only_the_tokens_that_see_it(n, lens, amplitude):
+    """Beside scales of any size, up to the top of fp32's range."""
+    case, q = make(dict(n=[n], lens=[lens], H=8, HKV=2, D=128, page=16), cache="e4m3", seed=50)
+    case.tensors["v"][1].mul_(amplitude)
+    case.tensors["v"][0].view(torch.uint8).bitwise_and_(0x80).bitwise_or_(0x38)     # 1 and -1: no value overflows
+    want, wlse, _ = attend(case, q)
+    assert bool(torch.isfinite(want).all())
+    i, pos = n // 2, lens - n + n // 2
+    for bad in (float("inf"), float("nan")):
+        case.tensors["v"][1][int(case.table[0, pos // 16]), 1, pos % 16] = bad
+        out, lse, status = attend(case, q)
+        assert status == 0 and torch.equal(out[:i], want[:i]) and torch.equal(lse, wlse)
+        assert torch.equal(out[:, :4], want[:, :4]) and not bool(torch.isfinite(out[i:, 4:]).any())
+
+
+@pytest.mark.parametrize("factor", [2.0 ** 6, 2.0 ** 12, 2.0 ** 22])
+@pytest.mark.parametrize("shape", FEW, ids=FEW_IDS)
+def test_scores_of_millions(shape, factor):
+    """Scores next to which the logarithm of a value's scale is a fraction of an fp32 step."""
+    case, q = make(shape, cache="e4m3", seed=49)
+    check(case, q * factor)
