@@ -17,7 +17,9 @@
 // widened) once, and no warp's output has to be joined with another's.
 // e4m3 codes are widened to f16 (one conversion for two; bf16 takes five operations on
 // the pipe that is busiest), so Q and P are f16 there too.  Q is scaled by a power of two
-// per item (its largest entry becomes 2^8 .. 2^9), P by one per CTA's part of an item:
+// per item (its largest entry becomes 2^8 .. 2^9) and exact: an item with entries too small
+// for f16 beside that one (26 octaves below it) keeps Q in bf16, and its codes of K are widened
+// to bf16.  P is scaled by a power of two per CTA's part of an item:
 //   w_j = 2^(x_j - m),  P_j = F w_j vs_j   (vs_j: the value's scale)
 // F takes the first key tile's largest vs to 2^7 .. 2^8; as long as every F vs_j that is not
 // 0 lies in 2^0 .. 2^15, P is within f16 and its error within 2^-11 of it or 2^-25 of the
@@ -30,7 +32,7 @@
 // size, where tcgen05 would spend 128 lanes on them.
 //
 // 128 single tokens over 5.05 GB of bf16 cache: 713 us, 7.07 TB/s (a copy: 6.70).
-// 64 over 628 MB of e4m3: 146 us, 4.31 TB/s (of which the look at V's scales 3 and the bf16
+// 64 over 628 MB of e4m3: 147 us, 4.27 TB/s (of which the look at V's scales 3 and the bf16
 // form beside the f16 one 3; two CTAs an SM and bf16 operands throughout: 178 us).
 // With more rows a warp reads as many
 // operands of Q and P as of K and V: 32 rows are for e4m3 only (89 us
@@ -90,6 +92,7 @@ struct Smem {
   float4 top[kRows];                               // the warps' row maxima
   float qinv[2];                                   // e4m3: what undoes Q's scaling
   int4 span[kComputeWarps];                        // e4m3: of the warps' scales of V (see below)
+  int qwide[2];                                    // e4m3: Q is bf16, f16 would lose bits
   StageNote note[S::kStages];
   uint64_t full[S::kStages], empty[S::kStages], qfull[2], qempty[2];
   long long part[kThreads / 32];
@@ -366,13 +369,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
       if (!ok) break;
       constexpr int kChunks = D / 8;  // 16-byte chunks of a row
       const int rows = w.r.n * p.G;
+      const int padding = max(0, w.r.n - w.r.L) * p.G;  // rows of tokens before position 0: zeros
       auto load = [&](int i) {
         const int row = i / kChunks, c = i % kChunks;
-        if (row >= rows) return make_uint4(0, 0, 0, 0);
+        if (row < padding || row >= rows) return make_uint4(0, 0, 0, 0);
         return *reinterpret_cast<const uint4*>(
             p.q + (w.r.t0 + row / p.G) * p.q_stride + (size_t)(w.h * p.G + row % p.G) * D + c * 8);
       };
-      auto store = [&](int i, uint4 x, float factor) {
+      auto store = [&](int i, uint4 x, float factor, bool wide) {
         const int row = i / kChunks, c = i % kChunks;
         unsigned char* to = sm.q[s] + (c / 8) * kRows * 128;
         if constexpr (kE4m3) {
@@ -383,23 +387,27 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
           const int c0 = (c & 7) & ~1;
           const uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
+          for (int e = 0; e < 4; ++e) {
+            const float lo = bf16_lo(v[e]) * factor, hi = bf16_hi(v[e]) * factor;
             *reinterpret_cast<uint32_t*>(to + swizzled<128>(row, c0 + (e & 1)) + j * 4 + (e >> 1) * 4) =
-                pack_f16(bf16_lo(v[e]) * factor, bf16_hi(v[e]) * factor);
+                wide ? pack_bf16(lo, hi) : pack_f16(lo, hi);
+          }
         } else {
           *reinterpret_cast<uint4*>(to + swizzled<128>(row, c & 7)) = x;
         }
       };
       constexpr int kLoads = kRows * kChunks / 32;
       if constexpr (kE4m3) {
-        // the largest finite entry's exponent e: factor 2^(135 - e)
-        uint32_t top = 0;
+        // the largest finite entry's exponent e: factor 2^(135 - e); the smallest's that is
+        // not 0 says whether f16 holds them all (least: its bits less 1, so that 0 is the most)
+        uint32_t top = 0, least = 0xffffffffu;
         auto raise = [&](const uint4& x) {
           const uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint32_t lo = v[e] & 0x7fffu, hi = (v[e] >> 16) & 0x7fffu;
             top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+            least = min(least, min(lo - 1u, hi - 1u));
           }
         };
         uint4 held[kLoads];
@@ -408,15 +416,24 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) raise(held[i]);
 #pragma unroll
-        for (int e = 16; e > 0; e >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, e));
+        for (int e = 16; e > 0; e >>= 1) {
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, e));
+          least = min(least, __shfl_xor_sync(0xffffffffu, least, e));
+        }
         const int field = min(253, 262 - (int)(top >> 7));  // its inverse is a normal number too
         const float factor = __uint_as_float((uint32_t)field << 23);
-        if (lane == 0) sm.qinv[s] = __uint_as_float((uint32_t)(254 - field) << 23);
+        // the last bit of the smallest, 2^(e - 134) of its exponent field e (1 for a subnormal),
+        // times 2^(field - 127): no smaller than f16's, 2^-24
+        const bool wide = least < 0x7f80u && max(1, (int)((least + 1u) >> 7)) + field < 237;
+        if (lane == 0) {
+          sm.qinv[s] = __uint_as_float((uint32_t)(254 - field) << 23);
+          sm.qwide[s] = wide;
+        }
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) store(i * 32 + lane, held[i], factor);
+        for (int i = 0; i < kLoads; ++i) store(i * 32 + lane, held[i], factor, wide);
       } else {
 #pragma unroll 8
-        for (int i = 0; i < kLoads; ++i) store(i * 32 + lane, load(i * 32 + lane), 1.f);
+        for (int i = 0; i < kLoads; ++i) store(i * 32 + lane, load(i * 32 + lane), 1.f, false);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.qfull[s]);
@@ -429,6 +446,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
     constexpr int kN = D / kComputeWarps / 8;  // blocks of 8 columns of O per warp
     const int quad = lane >> 2, j2 = (lane & 3) * 2;
     float xscale = p.scale * kLog2E;
+    [[maybe_unused]] bool q_wide = false;
     float o[kR][kN][4], m[kR][2], l[kR][2];
     // e4m3: F, the bits of 1 / F (kUnset: no scale has been seen, and F is 1), and whether P is
     // bf16 (then F is 1 too)
@@ -447,7 +465,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
       if (note.flags & kFirst) {
         ++item;
         ok = __all_sync(0xffffffffu, mbar_wait(&sm.qfull[item & 1], (item / 2) & 1));
-        if (kE4m3) xscale = p.scale * kLog2E * sm.qinv[item & 1];
+        if (kE4m3) {
+          xscale = p.scale * kLog2E * sm.qinv[item & 1];
+          q_wide = sm.qwide[item & 1] != 0;
+        }
         factor = 1.f;
         unit = kUnset;
         v_wide = false;
@@ -485,14 +506,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) x[r][n][i] = 0.f;
-      auto dot16 = [&](int kb, uint32_t b00, uint32_t b01, uint32_t b10, uint32_t b11) {
+      auto dot16 = [&](int kb, uint32_t b00, uint32_t b01, uint32_t b10, uint32_t b11, auto in_f16) {
         // entries 16 kb .. 16 kb + 15 of the head dimension
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
           uint32_t a[4];
           const int row = 16 * r + (lane & 15), c = 2 * kb + (lane >> 4);
           ldsm(q_addr + (c / 8) * kRows * 128 + swizzled<128>(row, c & 7), a);
-          if constexpr (kE4m3) {
+          if constexpr (decltype(in_f16)::value) {
             mma_f16(x[r][0], a, b00, b01);
             mma_f16(x[r][1], a, b10, b11);
           } else {
@@ -507,22 +528,40 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
           uint32_t b[4];
           const int row = my_pos + (lane >> 4) * 8 + (lane & 7), c = 2 * kb + ((lane >> 3) & 1);
           ldsm(k_addr + (c / 8) * kTile * 128 + swizzled<128>(row, c & 7), b);
-          dot16(kb, b[0], b[1], b[2], b[3]);
+          dot16(kb, b[0], b[1], b[2], b[3], std::false_type{});
         }
       } else {
-#pragma unroll
-        for (int kb = 0; kb < D / 32; ++kb) {
+        auto dot32 = [&](int kb, auto in_f16) {
           uint32_t b[4];
           const int row = my_pos + (lane >> 4) * 8 + (lane & 7), c = 2 * kb + ((lane >> 3) & 1);
           ldsm(k_addr + swizzled<S::kPanelBytes>(row, c), b);
           uint32_t w[4][2];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            w[i][0] = codes_f16(b[i]);
-            w[i][1] = codes_f16(b[i] >> 16);
+            if constexpr (decltype(in_f16)::value) {
+              w[i][0] = codes_f16(b[i]);
+              w[i][1] = codes_f16(b[i] >> 16);
+            } else {
+              w[i][0] = widen(__byte_perm(b[i], 0, 0x1404));
+              w[i][1] = widen(__byte_perm(b[i], 0, 0x3424));
+            }
           }
-          dot16(2 * kb, w[0][0], w[0][1], w[2][0], w[2][1]);
-          dot16(2 * kb + 1, w[1][0], w[1][1], w[3][0], w[3][1]);
+          dot16(2 * kb, w[0][0], w[0][1], w[2][0], w[2][1], in_f16);
+          dot16(2 * kb + 1, w[1][0], w[1][1], w[3][0], w[3][1], in_f16);
+        };
+        // (in f16 whatever Q is, and once more where it is bf16: with the two beside each other the
+        // usual key tile takes 4% longer)
+#pragma unroll
+        for (int kb = 0; kb < D / 32; ++kb) dot32(kb, std::true_type{});
+        if (q_wide) {
+#pragma unroll
+          for (int r = 0; r < kR; ++r)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[r][n][i] = 0.f;
+#pragma unroll 1
+          for (int kb = 0; kb < D / 32; ++kb) dot32(kb, std::false_type{});
         }
       }
       // scores in units of log 2, and what a row does not see

@@ -474,3 +474,48 @@ def test_scores_of_millions(shape, factor):
     """Scores next to which the logarithm of a value's scale is a fraction of an fp32 step."""
     case, q = make(shape, cache="e4m3", seed=49)
     check(case, q * factor)
+
+
+@pytest.mark.parametrize("factor", [2.0 ** 22, 2.0 ** 40, 2.0 ** 100, 2.0 ** -100])
+@pytest.mark.parametrize("shape", FEW, ids=FEW_IDS)
+def test_queries_of_different_size(shape, factor):
+    """A head's and a token's queries far larger or smaller than the others: no row of
+    queries has a say in another's scores."""
+    for which in ("head", "token"):
+        case, q = make(shape, cache="e4m3", seed=43)
+        q = q.clone()
+        if which == "head":
+            q[:, 1] = (q[:, 1].float() * factor).to(torch.bfloat16)
+        else:
+            q[-1:] = (q[-1:].float() * factor).to(torch.bfloat16)
+        check(case, q)
+
+
+@pytest.mark.parametrize("shape", [dict(n=[4, 6], lens=[2, 3], H=4, HKV=2, D=128, page=16),
+                                   dict(n=[7, 3], lens=[5, 90], H=8, HKV=2, D=64, page=16),
+                                   dict(n=[40], lens=[30], H=4, HKV=2, D=128, page=16)], ids=["16", "32", "chunk"])
+def test_queries_of_padding_tokens_have_no_influence(shape):
+    """Tokens before position 0 hold anything: huge numbers, infinities, NaN."""
+    case, q = make(shape, cache="e4m3", seed=44)
+    q = q.contiguous()
+    want, wlse, _ = attend(case, q)
+    at = cumulative(case.n)
+    for junk in (3e38, float("inf"), float("nan")):
+        for b in range(case.B):
+            q[at[b]:at[b] + max(0, case.n[b] - case.lens[b])] = junk
+        out, lse, status = attend(case, q)
+        assert status == 0 and torch.equal(out, want) and torch.equal(lse, wlse)
+
+
+@pytest.mark.parametrize("big", [2.0 ** 20, 2.0 ** 26, 2.0 ** 45, 2.0 ** 90])
+@pytest.mark.parametrize("shape", FEW, ids=FEW_IDS)
+def test_entries_of_one_query_of_different_size(shape, big):
+    """Where the keys are 0 the queries are huge: the scores come from the small entries alone."""
+    case, q = make(shape, cache="e4m3", seed=45)
+    q = q.clone()
+    q[..., 3] = big
+    q[..., 40] = -big
+    codes = case.tensors["k"][0].view(torch.uint8)
+    codes[..., 3] = 0
+    codes[..., 40] = 0x80
+    check(case, q)
