@@ -424,9 +424,10 @@ size_t kda_paged_attention_workspace_size(int B, int T, int max_tokens, int H, i
  *   x_i is accepted iff x_0 .. x_{i-1} were and u_i q_i(x_i) < p_i(x_i)
  *   j of them accepted: w = max(p_j - q_j, 0) if j < n_b, w = p_j if j = n_b
  *   drawn: the smallest v with w(0) + .. + w(v) > u' (w(0) + .. + w(V - 1))
- * The products, the comparisons and the sums are exact to 48 bits or more, so
- * the tokens do not depend on the order of summation.  Entries of w that are
- * not positive, or not a number, count as 0.
+ * The products and comparisons of the acceptance are exact; the sums are off by
+ * at most 2^-38 of themselves.  Where u' lies that close to a border between two
+ * entries, either may be drawn, and B, which sets the order of summation, may
+ * decide which.  Entries of w that are not positive, or not a number, count as 0.
  *
  *   tokens       [N + B] int32, written: request b's at cu_drafts[b] + b: its
  *                accepted drafts, the drawn token, then -1.

@@ -9,9 +9,13 @@
 // A draw reads two rows of V probabilities (one if all drafts were accepted) and
 // does about 13 operations per entry: HBM bounds it.  fp64 adds cannot keep
 // up (152 SMs x 2 per clock = 0.6 T/s against 0.8 T entries/s from HBM), so
-// sums are pairs of fp32 (hi + lo, about 48 bits) within a warp and fp64 only
-// where warps are joined: the drawn token has to be the same for any order of
-// summation, and neighbours in a large vocabulary lie 1e-6 of the sum apart.
+// sums are pairs of fp32 (hi + lo) for up to 32 entries of a lane, pairs of those for up to 16
+// such runs, and fp64 beyond that and where warps are joined: neighbours in a large vocabulary
+// lie 1e-6 of the sum apart.
+// A pair's low part takes a rounded addition per entry, so that after n of them it is off by
+// at most (n^2 / 2 + 3.5 n) 2^-48 of the sum: 2^-38.7 for 32, 2^-40.5 for the 16 runs (measured
+// on weights that span many octaves: 2^-48; with one pair for all 2^-45 after 128 entries,
+// 2^-34 after 16384).
 //
 // A cluster of CTAs serves a request, its warps a segment of the row each; the
 // segments' sums meet through distributed shared memory, so that one launch does
@@ -20,8 +24,11 @@
 //
 // 256 requests of 1 .. 7 drafts over 131072 tokens: 268 MB in 56 us, 4.8 TB/s (a copy:
 // 6.7): the pair sums take 13 operations an entry, and a cluster's last warp is waited
-// for twice.  Four over 32001: 12.5 us with the host's call.
+// for twice.  Four over 32001: 12.5 us with the host's call.  800 over 131072, runs of 32
+// entries: 247 us (one pair for all 128 of a lane: 234).
 #include <cooperative_groups.h>
+
+#include <type_traits>
 
 #include "kda_common.cuh"
 #include "kda_paged.h"
@@ -37,6 +44,8 @@ constexpr int kMaxCluster = 8;               // CTAs per request
 constexpr int kCtasPerSm = 16;
 constexpr int kSms = 152;
 constexpr int kBlocks = 8;                   // blocks a segment is searched by
+constexpr int kRun = 32;                     // entries that a lane adds in one pair,
+constexpr int kRuns = 16;                    // and such pairs in one more
 
 struct Pair {
   float hi, lo;
@@ -57,6 +66,12 @@ __device__ __forceinline__ double warp_total(Pair s) {
     add(s, hi, lo);
   }
   return (double)s.hi + (double)s.lo;
+}
+
+__device__ __forceinline__ double warp_total(double s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
 }
 
 __device__ __forceinline__ double warp_scan(double x, int lane) {
@@ -147,10 +162,16 @@ __device__ __forceinline__ int first_past(double c, double x, double target) {
   return past ? __ffs(past) - 1 : some ? 31 - __clz(some) : 0;
 }
 
-template <bool kVec>
+// The entries of a block of a warp's segment.
+__host__ __device__ __forceinline__ int segment_of(int V, int segments) { return ((V + segments - 1) / segments + 3) & ~3; }
+__host__ __device__ __forceinline__ int block_of(int segment) { return ((segment + kBlocks - 1) / kBlocks + 127) & ~127; }
+
+// kLong: a lane has more than kRun entries of a block.
+template <bool kVec, bool kLong>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const VerifyArgs a, const int size) {
   __shared__ int s_taken, s_found;
-  __shared__ Pair s_lane[kBlocks][kThreads];  // every lane's sum of each block of its segment
+  using Sum = std::conditional_t<kLong, double, Pair>;
+  __shared__ Sum s_lane[kBlocks][kThreads];  // every lane's sum of each block of its segment
   __shared__ double s_own[kWarps], s_base, s_target;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
@@ -203,17 +224,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
   w.skip = taken < n && !a.draft ? a.draft_tokens[d0 + taken] : -1;
 
   // ---- the sum of this warp's segment
-  const int seg = ((a.V + segments - 1) / segments + 3) & ~3;
+  const int seg = segment_of(a.V, segments);
   const int segment = rank * kWarps + warp;
   const int lo = (int)min((long long)a.V, (long long)segment * seg), hi = (int)min((long long)a.V, (long long)lo + seg);
-  const int step = (((hi - lo) + kBlocks - 1) / kBlocks + 127) & ~127;
-  Pair mine = {0.f, 0.f};
+  const int step = block_of(hi - lo);
+  Sum mine = {};
 #pragma unroll 1
   for (int i = 0; i < kBlocks; ++i) {
     const int from = min(hi, lo + i * step), to = min(hi, from + step);
-    const Pair x = lane_sum<kVec>(w, from, to, lane);
-    s_lane[i][tid] = x;
-    add(mine, x.hi, x.lo);
+    if constexpr (!kLong) {
+      const Pair x = lane_sum<kVec>(w, from, to, lane);
+      s_lane[i][tid] = x;
+      add(mine, x.hi, x.lo);
+    } else {
+      double sum = 0.0;
+      for (int at = from; at < to;) {
+        Pair some = {0.f, 0.f};
+#pragma unroll 1
+        for (int run = 0; run < kRuns && at < to; ++run, at += 32 * kRun) {
+          const Pair x = lane_sum<kVec>(w, at, min(to, at + 32 * kRun), lane);
+          add(some, x.hi, x.lo);
+        }
+        sum += (double)some.hi + (double)some.lo;
+      }
+      s_lane[i][tid] = sum;
+      mine += sum;
+    }
   }
   const double sum = warp_total(mine);
   if (lane == 0) s_own[warp] = sum;
@@ -291,7 +327,9 @@ cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t stream) {
   const bool vec = ((reinterpret_cast<uintptr_t>(a.target) | reinterpret_cast<uintptr_t>(a.draft)) & 15) == 0 &&
                    a.target_stride % 4 == 0 && (!a.draft || a.draft_stride % 4 == 0);
   const long long ctas = (long long)a.B * size;
-  void (*kernel)(VerifyArgs, int) = vec ? verify_kernel<true> : verify_kernel<false>;
+  const bool runs = block_of(segment_of(a.V, kWarps * size)) > 32 * kRun;
+  void (*kernel)(VerifyArgs, int) = runs ? (vec ? verify_kernel<true, true> : verify_kernel<false, true>)
+                                         : (vec ? verify_kernel<true, false> : verify_kernel<false, false>);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kThreads);

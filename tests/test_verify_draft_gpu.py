@@ -156,3 +156,39 @@ def test_the_drawn_tokens_follow_the_target():
     seen = np.bincount(tokens[::2], minlength=V) / B
     p = p.numpy().astype(float)
     assert np.all(np.abs(seen - p) <= 5 * np.sqrt(p * (1 - p) / B))
+
+
+def test_the_sums_hold_on_a_border_of_a_large_vocabulary():
+    """Long sums of weights that span many octaves, the target u' times the
+    sum at 2^-37 of itself before or behind a border: further than the sums' error lets it
+    move (less than 2^-38 of the sum before the border and of the target).  All lanes add the same
+    sequence, so that no error averages out."""
+    V, length = 1 << 27, 1 << 14
+    g = np.random.default_rng(6)
+    s = (np.exp(3 * g.standard_normal((2, 64, length))) * 2.0 ** -32).astype(np.float32)
+    s = s[0, 44], s[1, 59]                                   # (whose plain pair sums were off by 2^-34)
+    s = np.stack([s[0], s[1] * np.float32(0.9 * s[0].sum(dtype=float) / s[1].sum(dtype=float))])
+    s[0, -1] = s[1, 0] = np.float32(2.0 ** -32)                # at the border
+    rows = [torch.from_numpy(x).cuda().view(-1, 1, 4).expand(-1, 32, 4).reshape(1, -1) for x in s]
+    weights = torch.cat([x.expand(V // 2 // x.shape[1], -1).reshape(1, -1) for x in rows], 1)
+    unit = 2.0 ** 110                                           # every weight a whole number of 1 / unit
+    each = V // 2 // length
+    halves = [sum(int(float(y) * unit) for y in x) * each for x in s]
+    spare = weights[0, V - 3:].cpu().numpy()                    # three entries that make up the difference
+    for sign, drawn in ((1, V // 2), (-1, V // 2 - 1)):
+        rest = halves[0] + sign * (halves[0] >> 36) - (halves[1] - sum(int(float(y) * unit) for y in spare))
+        fill = []
+        for _ in range(3):
+            y = np.float32(rest / unit)
+            if int(float(y) * unit) > rest:                     # (rounded down: no weight is negative)
+                y = np.nextafter(y, np.float32(0))
+            fill.append(y)
+            rest -= int(float(y) * unit)
+        assert abs(rest) <= halves[0] >> 60
+        weights[0, V - 3:] = torch.tensor(fill)
+        tokens = torch.zeros(1, dtype=torch.int32, device="cuda")
+        accepted = torch.zeros(1, dtype=torch.int32, device="cuda")
+        none, half = torch.zeros(0, device="cuda"), torch.full((1,), 0.5, device="cuda")
+        status = kda.kda_verify_draft(tokens, accepted, weights, None, none.int(), none, half,
+                                      torch.zeros(2, dtype=torch.int32, device="cuda"))
+        assert int(status) == 0 and int(tokens) == drawn
