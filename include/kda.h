@@ -435,7 +435,8 @@ size_t kda_paged_attention_workspace_size(int B, int T, int max_tokens, int H, i
  *   target_probs [N + B, V] fp32, target_stride elements between rows (>= V).
  *   draft_probs  [N, V] fp32, draft_stride between rows, or NULL: every draft
  *                was proposed with probability 1 (q_i(x_i) = 1, else 0).
- *   draft_tokens [N] int32.  One outside 0..V-1 is rejected, KDA_DEV_BAD_TOKEN.
+ *   draft_tokens [N] int32.  One outside 0..V-1 is rejected, KDA_DEV_BAD_TOKEN
+ *                (also where a draft before it was rejected).
  *   accept_u     [N] fp32, sample_u [B] fp32, in [0, 1): u and u'.
  *   cu_drafts    [B + 1] int32, cu[0] = 0, cu[B] = N (else KDA_DEV_BAD_SEQLEN; a
  *                request with a bad range is skipped).

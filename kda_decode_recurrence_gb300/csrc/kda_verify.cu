@@ -202,8 +202,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
           const float p = a.target[(row0 + i) * a.target_stride + x];
           const float q = a.draft ? a.draft[(size_t)(d0 + i) * a.draft_stride + x] : 1.f;
           yes = (double)a.accept_u[d0 + i] * (double)q < (double)p;
-        } else if (rank == 0) {
-          raise_status(a.dev_status, KDA_DEV_BAD_TOKEN);
         }
       }
       const unsigned no = __ballot_sync(0xffffffffu, !yes);
@@ -212,8 +210,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
     if (lane == 0) s_taken = taken;
     if (rank == 0) {
       if (lane == 0) a.accepted[b] = taken;
-      for (int i = lane; i <= n; i += 32)
-        if (i != taken) a.tokens[row0 + i] = i < taken ? a.draft_tokens[d0 + i] : -1;
+      for (int i = lane; i <= n; i += 32) {
+        const int x = i < n ? a.draft_tokens[d0 + i] : 0;
+        if (x < 0 || x >= a.V) raise_status(a.dev_status, KDA_DEV_BAD_TOKEN);  // (behind a rejection too)
+        if (i != taken) a.tokens[row0 + i] = i < taken ? x : -1;
+      }
     }
   }
   __syncthreads();

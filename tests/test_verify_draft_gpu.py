@@ -192,3 +192,18 @@ def test_the_sums_hold_on_a_border_of_a_large_vocabulary():
         status = kda.kda_verify_draft(tokens, accepted, weights, None, none.int(), none, half,
                                       torch.zeros(2, dtype=torch.int32, device="cuda"))
         assert int(status) == 0 and int(tokens) == drawn
+
+
+@pytest.mark.parametrize("at", [0, 3, 31, 32, 50, 69])
+@pytest.mark.parametrize("point", [False, True], ids=["probs", "point"])
+def test_a_bad_token_is_reported_wherever_it_stands(at, point):
+    """Also behind a draft that was rejected, however far."""
+    d = draws([70, 2], 50, seed=12, point=point)
+    d["accept_u"][0] = 1.0 - 2.0 ** -24          # draft 0 of request 0: proposed with more than the target has
+    x = int(d["draft_tokens"][0])
+    d["target"][0] = (1.0 - torch.nn.functional.one_hot(torch.tensor(x), 50).float()) / 49
+    for bad in (50, -1, -2 ** 31):
+        d["draft_tokens"][at] = bad
+        tokens, accepted = call(d, status_expected=kda.DEV_BAD_TOKEN)
+        want = verify(*[None if d[k] is None else d[k].numpy() for k in ("target", "draft", "draft_tokens", "accept_u", "sample_u")], d["n"])
+        assert accepted[0] == 0 and np.array_equal(tokens, want[0]) and np.array_equal(accepted, want[1])
