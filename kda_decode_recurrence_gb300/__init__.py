@@ -95,6 +95,8 @@ def _stream_handle(stream) -> int:
 def _stream_of(stream, device) -> int:
     """The handle of the caller's stream, or of the current one of ``device`` (by the raw
     handle: the small calls take less time than building a Stream object)."""
+    if device.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got {device}")
     if stream is not None:
         return int(stream.cuda_stream)
     return torch._C._cuda_getCurrentRawStream(device.index)

@@ -128,3 +128,24 @@ def test_binding_refusals():
                           (dict(target_probs=f(10, 5).t()), ValueError), (dict(accept_u=f(2)), ValueError)]:
         with pytest.raises(error):
             kda.kda_verify_draft(**{**good, **change})
+
+
+def test_host_tensors_are_refused(lib):
+    """Tensors in host memory are refused also where a stream and a status word are given (no
+    address of theirs reaches a kernel)."""
+    class Stream:
+        cuda_stream = 0
+
+    i32 = dict(dtype=torch.int32)
+    k = torch.zeros(9, 2, 64, 128, dtype=torch.bfloat16)
+    x = torch.zeros(5, 2, 128, dtype=torch.bfloat16)
+    cu, lens, table = torch.zeros(3, **i32), torch.zeros(2, **i32), torch.zeros(2, 4, **i32)
+    f, rest = torch.zeros, dict(dev_status=torch.zeros(1, **i32), stream=Stream())
+    with pytest.raises(ValueError):
+        kda.kda_cache_append(k, k, x, x, cu, lens, table, **rest)
+    with pytest.raises(ValueError):
+        kda.kda_cache_read(x, x, k, k, cu, None, table, **rest)
+    with pytest.raises(ValueError):
+        kda.kda_paged_attention(x, x, k, k, cu, lens, table, 3, workspace=f(1 << 25, dtype=torch.uint8), **rest)
+    with pytest.raises(ValueError):
+        kda.kda_verify_draft(f(5, **i32), f(2, **i32), f(5, 10), f(3, 10), f(3, **i32), f(3), f(2), cu, **rest)
