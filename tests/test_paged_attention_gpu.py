@@ -6,7 +6,7 @@ import torch
 
 import kda_decode_recurrence_gb300 as kda
 
-from _paged import Case, attention, cumulative
+from _paged import Case, U_BF16, U_F32, attention, cumulative
 from _parity import Guarded
 
 pytestmark = pytest.mark.gpu
@@ -437,6 +437,54 @@ def test_value_rows_of_different_size(shape, factor):
     check(case, q)
 
 
+def whole_rows(case, name, b):
+    """Case.dense with all positions at once (every page exists)."""
+    x, scale = case.tensors[name]
+    pos = torch.arange(case.lens[b], device=x.device)
+    page, at = case.table[b, pos // case.page].long(), pos % case.page
+    if scale is None:
+        return x[page, :, at].double()
+    return x.view(torch.uint8)[page, :, at].view(x.dtype).float().double() * scale[page, :, at].double()[..., None]
+
+
+def whole_attention(case, q, causal, window):
+    """_paged.attention with all tokens of a request at once."""
+    T, H, D = q.shape
+    G, scale = H // case.HKV, D ** -0.5
+    parts = [[], [], [], []]
+    at = cumulative(case.n)
+    for b in range(case.B):
+        L, n = case.lens[b], case.n[b]
+        k, v = [whole_rows(case, x, b).transpose(0, 1).repeat_interleave(G, 0) for x in "kv"]  # [H, L, D]
+        qq = q[at[b]:at[b + 1]].double().transpose(0, 1)                                     # [H, n, D]
+        x = scale * qq @ k.transpose(1, 2)
+        size = abs(scale) * (qq.abs() @ k.abs().transpose(1, 2))
+        j, p = torch.arange(L, device=q.device)[None], (torch.arange(n, device=q.device) + L - n)[:, None]
+        see = (j <= p) if causal else (j >= 0).expand(n, L)
+        if window:
+            see = see & (j > p - window)
+        x = x.masked_fill(~see, -float("inf"))
+        lse = torch.logsumexp(x, -1)
+        P = torch.exp(x - lse[..., None])
+        off = (D + 4) * U_F32 * size.masked_fill(~see, 0).amax(-1) + x.masked_fill(~see, 0).abs().amax(-1) * 4 * U_F32 + 2.0 ** -21
+        many = see.sum(-1).double()[None]
+        out = P @ v
+        tol = (U_BF16 + 2 * off + many * U_F32)[..., None] * (P @ v.abs()) + U_BF16 * out.abs()
+        ltol = off + many * U_F32 + lse.abs() * 4 * U_F32
+        for to, y in zip(parts, (out, lse, tol, ltol)):
+            to.append(y.transpose(0, 1))
+    return [torch.cat(x) for x in parts]
+
+
+def whole_check(case, q, causal=True, window=0):
+    want, wlse, tol, ltol = whole_attention(case, q, causal, window)
+    out, lse, status = attend(case, q, causal, window)
+    assert status == 0
+    off = (out.double() - want).abs()
+    assert bool((off <= tol).all()), f"off by {float((off / tol.clamp_min(1e-300)).max()):.3g} tolerances"
+    assert bool(((lse.double() - wlse).abs() <= ltol).all())
+
+
 @pytest.mark.parametrize("H,D", [(8, 128), (16, 64)])
 @pytest.mark.parametrize("jump", [2.0 ** 5, 2.0 ** -12, 2.0 ** 60, 2.0 ** -60, 0.0])
 def test_value_sizes_that_change_along_the_sequence(H, D, jump):
@@ -448,7 +496,7 @@ def test_value_sizes_that_change_along_the_sequence(H, D, jump):
         pages = case.table[b, :-(-case.lens[b] // 64)].long()
         scale[pages[(b % 7) + 3:]] *= jump
         scale[pages[(b % 7) + 9:]] *= 2.0 ** 10
-    check(case, q)
+    whole_check(case, q)
 
 
 @pytest.mark.parametrize("amplitude", [1.0, 2.0 ** -60, 2.0 ** 126])
@@ -519,3 +567,28 @@ def test_entries_of_one_query_of_different_size(shape, big):
     codes[..., 3] = 0
     codes[..., 40] = 0x80
     check(case, q)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("G,D", [(24, 128), (32, 64), (43, 128), (64, 128), (65, 64), (100, 128), (128, 128), (128, 64)])
+def test_many_query_heads_per_key_head(G, D, cache):
+    """Items of five tokens down to one, boxes of up to 128 heads."""
+    case, q = make(dict(n=[1, 2, 12], lens=[200, 65, 140], H=G, HKV=1, D=D, page=32), cache=cache, seed=51)
+    check(case, q)
+    case, q = make(dict(n=[1] * 3, lens=[500, 1, 129], H=2 * G, HKV=2, D=D, page=16), cache=cache, seed=52)
+    check(case, q)
+
+
+LONG = [dict(n=[700], lens=[6000], H=8, HKV=2, D=128, page=64), dict(n=[1500, 33, 400], lens=[1500, 9000, 3100], H=4, HKV=2, D=64, page=16),
+        dict(n=[300, 2, 900, 64], lens=[4000, 2500, 900, 64], H=6, HKV=2, D=128, page=128), dict(n=[3001], lens=[3001], H=2, HKV=1, D=128, page=32),
+        dict(n=[20] * 40, lens=[1000 + 70 * i for i in range(40)], H=4, HKV=1, D=128, page=64),
+        dict(n=[1 + i % 8 for i in range(40)], lens=[900 + 131 * i for i in range(40)], H=8, HKV=2, D=64, page=16)]
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 1000), (False, 0), (False, 777)])
+@pytest.mark.parametrize("shape", LONG, ids=lambda s: f"n{max(s['n'])}_L{max(s['lens'])}")
+def test_long_sequences_in_many_pieces(shape, causal, window, cache):
+    """Items that several CTAs share, over thousands of positions."""
+    case, q = make(shape, cache=cache, seed=53)
+    whole_check(case, q, causal, window)

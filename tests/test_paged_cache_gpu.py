@@ -251,3 +251,59 @@ def test_every_malformed_request_is_reported(cache):
             assert np.array_equal(bits(held[name].t), bits(good[name].t))
         starts[1] = bad
         assert int(kda.kda_cache_read(*out, *caches, case.cu, starts, case.table, **scales)) == kda.DEV_BAD_SEQLEN
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T,HKV,D,page", [(38912, 1, 64, 128), (45001, 3, 128, 64), (100003, 2, 64, 16), (170001, 1, 128, 32)])
+def test_many_rows(T, HKV, D, page, cache):
+    """Calls in which a warp takes two tokens and more (from 2 x 152 x 128 on): every row of
+    ragged requests, some with padding, is in its place and reads back."""
+    cut = sorted(np.random.default_rng(T).integers(0, T, 9).tolist())
+    n = np.diff([0] + cut + [T]).tolist()
+    lens = [x + 5 * i for i, x in enumerate(n)]
+    lens[3] = max(0, n[3] - 2)                                  # two tokens of padding
+    need = [-(-x // page) for x in lens]
+    g = torch.Generator(device="cuda").manual_seed(T)
+    pages, width = sum(need) + 1, max(need) + 1
+    order = torch.randperm(pages, device="cuda", generator=g).to(torch.int32)
+    table = torch.full((len(n), width), -1, dtype=torch.int32, device="cuda")
+    for b, at in enumerate(cumulative(need)[:-1]):
+        table[b, :need[b]] = order[at:at + need[b]]
+    x = torch.randn(T, 2, HKV, D, device="cuda", generator=g).to(torch.bfloat16)
+    dtype = torch.bfloat16 if cache == "bf16" else torch.float8_e4m3fn
+    kc, vc = [torch.zeros(pages, HKV, page, D, device="cuda").to(dtype) for _ in range(2)]
+    scales = {} if cache == "bf16" else {s: torch.zeros(pages, HKV, page, device="cuda") for s in ("k_scale", "v_scale")}
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cu, seq = torch.tensor(cumulative(n), **i32), torch.tensor(lens, **i32)
+    assert int(kda.kda_cache_append(kc, vc, x[:, 0], x[:, 1], cu, seq, table, **scales)) == 0
+    b = torch.repeat_interleave(torch.arange(len(n), device="cuda"), torch.tensor(n, device="cuda"))
+    pos = seq.long()[b] - cu.long()[b + 1] + torch.arange(T, device="cuda")
+    real = pos >= 0
+    row = (table[b, pos.clamp_min(0) // page].long() * page + pos.clamp_min(0) % page)[real]   # place among all pages' rows
+    for c, s, y in ((kc, scales.get("k_scale"), x[:, 0]), (vc, scales.get("v_scale"), x[:, 1])):
+        got = c.view(torch.uint8).transpose(1, 2).reshape(pages * page, HKV, -1)
+        y = y[real].contiguous()
+        if s is None:
+            codes = y.view(torch.uint8).reshape(got[row].shape)
+        else:
+            code, scale = quantise(y.float().cpu().numpy())
+            codes = torch.from_numpy(code).cuda()
+            assert torch.equal(s.transpose(1, 2).reshape(pages * page, HKV)[row], torch.from_numpy(scale).cuda())
+        assert torch.equal(got[row], codes)
+        rest = torch.ones(pages * page, dtype=torch.bool, device="cuda")
+        rest[row] = False
+        assert not bool(got[rest].any())
+    out = [torch.full((T, HKV, D), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    starts = torch.tensor([L - m for L, m in zip(lens, n)], **i32)
+    starts[3] = 0                                               # its rows 0 .. lens, then two without a page in use
+    if need[3] * page < n[3]:
+        table[3, need[3]] = table[3, need[3] - 1]
+    assert int(kda.kda_cache_read(*out, kc, vc, cu, starts, table, **scales)) == 0
+    place = torch.arange(T, device="cuda") - cu.long()[b] + starts.long()[b]
+    at = table[b, place // page].long() * page + place % page
+    for c, s, y in ((kc, scales.get("k_scale"), out[0]), (vc, scales.get("v_scale"), out[1])):
+        flat = c.transpose(1, 2).reshape(pages * page, HKV, D)
+        want = flat.view(torch.uint8)[at].view(c.dtype).float() if s is not None else flat[at].float()
+        if s is not None:
+            want = (want * s.transpose(1, 2).reshape(pages * page, HKV)[at][..., None]).to(torch.bfloat16).float()
+        assert torch.equal(y.float(), want)

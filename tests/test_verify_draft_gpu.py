@@ -207,3 +207,10 @@ def test_a_bad_token_is_reported_wherever_it_stands(at, point):
         tokens, accepted = call(d, status_expected=kda.DEV_BAD_TOKEN)
         want = verify(*[None if d[k] is None else d[k].numpy() for k in ("target", "draft", "draft_tokens", "accept_u", "sample_u")], d["n"])
         assert accepted[0] == 0 and np.array_equal(tokens, want[0]) and np.array_equal(accepted, want[1])
+
+
+@pytest.mark.parametrize("B", [304, 305, 400, 608, 609, 800, 1216, 1217, 2000])
+@pytest.mark.parametrize("V", [257, 1024])
+def test_many_requests_of_every_cluster_size(B, V):
+    """Clusters of 8, 4, 2 and 1 CTAs per request, compared exactly."""
+    check(draws([i % 3 for i in range(B)], V, seed=B, point=V == 257), pad=0 if V == 1024 else 3)
