@@ -61,6 +61,7 @@ constexpr int kM = 128;             // rows per row tile
 constexpr int kMmaWarp = 8, kCopyWarp = 10, kWidenWarp = 12;
 constexpr int kSteps = 8;           // steps whose notes and barriers are kept: more than the rings hold
 constexpr float kGrow = 8.f;        // growth of a maximum (log 2) that rescales O
+constexpr float kRounds = 4194304.f;  // maxima past 2^22: half an fp32 step is more than 2^-2
 
 // What the product and the fixing warps need to know of a step (one key tile of
 // one item); the copying warp for K and V writes it before K.
@@ -861,6 +862,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, kPair>::kThreads, 1)
       float m = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       bool begun = false;
+      [[maybe_unused]] bool rounds = false;  // a maximum of the warp's is past kRounds
       // e4m3: the four rows of the fragment layout, 8 k + lane / 4 of the warp's 32
       [[maybe_unused]] float m4[4], l4[4];
       [[maybe_unused]] int lo4[4], hi4[4];
@@ -931,6 +933,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, kPair>::kThreads, 1)
               }
             }
             m = now;
+            rounds = __any_sync(0xffffffffu, fabsf(m) > kRounds && m != -INFINITY);
           }
           begun = true;
         };
@@ -971,9 +974,16 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, kPair>::kThreads, 1)
             for (int q = 0; q < 4; ++q) scored(x[q], 32 * q);
           const float top = fmaxf(max3(highest(x[0]), highest(x[1]), highest(x[2])), highest(x[3]));
           move(plain ? top * c : top);
+          // x = c S is exact in the one product and the maximum rounded, by hundreds where scores
+          // are billions: there both are rounded, so that the largest weight is 1
+          const bool fused = plain && !rounds;
+          if (__builtin_expect(plain && rounds, 0)) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) scored(x[q], 32 * q);
+          }
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            if (plain) weigh(x[q], 32 * q, std::true_type{});
+            if (fused) weigh(x[q], 32 * q, std::true_type{});
             else weigh(x[q], 32 * q, std::false_type{});
             if (q == 1) hand_over(&sm.p_half[t]);
           }

@@ -592,3 +592,16 @@ def test_long_sequences_in_many_pieces(shape, causal, window, cache):
     """Items that several CTAs share, over thousands of positions."""
     case, q = make(shape, cache=cache, seed=53)
     whole_check(case, q, causal, window)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("log2", [28, 31, 33, 36, 60])
+@pytest.mark.parametrize("n,lens,G", KERNELS)
+def test_scores_of_billions(n, lens, G, log2, cache):
+    """Where an fp32 step of a score is hundreds, the largest one's weight is 1 all the same:
+    outputs stay within the values."""
+    case, q = make(dict(n=[n], lens=[lens], H=2 * G, HKV=2, D=128, page=16), cache=cache, seed=54)
+    most = float(max(whole_rows(case, "v", 0).abs().max(), 1))
+    out, lse, status = attend(case, q * 2.0 ** log2)
+    assert status == 0 and bool((out.double().abs() <= most * (1 + 2 * U_BF16)).all())
+    assert bool(torch.isfinite(lse).all())
