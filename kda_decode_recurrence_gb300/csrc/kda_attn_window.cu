@@ -490,11 +490,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
       const int lo_all = seen_lo(p, max(0, pos0));
       const bool v_whole = note.start >= lo_all && note.start + kTile <= note.L;  // all seen by some token
       bool narrow = true;
-      [[maybe_unused]] uint32_t bits = 0;  // of one of the warp's 16 scales of V, each in two lanes
-      if constexpr (kE4m3) {
+      // the bits of one of the warp's 16 scales of V, each in two lanes
+      auto scale_bits = [&]() {
         const int at = my_pos + (lane & 15);
-        bits = __float_as_uint(sm.scales[s][1][at]) & 0x7fffffffu;
-        if (!v_whole && (note.start + at < lo_all || note.start + at >= note.L)) bits = 0;
+        const uint32_t bits = __float_as_uint(sm.scales[s][1][at]) & 0x7fffffffu;
+        return !v_whole && (note.start + at < lo_all || note.start + at >= note.L) ? 0u : bits;
+      };
+      if constexpr (kE4m3) {
+        const uint32_t bits = scale_bits();
         narrow = v_wide | (bits == 0) | (bits - unit < kRoom);
       }
 
@@ -611,6 +614,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, kRows, kE4m3>::kCtas)
       if (!compute_sync_and(ok && narrow)) {
         // (out of the way: a part's first scales, ones that do not fit or are not finite)
         if constexpr (kE4m3) {
+          const uint32_t bits = scale_bits();
           const bool some = bits != 0, finite = bits < 0x7f800000u;
           int4 span;  // largest and smallest exponent; whether one does not fit, is not finite
           span.x = __reduce_max_sync(0xffffffffu, some && finite ? (int)(bits >> 23) : -1);
