@@ -382,10 +382,10 @@ kda_status kda_cache_read(kda_bf16* k_rows, kda_bf16* v_rows, const void* k_cach
  *   out = sum_j e^(x_j - m) v_j / sum_j e^(x_j - m),  m = max_j x_j
  *   lse = ln sum_j e^(x_j)
  * A token that sees nothing gets out = 0, lse = -inf.  Scores, sums and outputs
- * are accumulated in fp32; the weights are rounded for the product with V: to
- * bf16, or (an e4m3 cache, requests with few rows) times v's scale to f16, which is
- * off by 2^-11 of them or 2^-25 of the row's largest.  What
- * a position beyond seq_lens[b] or outside every token's window holds (not a
+ * are accumulated in fp32; the weights (over an e4m3 cache times v's scale) are
+ * rounded for the product with V: to bf16, 2^-8 of each at most, or, for requests
+ * with few rows over an e4m3 cache whose v scales are of one size, to f16, 2^-11 of
+ * each or 2^-25 of the row's largest.  What a position beyond seq_lens[b] or outside every token's window holds (not a
  * number, an infinity) has no influence.
  *
  *   out          [T, H, D] bf16, written.  Alignment 16 B.

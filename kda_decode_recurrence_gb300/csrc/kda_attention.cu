@@ -112,8 +112,9 @@ size_t attention_workspace_bytes(int B, int T, int max_tokens, int H, int HKV, i
 }
 
 // Rows up to which a request is the window kernel's (none: 0).  Measured with 32 requests
-// over 200 .. 6000 positions, 8 key heads of 128, window kernel against chunk kernel: e4m3 32
-// rows 89 us against 116, 64 rows 206 against 158; bf16 20 rows 99 against 85, 32 rows 118
+// over 200 .. 6000 positions, 8 key heads of 128, window kernel against chunk kernel: e4m3 (from
+// a cold L2) 20 rows 110 us against 138, 32 rows 114 against 140, 1 to 8 tokens of 4 heads 106
+// against 139; with a warm one 64 rows 206 against 158; bf16 20 rows 99 against 85, 32 rows 118
 // against 87.  bf16 windows that differ, the chunk kernel for all against the window kernel
 // for the short ones: 1 to 8 tokens of 4 heads 86 us against 95, 1 to 16 85 against 112 (128
 // requests of up to 16000 positions 664 against 689), 1 to 8 of 8 heads of 64 55 against 73.

@@ -11,7 +11,7 @@
 // head dimension:
 //   S[rows, 16 w .. 16 w + 15] = Q K^T        warp w's 16 positions
 //   the rows' maxima are exchanged through shared memory, P = 2^(S - m) goes
-//   there as bf16
+//   there in V's type (the instruction takes one for both), bf16 here
 //   O[rows, D/4 w ..] = O 2^(m_old - m) + P V  warp w's quarter of D
 // so that each entry of K and V is read from shared memory (and, for e4m3,
 // widened) once, and no warp's output has to be joined with another's.
@@ -32,13 +32,14 @@
 // size, where tcgen05 would spend 128 lanes on them.
 //
 // 128 single tokens over 5.05 GB of bf16 cache: 713 us, 7.07 TB/s (a copy: 6.70).
-// 64 over 628 MB of e4m3: 147 us, 4.27 TB/s (of which the look at V's scales 3 and the bf16
-// form beside the f16 one 3; two CTAs an SM and bf16 operands throughout: 178 us).
-// With more rows a warp reads as many
-// operands of Q and P as of K and V: 32 rows are for e4m3 only (89 us
-// against the chunk kernel's 116 for 32 such requests).  Eight warps that split D by eight:
-// 165 us and 755 us on these two; streams of 32 positions per warp that exchange nothing until
-// an item's end, one CTA an SM: 265 us and 1320 us.
+// 64 over 628 MB of e4m3: 146 us, 4.30 TB/s (142 without the look at V's scales; two CTAs an SM
+// and bf16 operands throughout: 178).  Its schedulers issue in 49% of the cycles, with three
+// computing warps each, and DRAM is at 55%: what bounds it are the tile's dependent steps (per
+// instruction 2.0 cycles of fixed latencies, 1.7 of loads, 0.6 at barriers, of 7.4).
+// With more rows a warp reads as many operands of Q and P as of K and V: 32 rows are for e4m3
+// only (32 such requests, cold L2: 114 us against the chunk kernel's 140).  Eight warps that
+// split D by eight: 165 us and 755 us on these two; streams of 32 positions per warp that
+// exchange nothing until an item's end, one CTA an SM: 265 us and 1320 us.
 #include <cuda.h>
 #include <cuda_fp16.h>
 

@@ -23,9 +23,12 @@
 // once: a second wave would find few CTAs left to keep HBM busy.
 //
 // 256 requests of 1 .. 7 drafts over 131072 tokens: 268 MB in 56 us, 4.8 TB/s (a copy:
-// 6.7): the pair sums take 13 operations an entry, and a cluster's last warp is waited
-// for twice.  Four over 32001: 12.5 us with the host's call.  800 over 131072, runs of 32
-// entries: 247 us (one pair for all 128 of a lane: 234).
+// 6.7); point drafts 134 MB in 47.  Loads are waited for (8.7 of 16 cycles per instruction),
+// barriers 2.5, issue is at 42% and the SMs are busy for 80% of the time: the chain before a
+// request's first row (offsets, drafted token, two probabilities) and the cluster's two
+// barriers after its last have nothing beside them, all requests being in one wave.
+// Four over 32001: 12.5 us with the host's call.  800 over 131072, four runs of 32 entries per
+// lane: 247 us (one pair for all 128: 234).
 #include <cooperative_groups.h>
 
 #include <type_traits>
