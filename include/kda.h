@@ -385,8 +385,8 @@ kda_status kda_cache_read(kda_bf16* k_rows, kda_bf16* v_rows, const void* k_cach
  * are accumulated in fp32; the weights (over an e4m3 cache times v's scale) are
  * rounded for the product with V: to bf16, 2^-8 of each at most, or, for requests
  * with few rows over an e4m3 cache whose v scales are of one size, to f16, 2^-11 of
- * each or 2^-25 of the row's largest.  What a position beyond seq_lens[b] or outside every token's window holds (not a
- * number, an infinity) has no influence.
+ * each or 2^-25 of the row's largest.  What a position beyond seq_lens[b] or
+ * outside every token's window holds (not a number, an infinity) has no influence.
  *
  *   out          [T, H, D] bf16, written.  Alignment 16 B.
  *   lse          [T, H] fp32, written, or NULL.
