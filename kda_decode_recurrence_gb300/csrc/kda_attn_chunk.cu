@@ -28,9 +28,9 @@
 // Items' key tiles are divided evenly over the CTAs, an item's ends counted as some.
 //
 // 2048 new tokens over 28001 cached, 32 / 8 heads, D = 128, bf16: 638 us alone, 1.53 PFLOP/s,
-// 706 among other calls, 1.38 (a cuBLAS product: 1.89), the tensor cores busy for two thirds; a softmax task is a
-// chain of some 3000 cycles beside the 1280 of its products, and two of them overlap.  Four
-// prompts of 1500 .. 6001 from an e4m3 cache: 727 us, 0.68 PFLOP/s: the scales are a
+// 706 among other calls, 1.38 (a cuBLAS product: 1.89), the tensor cores busy for two thirds;
+// a softmax task is a chain of some 3000 cycles beside the 1280 of its products, and two of
+// them overlap.  Four prompts of 1500 .. 6001 from an e4m3 cache: 727 us, 0.68 PFLOP/s: the scales are a
 // product and the widening five operations per pair, and the schedulers issue in 54% of their cycles.
 // (e4m3 operands widened to f16 as in the window kernel: 1149 us against 818 then, the
 // conversions run where the exponentials do.  Codes taken to registers one part ahead:
