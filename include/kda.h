@@ -16,6 +16,9 @@
  *   kda_cache_append, kda_cache_read  K and V rows into a paged cache (bf16 or
  *                  e4m3 with one scale per row) and back
  *   kda_paged_attention  new tokens (one, a drafted window, a chunk) over it
+ *   kda_tree_attention  a tree of drafted tokens over it
+ *   kda_latent_append, kda_latent_attention, kda_latent_expanded  the same for layers whose heads
+ *                share one latent row a token
  *   kda_verify_draft  drafted tokens against the target's probabilities, from
  *                  given uniform numbers
  *
@@ -414,6 +417,104 @@ kda_status kda_paged_attention(kda_bf16* out, float* lse, const kda_bf16* q, con
  * sizes are invalid); it does not decrease in B, T or max_tokens.  Host-only, no
  * CUDA call. */
 size_t kda_paged_attention_workspace_size(int B, int T, int max_tokens, int H, int HKV, int D);
+
+/*
+ * kda_tree_attention -- kda_paged_attention for a tree of drafted tokens: the new tokens of a
+ * request are a tree's nodes, each at the position after its row in the cache (append them first),
+ * and a node sees
+ *   every position 0 .. seq_lens[b] - n_b - 1 before the tree, and
+ *   position seq_lens[b] - n_b + a for each new token a whose bit is set in its mask
+ * (itself among them, if it is to see itself).  A node at a negative position is padding, and
+ * sees nothing.  Everything else is as in kda_paged_attention without a window.
+ *
+ *   tree_mask    [T, mask_words] int32: bit i of word w of token t stands for new token 32 w + i
+ *                of t's request; bits past the request's last token are ignored.
+ *   max_tokens   at most 32 * mask_words.
+ *   workspace    kda_tree_attention_workspace_size(...) bytes, 256-byte aligned.
+ */
+kda_status kda_tree_attention(kda_bf16* out, float* lse, const kda_bf16* q, const void* k_cache,
+                              const void* v_cache, const float* k_scale, const float* v_scale,
+                              const int32_t* cu_seqlens, const int32_t* seq_lens,
+                              const int32_t* page_table, const int32_t* tree_mask, float scale,
+                              int cache_dtype, int B, int T, int max_tokens, int mask_words, int H,
+                              int HKV, int D, int page_size, int num_pages, int max_pages,
+                              long long q_stride, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_status, void* stream);
+
+/* Bytes of device workspace kda_tree_attention needs for these sizes (0 when the sizes are
+ * invalid).  Host-only, no CUDA call. */
+size_t kda_tree_attention_workspace_size(int B, int T, int max_tokens, int H, int HKV, int D);
+
+/* ------------------------------------------------------------------------
+ * Latent attention: keys and values of all heads from one latent row a token.
+ *
+ * A latent row has 576 bf16 entries: 512 that are key and value at once, then 64 that tell the
+ * position and belong to the key only.  A latent cache is [num_pages, page_size, 576] bf16,
+ * aligned to 16 B; page_table, cu_seqlens, seq_lens, page_size, positions and padding are as in
+ * the K/V cache above, and so are the status bits.
+ *
+ * With a head's up-projections W_k [128, 512] and W_v [128, 512], key (W_k c, p) and value W_v c:
+ *   absorbed form (kda_latent_attention): the query is (W_k^T q_nope, q_rope), 512 + 64, and the
+ *     output sum P c, 512, which the caller projects by W_v; the cache is read as it is.  For
+ *     single tokens, drafted windows and trees.
+ *   expanded form (kda_latent_expanded): keys and values are expanded first (a matrix product of
+ *     the rows with all heads' W_k and W_v), 3.4 times fewer operations per pair.  For prompts.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * kda_latent_append -- write the new tokens' latent rows into the cache.
+ *
+ * With gamma: c' = c (mean(c^2) + eps)^-1/2 gamma over the row's first 512 entries, in fp32, rounded
+ * to bf16; the last 64 are copied.  Without: rows are copied.
+ *
+ *   cache        [num_pages, page_size, 576], written.
+ *   rows         [T, 576] bf16, row_stride elements between tokens (a multiple of 8, at least
+ *                576: a view of a fused projection's output needs no copy).  Alignment 16 B.
+ *   gamma        [512] fp32, alignment 16 B, or NULL.      eps  finite, >= 0.
+ *   seq_lens     the lengths WITH the new tokens.
+ * Rows of the cache that no new token names are left as they are.  Two tokens of one call must
+ * not name the same page row.
+ */
+kda_status kda_latent_append(kda_bf16* cache, const kda_bf16* rows, const float* gamma, float eps,
+                             const int32_t* cu_seqlens, const int32_t* seq_lens,
+                             const int32_t* page_table, int B, int T, int page_size, int num_pages,
+                             int max_pages, long long row_stride, int32_t* dev_status, void* stream);
+
+/*
+ * kda_latent_attention -- softmax attention of the new tokens over the latent cache (absorbed
+ * form); every head reads the same rows.  The new tokens' own rows are read from it too.
+ *
+ * For token i of request b at position p = seq_lens[b] - n_b + i >= 0, head h, cached rows
+ * r_j = (c_j, p_j):
+ *   x_j = scale q . r_j  for the positions j it sees: 0 <= j < seq_lens[b], and j <= p if causal;
+ *         with tree_mask those of kda_tree_attention instead
+ *   out = sum_j e^(x_j - m) c_j / sum_j e^(x_j - m),  m = max_j x_j;   lse = ln sum_j e^(x_j)
+ * A token that sees nothing gets out = 0, lse = -inf.  Scores, sums and outputs are accumulated in
+ * fp32; the weights are rounded to bf16 for the product with c, 2^-8 of each at most.  What a row
+ * holds that a token does not see (not a number, an infinity) has no influence on it; rows that it
+ * sees must be finite (one with a NaN makes its output NaN).
+ *
+ *   out          [T, H, 512] bf16, written.  Alignment 16 B.
+ *   lse          [T, H] fp32, written, or NULL.
+ *   q            [T, H, 576] bf16, q_stride elements between tokens (a multiple of 8, at least
+ *                H * 576).  Alignment 16 B.
+ *   tree_mask    [T, mask_words] int32 as in kda_tree_attention, or NULL; a request with more
+ *                than 32 * mask_words new tokens is skipped with KDA_DEV_BAD_SEQLEN.
+ *   scale        finite.       causal  0 or 1, without tree_mask.
+ *   workspace    device scratch of kda_latent_attention_workspace_size(...) bytes, 256-byte aligned,
+ *                contents need not be initialised.
+ * The rows of a skipped request are not written.
+ */
+kda_status kda_latent_attention(kda_bf16* out, float* lse, const kda_bf16* q, const kda_bf16* cache,
+                                const int32_t* cu_seqlens, const int32_t* seq_lens,
+                                const int32_t* page_table, const int32_t* tree_mask, float scale,
+                                int causal, int B, int T, int H, int mask_words, int page_size,
+                                int num_pages, int max_pages, long long q_stride, void* workspace,
+                                size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* Bytes of device workspace kda_latent_attention needs for these sizes (0 when the sizes are
+ * invalid).  Host-only, no CUDA call. */
+size_t kda_latent_attention_workspace_size(int B, int T, int H);
 
 /*
  * kda_verify_draft -- accept a prefix of each request's drafted tokens and draw

@@ -426,6 +426,169 @@ def kda_paged_attention(out, q, k_cache, v_cache, cu_seqlens, seq_lens, page_tab
     return _finish(rc, status, "kda_paged_attention", check, check_device, stream)
 
 
+def _check_current(device) -> None:
+    """The calls run on the current device: its kernels cannot take another's tensors."""
+    if device.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got {device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}, but the current device is {torch.cuda.current_device()}")
+
+
+def _check_outputs(out, lse, T, H, D, device) -> None:
+    _check(out, "out", torch.bfloat16, device)
+    if out.shape != (T, H, D):
+        raise ValueError(f"out shape {tuple(out.shape)} != {(T, H, D)}")
+    if lse is not None:
+        _check(lse, "lse", torch.float32, device)
+        if lse.shape != (T, H):
+            raise ValueError(f"lse shape {tuple(lse.shape)} != [{T}, {H}]")
+
+
+def _workspace(workspace, need, device, stream):
+    """The caller's workspace, or a new one on the call's stream."""
+    if workspace is not None:
+        _check(workspace, "workspace", torch.uint8, device)
+        return workspace
+    with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+
+
+def _check_mask(mask, T, device) -> int:
+    """A tree's mask [T, words]; returns its words per token."""
+    _check(mask, "tree_mask", torch.int32, device)
+    if mask.dim() != 2 or mask.shape[0] != T or mask.shape[1] < 1:
+        raise ValueError(f"tree_mask shape {tuple(mask.shape)} != [{T}, words]")
+    return mask.shape[1]
+
+
+def _check_lens(seq_lens, B, device) -> None:
+    _check(seq_lens, "seq_lens", torch.int32, device)
+    if seq_lens.numel() != B:
+        raise ValueError("seq_lens must have B entries")
+
+
+def tree_attention_workspace_size(B, T, max_tokens, H, HKV, D) -> int:
+    return int(_lib.load().kda_tree_attention_workspace_size(B, T, max_tokens, H, HKV, D))
+
+
+def kda_tree_attention(out, q, k_cache, v_cache, cu_seqlens, seq_lens, page_table, tree_mask,
+                       max_tokens, scale=None, k_scale=None, v_scale=None, lse=None,
+                       workspace=None, dev_status=None, stream=None, check=True,
+                       check_device=False) -> torch.Tensor:
+    """kda_paged_attention of a tree of drafted tokens (see include/kda.h): a request's new
+    tokens see all that was cached before them, and of each other those whose bits their masks set.
+
+    ``tree_mask`` [T, words] int32: bit i of word w of a token stands for new token
+    32 w + i of its request; ``max_tokens`` is at most 32 words.  The other arguments are
+    kda_paged_attention's, the workspace is of tree_attention_workspace_size(...) bytes.
+    """
+    dev = k_cache.device
+    dtype, B, HKV, D, page, N, max_pages = _check_cache(k_cache, v_cache, k_scale, v_scale,
+                                                        page_table, cu_seqlens, "cu_seqlens")
+    if q.dim() != 3:
+        raise ValueError(f"q shape {tuple(q.shape)} != [T, H, {D}]")
+    T, H = q.shape[0], q.shape[1]
+    qs = _check_rows(q, "q", H, D, dev)
+    _check_outputs(out, lse, T, H, D, dev)
+    _check_lens(seq_lens, B, dev)
+    words = _check_mask(tree_mask, T, dev)
+    _check_current(dev)
+    workspace = _workspace(workspace, tree_attention_workspace_size(B, T, max_tokens, H, HKV, D), dev, stream)
+    status = _status_word(dev_status, dev, stream)
+    rc = _lib.load().kda_tree_attention(
+        out.data_ptr(), _ptr(lse), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        _ptr(k_scale), _ptr(v_scale), cu_seqlens.data_ptr(), seq_lens.data_ptr(),
+        page_table.data_ptr(), tree_mask.data_ptr(), float(D ** -0.5 if scale is None else scale),
+        dtype, B, T, int(max_tokens), words, H, HKV, D, page, N, max_pages, qs,
+        workspace.data_ptr(), workspace.numel(), status.data_ptr(), _stream_of(stream, dev))
+    return _finish(rc, status, "kda_tree_attention", check, check_device, stream)
+
+
+LATENT, LATENT_ROPE = 512, 64        # a latent row: entries that are key and value, then the position's
+LATENT_ROW = LATENT + LATENT_ROPE
+EXPANDED = 128                       # an expanded head's own key entries, and its values
+_LATENT_SCALE = (EXPANDED + LATENT_ROPE) ** -0.5
+
+
+def _check_latent(cache, page_table, cu, what):
+    """The tensors of a call on a latent cache; returns (B, page_size, num_pages, max_pages)."""
+    dev, shape = cache.device, cache.shape
+    _check(cache, "cache", torch.bfloat16, dev)
+    if len(shape) != 3 or shape[2] != LATENT_ROW:
+        raise ValueError(f"cache shape {tuple(shape)} != [num_pages, page_size, {LATENT_ROW}]")
+    _check(page_table, "page_table", torch.int32, dev)
+    _check(cu, what, torch.int32, dev)
+    table = page_table.shape
+    if len(table) != 2 or cu.numel() != table[0] + 1:
+        raise ValueError(f"page_table must be [B, max_pages] and {what} have B + 1 entries")
+    return table[0], shape[1], shape[0], table[1]
+
+
+def kda_latent_append(cache, rows, cu_seqlens, seq_lens, page_table, gamma=None, eps=1e-5,
+                      dev_status=None, stream=None, check=True, check_device=False) -> torch.Tensor:
+    """Write the new tokens' latent rows into a paged latent cache (see include/kda.h).
+
+    Shapes: cache [num_pages, page_size, 576] bf16; rows [T, 576] bf16, tokens may be
+    strided; gamma [512] fp32 (the rows' first 512 entries are RMS-normed with it and
+    ``eps``) or None; cu_seqlens, seq_lens and page_table as kda_cache_append.
+    """
+    dev = cache.device
+    B, page, N, max_pages = _check_latent(cache, page_table, cu_seqlens, "cu_seqlens")
+    if rows.dim() != 2:
+        raise ValueError(f"rows shape {tuple(rows.shape)} != [T, {LATENT_ROW}]")
+    stride = _check_rows(rows.unsqueeze(1), "rows", 1, LATENT_ROW, dev)
+    _check_lens(seq_lens, B, dev)
+    if gamma is not None:
+        _check(gamma, "gamma", torch.float32, dev)
+        if gamma.shape != (LATENT,):
+            raise ValueError(f"gamma shape {tuple(gamma.shape)} != [{LATENT}]")
+    _check_current(dev)
+    status = _status_word(dev_status, dev, stream)
+    rc = _lib.load().kda_latent_append(
+        cache.data_ptr(), rows.data_ptr(), _ptr(gamma), float(eps), cu_seqlens.data_ptr(),
+        seq_lens.data_ptr(), page_table.data_ptr(), B, rows.shape[0], page, N, max_pages, stride,
+        status.data_ptr(), _stream_of(stream, dev))
+    return _finish(rc, status, "kda_latent_append", check, check_device, stream)
+
+
+def latent_attention_workspace_size(B, T, H) -> int:
+    return int(_lib.load().kda_latent_attention_workspace_size(B, T, H))
+
+
+def kda_latent_attention(out, q, cache, cu_seqlens, seq_lens, page_table, scale=None, causal=True,
+                         tree_mask=None, lse=None, workspace=None, dev_status=None, stream=None,
+                         check=True, check_device=False) -> torch.Tensor:
+    """Softmax attention of the new tokens over a paged latent cache that holds their own
+    rows too, in the absorbed form: every head reads the same rows (see include/kda.h).
+
+    Shapes: out [T, H, 512] bf16; q [T, H, 576] bf16, tokens may be strided; cache,
+    cu_seqlens, seq_lens and page_table as kda_latent_append; lse [T, H] fp32 or None.
+    With ``tree_mask`` (as in kda_tree_attention) the new tokens are trees, and ``causal`` is not
+    looked at.  ``scale`` defaults to 192 ** -0.5 (the heads' 128 + 64 key entries before
+    absorption).  ``workspace`` is a uint8 CUDA tensor of at least
+    latent_attention_workspace_size(...) bytes; when None one is allocated here.
+    """
+    dev = cache.device
+    B, page, N, max_pages = _check_latent(cache, page_table, cu_seqlens, "cu_seqlens")
+    if q.dim() != 3:
+        raise ValueError(f"q shape {tuple(q.shape)} != [T, H, {LATENT_ROW}]")
+    T, H = q.shape[0], q.shape[1]
+    qs = _check_rows(q, "q", H, LATENT_ROW, dev)
+    _check_outputs(out, lse, T, H, LATENT, dev)
+    _check_lens(seq_lens, B, dev)
+    words = _check_mask(tree_mask, T, dev) if tree_mask is not None else 0
+    _check_current(dev)
+    workspace = _workspace(workspace, latent_attention_workspace_size(B, T, H), dev, stream)
+    status = _status_word(dev_status, dev, stream)
+    rc = _lib.load().kda_latent_attention(
+        out.data_ptr(), _ptr(lse), q.data_ptr(), cache.data_ptr(), cu_seqlens.data_ptr(),
+        seq_lens.data_ptr(), page_table.data_ptr(), _ptr(tree_mask),
+        float(_LATENT_SCALE if scale is None else scale), int(causal), B, T, H, words, page, N,
+        max_pages, qs, workspace.data_ptr(), workspace.numel(), status.data_ptr(),
+        _stream_of(stream, dev))
+    return _finish(rc, status, "kda_latent_attention", check, check_device, stream)
+
+
 def kda_verify_draft(tokens, accepted, target_probs, draft_probs, draft_tokens, accept_u, sample_u,
                      cu_drafts, dev_status=None, stream=None, check=True,
                      check_device=False) -> torch.Tensor:

@@ -5,6 +5,7 @@
 
 #include "kda.h"
 #include "kda_internal.h"
+#include "kda_latent.h"
 #include "kda_paged.h"
 
 namespace {
@@ -240,6 +241,54 @@ kda_status check_cache(kda::PagedCache& c, const void* k, const void* v, const f
   return KDA_OK;
 }
 
+// The other tensors of an attention call on a paged cache, once the sizes are found right; fills `a`
+// when it returns KDA_OK.
+kda_status attention_tensors(kda::AttentionArgs& a, kda_bf16* out, float* lse, const kda_bf16* q,
+                             const int32_t* cu_seqlens, const int32_t* seq_lens, float scale, int B,
+                             int T, int max_tokens, int H, long long q_stride, void* workspace,
+                             size_t workspace_bytes, size_t need, int32_t* dev_status) {
+  if (!out || !q || !cu_seqlens || !seq_lens) return KDA_ERR_NULL;
+  if (!aligned(out, 16) || !aligned(q, 16) || q_stride % 8 != 0 || !aligned(lse, 4) ||
+      !aligned(cu_seqlens, 4) || !aligned(seq_lens, 4))
+    return KDA_ERR_ALIGN;
+  if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return KDA_ERR_ALIGN;
+  a.out = out;
+  a.lse = lse;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.cu = cu_seqlens;
+  a.lens = seq_lens;
+  a.scale = scale;
+  a.B = B;
+  a.T = T;
+  a.max_tokens = max_tokens;
+  a.H = H;
+  a.G = H / a.c.HKV;
+  a.workspace = workspace;
+  a.dev_status = dev_status;
+  return KDA_OK;
+}
+
+// What the calls on a latent cache check first; fills `c` when it returns KDA_OK.
+kda_status check_latent_cache(kda::LatentCache& c, const kda_bf16* cache, const int32_t* page_table,
+                              int B, int T, int page_size, int num_pages, int max_pages) {
+  if (B < 0 || T < 0 || page_size < 1 || num_pages < 1 || max_pages < 1) return KDA_ERR_SHAPE;
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return KDA_ERR_UNSUPPORTED;
+  // Positions are 32-bit, and so are row numbers of the cache (a copy's coordinate).
+  if ((long long)max_pages * page_size > 0x40000000LL || (long long)num_pages * page_size > 0x7fffffffLL - 128)
+    return KDA_ERR_UNSUPPORTED;
+  if (B == 0 || T == 0) return KDA_OK;
+  if (!cache || !page_table) return KDA_ERR_NULL;
+  if (!aligned(cache, 16) || !aligned(page_table, 4)) return KDA_ERR_ALIGN;
+  c.rows = const_cast<kda_bf16*>(cache);
+  c.page_table = page_table;
+  c.page_size = page_size;
+  c.num_pages = num_pages;
+  c.max_pages = max_pages;
+  return KDA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -318,12 +367,96 @@ kda_status kda_paged_attention(kda_bf16* out, float* lse, const kda_bf16* q, con
   if (H / HKV > 128 || (long long)T * H > 0x3fffffffLL) return KDA_ERR_UNSUPPORTED;
   if (!std::isfinite(scale) || window < 0 || (causal != 0 && causal != 1)) return KDA_ERR_VALUE;
   if (B == 0 || T == 0) return KDA_OK;
+  const kda_status tensors = attention_tensors(
+      a, out, lse, q, cu_seqlens, seq_lens, scale, B, T, max_tokens, H, q_stride, workspace,
+      workspace_bytes, kda::attention_workspace_bytes(B, T, max_tokens, H, HKV, D), dev_status);
+  if (tensors != KDA_OK) return tensors;
+  a.causal = causal;
+  a.window = window < 0x40000000 ? window : 0x40000000;  // longer than any sequence
+  return kda::launch_paged_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? KDA_OK : KDA_ERR_CUDA;
+}
+
+size_t kda_tree_attention_workspace_size(int B, int T, int max_tokens, int H, int HKV, int D) {
+  return kda::tree_workspace_bytes(B, T, max_tokens, H, HKV, D);
+}
+
+kda_status kda_tree_attention(kda_bf16* out, float* lse, const kda_bf16* q, const void* k_cache,
+                              const void* v_cache, const float* k_scale, const float* v_scale,
+                              const int32_t* cu_seqlens, const int32_t* seq_lens,
+                              const int32_t* page_table, const int32_t* tree_mask, float scale,
+                              int cache_dtype, int B, int T, int max_tokens, int mask_words, int H,
+                              int HKV, int D, int page_size, int num_pages, int max_pages,
+                              long long q_stride, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_status, void* stream) {
+  kda::AttentionArgs a = {};
+  const kda_status st = check_cache(a.c, k_cache, v_cache, k_scale, v_scale, page_table,
+                                    cache_dtype, B, T, HKV, D, page_size, num_pages, max_pages);
+  if (st != KDA_OK) return st;
+  if (H < 1 || H % HKV != 0 || max_tokens < 0 || mask_words < 1 || mask_words > 0x1000000 ||
+      max_tokens > 32 * mask_words || q_stride < (long long)H * D)
+    return KDA_ERR_SHAPE;
+  if (H / HKV > 128 || (long long)T * H > 0x3fffffffLL) return KDA_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale)) return KDA_ERR_VALUE;
+  if (B == 0 || T == 0) return KDA_OK;
+  if (!tree_mask) return KDA_ERR_NULL;
+  if (!aligned(tree_mask, 4)) return KDA_ERR_ALIGN;
+  const kda_status tensors = attention_tensors(
+      a, out, lse, q, cu_seqlens, seq_lens, scale, B, T, max_tokens, H, q_stride, workspace,
+      workspace_bytes, kda::tree_workspace_bytes(B, T, max_tokens, H, HKV, D), dev_status);
+  if (tensors != KDA_OK) return tensors;
+  a.tree = tree_mask;
+  a.tree_words = mask_words;
+  return kda::launch_tree_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_latent_append(kda_bf16* cache, const kda_bf16* rows, const float* gamma, float eps,
+                             const int32_t* cu_seqlens, const int32_t* seq_lens,
+                             const int32_t* page_table, int B, int T, int page_size, int num_pages,
+                             int max_pages, long long row_stride, int32_t* dev_status, void* stream) {
+  kda::LatentAppendArgs a = {};
+  const kda_status st = check_latent_cache(a.c, cache, page_table, B, T, page_size, num_pages, max_pages);
+  if (st != KDA_OK) return st;
+  if (row_stride < kda::kLatentRow) return KDA_ERR_SHAPE;
+  if (!std::isfinite(eps) || eps < 0.f) return KDA_ERR_VALUE;
+  if (B == 0 || T == 0) return KDA_OK;
+  if (!rows || !cu_seqlens || !seq_lens) return KDA_ERR_NULL;
+  if (!aligned(rows, 16) || row_stride % 8 != 0 || !aligned(gamma, 16) || !aligned(cu_seqlens, 4) ||
+      !aligned(seq_lens, 4))
+    return KDA_ERR_ALIGN;
+  a.rows = rows;
+  a.stride = row_stride;
+  a.gamma = gamma;
+  a.eps = eps;
+  a.cu = cu_seqlens;
+  a.lens = seq_lens;
+  a.B = B;
+  a.T = T;
+  a.dev_status = dev_status;
+  return kda::launch_latent_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+size_t kda_latent_attention_workspace_size(int B, int T, int H) { return kda::latent_workspace_bytes(B, T, H); }
+
+kda_status kda_latent_attention(kda_bf16* out, float* lse, const kda_bf16* q, const kda_bf16* cache,
+                                const int32_t* cu_seqlens, const int32_t* seq_lens,
+                                const int32_t* page_table, const int32_t* tree_mask, float scale,
+                                int causal, int B, int T, int H, int mask_words, int page_size,
+                                int num_pages, int max_pages, long long q_stride, void* workspace,
+                                size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  kda::LatentArgs a = {};
+  const kda_status st = check_latent_cache(a.c, cache, page_table, B, T, page_size, num_pages, max_pages);
+  if (st != KDA_OK) return st;
+  if (H < 1 || q_stride < (long long)H * kda::kLatentRow || (tree_mask && mask_words < 1)) return KDA_ERR_SHAPE;
+  if ((long long)T * H > 0x3fffffffLL || (tree_mask && mask_words > 0x1000000)) return KDA_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale) || (causal != 0 && causal != 1)) return KDA_ERR_VALUE;
+  if (B == 0 || T == 0) return KDA_OK;
   if (!out || !q || !cu_seqlens || !seq_lens) return KDA_ERR_NULL;
   if (!aligned(out, 16) || !aligned(q, 16) || q_stride % 8 != 0 || !aligned(lse, 4) ||
-      !aligned(cu_seqlens, 4) || !aligned(seq_lens, 4))
+      !aligned(cu_seqlens, 4) || !aligned(seq_lens, 4) || !aligned(tree_mask, 4))
     return KDA_ERR_ALIGN;
-  if (!workspace || workspace_bytes < kda::attention_workspace_bytes(B, T, max_tokens, H, HKV, D))
-    return KDA_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < kda::latent_workspace_bytes(B, T, H)) return KDA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return KDA_ERR_ALIGN;
   a.out = out;
   a.lse = lse;
@@ -331,18 +464,16 @@ kda_status kda_paged_attention(kda_bf16* out, float* lse, const kda_bf16* q, con
   a.q_stride = q_stride;
   a.cu = cu_seqlens;
   a.lens = seq_lens;
+  a.mask = tree_mask;
+  a.mask_words = mask_words;
   a.scale = scale;
-  a.causal = causal;
-  a.window = window < 0x40000000 ? window : 0x40000000;  // longer than any sequence
+  a.causal = tree_mask ? 0 : causal;
   a.B = B;
   a.T = T;
-  a.max_tokens = max_tokens;
   a.H = H;
-  a.G = H / HKV;
   a.workspace = workspace;
   a.dev_status = dev_status;
-  return kda::launch_paged_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? KDA_OK : KDA_ERR_CUDA;
+  return kda::launch_latent_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 kda_status kda_verify_draft(int32_t* tokens, int32_t* accepted, const float* target_probs,

@@ -119,6 +119,72 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// The bits of columns lo .. hi - 1 among columns 0 .. 31.
+__device__ __forceinline__ uint32_t below(int k) { return k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u; }
+__device__ __forceinline__ uint32_t columns(int lo, int hi) { return below(hi) & ~below(lo); }
+
+// Drafted trees: which of 32 positions a new token sees, the first being a positions behind the
+// cached ones (a < 0: before their end).  words: the token's mask, bit i of word w for new token
+// 32 w + i of its request, which has n (at most 32 mask_words).
+__device__ __forceinline__ uint32_t tree_bits(const int32_t* words, int mask_words, int n, int a) {
+  const int w = a >> 5;
+  const uint32_t lo = w < 0 ? 0xffffffffu : w < mask_words ? (uint32_t)words[w] : 0u;
+  const uint32_t hi = w + 1 < 0 ? 0xffffffffu : w + 1 < mask_words ? (uint32_t)words[w + 1] : 0u;
+  return __funnelshift_r(lo, hi, a & 31) & below(n - a);
+}
+
+// Lanes 4 i .. 4 i + 3: x[e] of lane j becomes x[j] of lane e.
+__device__ __forceinline__ void transpose4(uint4 (&x)[4], int lane) {
+#pragma unroll
+  for (int bit = 1; bit < 4; bit *= 2) {
+    const bool up = (lane & bit) != 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & bit) continue;
+      uint4& lo = x[i];
+      uint4& hi = x[i + bit];
+      uint4 y = up ? lo : hi;
+      y.x = __shfl_xor_sync(0xffffffffu, y.x, bit);
+      y.y = __shfl_xor_sync(0xffffffffu, y.y, bit);
+      y.z = __shfl_xor_sync(0xffffffffu, y.z, bit);
+      y.w = __shfl_xor_sync(0xffffffffu, y.w, bit);
+      if (up) lo = y;
+      else hi = y;
+    }
+  }
+}
+
+// A wait of a whole warp; what follows when the phase is not there at once is out of
+// line, so that the product warps' waits take little room in the instruction cache.
+static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity) {
+  const unsigned long long t0 = global_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, global_ns() - t0 > kWaitLimitNs)) return false;
+  }
+}
+__device__ __forceinline__ bool wait_together(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_try(bar, parity)) || wait_on(bar, parity);
+}
+
+// A role's share of the registers that the block was launched with.
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 // Sum of x over the CTA's threads before this one, and over all; kWarps warps, `part`
 // in shared memory (one entry a warp).
 template <int kWarps>

@@ -1,0 +1,768 @@
+// kda_attn_latent.cu -- attention of new tokens over a paged latent cache, absorbed form.
+//
+//   Every query head reads the same cached row r_j = (c_j, p_j) of 512 + 64 entries:
+//     x_j = scale q . r_j,   o = sum e^(x_j - m) c_j / sum e^(x_j - m),   lse = m + ln sum
+//   over the positions j that the token sees (all before it, all of its request, or all
+//   cached ones and the nodes of a drafted tree that its mask names).
+//
+// A row is 1152 bytes and takes 2176 operations per query row: HBM bounds up to about
+// 100 rows per cached row, the tensor cores more.  Query rows (token x head) of a request lie
+// one behind the other, 128 to a row tile.  A cluster of two CTAs works on (request, row tile)
+// items, key tiles of 128 positions, with products of the pair (cta_group::2, M = 128):
+//   S = Q R^T     128 x 128, contraction 576; a CTA holds 64 of the rows and 64 of the keys
+//   P = 2^(S - m) in bf16, by the CTA that owns the rows, into its shared memory
+//   O += P C      128 x 512, twice N = 256; a CTA holds 256 columns of C, all 128 keys
+// A single CTA cannot: 128 rows of O take the whole tensor memory, and of Q 144 KB.  In the
+// pair a CTA has 64 rows of Q (72 KB), and O and two S take 384 of its 512 columns.
+//
+// K and V panels are streamed: a panel of 64 keys x 64 entries is given back as soon as its
+// products are done, so 128 KB of the shared memory are copies under way.  C comes twice (a
+// CTA's keys for S, its columns for O): a pair's operands must lie at the same addresses in both
+// CTAs, and a CTA's keys hold the columns of O in another place than its partner's.
+//
+// Items' key tiles are divided evenly over the pairs (the last item of a share may be
+// unfinished: its pieces are joined by a second kernel).  O is rescaled only when a row's
+// maximum has grown by more than 2^8.
+#include <cuda.h>
+
+#include "kda_attn.cuh"
+#include "kda_latent.h"
+#include "kda_launch.h"
+#include "kda_tcgen05.cuh"
+#include "kda_tmap.h"
+
+namespace kda {
+namespace {
+
+constexpr int kPairs = 76;          // of CTAs, one CTA per SM
+constexpr int kTile = 128;          // positions per key tile
+constexpr int kHalf = 64;           // of them per CTA, and rows of a row tile per CTA
+constexpr int kRows = 128;          // rows per row tile
+constexpr int kPanels = kLatentRow / 64;
+constexpr int kPanelBytes = kHalf * 128;
+// Rings of keys (one panel: 64 keys x 64 entries) and values (two: 64 keys x 128 columns).
+constexpr int kKeys = 8, kValues = 4;
+constexpr int kValuesPerTile = 4;
+constexpr int kNotes = 4;           // items whose notes are kept
+constexpr int kItemCost = 2;        // what an item's beginning and end take, in key tiles
+constexpr float kGrow = 8.f;        // growth of a maximum (log 2) that rescales O
+// Warps: 0-3 the softmax, 4 the products (of the pair's first CTA), 5 the copies, 6 passes on that
+// keys are there, 8-11 load queries and pass on values.
+constexpr int kMmaWarp = 4, kCopyWarp = 5, kKeyWarp = 6, kValueWarp = 8, kWarps = 12;
+constexpr int kThreads = 32 * kWarps;
+constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256;
+
+// One pair's part of an item; count 0: no more.
+struct Part {
+  int b, t0, n, L;
+  int row0;       // of the row tile, among the request's n H rows
+  int tile0, count;
+  int whole;      // key tiles that end at or before this position are seen by every row
+  int flags;
+  int pieces;     // pairs that share the item
+};
+constexpr int kBegins = 1, kEnds = 2;
+
+struct Smem {
+  unsigned char q[kPanels][kPanelBytes];    // this CTA's 64 rows, 1024-aligned, swizzled panels
+  unsigned char key[kKeys][kPanelBytes];
+  unsigned char value[kValues][2 * kPanelBytes];
+  unsigned char p[2][kPanelBytes];          // 64 rows x 64 keys, twice
+  Part part[kNotes];
+  float red[2][2 * kHalf];
+  long long scan[2][kWarps];
+  long long first_unit;                     // of the request that holds the share's first unit
+  int first_request;
+  uint32_t tmem;
+  // this CTA's own
+  uint64_t key_full[kKeys], key_empty[kKeys], value_full[kValues], value_empty[kValues];
+  uint64_t part_full[kNotes], part_empty[kNotes];
+  uint64_t s_full[2], o_done, q_empty, halves[2], done;
+  // the first CTA's, arrived at by both
+  uint64_t key_ready[kKeys], value_ready[kValues], q_ready, p_ready, o_free;
+};
+
+__device__ __forceinline__ Request load_request(const LatentArgs& p, int b, bool report) {
+  Request r;
+  r.t0 = fresh(p.cu + b);
+  r.n = fresh(p.cu + b + 1) - r.t0;
+  r.L = fresh(p.lens + b);
+  const bool good = r.t0 >= 0 && r.n >= 0 && r.t0 + (long long)r.n <= p.T &&
+                    (!p.mask || r.n <= 32ll * p.mask_words) && r.L >= 0 &&
+                    r.L <= (long long)p.c.max_pages * p.c.page_size;
+  if (!good) {
+    if (report) raise_status(p.dev_status, KDA_DEV_BAD_SEQLEN);
+    r.n = 0;
+  }
+  return r;
+}
+__device__ __forceinline__ int row_tiles(const LatentArgs& p, const Request& r) {
+  return (int)(((long long)r.n * p.H + kRows - 1) / kRows);
+}
+// Positions that some row of the tile sees end before this.
+__device__ __forceinline__ int tile_end(const LatentArgs& p, const Request& r, int tile) {
+  if (!p.causal) return r.L;
+  const int last = (int)min((long long)r.n * p.H, (long long)(tile + 1) * kRows) - 1;
+  return min(r.L, max(0, r.L - r.n + last / p.H + 1));
+}
+// An item's key tiles: at least one, since rows that see nothing are written too.
+__device__ __forceinline__ int key_tiles(int end) { return max(1, (end + kTile - 1) / kTile); }
+__device__ __forceinline__ int item_units(const LatentArgs& p, const Request& r, int tile) {
+  return kItemCost + key_tiles(tile_end(p, r, tile));
+}
+
+// Units of the requests of a warp's lanes: by the lane where there are few row tiles, together
+// where there are many.
+__device__ __forceinline__ long long request_units(const LatentArgs& p, const Request& r, int lane) {
+  const int tiles = row_tiles(p, r);
+  if (!p.causal) return (long long)tiles * item_units(p, r, 0);
+  const bool many = tiles > 8;
+  long long sum = 0;
+  if (!many)
+    for (int t = 0; t < tiles; ++t) sum += item_units(p, r, t);
+  for (unsigned left = __ballot_sync(0xffffffffu, many); left; left &= left - 1) {
+    const int src = __ffs(left) - 1;
+    Request x;
+    x.t0 = __shfl_sync(0xffffffffu, r.t0, src);
+    x.n = __shfl_sync(0xffffffffu, r.n, src);
+    x.L = __shfl_sync(0xffffffffu, r.L, src);
+    const int all = row_tiles(p, x);
+    long long part = 0;
+    for (int t = lane; t < all; t += 32) part += item_units(p, x, t);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+    if (lane == src) sum = part;
+  }
+  return sum;
+}
+
+// A bounded wait of a whole warp that orders what the other CTA wrote, too.
+static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity) {
+  const unsigned long long t0 = global_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (__all_sync(0xffffffffu, mbar_try_cluster(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, global_ns() - t0 > kWaitLimitNs)) return false;
+  }
+}
+__device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity) {
+  const uint32_t addr = smem_u32(bar);
+  return __all_sync(0xffffffffu, mbar_try_cluster(addr, parity)) || wait_long(addr, parity);
+}
+
+// The entries of x (eight bf16) that are not finite become zeros.
+__device__ __forceinline__ uint4 finite(uint4 x) {
+  auto keep = [](uint32_t v) {
+    return ((v & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) & v | ((v & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u) & v;
+  };
+  return make_uint4(keep(x.x), keep(x.y), keep(x.z), keep(x.w));
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_kernel(const __grid_constant__ CUtensorMap rows_map, const LatentArgs p, const Pieces pieces) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (tid == 0) {
+    for (int s = 0; s < kKeys; ++s) {
+      mbar_init(&sm.key_full[s], 1);
+      mbar_init(&sm.key_empty[s], 1);
+      mbar_init(&sm.key_ready[s], 2);
+    }
+    for (int s = 0; s < kValues; ++s) {
+      mbar_init(&sm.value_full[s], 1);
+      mbar_init(&sm.value_empty[s], 1);
+      mbar_init(&sm.value_ready[s], 8);
+    }
+    for (int s = 0; s < kNotes; ++s) {
+      mbar_init(&sm.part_full[s], 1);
+      mbar_init(&sm.part_empty[s], 10);  // warps that read notes
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.s_full[s], 1);
+      mbar_init(&sm.halves[s], 2);
+    }
+    mbar_init(&sm.o_done, 1);
+    mbar_init(&sm.q_empty, 1);
+    mbar_init(&sm.done, 1);
+    mbar_init(&sm.q_ready, 8);
+    mbar_init(&sm.p_ready, 8);
+    mbar_init(&sm.o_free, 8);
+    mbar_fence_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc_pair(&sm.tmem, kTmemCols);
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- this pair's share: a thread counts a request, in passes
+  if (blockIdx.x == 0 && tid == 0 && (fresh(p.cu) != 0 || fresh(p.cu + p.B) != p.T))
+    raise_status(p.dev_status, KDA_DEV_BAD_SEQLEN);
+  if (rank == 0 && tid == 0) pieces.notes[pair].tokens = 0;
+  const int passes = (p.B + kThreads - 1) / kThreads;
+  long long mine = 0, before = 0, units = 0;
+  for (int i = 0; i < passes; ++i) {
+    const int b = i * kThreads + tid;
+    Request r{0, 0, 0};
+    if (b < p.B) r = load_request(p, b, blockIdx.x == 0);
+    mine = request_units(p, r, lane);
+    long long all;
+    before = units + scan_before<kWarps>(mine, sm.scan[i & 1], all);
+    units += all;
+  }
+  const int used = (int)min((long long)pairs, units);
+  const long long u0 = pair < used ? share_begin(units, used, pair) : 0;
+  const long long u1 = pair < used ? share_begin(units, used, pair + 1) : 0;
+  for (int i = 0; i < passes && u1 > u0; ++i) {
+    const int b = i * kThreads + tid;
+    if (passes > 1) {  // counted again
+      if (i == 0) units = 0;
+      Request r{0, 0, 0};
+      if (b < p.B) r = load_request(p, b, false);
+      mine = request_units(p, r, lane);
+      long long all;
+      __syncthreads();
+      before = units + scan_before<kWarps>(mine, sm.scan[i & 1], all);
+      units += all;
+    }
+    if (u0 >= before && u0 < before + mine) {
+      sm.first_request = b;
+      sm.first_unit = before;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();  // barriers and tensor memory of both CTAs are there
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  bool ok = true;
+
+  auto read_part = [&](int item, Part& part) {
+    ok = ok && wait_pair(&sm.part_full[item % kNotes], (item / kNotes) & 1);
+    if (!ok) return false;
+    part = sm.part[item % kNotes];
+    return part.count > 0;
+  };
+  auto leave_part = [&](int item) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.part_empty[item % kNotes]);
+  };
+
+  if (warp == kCopyWarp) {
+    // ---- the share's items, and their keys and values into the rings
+    const int rows_per_box = min(p.c.page_size, kHalf);
+    const int half_boxes = kHalf / rows_per_box, boxes = 2 * half_boxes;  // of a half, of a key tile
+    int key_put = 0, value_put = 0, item = 0;
+    auto put_note = [&](const Part& part) {
+      if (item >= kNotes) ok = wait_pair(&sm.part_empty[item % kNotes], (item / kNotes - 1) & 1);
+      if (ok && lane == 0) {
+        sm.part[item % kNotes] = part;
+        mbar_arrive(&sm.part_full[item % kNotes]);
+      }
+      __syncwarp();
+      ++item;
+    };
+    long long unit = 0;
+    int b = 0, tile = 0, tiles = 0, base = 0;
+    Request r{0, 0, 0}, held{0, 0, 0};  // held: request base + lane
+    auto fetch = [&]() {
+      base = b;
+      held = Request{0, 0, 0};
+      if (b + lane < p.B) held = load_request(p, b + lane, false);
+    };
+    auto take = [&]() {  // the first request from b on that has rows
+      while (b < p.B) {
+        if (b >= base + 32) fetch();
+        const unsigned some = __ballot_sync(0xffffffffu, held.n > 0) & (0xffffffffu << (b - base));
+        if (some) {
+          const int src = __ffs(some) - 1;
+          b = base + src;
+          r.t0 = __shfl_sync(0xffffffffu, held.t0, src);
+          r.n = __shfl_sync(0xffffffffu, held.n, src);
+          r.L = __shfl_sync(0xffffffffu, held.L, src);
+          tile = 0;
+          tiles = row_tiles(p, r);
+          return;
+        }
+        b = base + 32;
+      }
+    };
+    if (u1 > u0) {
+      b = sm.first_request;
+      unit = sm.first_unit;
+      fetch();
+      take();
+      // the row tile that holds u0
+      if (!p.causal) {
+        const int each = item_units(p, r, 0);
+        tile = (int)((u0 - unit) / each);
+        unit += (long long)tile * each;
+      } else {
+        while (true) {
+          const int x = tile + lane < tiles ? item_units(p, r, tile + lane) : 0;
+          long long upto = x;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+          }
+          const unsigned past = __ballot_sync(0xffffffffu, unit + upto > u0);
+          if (past || tile + 32 >= tiles) {
+            const int in = past ? __ffs(past) - 1 : 0;
+            unit += __shfl_sync(0xffffffffu, upto - x, in);
+            tile += in;
+            break;
+          }
+          unit += __shfl_sync(0xffffffffu, upto, 31);
+          tile += 32;
+        }
+      }
+    }
+    while (u1 > u0 && unit < u1 && b < p.B && ok) {
+      const int end = tile_end(p, r, tile), all = key_tiles(end);
+      const int from = (int)max(0ll, u0 - unit - kItemCost), to = (int)min((long long)all, u1 - unit - kItemCost);
+      if (to > from) {
+        Part part;
+        part.b = b;
+        part.t0 = r.t0;
+        part.n = r.n;
+        part.L = r.L;
+        part.row0 = tile * kRows;
+        part.tile0 = from;
+        part.count = to - from;
+        const int pos0 = r.L - r.n, first = pos0 + part.row0 / p.H;
+        part.whole = p.mask ? (first >= 0 ? pos0 : 0) : p.causal ? first + 1 : first >= 0 ? r.L : 0;
+        part.flags = (from == 0 ? kBegins : 0) | (to == all ? kEnds : 0);
+        part.pieces = share_of(units, used, unit + kItemCost + all - 1) - pair + 1;
+        put_note(part);
+        const int32_t* table = p.c.page_table + (size_t)b * p.c.max_pages;
+        const int box0 = from * boxes;
+        int page = -1, page_before = -1;  // lanes: of the 32 boxes under way, of the 32 before
+        int window = -1;                  // which 32 boxes `page` is of
+        auto find_pages = [&](int i) {
+          if ((i * boxes) >> 5 == window) return;
+          window = (i * boxes) >> 5;
+          page_before = page;
+          const int pos = (box0 + window * 32 + lane) * rows_per_box;
+          page = -1;
+          if (pos < end && pos < to * kTile) {
+            page = fresh(table + pos / p.c.page_size);
+            if (page < 0 || page >= p.c.num_pages) {
+              raise_status(p.dev_status, KDA_DEV_BAD_PAGE);
+              page = -1;
+            }
+          }
+        };
+        // row of the cache where `box` (per lane) of the part's key tile i starts; past the end: zeros
+        auto cache_row = [&](int i, int box) {
+          const int at = i * boxes + box;
+          const int now = __shfl_sync(0xffffffffu, page, at & 31);
+          const int then = __shfl_sync(0xffffffffu, page_before, at & 31);
+          const int pg = (at >> 5) == window ? now : then;
+          const int pos = (box0 + at) * rows_per_box;
+          return pg >= 0 ? pg * p.c.page_size + pos % p.c.page_size : p.c.num_pages * p.c.page_size;
+        };
+        for (int i = 0; i <= part.count && ok; ++i) {
+          if (i < part.count) {
+            find_pages(i);
+            const int row = cache_row(i, rank * half_boxes + min(lane, half_boxes - 1));
+#pragma unroll 1
+            for (int pn = 0; pn < kPanels && ok; ++pn, ++key_put) {
+              const int s = key_put % kKeys;
+              if (key_put >= kKeys) ok = wait_pair(&sm.key_empty[s], (key_put / kKeys - 1) & 1);
+              if (!ok) break;
+              if (lane == 0) mbar_expect_tx(&sm.key_full[s], kPanelBytes);
+              __syncwarp();
+              if (lane < half_boxes)
+                tma_load_2d(sm.key[s] + lane * rows_per_box * 128, &rows_map, &sm.key_full[s], pn * 64, row);
+            }
+          }
+          if (i > 0 && ok) {
+            const int in = lane % half_boxes, panel = (lane / half_boxes) & 1;
+            const int row_lo = cache_row(i - 1, in), row_hi = cache_row(i - 1, half_boxes + in);
+#pragma unroll 1
+            for (int v = 0; v < kValuesPerTile && ok; ++v, ++value_put) {  // keys v / 2, columns v % 2
+              const int s = value_put % kValues;
+              if (value_put >= kValues) ok = wait_pair(&sm.value_empty[s], (value_put / kValues - 1) & 1);
+              if (!ok) break;
+              if (lane == 0) mbar_expect_tx(&sm.value_full[s], 2 * kPanelBytes);
+              __syncwarp();
+              if (lane < 2 * half_boxes)
+                tma_load_2d(sm.value[s] + panel * kPanelBytes + in * rows_per_box * 128, &rows_map, &sm.value_full[s],
+                            rank * (kLatent / 2) + (v & 1) * 128 + panel * 64, v < 2 ? row_lo : row_hi);
+            }
+          }
+        }
+      }
+      unit += kItemCost + all;
+      if (++tile >= tiles) {
+        ++b;
+        take();
+      }
+    }
+    if (ok) put_note(Part{0, 0, 0, 0, 0, 0, 0, 0, 0, 0});
+    if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
+    // Every copy lands before the CTA's memory is released, also when a wait gave up.
+    for (int u = max(0, key_put - kKeys); u < key_put; ++u) mbar_wait(&sm.key_full[u % kKeys], (u / kKeys) & 1);
+    for (int u = max(0, value_put - kValues); u < value_put; ++u)
+      mbar_wait(&sm.value_full[u % kValues], (u / kValues) & 1);
+  } else if (warp == kMmaWarp) {
+    // ---- the products
+    const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t q0 = smem_u32(sm.q[0]), key0 = smem_u32(sm.key[0]), value0 = smem_u32(sm.value[0]),
+                   p0 = smem_u32(sm.p[0]);
+    const uint32_t idesc_s = idesc_bf16(kTile, kRows, false, false), idesc_o = idesc_bf16(256, kRows, false, true);
+    int keys = 0, values = 0, task = 0;  // panels, value units and key tiles so far
+    Part part;
+    for (int item = 0; read_part(item, part); leave_part(item), ++item) {
+      if (rank != 0) continue;
+      const int count = __shfl_sync(0xffffffffu, part.count, 0);
+      ok = wait_pair(&sm.q_ready, item & 1);
+      for (int i = 0; i <= count && ok; ++i) {
+        if (i < count) {
+          const uint32_t s_col = base + kColS + (uint32_t)((task + i) & 1) * kHalf;
+#pragma unroll 1
+          for (int pn = 0; pn < kPanels && ok; ++pn, ++keys) {
+            const int s = keys % kKeys;
+            ok = wait_pair(&sm.key_ready[s], (keys / kKeys) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t a = smem_desc_sw128(q0 + pn * kPanelBytes, 16, 1024);
+              const uint64_t k = smem_desc_sw128(key0 + s * kPanelBytes, 16, 1024);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) mma_bf16_pair(s_col, a + 2 * j, k + 2 * j, idesc_s, pn + j > 0 ? 1u : 0u);
+              mma_commit_pair(&sm.key_empty[s]);
+              if (pn == kPanels - 1) {
+                mma_commit_pair(&sm.s_full[(task + i) & 1]);
+                if (i == count - 1) mma_commit_pair(&sm.q_empty);
+              }
+            }
+            __syncwarp();
+          }
+        }
+        if (i > 0 && ok) {
+          const int g = task + i - 1;
+          if (i == 1 && item > 0) ok = wait_pair(&sm.o_free, (item - 1) & 1);
+          ok = ok && wait_pair(&sm.p_ready, g & 1);
+#pragma unroll 1
+          for (int v = 0; v < kValuesPerTile && ok; ++v, ++values) {
+            const int s = values % kValues;
+            ok = wait_pair(&sm.value_ready[s], (values / kValues) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t a = smem_desc_sw128(p0 + (v >> 1) * kPanelBytes, 16, 1024);
+              const uint64_t c = smem_desc_sw128(value0 + s * 2 * kPanelBytes, kPanelBytes, 1024);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                mma_bf16_pair(base + kColO + (v & 1) * 128, a + 2 * j, c + ((j * 16 * 128) >> 4), idesc_o,
+                              i > 1 || v > 1 || j > 0 ? 1u : 0u);
+              mma_commit_pair(&sm.value_empty[s]);
+              if (v == kValuesPerTile - 1) mma_commit_pair(&sm.o_done);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      task += count;
+      if (!ok) break;
+    }
+    if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
+    if (rank == 0 && elect_one()) mma_commit_pair(&sm.done);  // arrives when every product issued has completed
+    __syncwarp();
+    mbar_wait(&sm.done, 0);
+  } else if (warp == kKeyWarp) {
+    // ---- keys that have arrived here, for the first CTA's products
+    int keys = 0;
+    Part part;
+    for (int item = 0; read_part(item, part); leave_part(item), ++item) {
+      const int all = keys + part.count * kPanels;
+      for (; keys < all && ok; ++keys) {
+        const int s = keys % kKeys;
+        ok = wait_pair(&sm.key_full[s], (keys / kKeys) & 1);
+        if (ok && lane == 0) mbar_arrive_cluster(cluster_addr(&sm.key_ready[s], 0));
+        __syncwarp();
+      }
+      if (!ok) break;
+    }
+    if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
+  } else if (warp >= kValueWarp) {
+    // ---- each item's queries; values that have arrived, without the entries that some row must not see
+    const int at = tid - 32 * kValueWarp, wv = warp - kValueWarp;
+    int values = 0;
+    Part part;
+    for (int item = 0; read_part(item, part); leave_part(item), ++item) {
+      if (item > 0) ok = wait_pair(&sm.q_empty, (item - 1) & 1);
+      if (!ok) break;
+      const int rows = (int)min((long long)kRows, (long long)part.n * p.H - part.row0);
+#pragma unroll 4
+      for (int i = 0; i < kHalf * kPanels * 8 / 128; ++i) {
+        const int n = i * 128 + at, row = n / (kPanels * 8), ch = n - row * (kPanels * 8);
+        const int in = rank * kHalf + row, flat = part.row0 + in;
+        const int token = flat / p.H, head = flat - token * p.H;
+        const bool live = in < rows;
+        const kda_bf16* src = p.q + (live ? (part.t0 + token) * p.q_stride + (size_t)head * kLatentRow + ch * 8 : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         smem_u32(sm.q[ch >> 3] + swizzled<128>(row, ch & 7))),
+                     "l"(src), "r"(live ? 16 : 0)
+                     : "memory");
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&sm.q_ready, 0));
+      for (int i = 0; i < part.count && ok; ++i) {
+        const int start = (part.tile0 + i) * kTile;
+#pragma unroll 1
+        for (int v = 0; v < kValuesPerTile && ok; ++v, ++values) {
+          const int s = values % kValues;
+          ok = wait_pair(&sm.value_full[s], (values / kValues) & 1);
+          if (!ok) break;
+          if (start + kTile > part.whole) {
+            // A quarter of the unit's 64 keys, two panels of eight chunks each.  0 x NaN would reach
+            // rows that do not see it; rows that do have a score that is not finite.
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int n = k * 32 + lane, key = wv * 16 + ((n >> 3) & 15);
+              uint4* x = reinterpret_cast<uint4*>(sm.value[s] + (n >> 7) * kPanelBytes + swizzled<128>(key, n & 7));
+              const uint4 y = *x;
+              const uint4 z = start + (v >> 1) * kHalf + key < part.L ? finite(y) : make_uint4(0, 0, 0, 0);
+              if (y.x != z.x || y.y != z.y || y.z != z.z || y.w != z.w) *x = z;
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(&sm.value_ready[s], 0));
+        }
+      }
+      if (!ok) break;
+    }
+    if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
+  } else if (warp < 4) {
+    // ---- the softmax: thread (row, half of the keys)
+    const int row = tid & (kHalf - 1), half = tid >> 6;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
+    const float c = p.scale * kLog2E;
+    const float2 c2 = make_float2(c, c);
+    const uint32_t p_ready = cluster_addr(&sm.p_ready, 0), o_free = cluster_addr(&sm.o_free, 0);
+    unsigned char* const p_row = sm.p[half];
+    int task = 0, swaps = 0;
+    // The partner's value: the other half of this row's keys.
+    auto swap = [&](float x) {
+      sm.red[swaps & 1][tid] = x;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.halves[warp & 1]);
+      ok = ok && wait_pair(&sm.halves[warp & 1], swaps & 1);
+      const float y = sm.red[swaps & 1][tid ^ kHalf];
+      ++swaps;
+      return y;
+    };
+    Part part;
+    for (int item = 0; read_part(item, part); leave_part(item), ++item) {
+      const int L = part.L, n = part.n;
+      const int in = rank * kHalf + row, flat = part.row0 + in;
+      const int token = flat / p.H, pos = L - n + token;
+      const bool live = flat < (long long)n * p.H;
+      const int row_hi = pos < 0 || !live ? 0 : p.causal ? min(pos + 1, L) : L;
+      const int32_t* words = p.mask && live ? p.mask + (size_t)(part.t0 + token) * p.mask_words : nullptr;
+      float m = -INFINITY;
+      float2 l2 = make_float2(0.f, 0.f);
+      for (int i = 0; i < part.count; ++i, ++task) {
+        ok = wait_pair(&sm.s_full[task & 1], (task >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const int start = (part.tile0 + i) * kTile + half * kHalf;
+        float x[2][32];
+        const uint32_t s_col = lanes + kColS + (uint32_t)(task & 1) * kHalf;
+        tmem_ld_32cols(s_col, x[0]);
+        tmem_ld_32cols(s_col + 32, x[1]);
+        tmem_ld_wait();
+        const bool whole = (part.tile0 + i + 1) * kTile <= part.whole;
+        float top = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 a = __fmul2_rn(make_float2(x[h][e], x[h][e + 1]), c2);
+            x[h][e] = a.x;
+            x[h][e + 1] = a.y;
+          }
+          if (!whole) {
+            const int at = start + 32 * h;
+            uint32_t see = columns(0, row_hi - at);
+            if (words && row_hi > 0) see &= tree_bits(words, p.mask_words, n, at - (L - n));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((see >> e) & 1)) x[h][e] = -INFINITY;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) top = max3(top, x[h][e], x[h][e + 1]);
+        }
+        const float now = max3(m, top, swap(top));
+        if (task > 0) ok = ok && wait_pair(&sm.o_done, (task - 1) & 1);  // O and P are at rest
+        if (!ok) break;
+        // (both warps of a row decide alike: they have the same rows, maxima and so references)
+        if (__any_sync(0xffffffffu, now > m + kGrow)) {
+          const float keep = exp2_approx(m - (now == -INFINITY ? 0.f : now));
+          l2.x *= keep;
+          l2.y *= keep;
+          if (i > 0) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int cc = 0; cc < 256; cc += 16) {
+              float o[16];
+              tmem_ld_16cols(lanes + kColO + cc, o);
+              tmem_ld_wait();
+              uint32_t ob[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ob[e] = __float_as_uint(o[e] * keep);
+              tmem_st_16cols(lanes + kColO + cc, ob);
+            }
+            tmem_st_wait();
+          }
+          m = now;
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        const float2 nref = make_float2(-ref, -ref);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) {
+              const float2 y = __fadd2_rn(make_float2(x[h][e + k], x[h][e + k + 1]), nref);
+              const float2 v = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+              l2 = __fadd2_rn(l2, v);
+              w[k / 2] = pack_bf16(v.x, v.y);
+            }
+            *reinterpret_cast<uint4*>(p_row + swizzled<128>(row, 4 * h + e / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(p_ready);
+      }
+      if (!ok) break;
+      const float l_half = l2.x + l2.y, l = l_half + swap(l_half);
+      ok = ok && wait_pair(&sm.o_done, (task - 1) & 1);
+      if (!ok) break;
+      // ---- the end of this pair's part of the item
+      tc_fence_after();
+      const bool done = (part.flags & (kBegins | kEnds)) == (kBegins | kEnds);
+      const size_t out_row = (size_t)part.t0 * p.H + flat;
+      const size_t piece = ((size_t)pair * 2 + (part.flags & kBegins ? 1 : 0)) * kRows + in;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      if (live && half == 0) {
+        if (!done) pieces.ml[piece] = make_float2(m, l);
+        else if (p.lse) p.lse[out_row] = (m + log2f(l)) * kLn2;
+      }
+      if (rank == 0 && tid == 0 && (part.flags & (kBegins | kEnds)) == kBegins)
+        pieces.notes[pair] = PieceNote{part.t0 * p.H + part.row0,
+                                       (int)min((long long)kRows, (long long)n * p.H - part.row0), part.pieces, 0};
+      int to_rows[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) to_rows[e] = __shfl_sync(0xffffffffu, live ? (int)out_row : -1, (lane & ~3) + e);
+#pragma unroll 1
+      for (int cc = 0; cc < 256; cc += 32) {
+        float o[32];
+        tmem_ld_32cols(lanes + kColO + cc, o);
+        tmem_ld_wait();
+        const int col = half * 256 + cc;
+        if (done) {
+          uint4 y[4];
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            y[e / 8] = make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                                  pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+          transpose4(y, lane);  // four lanes write 64 bytes of one row together
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (to_rows[e] >= 0)
+              *reinterpret_cast<uint4*>(p.out + (size_t)to_rows[e] * kLatent + col + 8 * (lane & 3)) = y[e];
+        } else if (live) {
+          float4* to = reinterpret_cast<float4*>(pieces.o + piece * kLatent + col);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) to[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+        __syncwarp();  // the next load is the whole warp's
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(o_free);
+    }
+    if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();  // nothing of the pair is under way
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
+  __syncwarp();
+  cluster_sync();
+}
+
+// The pieces of one shared item into its outputs: with m = max m_i,
+//   o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i,   lse = (m + log2 l) ln 2.
+// CTA (c, y) takes rows of the item that pair c began, a row at a time: four columns a thread.
+__global__ void __launch_bounds__(128) latent_join_kernel(const LatentArgs p, const Pieces s) {
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const PieceNote note = s.notes[c];
+  for (int row = blockIdx.y; row < note.tokens; row += gridDim.y) {
+    auto at = [&](int i) { return ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * kRows + row; };
+    float m = -INFINITY;
+    for (int i = lane; i < note.pieces; i += 32) m = fmaxf(m, s.ml[at(i)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < note.pieces; ++i) {
+      const float2 ml = s.ml[at(i)];
+      const float w = exp2_approx(ml.x - ref);
+      const float4 x = *reinterpret_cast<const float4*>(s.o + at(i) * kLatent + 4 * threadIdx.x);
+      l = fmaf(w, ml.y, l);
+      o.x = fmaf(w, x.x, o.x);
+      o.y = fmaf(w, x.y, o.y);
+      o.z = fmaf(w, x.z, o.z);
+      o.w = fmaf(w, x.w, o.w);
+    }
+    const size_t out_row = (size_t)note.row0 + row;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<uint2*>(p.out + out_row * kLatent + 4 * threadIdx.x) =
+        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    if (p.lse && threadIdx.x == 0) p.lse[out_row] = (m + log2f(l)) * kLn2;
+  }
+}
+
+}  // namespace
+
+size_t latent_workspace_bytes(int B, int T, int H) {
+  if (B < 0 || T < 0 || H < 1) return 0;
+  return (pieces_bytes(kPairs, kRows, kLatent) + 255) & ~(size_t)255;
+}
+
+cudaError_t launch_latent_attention(const LatentArgs& a, cudaStream_t stream) {
+  static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "a CTA fits an SM");
+  CUtensorMap map;
+  const int rows_per_box = a.c.page_size < kHalf ? a.c.page_size : kHalf;
+  if (!make_map_2d(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.c.rows, kLatentRow,
+                   (uint64_t)a.c.num_pages * a.c.page_size, 64, rows_per_box))
+    return cudaErrorInvalidValue;
+  const size_t smem = sizeof(Smem) + 1024;
+  static SmemSet set;
+  cudaError_t e = allow_smem(latent_kernel, smem, set);
+  if (e != cudaSuccess) return e;
+  const Pieces pieces = pieces_at(a.workspace, kPairs, kRows);
+  e = launch_pairs(latent_kernel, dim3(2 * kPairs), dim3(kThreads), smem, stream, map, a, pieces);
+  if (e != cudaSuccess) return e;
+  return launch(latent_join_kernel, dim3(kPairs, 32), dim3(128), 0, stream, true, a, pieces);
+}
+
+}  // namespace kda

@@ -1,0 +1,22 @@
+// kda_attn_tree.cu -- attention of drafted trees over a paged K/V cache: the chunk kernel with a
+// mask of the new tokens that each of them sees.
+//
+// Trees of a few nodes take it too.  Their rows (nodes x query heads per key head) are mostly more
+// than the 16 up to which the window kernel wins over bf16, and everything before the tree is seen by
+// every row, so that only the last key tiles differ from a chunk's.
+#include "kda_attn_chunk.cuh"
+
+namespace kda {
+
+size_t tree_workspace_bytes(int B, int T, int max_tokens, int H, int HKV, int D) {
+  if (B < 0 || T < 0 || max_tokens < 0 || H < 1 || HKV < 1 || H % HKV != 0 || (D != 64 && D != 128)) return 0;
+  return (pieces_bytes(kChunkCtas, kChunkRows, D) + 255) & ~(size_t)255;
+}
+
+cudaError_t launch_tree_attention(const AttentionArgs& in, cudaStream_t stream) {
+  AttentionArgs a = in;
+  a.window_rows = 0;
+  return by_type<true>(a, stream);
+}
+
+}  // namespace kda

@@ -25,17 +25,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kE4m3Max = 448.0f;
 
-// Request of packed row t: the b with cu[b] <= t < cu[b + 1].  For a malformed
-// cu the result is still in 0..B-1 and the caller's range check rejects it.
-__device__ __forceinline__ int find_request(const int32_t* cu, int B, int t) {
-  int lo = 0, hi = B - 1;  // the answer lies in lo..hi
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (fresh(cu + mid + 1) > t) hi = mid; else lo = mid + 1;
-  }
-  return lo;
-}
-
 // Whether request b with rows t0 .. t1 - 1 and at[b] = `at` is well formed.
 template <bool kAppend>
 __device__ __forceinline__ bool good_request(const CacheRowsArgs& p, int t0, int t1, long long at) {

@@ -42,6 +42,17 @@ __device__ __forceinline__ void pdl_trigger() {
 template <typename T>
 __device__ __forceinline__ T fresh(const T* p) { return *p; }
 
+// Request of packed row t: the b with cu[b] <= t < cu[b + 1].  For a malformed
+// cu the result is still in 0..B-1 and the caller's range check rejects it.
+__device__ __forceinline__ int find_request(const int32_t* cu, int B, int t) {
+  int lo = 0, hi = B - 1;  // the answer lies in lo..hi
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (fresh(cu + mid + 1) > t) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
 __device__ __forceinline__ void raise_status(int32_t* status, int32_t bit) {
   if (status != nullptr) atomicOr(status, bit);
 }

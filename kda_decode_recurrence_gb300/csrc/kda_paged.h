@@ -48,12 +48,17 @@ struct AttentionArgs {
   int causal, window;
   int B, T, max_tokens, H, G;
   int window_rows;  // requests of at most so many rows are the window kernel's
+  const int32_t* tree;  // [T, tree_words] bits of the new tokens that a token sees (trees only)
+  int tree_words;       // 32 tree_words >= max_tokens
   void* workspace;
   int32_t* dev_status;
 };
 
 size_t attention_workspace_bytes(int B, int T, int max_tokens, int H, int HKV, int D);
 cudaError_t launch_paged_attention(const AttentionArgs& args, cudaStream_t stream);
+
+size_t tree_workspace_bytes(int B, int T, int max_tokens, int H, int HKV, int D);
+cudaError_t launch_tree_attention(const AttentionArgs& args, cudaStream_t stream);
 
 struct VerifyArgs {
   int32_t* tokens;
