@@ -15,10 +15,10 @@
 // A single CTA cannot: 128 rows of O take the whole tensor memory, and of Q 144 KB.  In the
 // pair a CTA has 64 rows of Q (72 KB), and O and two S take 384 of its 512 columns.
 //
-// K and V panels are streamed: a panel of 64 keys x 64 entries is given back as soon as its
-// products are done, so 128 KB of the shared memory are copies under way.  C comes twice (a
-// CTA's keys for S, its columns for O): a pair's operands must lie at the same addresses in both
-// CTAs, and a CTA's keys hold the columns of O in another place than its partner's.
+// Keys and values are streamed: their memory is given back as soon as their products are done.
+// C comes twice (a CTA's keys for S, its columns for O): a pair's operands must lie at the same
+// addresses in both CTAs, and a CTA's keys hold the columns of O in another place than its
+// partner's.  The second copy comes from L2, into which rows are fetched two key tiles ahead.
 //
 // Items' key tiles are divided evenly over the pairs (the last item of a share may be
 // unfinished: its pieces are joined by a second kernel).  O is rescaled only when a row's
@@ -40,15 +40,17 @@ constexpr int kHalf = 64;           // of them per CTA, and rows of a row tile p
 constexpr int kRows = 128;          // rows per row tile
 constexpr int kPanels = kLatentRow / 64;
 constexpr int kPanelBytes = kHalf * 128;
-// Rings of keys (one panel: 64 keys x 64 entries) and values (two: 64 keys x 128 columns).
-constexpr int kKeys = 8, kValues = 4;
-constexpr int kValuesPerTile = 4;
+// A unit of keys is three panels (64 keys x 192 entries), one of values four (64 keys x this CTA's 256
+// columns); the rings hold a key tile's.
+constexpr int kKeyPanels = 3, kKeys = kPanels / kKeyPanels, kKeyBytes = kKeyPanels * kPanelBytes;
+constexpr int kValuePanels = 4, kValues = 2, kValueBytes = kValuePanels * kPanelBytes;
+constexpr int kAhead = 2;           // key tiles that are fetched into L2 before their copies
 constexpr int kNotes = 4;           // items whose notes are kept
 constexpr int kItemCost = 2;        // what an item's beginning and end take, in key tiles
 constexpr float kGrow = 8.f;        // growth of a maximum (log 2) that rescales O
 // Warps: 0-3 the softmax, 4 the products (of the pair's first CTA), 5 the copies, 6 passes on that
-// keys are there, 8-11 load queries and pass on values.
-constexpr int kMmaWarp = 4, kCopyWarp = 5, kKeyWarp = 6, kValueWarp = 8, kWarps = 12;
+// keys are there, 7 finds the share's items, 8-11 load queries and pass on values.
+constexpr int kMmaWarp = 4, kCopyWarp = 5, kKeyWarp = 6, kItemWarp = 7, kValueWarp = 8, kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
 constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256;
 
@@ -57,6 +59,7 @@ struct Part {
   int b, t0, n, L;
   int row0;       // of the row tile, among the request's n H rows
   int tile0, count;
+  int end;        // positions that some row sees end before this
   int whole;      // key tiles that end at or before this position are seen by every row
   int flags;
   int pieces;     // pairs that share the item
@@ -65,8 +68,8 @@ constexpr int kBegins = 1, kEnds = 2;
 
 struct Smem {
   unsigned char q[kPanels][kPanelBytes];    // this CTA's 64 rows, 1024-aligned, swizzled panels
-  unsigned char key[kKeys][kPanelBytes];
-  unsigned char value[kValues][2 * kPanelBytes];
+  unsigned char key[kKeys][kKeyBytes];
+  unsigned char value[kValues][kValueBytes];
   unsigned char p[2][kPanelBytes];          // 64 rows x 64 keys, twice
   Part part[kNotes];
   float red[2][2 * kHalf];
@@ -136,19 +139,11 @@ __device__ __forceinline__ long long request_units(const LatentArgs& p, const Re
   return sum;
 }
 
-// A bounded wait of a whole warp that orders what the other CTA wrote, too.
-static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity) {
-  const unsigned long long t0 = global_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 16; ++i)
-      if (__all_sync(0xffffffffu, mbar_try_cluster(bar, parity))) return true;
-    if (__any_sync(0xffffffffu, global_ns() - t0 > kWaitLimitNs)) return false;
-  }
-}
+// A bounded wait of a whole warp.  Barriers of the first CTA that the other one arrives at carry no
+// data between the CTAs: what their arrivals stand for (a copy, P, an O that has been read) is in the
+// arriving SM's own memory, complete or fenced for its tensor core before the arrival.
 __device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity) {
-  const uint32_t addr = smem_u32(bar);
-  return __all_sync(0xffffffffu, mbar_try_cluster(addr, parity)) || wait_long(addr, parity);
+  return wait_together(smem_u32(bar), parity);
 }
 
 // The entries of x (eight bf16) that are not finite become zeros.
@@ -179,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kNotes; ++s) {
       mbar_init(&sm.part_full[s], 1);
-      mbar_init(&sm.part_empty[s], 10);  // warps that read notes
+      mbar_init(&sm.part_empty[s], 11);  // warps that read notes
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.s_full[s], 1);
@@ -250,11 +245,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(&sm.part_empty[item % kNotes]);
   };
 
-  if (warp == kCopyWarp) {
-    // ---- the share's items, and their keys and values into the rings
-    const int rows_per_box = min(p.c.page_size, kHalf);
-    const int half_boxes = kHalf / rows_per_box, boxes = 2 * half_boxes;  // of a half, of a key tile
-    int key_put = 0, value_put = 0, item = 0;
+  if (warp == kItemWarp) {
+    // ---- the share's items
+    int item = 0;
     auto put_note = [&](const Part& part) {
       if (item >= kNotes) ok = wait_pair(&sm.part_empty[item % kNotes], (item / kNotes - 1) & 1);
       if (ok && lane == 0) {
@@ -332,69 +325,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         part.row0 = tile * kRows;
         part.tile0 = from;
         part.count = to - from;
+        part.end = end;
         const int pos0 = r.L - r.n, first = pos0 + part.row0 / p.H;
         part.whole = p.mask ? (first >= 0 ? pos0 : 0) : p.causal ? first + 1 : first >= 0 ? r.L : 0;
         part.flags = (from == 0 ? kBegins : 0) | (to == all ? kEnds : 0);
         part.pieces = share_of(units, used, unit + kItemCost + all - 1) - pair + 1;
         put_note(part);
-        const int32_t* table = p.c.page_table + (size_t)b * p.c.max_pages;
-        const int box0 = from * boxes;
-        int page = -1, page_before = -1;  // lanes: of the 32 boxes under way, of the 32 before
-        int window = -1;                  // which 32 boxes `page` is of
-        auto find_pages = [&](int i) {
-          if ((i * boxes) >> 5 == window) return;
-          window = (i * boxes) >> 5;
-          page_before = page;
-          const int pos = (box0 + window * 32 + lane) * rows_per_box;
-          page = -1;
-          if (pos < end && pos < to * kTile) {
-            page = fresh(table + pos / p.c.page_size);
-            if (page < 0 || page >= p.c.num_pages) {
-              raise_status(p.dev_status, KDA_DEV_BAD_PAGE);
-              page = -1;
-            }
-          }
-        };
-        // row of the cache where `box` (per lane) of the part's key tile i starts; past the end: zeros
-        auto cache_row = [&](int i, int box) {
-          const int at = i * boxes + box;
-          const int now = __shfl_sync(0xffffffffu, page, at & 31);
-          const int then = __shfl_sync(0xffffffffu, page_before, at & 31);
-          const int pg = (at >> 5) == window ? now : then;
-          const int pos = (box0 + at) * rows_per_box;
-          return pg >= 0 ? pg * p.c.page_size + pos % p.c.page_size : p.c.num_pages * p.c.page_size;
-        };
-        for (int i = 0; i <= part.count && ok; ++i) {
-          if (i < part.count) {
-            find_pages(i);
-            const int row = cache_row(i, rank * half_boxes + min(lane, half_boxes - 1));
-#pragma unroll 1
-            for (int pn = 0; pn < kPanels && ok; ++pn, ++key_put) {
-              const int s = key_put % kKeys;
-              if (key_put >= kKeys) ok = wait_pair(&sm.key_empty[s], (key_put / kKeys - 1) & 1);
-              if (!ok) break;
-              if (lane == 0) mbar_expect_tx(&sm.key_full[s], kPanelBytes);
-              __syncwarp();
-              if (lane < half_boxes)
-                tma_load_2d(sm.key[s] + lane * rows_per_box * 128, &rows_map, &sm.key_full[s], pn * 64, row);
-            }
-          }
-          if (i > 0 && ok) {
-            const int in = lane % half_boxes, panel = (lane / half_boxes) & 1;
-            const int row_lo = cache_row(i - 1, in), row_hi = cache_row(i - 1, half_boxes + in);
-#pragma unroll 1
-            for (int v = 0; v < kValuesPerTile && ok; ++v, ++value_put) {  // keys v / 2, columns v % 2
-              const int s = value_put % kValues;
-              if (value_put >= kValues) ok = wait_pair(&sm.value_empty[s], (value_put / kValues - 1) & 1);
-              if (!ok) break;
-              if (lane == 0) mbar_expect_tx(&sm.value_full[s], 2 * kPanelBytes);
-              __syncwarp();
-              if (lane < 2 * half_boxes)
-                tma_load_2d(sm.value[s] + panel * kPanelBytes + in * rows_per_box * 128, &rows_map, &sm.value_full[s],
-                            rank * (kLatent / 2) + (v & 1) * 128 + panel * 64, v < 2 ? row_lo : row_hi);
-            }
-          }
-        }
       }
       unit += kItemCost + all;
       if (++tile >= tiles) {
@@ -402,7 +338,104 @@ __global__ void __launch_bounds__(kThreads, 1)
         take();
       }
     }
-    if (ok) put_note(Part{0, 0, 0, 0, 0, 0, 0, 0, 0, 0});
+    if (ok) put_note(Part{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0});
+    if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
+  } else if (warp == kCopyWarp) {
+    // ---- keys and values into the rings
+    const int rows_per_box = min(p.c.page_size, kHalf);
+    const int half_boxes = kHalf / rows_per_box, boxes = 2 * half_boxes;  // of a half, of a key tile
+    const int in = lane % half_boxes, panel = lane / half_boxes;          // of a unit's copies: lane's box and panel
+    int key_put = 0, value_put = 0;
+    int soon = -1;       // row of the cache to be fetched into L2 next (lane's box of this CTA's keys)
+    Part part;
+    for (int item = 0; read_part(item, part); leave_part(item), ++item) {
+      const int32_t* table = p.c.page_table + (size_t)part.b * p.c.max_pages;
+      const int box0 = part.tile0 * boxes, last = (part.tile0 + part.count) * kTile;
+      int page = -1, page_before = -1;  // lanes: of the 32 boxes under way, of the 32 before
+      int window = -1;                  // which 32 boxes `page` is of
+      auto find_pages = [&](int i) {
+        if ((i * boxes) >> 5 == window) return;
+        window = (i * boxes) >> 5;
+        page_before = page;
+        const int pos = (box0 + window * 32 + lane) * rows_per_box;
+        page = -1;
+        if (pos < part.end && pos < last) {
+          page = fresh(table + pos / p.c.page_size);
+          if (page < 0 || page >= p.c.num_pages) {
+            raise_status(p.dev_status, KDA_DEV_BAD_PAGE);
+            page = -1;
+          }
+        }
+      };
+      // row of the cache where `box` (per lane) of the part's key tile i starts; past the end: zeros
+      auto cache_row = [&](int i, int box) {
+        const int at = i * boxes + box;
+        const int now = __shfl_sync(0xffffffffu, page, at & 31);
+        const int then = __shfl_sync(0xffffffffu, page_before, at & 31);
+        const int pg = (at >> 5) == window ? now : then;
+        const int pos = (box0 + at) * rows_per_box;
+        return pg >= 0 ? pg * p.c.page_size + pos % p.c.page_size : p.c.num_pages * p.c.page_size;
+      };
+      // Rows of a later key tile (this part's, or the next one's where its note is there) are fetched into
+      // L2: copies wait for room in the rings, which a key tile fills, and HBM is further away than that.
+      // A tile's page is looked up one tile before it is needed.
+      auto fetch_ahead = [&](int i) {
+        if (soon >= 0)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.c.rows + (size_t)soon * kLatentRow),
+                       "r"(rows_per_box * kLatentRow * 2)
+                       : "memory");
+        soon = -1;
+        int at = i + kAhead, b = part.b, tile0 = part.tile0, count = part.count, end = part.end;
+        if (at >= count) {
+          if (!__all_sync(0xffffffffu, mbar_try(smem_u32(&sm.part_full[(item + 1) % kNotes]), ((item + 1) / kNotes) & 1)))
+            return;
+          const Part& next = sm.part[(item + 1) % kNotes];
+          at -= count;
+          b = next.b;
+          tile0 = next.tile0;
+          count = next.count;
+          end = next.end;
+        }
+        const int pos = (tile0 + at) * kTile + rank * kHalf + lane * rows_per_box;
+        if (at < count && lane < half_boxes && pos < end) {
+          const int pg = fresh(p.c.page_table + (size_t)b * p.c.max_pages + pos / p.c.page_size);
+          if (pg >= 0 && pg < p.c.num_pages) soon = pg * p.c.page_size + pos % p.c.page_size;
+        }
+      };
+      for (int i = 0; i <= part.count && ok; ++i) {
+        if (i < part.count) {
+          find_pages(i);
+          const int row = cache_row(i, rank * half_boxes + in);
+#pragma unroll 1
+          for (int k = 0; k < kKeys && ok; ++k, ++key_put) {
+            const int s = key_put % kKeys;
+            if (key_put >= kKeys) ok = wait_pair(&sm.key_empty[s], (key_put / kKeys - 1) & 1);
+            if (!ok) break;
+            if (lane == 0) mbar_expect_tx(&sm.key_full[s], kKeyBytes);
+            __syncwarp();
+            if (panel < kKeyPanels)
+              tma_load_2d(sm.key[s] + panel * kPanelBytes + in * rows_per_box * 128, &rows_map, &sm.key_full[s],
+                          (k * kKeyPanels + panel) * 64, row);
+          }
+          fetch_ahead(i);
+        }
+        if (i > 0 && ok) {
+          const int row_lo = cache_row(i - 1, in), row_hi = cache_row(i - 1, half_boxes + in);
+#pragma unroll 1
+          for (int v = 0; v < kValues && ok; ++v, ++value_put) {  // this CTA's columns of half the keys
+            const int s = value_put % kValues;
+            if (value_put >= kValues) ok = wait_pair(&sm.value_empty[s], (value_put / kValues - 1) & 1);
+            if (!ok) break;
+            if (lane == 0) mbar_expect_tx(&sm.value_full[s], kValueBytes);
+            __syncwarp();
+            if (panel < kValuePanels)
+              tma_load_2d(sm.value[s] + panel * kPanelBytes + in * rows_per_box * 128, &rows_map, &sm.value_full[s],
+                          rank * (kLatent / 2) + panel * 64, v ? row_hi : row_lo);
+          }
+        }
+      }
+      if (!ok) break;
+    }
     if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
     // Every copy lands before the CTA's memory is released, also when a wait gave up.
     for (int u = max(0, key_put - kKeys); u < key_put; ++u) mbar_wait(&sm.key_full[u % kKeys], (u / kKeys) & 1);
@@ -414,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t q0 = smem_u32(sm.q[0]), key0 = smem_u32(sm.key[0]), value0 = smem_u32(sm.value[0]),
                    p0 = smem_u32(sm.p[0]);
     const uint32_t idesc_s = idesc_bf16(kTile, kRows, false, false), idesc_o = idesc_bf16(256, kRows, false, true);
-    int keys = 0, values = 0, task = 0;  // panels, value units and key tiles so far
+    int keys = 0, values = 0, task = 0;  // units and key tiles so far
     Part part;
     for (int item = 0; read_part(item, part); leave_part(item), ++item) {
       if (rank != 0) continue;
@@ -424,18 +457,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i < count) {
           const uint32_t s_col = base + kColS + (uint32_t)((task + i) & 1) * kHalf;
 #pragma unroll 1
-          for (int pn = 0; pn < kPanels && ok; ++pn, ++keys) {
+          for (int k = 0; k < kKeys && ok; ++k, ++keys) {
             const int s = keys % kKeys;
             ok = wait_pair(&sm.key_ready[s], (keys / kKeys) & 1);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-              const uint64_t a = smem_desc_sw128(q0 + pn * kPanelBytes, 16, 1024);
-              const uint64_t k = smem_desc_sw128(key0 + s * kPanelBytes, 16, 1024);
+              const uint64_t a = smem_desc_sw128(q0 + k * kKeyBytes, 16, 1024);
+              const uint64_t b = smem_desc_sw128(key0 + s * kKeyBytes, 16, 1024);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) mma_bf16_pair(s_col, a + 2 * j, k + 2 * j, idesc_s, pn + j > 0 ? 1u : 0u);
+              for (int j = 0; j < 4 * kKeyPanels; ++j) {  // 32 bytes on, or the next panel
+                const uint64_t at = (j & 3) * 2 + (j >> 2) * (kPanelBytes / 16);
+                mma_bf16_pair(s_col, a + at, b + at, idesc_s, k + j > 0 ? 1u : 0u);
+              }
               mma_commit_pair(&sm.key_empty[s]);
-              if (pn == kPanels - 1) {
+              if (k == kKeys - 1) {
                 mma_commit_pair(&sm.s_full[(task + i) & 1]);
                 if (i == count - 1) mma_commit_pair(&sm.q_empty);
               }
@@ -448,20 +484,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (i == 1 && item > 0) ok = wait_pair(&sm.o_free, (item - 1) & 1);
           ok = ok && wait_pair(&sm.p_ready, g & 1);
 #pragma unroll 1
-          for (int v = 0; v < kValuesPerTile && ok; ++v, ++values) {
+          for (int v = 0; v < kValues && ok; ++v, ++values) {
             const int s = values % kValues;
             ok = wait_pair(&sm.value_ready[s], (values / kValues) & 1);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-              const uint64_t a = smem_desc_sw128(p0 + (v >> 1) * kPanelBytes, 16, 1024);
-              const uint64_t c = smem_desc_sw128(value0 + s * 2 * kPanelBytes, kPanelBytes, 1024);
+              const uint64_t a = smem_desc_sw128(p0 + v * kPanelBytes, 16, 1024);
+              const uint64_t c = smem_desc_sw128(value0 + s * kValueBytes, kPanelBytes, 1024);
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                mma_bf16_pair(base + kColO + (v & 1) * 128, a + 2 * j, c + ((j * 16 * 128) >> 4), idesc_o,
-                              i > 1 || v > 1 || j > 0 ? 1u : 0u);
+              for (int j = 0; j < 8; ++j)  // 16 keys, then this CTA's next 128 columns
+                mma_bf16_pair(base + kColO + (j >> 2) * 128, a + 2 * (j & 3),
+                              c + (((j & 3) * 16 * 128) >> 4) + (j >> 2) * (2 * kPanelBytes / 16), idesc_o,
+                              i > 1 || v > 0 || (j & 3) > 0 ? 1u : 0u);
               mma_commit_pair(&sm.value_empty[s]);
-              if (v == kValuesPerTile - 1) mma_commit_pair(&sm.o_done);
+              if (v == kValues - 1) mma_commit_pair(&sm.o_done);
             }
             __syncwarp();
           }
@@ -479,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int keys = 0;
     Part part;
     for (int item = 0; read_part(item, part); leave_part(item), ++item) {
-      const int all = keys + part.count * kPanels;
+      const int all = keys + part.count * kKeys;
       for (; keys < all && ok; ++keys) {
         const int s = keys % kKeys;
         ok = wait_pair(&sm.key_full[s], (keys / kKeys) & 1);
@@ -517,19 +554,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < part.count && ok; ++i) {
         const int start = (part.tile0 + i) * kTile;
 #pragma unroll 1
-        for (int v = 0; v < kValuesPerTile && ok; ++v, ++values) {
+        for (int v = 0; v < kValues && ok; ++v, ++values) {
           const int s = values % kValues;
           ok = wait_pair(&sm.value_full[s], (values / kValues) & 1);
           if (!ok) break;
           if (start + kTile > part.whole) {
-            // A quarter of the unit's 64 keys, two panels of eight chunks each.  0 x NaN would reach
+            // A quarter of the unit's 64 keys, four panels of eight chunks each.  0 x NaN would reach
             // rows that do not see it; rows that do have a score that is not finite.
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
+#pragma unroll 8
+            for (int k = 0; k < 16; ++k) {
               const int n = k * 32 + lane, key = wv * 16 + ((n >> 3) & 15);
               uint4* x = reinterpret_cast<uint4*>(sm.value[s] + (n >> 7) * kPanelBytes + swizzled<128>(key, n & 7));
               const uint4 y = *x;
-              const uint4 z = start + (v >> 1) * kHalf + key < part.L ? finite(y) : make_uint4(0, 0, 0, 0);
+              const uint4 z = start + v * kHalf + key < part.L ? finite(y) : make_uint4(0, 0, 0, 0);
               if (y.x != z.x || y.y != z.y || y.z != z.z || y.w != z.w) *x = z;
             }
             fence_proxy_async_smem();
