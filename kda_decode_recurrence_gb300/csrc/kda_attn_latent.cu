@@ -48,9 +48,9 @@ constexpr int kAhead = 2;           // key tiles that are fetched into L2 before
 constexpr int kNotes = 4;           // items whose notes are kept
 constexpr int kItemCost = 2;        // what an item's beginning and end take, in key tiles
 constexpr float kGrow = 8.f;        // growth of a maximum (log 2) that rescales O
-// Warps: 0-3 the softmax, 4 the products (of the pair's first CTA), 5 the copies, 6 passes on that
-// keys are there, 7 finds the share's items, 8-11 load queries and pass on values.
-constexpr int kMmaWarp = 4, kCopyWarp = 5, kKeyWarp = 6, kItemWarp = 7, kValueWarp = 8, kWarps = 12;
+// Warps: 0-3 the softmax, 4 the products (of the pair's first CTA), 5 copies keys, 6 values, 7 finds the
+// share's items, 8-11 load queries and pass on values.
+constexpr int kMmaWarp = 4, kKeyWarp = 5, kCopyWarp = 6, kItemWarp = 7, kValueWarp = 8, kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
 constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256;
 
@@ -78,10 +78,10 @@ struct Smem {
   int first_request;
   uint32_t tmem;
   // this CTA's own
-  uint64_t key_full[kKeys], key_empty[kKeys], value_full[kValues], value_empty[kValues];
+  uint64_t key_empty[kKeys], value_full[kValues], value_empty[kValues];
   uint64_t part_full[kNotes], part_empty[kNotes];
   uint64_t s_full[2], o_done, q_empty, halves[2], done;
-  // the first CTA's, arrived at by both
+  // the first CTA's, arrived at by both (key_ready: by both CTAs' copies)
   uint64_t key_ready[kKeys], value_ready[kValues], q_ready, p_ready, o_free;
 };
 
@@ -163,9 +163,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < kKeys; ++s) {
-      mbar_init(&sm.key_full[s], 1);
       mbar_init(&sm.key_empty[s], 1);
-      mbar_init(&sm.key_ready[s], 2);
+      mbar_init(&sm.key_ready[s], 1);
     }
     for (int s = 0; s < kValues; ++s) {
       mbar_init(&sm.value_full[s], 1);
@@ -340,48 +339,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (ok) put_note(Part{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0});
     if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
-  } else if (warp == kCopyWarp) {
-    // ---- keys and values into the rings
+  } else if (warp == kKeyWarp || warp == kCopyWarp) {
+    // ---- keys or values into their ring
     const int rows_per_box = min(p.c.page_size, kHalf);
     const int half_boxes = kHalf / rows_per_box, boxes = 2 * half_boxes;  // of a half, of a key tile
     const int in = lane % half_boxes, panel = lane / half_boxes;          // of a unit's copies: lane's box and panel
-    int key_put = 0, value_put = 0;
-    int soon = -1;       // row of the cache to be fetched into L2 next (lane's box of this CTA's keys)
+    const bool keys = warp == kKeyWarp;
+    const uint32_t ready0 = cluster_addr(&sm.key_ready[0], 0);
+    int put = 0;
+    int soon = -1, soon_in = 0;  // page and position in it to be fetched into L2 next, by lane
     Part part;
     for (int item = 0; read_part(item, part); leave_part(item), ++item) {
       const int32_t* table = p.c.page_table + (size_t)part.b * p.c.max_pages;
-      const int box0 = part.tile0 * boxes, last = (part.tile0 + part.count) * kTile;
-      int page = -1, page_before = -1;  // lanes: of the 32 boxes under way, of the 32 before
-      int window = -1;                  // which 32 boxes `page` is of
-      auto find_pages = [&](int i) {
-        if ((i * boxes) >> 5 == window) return;
-        window = (i * boxes) >> 5;
-        page_before = page;
-        const int pos = (box0 + window * 32 + lane) * rows_per_box;
-        page = -1;
-        if (pos < part.end && pos < last) {
-          page = fresh(table + pos / p.c.page_size);
-          if (page < 0 || page >= p.c.num_pages) {
-            raise_status(p.dev_status, KDA_DEV_BAD_PAGE);
-            page = -1;
-          }
-        }
-      };
+      const int box0 = part.tile0 * boxes, last = min(part.end, (part.tile0 + part.count) * kTile);
+      int page = -1;  // of the 32 boxes under way, by lane
       // row of the cache where `box` (per lane) of the part's key tile i starts; past the end: zeros
       auto cache_row = [&](int i, int box) {
-        const int at = i * boxes + box;
-        const int now = __shfl_sync(0xffffffffu, page, at & 31);
-        const int then = __shfl_sync(0xffffffffu, page_before, at & 31);
-        const int pg = (at >> 5) == window ? now : then;
-        const int pos = (box0 + at) * rows_per_box;
+        const int at = i * boxes + box, pos = (box0 + at) * rows_per_box;
+        const int pg = __shfl_sync(0xffffffffu, page, at & 31);
         return pg >= 0 ? pg * p.c.page_size + pos % p.c.page_size : p.c.num_pages * p.c.page_size;
       };
       // Rows of a later key tile (this part's, or the next one's where its note is there) are fetched into
       // L2: copies wait for room in the rings, which a key tile fills, and HBM is further away than that.
       // A tile's page is looked up one tile before it is needed.
       auto fetch_ahead = [&](int i) {
-        if (soon >= 0)
-          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.c.rows + (size_t)soon * kLatentRow),
+        if (soon >= 0 && soon < p.c.num_pages)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                           p.c.rows + ((size_t)soon * p.c.page_size + soon_in) * kLatentRow),
                        "r"(rows_per_box * kLatentRow * 2)
                        : "memory");
         soon = -1;
@@ -398,33 +382,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int pos = (tile0 + at) * kTile + rank * kHalf + lane * rows_per_box;
         if (at < count && lane < half_boxes && pos < end) {
-          const int pg = fresh(p.c.page_table + (size_t)b * p.c.max_pages + pos / p.c.page_size);
-          if (pg >= 0 && pg < p.c.num_pages) soon = pg * p.c.page_size + pos % p.c.page_size;
+          soon = fresh(p.c.page_table + (size_t)b * p.c.max_pages + pos / p.c.page_size);
+          soon_in = pos % p.c.page_size;
         }
       };
-      for (int i = 0; i <= part.count && ok; ++i) {
-        if (i < part.count) {
-          find_pages(i);
+      for (int i = 0; i < part.count && ok; ++i) {
+        if (((i * boxes) & 31) == 0) {
+          const int pos = (box0 + i * boxes + lane) * rows_per_box;
+          page = -1;
+          if (pos < last) {
+            page = fresh(table + pos / p.c.page_size);
+            if (page < 0 || page >= p.c.num_pages) {
+              raise_status(p.dev_status, KDA_DEV_BAD_PAGE);
+              page = -1;
+            }
+          }
+        }
+        if (keys) {
+          // this CTA's half of the keys, three panels at a time; both CTAs' copies arrive at the first's barrier
           const int row = cache_row(i, rank * half_boxes + in);
 #pragma unroll 1
-          for (int k = 0; k < kKeys && ok; ++k, ++key_put) {
-            const int s = key_put % kKeys;
-            if (key_put >= kKeys) ok = wait_pair(&sm.key_empty[s], (key_put / kKeys - 1) & 1);
+          for (int k = 0; k < kKeys && ok; ++k, ++put) {
+            const int s = put % kKeys;
+            if (put >= kKeys) ok = wait_pair(&sm.key_empty[s], (put / kKeys - 1) & 1);
             if (!ok) break;
-            if (lane == 0) mbar_expect_tx(&sm.key_full[s], kKeyBytes);
+            if (rank == 0 && lane == 0) mbar_expect_tx(&sm.key_ready[s], 2 * kKeyBytes);
             __syncwarp();
             if (panel < kKeyPanels)
-              tma_load_2d(sm.key[s] + panel * kPanelBytes + in * rows_per_box * 128, &rows_map, &sm.key_full[s],
-                          (k * kKeyPanels + panel) * 64, row);
+              tma_load_2d_pair(sm.key[s] + panel * kPanelBytes + in * rows_per_box * 128, &rows_map, ready0 + 8 * s,
+                               (k * kKeyPanels + panel) * 64, row);
           }
           fetch_ahead(i);
-        }
-        if (i > 0 && ok) {
-          const int row_lo = cache_row(i - 1, in), row_hi = cache_row(i - 1, half_boxes + in);
+        } else {
+          // this CTA's columns, half of the keys at a time
+          const int row_lo = cache_row(i, in), row_hi = cache_row(i, half_boxes + in);
 #pragma unroll 1
-          for (int v = 0; v < kValues && ok; ++v, ++value_put) {  // this CTA's columns of half the keys
-            const int s = value_put % kValues;
-            if (value_put >= kValues) ok = wait_pair(&sm.value_empty[s], (value_put / kValues - 1) & 1);
+          for (int v = 0; v < kValues && ok; ++v, ++put) {
+            const int s = put % kValues;
+            if (put >= kValues) ok = wait_pair(&sm.value_empty[s], (put / kValues - 1) & 1);
             if (!ok) break;
             if (lane == 0) mbar_expect_tx(&sm.value_full[s], kValueBytes);
             __syncwarp();
@@ -437,10 +432,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
     }
     if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
-    // Every copy lands before the CTA's memory is released, also when a wait gave up.
-    for (int u = max(0, key_put - kKeys); u < key_put; ++u) mbar_wait(&sm.key_full[u % kKeys], (u / kKeys) & 1);
-    for (int u = max(0, value_put - kValues); u < value_put; ++u)
-      mbar_wait(&sm.value_full[u % kValues], (u / kValues) & 1);
+    // Every copy lands before the CTA's memory is released, also when a wait gave up (keys: the first CTA
+    // waits for both).
+    if (!keys)
+      for (int u = max(0, put - kValues); u < put; ++u) mbar_wait(&sm.value_full[u % kValues], (u / kValues) & 1);
+    else if (rank == 0)
+      for (int u = max(0, put - kKeys); u < put; ++u) mbar_wait(&sm.key_ready[u % kKeys], (u / kKeys) & 1);
   } else if (warp == kMmaWarp) {
     // ---- the products
     const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
@@ -511,21 +508,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rank == 0 && elect_one()) mma_commit_pair(&sm.done);  // arrives when every product issued has completed
     __syncwarp();
     mbar_wait(&sm.done, 0);
-  } else if (warp == kKeyWarp) {
-    // ---- keys that have arrived here, for the first CTA's products
-    int keys = 0;
-    Part part;
-    for (int item = 0; read_part(item, part); leave_part(item), ++item) {
-      const int all = keys + part.count * kKeys;
-      for (; keys < all && ok; ++keys) {
-        const int s = keys % kKeys;
-        ok = wait_pair(&sm.key_full[s], (keys / kKeys) & 1);
-        if (ok && lane == 0) mbar_arrive_cluster(cluster_addr(&sm.key_ready[s], 0));
-        __syncwarp();
-      }
-      if (!ok) break;
-    }
-    if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
   } else if (warp >= kValueWarp) {
     // ---- each item's queries; values that have arrived, without the entries that some row must not see
     const int at = tid - 32 * kValueWarp, wv = warp - kValueWarp;
