@@ -510,24 +510,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait(&sm.done, 0);
   } else if (warp >= kValueWarp) {
     // ---- each item's queries; values that have arrived, without the entries that some row must not see
-    const int at = tid - 32 * kValueWarp, wv = warp - kValueWarp;
+    const int wv = warp - kValueWarp;
     int values = 0;
     Part part;
     for (int item = 0; read_part(item, part); leave_part(item), ++item) {
+      // A warp takes 16 rows of the 64, 72 chunks each; lanes find a row's place each.
+      const int first = part.row0 + rank * kHalf + wv * 16;
+      const int live = (int)max(0ll, min(16ll, (long long)part.n * p.H - first));
+      const int token = (first + lane) / p.H;
+      const kda_bf16* mine = p.q;
+      if (lane < live) {
+        mine += (part.t0 + token) * p.q_stride + (size_t)(first + lane - token * p.H) * kLatentRow;
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(mine), "r"(kLatentRow * 2) : "memory");
+      }
       if (item > 0) ok = wait_pair(&sm.q_empty, (item - 1) & 1);
       if (!ok) break;
-      const int rows = (int)min((long long)kRows, (long long)part.n * p.H - part.row0);
 #pragma unroll 4
-      for (int i = 0; i < kHalf * kPanels * 8 / 128; ++i) {
-        const int n = i * 128 + at, row = n / (kPanels * 8), ch = n - row * (kPanels * 8);
-        const int in = rank * kHalf + row, flat = part.row0 + in;
-        const int token = flat / p.H, head = flat - token * p.H;
-        const bool live = in < rows;
-        const kda_bf16* src = p.q + (live ? (part.t0 + token) * p.q_stride + (size_t)head * kLatentRow + ch * 8 : 0);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                         smem_u32(sm.q[ch >> 3] + swizzled<128>(row, ch & 7))),
-                     "l"(src), "r"(live ? 16 : 0)
-                     : "memory");
+      for (int i = 0; i < 16; ++i) {
+        const int row = wv * 16 + i;
+        const kda_bf16* src = reinterpret_cast<const kda_bf16*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), i));
+        const uint32_t to = smem_u32(sm.q[lane >> 3] + swizzled<128>(row, lane & 7));
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          if (k < 2 || lane < 8)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + k * 4 * kPanelBytes),
+                         "l"(src + (k * 32 + lane) * 8), "r"(i < live ? 16 : 0)
+                         : "memory");
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
@@ -703,9 +712,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (to_rows[e] >= 0)
               *reinterpret_cast<uint4*>(p.out + (size_t)to_rows[e] * kLatent + col + 8 * (lane & 3)) = y[e];
         } else if (live) {
-          float4* to = reinterpret_cast<float4*>(pieces.o + piece * kLatent + col);
+          // [64 quarters of a half row][2 CTAs][128 threads]: the lanes of a warp write 512 bytes together
+          float4* to = reinterpret_cast<float4*>(pieces.o + (piece - in) * kLatent) + (cc / 4 * 2 + rank) * 128 + tid;
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) to[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int e = 0; e < 32; e += 4) to[e / 4 * 256] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
         __syncwarp();  // the next load is the whole warp's
       }
@@ -726,38 +736,46 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The pieces of one shared item into its outputs: with m = max m_i,
 //   o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i,   lse = (m + log2 l) ln 2.
-// CTA (c, y) takes rows of the item that pair c began, a row at a time: four columns a thread.
+// CTA (c, y) takes 16 columns from 16 (y / 2) on of either half of the 64 rows of the pair's CTA y % 2 in
+// the item that pair c began: thread (row, half) as in the softmax.
+constexpr int kJoinY = 32;
 __global__ void __launch_bounds__(128) latent_join_kernel(const LatentArgs p, const Pieces s) {
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const int c = blockIdx.x, rank = blockIdx.y & 1, cc = blockIdx.y >> 1;
   const PieceNote note = s.notes[c];
-  for (int row = blockIdx.y; row < note.tokens; row += gridDim.y) {
-    auto at = [&](int i) { return ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * kRows + row; };
-    float m = -INFINITY;
-    for (int i = lane; i < note.pieces; i += 32) m = fmaxf(m, s.ml[at(i)].x);
+  const int row = rank * kHalf + (threadIdx.x & (kHalf - 1));
+  if (row >= note.tokens) return;
+  auto at = [&](int i) { return ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * kRows; };
+  float m = -INFINITY, l = 0.f;
+  float4 o[4] = {};
+#pragma unroll 2
+  for (int i = 0; i < note.pieces; ++i) {
+    const float2 ml = s.ml[at(i) + row];
+    const float4* from = reinterpret_cast<const float4*>(s.o + at(i) * kLatent) + (cc * 8 + rank) * 128 + threadIdx.x;
+    float4 x[4];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < note.pieces; ++i) {
-      const float2 ml = s.ml[at(i)];
-      const float w = exp2_approx(ml.x - ref);
-      const float4 x = *reinterpret_cast<const float4*>(s.o + at(i) * kLatent + 4 * threadIdx.x);
-      l = fmaf(w, ml.y, l);
-      o.x = fmaf(w, x.x, o.x);
-      o.y = fmaf(w, x.y, o.y);
-      o.z = fmaf(w, x.z, o.z);
-      o.w = fmaf(w, x.w, o.w);
+    for (int e = 0; e < 4; ++e) x[e] = from[e * 256];
+    const float now = fmaxf(m, ml.x), ref = now == -INFINITY ? 0.f : now;
+    const float keep = exp2_approx(m - ref), w = exp2_approx(ml.x - ref);
+    m = now;
+    l = fmaf(w, ml.y, l * keep);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      o[e].x = fmaf(w, x[e].x, o[e].x * keep);
+      o[e].y = fmaf(w, x[e].y, o[e].y * keep);
+      o[e].z = fmaf(w, x[e].z, o[e].z * keep);
+      o[e].w = fmaf(w, x[e].w, o[e].w * keep);
     }
-    const size_t out_row = (size_t)note.row0 + row;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<uint2*>(p.out + out_row * kLatent + 4 * threadIdx.x) =
-        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    if (p.lse && threadIdx.x == 0) p.lse[out_row] = (m + log2f(l)) * kLn2;
   }
+  const size_t out_row = (size_t)note.row0 + row;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint4* to = reinterpret_cast<uint4*>(p.out + out_row * kLatent + (threadIdx.x >= kHalf ? kLatent / 2 : 0) + 16 * cc);
+#pragma unroll
+  for (int e = 0; e < 4; e += 2)
+    to[e / 2] = make_uint4(pack_bf16(o[e].x * inv, o[e].y * inv), pack_bf16(o[e].z * inv, o[e].w * inv),
+                           pack_bf16(o[e + 1].x * inv, o[e + 1].y * inv), pack_bf16(o[e + 1].z * inv, o[e + 1].w * inv));
+  if (p.lse && cc == 0 && threadIdx.x < kHalf) p.lse[out_row] = (m + log2f(l)) * kLn2;
 }
 
 }  // namespace
@@ -781,7 +799,7 @@ cudaError_t launch_latent_attention(const LatentArgs& a, cudaStream_t stream) {
   const Pieces pieces = pieces_at(a.workspace, kPairs, kRows);
   e = launch_pairs(latent_kernel, dim3(2 * kPairs), dim3(kThreads), smem, stream, map, a, pieces);
   if (e != cudaSuccess) return e;
-  return launch(latent_join_kernel, dim3(kPairs, 32), dim3(128), 0, stream, true, a, pieces);
+  return launch(latent_join_kernel, dim3(kPairs, kJoinY), dim3(128), 0, stream, true, a, pieces);
 }
 
 }  // namespace kda
