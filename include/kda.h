@@ -517,6 +517,40 @@ kda_status kda_latent_attention(kda_bf16* out, float* lse, const kda_bf16* q, co
 size_t kda_latent_attention_workspace_size(int B, int T, int H);
 
 /*
+ * kda_latent_expanded -- softmax attention of new tokens over expanded latents: every head has 128 key
+ * entries and 128 values of its own, and shares the 64 position entries (dense rows, no cache).
+ *
+ * Request b has n_b = cu_q[b+1] - cu_q[b] new tokens and L_b = cu_k[b+1] - cu_k[b] keys, the new tokens'
+ * own among them at the end: token i is at position p = L_b - n_b + i.  For p >= 0, head h:
+ *   x_j = scale (q[0..127] . k_j + q[128..191] . p_j)  for 0 <= j < L_b, and j <= p if causal
+ *   out = sum_j e^(x_j - m) v_j / sum_j e^(x_j - m),  m = max_j x_j;   lse = ln sum_j e^(x_j)
+ * A token that sees nothing (p < 0, or L_b = 0) gets out = 0, lse = -inf.  Accumulation and roundings
+ * are those of kda_paged_attention over a bf16 cache.  What a token does not see has no influence on it.
+ *
+ *   out          [Tq, H, 128] bf16, written.  Alignment 16 B.
+ *   lse          [Tq, H] fp32, written, or NULL.
+ *   q            [Tq, H, 192] bf16, q_stride elements between tokens (at least H * 192).
+ *   kv           [Tk, H, 256] bf16: key entries, then values; kv_stride (at least H * 256).
+ *   k_pe         [Tk, 64] bf16, pe_stride (at least 64; the last columns of latent rows need no copy).
+ *                Strides are multiples of 8, q, kv and k_pe aligned to 16 B.
+ *   cu_q, cu_k   [B + 1] int32, from 0 to Tq and to Tk, not decreasing (else KDA_DEV_BAD_SEQLEN; a
+ *                request with a bad range is skipped, its rows are not written).
+ *   scale        finite.       causal  0 or 1.       Tq * H < 2^30, Tk <= 2^30.
+ *   workspace    device scratch of kda_latent_expanded_workspace_size(...) bytes, 256-byte aligned,
+ *                contents need not be initialised.
+ */
+kda_status kda_latent_expanded(kda_bf16* out, float* lse, const kda_bf16* q, const kda_bf16* kv,
+                               const kda_bf16* k_pe, const int32_t* cu_q, const int32_t* cu_k,
+                               float scale, int causal, int B, int Tq, int Tk, int H,
+                               long long q_stride, long long kv_stride, long long pe_stride,
+                               void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                               void* stream);
+
+/* Bytes of device workspace kda_latent_expanded needs for these sizes (0 when the sizes are
+ * invalid).  Host-only, no CUDA call. */
+size_t kda_latent_expanded_workspace_size(int B, int Tq, int H);
+
+/*
  * kda_verify_draft -- accept a prefix of each request's drafted tokens and draw
  * the token after it, so that the tokens are distributed as the target's.
  *

@@ -589,6 +589,51 @@ def kda_latent_attention(out, q, cache, cu_seqlens, seq_lens, page_table, scale=
     return _finish(rc, status, "kda_latent_attention", check, check_device, stream)
 
 
+def latent_expanded_workspace_size(B, Tq, H) -> int:
+    return int(_lib.load().kda_latent_expanded_workspace_size(B, Tq, H))
+
+
+def kda_latent_expanded(out, q, kv, k_pe, cu_q, cu_k, scale=None, causal=True, lse=None,
+                        workspace=None, dev_status=None, stream=None, check=True,
+                        check_device=False) -> torch.Tensor:
+    """Softmax attention of prompts' tokens over keys and values expanded from their latents
+    (see include/kda.h).
+
+    Shapes: out [Tq, H, 128] bf16; q [Tq, H, 192] bf16 (128 entries against a head's keys, 64
+    against the shared ones); kv [Tk, H, 256] bf16 (keys, then values); k_pe [Tk, 64] bf16; tokens
+    of q, kv and k_pe may be strided; cu_q, cu_k [B+1] int32: request b's tokens and keys, the
+    tokens' own keys at the end of them; lse [Tq, H] fp32 or None.  ``scale`` defaults to
+    192 ** -0.5.  ``workspace`` is a uint8 CUDA tensor of at least
+    latent_expanded_workspace_size(...) bytes; when None one is allocated here.
+    """
+    dev = q.device
+    if q.dim() != 3 or kv.dim() != 3 or k_pe.dim() != 2:
+        raise ValueError(f"q {tuple(q.shape)}, kv {tuple(kv.shape)}, k_pe {tuple(k_pe.shape)} must be "
+                         f"[Tq, H, {EXPANDED + LATENT_ROPE}], [Tk, H, {2 * EXPANDED}], [Tk, {LATENT_ROPE}]")
+    Tq, H = q.shape[0], q.shape[1]
+    Tk = kv.shape[0]
+    qs = _check_rows(q, "q", H, EXPANDED + LATENT_ROPE, dev)
+    ks = _check_rows(kv, "kv", H, 2 * EXPANDED, dev)
+    ps = _check_rows(k_pe.unsqueeze(1), "k_pe", 1, LATENT_ROPE, dev)
+    if k_pe.shape[0] != Tk:
+        raise ValueError(f"kv has {Tk} tokens, k_pe {k_pe.shape[0]}")
+    _check_outputs(out, lse, Tq, H, EXPANDED, dev)
+    for t, n in ((cu_q, "cu_q"), (cu_k, "cu_k")):
+        _check(t, n, torch.int32, dev)
+    B = cu_q.numel() - 1
+    if B < 0 or cu_k.numel() != B + 1:
+        raise ValueError("cu_q and cu_k must have B + 1 entries")
+    _check_current(dev)
+    workspace = _workspace(workspace, latent_expanded_workspace_size(B, Tq, H), dev, stream)
+    status = _status_word(dev_status, dev, stream)
+    rc = _lib.load().kda_latent_expanded(
+        out.data_ptr(), _ptr(lse), q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), cu_q.data_ptr(),
+        cu_k.data_ptr(), float(_LATENT_SCALE if scale is None else scale), int(causal), B, Tq, Tk,
+        H, qs, ks, ps, workspace.data_ptr(), workspace.numel(), status.data_ptr(),
+        _stream_of(stream, dev))
+    return _finish(rc, status, "kda_latent_expanded", check, check_device, stream)
+
+
 def kda_verify_draft(tokens, accepted, target_probs, draft_probs, draft_tokens, accept_u, sample_u,
                      cu_drafts, dev_status=None, stream=None, check=True,
                      check_device=False) -> torch.Tensor:

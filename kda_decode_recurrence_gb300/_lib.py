@@ -18,7 +18,8 @@ EXPORTS = ("kda_decode", "kda_decode_ex", "kda_prefill", "kda_block_tkg", "kda_b
            "kda_block_tkg_workspace_size", "kda_cache_append", "kda_cache_read",
            "kda_paged_attention", "kda_paged_attention_workspace_size", "kda_tree_attention",
            "kda_tree_attention_workspace_size", "kda_latent_append", "kda_latent_attention",
-           "kda_latent_attention_workspace_size", "kda_verify_draft",
+           "kda_latent_attention_workspace_size", "kda_latent_expanded",
+           "kda_latent_expanded_workspace_size", "kda_verify_draft",
            "kda_status_string", "kda_version")
 
 STATUS = {
@@ -61,6 +62,10 @@ def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.kda_latent_attention.argtypes = [vp] * 8 + [f] + [i] * 8 + [ll, vp, ctypes.c_size_t, vp, vp]
     lib.kda_latent_attention_workspace_size.restype = ctypes.c_size_t
     lib.kda_latent_attention_workspace_size.argtypes = [i] * 3
+    lib.kda_latent_expanded.restype = i
+    lib.kda_latent_expanded.argtypes = [vp] * 7 + [f] + [i] * 5 + [ll] * 3 + [vp, ctypes.c_size_t, vp, vp]
+    lib.kda_latent_expanded_workspace_size.restype = ctypes.c_size_t
+    lib.kda_latent_expanded_workspace_size.argtypes = [i] * 3
     lib.kda_verify_draft.restype = i
     lib.kda_verify_draft.argtypes = [vp] * 8 + [i] * 3 + [ll, ll, vp, vp]
     lib.kda_status_string.restype = ctypes.c_char_p

@@ -476,6 +476,48 @@ kda_status kda_latent_attention(kda_bf16* out, float* lse, const kda_bf16* q, co
   return kda::launch_latent_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
+size_t kda_latent_expanded_workspace_size(int B, int Tq, int H) { return kda::expanded_workspace_bytes(B, Tq, H); }
+
+kda_status kda_latent_expanded(kda_bf16* out, float* lse, const kda_bf16* q, const kda_bf16* kv,
+                               const kda_bf16* k_pe, const int32_t* cu_q, const int32_t* cu_k,
+                               float scale, int causal, int B, int Tq, int Tk, int H,
+                               long long q_stride, long long kv_stride, long long pe_stride,
+                               void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                               void* stream) {
+  if (B < 0 || Tq < 0 || Tk < 0 || H < 1 || q_stride < (long long)H * (kda::kExpanded + kda::kRope) ||
+      kv_stride < (long long)H * 2 * kda::kExpanded || pe_stride < kda::kRope)
+    return KDA_ERR_SHAPE;
+  if ((long long)Tq * H > 0x3fffffffLL || Tk > 0x40000000) return KDA_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale) || (causal != 0 && causal != 1)) return KDA_ERR_VALUE;
+  if (B == 0 || Tq == 0) return KDA_OK;
+  if (!out || !q || !cu_q || !cu_k || (Tk > 0 && (!kv || !k_pe))) return KDA_ERR_NULL;
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(kv, 16) || !aligned(k_pe, 16) || q_stride % 8 != 0 ||
+      kv_stride % 8 != 0 || pe_stride % 8 != 0 || !aligned(lse, 4) || !aligned(cu_q, 4) || !aligned(cu_k, 4))
+    return KDA_ERR_ALIGN;
+  if (!workspace || workspace_bytes < kda::expanded_workspace_bytes(B, Tq, H)) return KDA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return KDA_ERR_ALIGN;
+  kda::ExpandedArgs a = {};
+  a.out = out;
+  a.lse = lse;
+  a.q = q;
+  a.kv = kv;
+  a.k_pe = k_pe;
+  a.q_stride = q_stride;
+  a.kv_stride = kv_stride;
+  a.pe_stride = pe_stride;
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.scale = scale;
+  a.causal = causal;
+  a.B = B;
+  a.Tq = Tq;
+  a.Tk = Tk;
+  a.H = H;
+  a.workspace = workspace;
+  a.dev_status = dev_status;
+  return kda::launch_latent_expanded(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
 kda_status kda_verify_draft(int32_t* tokens, int32_t* accepted, const float* target_probs,
                             const float* draft_probs, const int32_t* draft_tokens,
                             const float* accept_u, const float* sample_u, const int32_t* cu_drafts,

@@ -43,7 +43,8 @@ constexpr int kPanelBytes = kHalf * 128;
 // A unit of keys is three panels (64 keys x 192 entries), one of values four (64 keys x this CTA's 256
 // columns); the rings hold a key tile's.
 constexpr int kKeyPanels = 3, kKeys = kPanels / kKeyPanels, kKeyBytes = kKeyPanels * kPanelBytes;
-constexpr int kValuePanels = 4, kValues = 2, kValueBytes = kValuePanels * kPanelBytes;
+constexpr int kValuePanels = 4, kValues = 8 / kValuePanels, kValueBytes = kValuePanels * kPanelBytes;
+constexpr int kValueSplit = 4 / kValuePanels;  // units of half the keys
 constexpr int kAhead = 2;           // key tiles that are fetched into L2 before their copies
 constexpr int kNotes = 4;           // items whose notes are kept
 constexpr int kItemCost = 2;        // what an item's beginning and end take, in key tiles
@@ -425,7 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (panel < kValuePanels)
               tma_load_2d(sm.value[s] + panel * kPanelBytes + in * rows_per_box * 128, &rows_map, &sm.value_full[s],
-                          rank * (kLatent / 2) + panel * 64, v ? row_hi : row_lo);
+                          rank * (kLatent / 2) + (v % kValueSplit * kValuePanels + panel) * 64,
+                          v / kValueSplit ? row_hi : row_lo);
           }
         }
       }
@@ -487,13 +489,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-              const uint64_t a = smem_desc_sw128(p0 + v * kPanelBytes, 16, 1024);
+              const uint64_t a = smem_desc_sw128(p0 + v / kValueSplit * kPanelBytes, 16, 1024);
               const uint64_t c = smem_desc_sw128(value0 + s * kValueBytes, kPanelBytes, 1024);
 #pragma unroll
-              for (int j = 0; j < 8; ++j)  // 16 keys, then this CTA's next 128 columns
-                mma_bf16_pair(base + kColO + (j >> 2) * 128, a + 2 * (j & 3),
+              for (int j = 0; j < 2 * kValuePanels; ++j)  // 16 keys, then this CTA's next 128 columns
+                mma_bf16_pair(base + kColO + (v % kValueSplit + (j >> 2)) * 128, a + 2 * (j & 3),
                               c + (((j & 3) * 16 * 128) >> 4) + (j >> 2) * (2 * kPanelBytes / 16), idesc_o,
-                              i > 1 || v > 0 || (j & 3) > 0 ? 1u : 0u);
+                              i > 1 || v >= kValueSplit || (j & 3) > 0 ? 1u : 0u);
               mma_commit_pair(&sm.value_empty[s]);
               if (v == kValues - 1) mma_commit_pair(&sm.o_done);
             }
@@ -553,11 +555,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // A quarter of the unit's 64 keys, four panels of eight chunks each.  0 x NaN would reach
             // rows that do not see it; rows that do have a score that is not finite.
 #pragma unroll 8
-            for (int k = 0; k < 16; ++k) {
+            for (int k = 0; k < 4 * kValuePanels; ++k) {
               const int n = k * 32 + lane, key = wv * 16 + ((n >> 3) & 15);
               uint4* x = reinterpret_cast<uint4*>(sm.value[s] + (n >> 7) * kPanelBytes + swizzled<128>(key, n & 7));
               const uint4 y = *x;
-              const uint4 z = start + v * kHalf + key < part.L ? finite(y) : make_uint4(0, 0, 0, 0);
+              const uint4 z = start + v / kValueSplit * kHalf + key < part.L ? finite(y) : make_uint4(0, 0, 0, 0);
               if (y.x != z.x || y.y != z.y || y.z != z.z || y.w != z.w) *x = z;
             }
             fence_proxy_async_smem();

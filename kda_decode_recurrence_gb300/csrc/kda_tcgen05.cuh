@@ -226,6 +226,15 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t tmem_d, uint64_t adesc, u
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
 }
 
+// The same with A in tensor memory (M = 256: each CTA's 128 rows in its own).
+__device__ __forceinline__ void mma_bf16_pair_tmem_a(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                                     uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
 // Arrive once on `bar` of both CTAs when every MMA this thread issued so far has completed.
 __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
   asm volatile(
