@@ -42,6 +42,19 @@ __device__ __forceinline__ bool mbar_try(uint32_t addr, uint32_t parity) {
   return done != 0;
 }
 
+// Whether the phase with the given parity has completed, at once (a try_wait may put the thread to
+// sleep until it has).
+__device__ __forceinline__ bool mbar_test(uint32_t addr, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(addr), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // Wait until the phase with the given parity has completed; false once
 // limit_ns have passed without it.  The timer is read only when the phase is not
 // there at once (a read costs more than a wait that succeeds).

@@ -42,7 +42,7 @@ constexpr int D = kExpanded, kKeyWidth = kExpanded + kRope;
 constexpr int kPanels = kKeyWidth / 64;
 constexpr int kQPanel = kM * 128, kKeyPanel = kTile / 2 * 128;  // bytes: 128 rows, 64 keys
 constexpr int kKeyBytes = kPanels * kKeyPanel, kValueBytes = kTile * 128;
-constexpr int kKeys = 2;              // key units kept per slot (V: one)
+constexpr int kKeys = 1, kValues = 2; // units kept per slot
 constexpr int kNotes = 4;             // items whose notes are kept
 constexpr int kItemCost = 3;          // what an item's beginning and end take, in key tiles
 constexpr float kGrow = 8.f;          // growth of a maximum (log 2) that rescales O
@@ -66,7 +66,7 @@ constexpr int kBegins = 1, kEnds = 2;
 struct Slot {
   unsigned char q[kPanels][kQPanel];       // this CTA's 128 rows, 1024-aligned, swizzled panels
   unsigned char key[kKeys][kKeyBytes];     // its 64 keys of a tile
-  unsigned char value[kValueBytes];        // its 64 columns of a tile's values
+  unsigned char value[kValues][kValueBytes];  // its 64 columns of a tile's values
 };
 
 struct Smem {
@@ -78,10 +78,10 @@ struct Smem {
   int first_request[2];
   uint32_t tmem;
   // this CTA's own
-  uint64_t key_empty[2][kKeys], value_full[2], value_empty[2], q_empty[2], s_full[2], o_done[2];
+  uint64_t key_empty[2][kKeys], value_full[2][kValues], value_empty[2][kValues], q_empty[2], s_full[2], o_done[2];
   uint64_t part_full[2][kNotes], part_empty[2][kNotes], done;
   // the first CTA's (key_ready, q_ready: both CTAs' copies arrive; the others: both CTAs' warps)
-  uint64_t key_ready[2][kKeys], q_ready[2], value_ready[2], p_half[2], p_full[2];
+  uint64_t key_ready[2][kKeys], q_ready[2], value_ready[2][kValues], p_half[2], p_full[2];
 };
 
 struct Pairing {  // a request: tokens q0 .. q0 + n - 1, keys k0 .. k0 + L - 1
@@ -177,9 +177,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sm.key_empty[t][s], 1);
         mbar_init(&sm.key_ready[t][s], 1);
       }
-      mbar_init(&sm.value_full[t], 1);
-      mbar_init(&sm.value_empty[t], 1);
-      mbar_init(&sm.value_ready[t], 2);
+      for (int s = 0; s < kValues; ++s) {
+        mbar_init(&sm.value_full[t][s], 1);
+        mbar_init(&sm.value_empty[t][s], 1);
+        mbar_init(&sm.value_ready[t][s], 2);
+      }
       mbar_init(&sm.q_empty[t], 1);
       mbar_init(&sm.q_ready[t], 1);
       mbar_init(&sm.s_full[t], 1);
@@ -525,29 +527,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane < kPanels)
             tma_load_3d_pair(slot.q[lane], &q_map, q_ready, lane * 64, h, r.q0 + part.row0 + rank * kM);
-          for (int i = 0; i <= part.count && ok; ++i) {
-            if (i < part.count) {
-              // this CTA's half of the keys; both CTAs' copies arrive at the first's barrier
-              const int s = key_put % kKeys;
-              if (key_put >= kKeys) wait(&sm.key_empty[t][s], (key_put / kKeys - 1) & 1);
-              if (!ok) break;
-              ++key_put;
-              if (rank == 0 && lane == 0) mbar_expect_tx(&sm.key_ready[t][s], 2 * kKeyBytes);
-              __syncwarp();
-              const int at = r.k0 + (from + i) * kTile + rank * (kTile / 2);
-              if (lane < 2) tma_load_3d_pair(slot.key[s] + lane * kKeyPanel, &kv_map, key_ready + 8 * s, lane * 64, h, at);
-              else if (lane == 2) tma_load_3d_pair(slot.key[s] + 2 * kKeyPanel, &pe_map, key_ready + 8 * s, 0, 0, at);
-            }
-            if (i > 0) {  // this CTA's columns of all keys
-              if (value_put >= 1) wait(&sm.value_empty[t], (value_put - 1) & 1);
-              if (!ok) break;
-              ++value_put;
-              if (lane == 0) mbar_expect_tx(&sm.value_full[t], kValueBytes);
-              __syncwarp();
-              if (lane < 2)
-                tma_load_3d(slot.value + lane * kKeyPanel, &kv_map, &sm.value_full[t], D + rank * 64, h,
-                            r.k0 + (from + i - 1) * kTile + lane * (kTile / 2));
-            }
+          for (int i = 0; i < part.count; ++i) {
+            // this CTA's half of the keys; both CTAs' copies arrive at the first's barrier
+            const int s = key_put % kKeys, v = value_put % kValues, at = r.k0 + (from + i) * kTile;
+            if (key_put >= kKeys) wait(&sm.key_empty[t][s], (key_put / kKeys - 1) & 1);
+            if (!ok) break;
+            ++key_put;
+            if (rank == 0 && lane == 0) mbar_expect_tx(&sm.key_ready[t][s], 2 * kKeyBytes);
+            __syncwarp();
+            const int mine = at + rank * (kTile / 2);
+            if (lane < 2) tma_load_3d_pair(slot.key[s] + lane * kKeyPanel, &kv_map, key_ready + 8 * s, lane * 64, h, mine);
+            else if (lane == 2) tma_load_3d_pair(slot.key[s] + 2 * kKeyPanel, &pe_map, key_ready + 8 * s, 0, 0, mine);
+            // its columns of all values
+            if (value_put >= kValues) wait(&sm.value_empty[t][v], (value_put / kValues - 1) & 1);
+            if (!ok) break;
+            ++value_put;
+            if (lane == 0) mbar_expect_tx(&sm.value_full[t][v], kValueBytes);
+            __syncwarp();
+            if (lane < 2)
+              tma_load_3d(slot.value[v] + lane * kKeyPanel, &kv_map, &sm.value_full[t][v], D + rank * 64, h,
+                          at + lane * (kTile / 2));
           }
         }
         unit += kItemCost + all;
@@ -563,7 +562,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
       // Every copy lands before the CTA's memory is released, also when a wait gave up (keys and queries: the
       // first CTA waits for both).
-      if (value_put > 0) mbar_wait(&sm.value_full[t], (value_put - 1) & 1);
+      for (int u = max(0, value_put - kValues); u < value_put; ++u)
+        mbar_wait(&sm.value_full[t][u % kValues], (u / kValues) & 1);
       if (rank == 0) {
         for (int u = max(0, key_put - kKeys); u < key_put; ++u) mbar_wait(&sm.key_ready[t][u % kKeys], (u / kKeys) & 1);
         if (item > 0) mbar_wait(&sm.q_ready[t], (item - 1) & 1);
@@ -607,8 +607,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto output = [&](State& st, int t) {  // PV of the slot's S under way
         const uint32_t d = base + kColO + t * D, pc = base + t * kTile + 64;
-        const uint64_t v = smem_desc_sw128(smem_u32(sm.slot[t].value), kTile * 128, 1024);
-        wait(&sm.value_ready[t], st.tasks & 1);
+        const int s = st.tasks % kValues;
+        const uint64_t v = smem_desc_sw128(smem_u32(sm.slot[t].value[s]), kTile * 128, 1024);
+        wait(&sm.value_ready[t][s], (st.tasks / kValues) & 1);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (!wait(half ? &sm.p_full[t] : &sm.p_half[t], st.tasks & 1)) return;
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_bf16_pair_tmem_a(d, pc + 8 * j, v + ((j * 16 * 128) >> 4), idesc_o, !st.first || j > 0 ? 1u : 0u);
             if (half) {
               mma_commit_pair(&sm.o_done[t]);
-              mma_commit_pair(&sm.value_empty[t]);
+              mma_commit_pair(&sm.value_empty[t][s]);
             }
           }
           __syncwarp();
@@ -648,12 +649,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kValueWarp) {
       // ---- values that have arrived, without the entries that some row must not see; both slots' in
       // the order of their arrival
-      const uint32_t ready[2] = {cluster_addr(&sm.value_ready[0], 0), cluster_addr(&sm.value_ready[1], 0)};
+      const uint32_t ready[2] = {cluster_addr(sm.value_ready[0], 0), cluster_addr(sm.value_ready[1], 0)};
       Part part[2];
       int item[2] = {0, 0}, at[2] = {0, 0}, tasks[2] = {0, 0};
       bool have[2] = {false, false}, over[2] = {false, false};
       unsigned long long since = global_ns();
-      auto there = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_try(smem_u32(bar), parity)); };
+      auto there = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(smem_u32(bar), parity)); };
       while (ok && !(over[0] && over[1])) {
         bool moved = false;
 #pragma unroll
@@ -665,10 +666,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             at[t] = 0;
             moved = true;
           }
-          if (have[t] && there(&sm.value_full[t], tasks[t] & 1)) {
+          const int s = tasks[t] % kValues;
+          if (have[t] && there(&sm.value_full[t][s], (tasks[t] / kValues) & 1)) {
             const int start = (part[t].tile0 + at[t]) * kTile;
             if (start + kTile > part[t].whole) {
-              unsigned char* v = sm.slot[t].value;
+              unsigned char* v = sm.slot[t].value[s];
               const int to = part[t].L - start;  // the request's keys
               auto chunk = [&](int i) { return reinterpret_cast<uint4*>(v + swizzled<128>(i >> 3, i & 7)); };
               if (to < kTile) {
@@ -711,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               fence_proxy_async_smem();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(ready[t]);
+            if (lane == 0) mbar_arrive_cluster(ready[t] + 8 * s);
             ++tasks[t];
             if (++at[t] == part[t].count) {
               leave_part(t, item[t]++);
@@ -787,10 +789,16 @@ size_t expanded_workspace_bytes(int B, int Tq, int H) {
 cudaError_t launch_latent_expanded(const ExpandedArgs& a, cudaStream_t stream) {
   static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "a CTA fits an SM");
   CUtensorMap q_map, kv_map, pe_map;
-  if (!make_map_3d_bf16(&q_map, a.q, kKeyWidth, a.H, a.Tq, kKeyWidth * 2, (uint64_t)a.q_stride * 2, 64, 1, kM) ||
-      !make_map_3d_bf16(&kv_map, a.kv, 2 * D, a.H, a.Tk, 2 * D * 2, (uint64_t)a.kv_stride * 2, 64, 1, kTile / 2) ||
-      !make_map_3d_bf16(&pe_map, a.k_pe, kRope, 1, a.Tk, kRope * 2, (uint64_t)a.pe_stride * 2, 64, 1, kTile / 2))
+  auto q_like = [&](CUtensorMap* map, int rows) {
+    return make_map_3d_bf16(map, a.q, kKeyWidth, a.H, a.Tq, kKeyWidth * 2, (uint64_t)a.q_stride * 2, 64, 1, rows);
+  };
+  if (!q_like(&q_map, kM)) return cudaErrorInvalidValue;
+  if (a.Tk == 0) {  // no rows to make maps of: any will do, nobody sees a key
+    if (!q_like(&kv_map, kTile / 2) || !q_like(&pe_map, kTile / 2)) return cudaErrorInvalidValue;
+  } else if (!make_map_3d_bf16(&kv_map, a.kv, 2 * D, a.H, a.Tk, 2 * D * 2, (uint64_t)a.kv_stride * 2, 64, 1, kTile / 2) ||
+             !make_map_3d_bf16(&pe_map, a.k_pe, kRope, 1, a.Tk, kRope * 2, (uint64_t)a.pe_stride * 2, 64, 1, kTile / 2)) {
     return cudaErrorInvalidValue;
+  }
   const size_t smem = sizeof(Smem) + 1024;
   static SmemSet set;
   cudaError_t e = allow_smem(expanded_kernel, smem, set);

@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         soon = -1;
         int at = i + kAhead, b = part.b, tile0 = part.tile0, count = part.count, end = part.end;
         if (at >= count) {
-          if (!__all_sync(0xffffffffu, mbar_try(smem_u32(&sm.part_full[(item + 1) % kNotes]), ((item + 1) / kNotes) & 1)))
+          if (!__all_sync(0xffffffffu, mbar_test(smem_u32(&sm.part_full[(item + 1) % kNotes]), ((item + 1) / kNotes) & 1)))
             return;
           const Part& next = sm.part[(item + 1) % kNotes];
           at -= count;
