@@ -42,7 +42,7 @@ constexpr int D = kExpanded, kKeyWidth = kExpanded + kRope;
 constexpr int kPanels = kKeyWidth / 64;
 constexpr int kQPanel = kM * 128, kKeyPanel = kTile / 2 * 128;  // bytes: 128 rows, 64 keys
 constexpr int kKeyBytes = kPanels * kKeyPanel, kValueBytes = kTile * 128;
-constexpr int kKeys = 1, kValues = 2; // units kept per slot
+constexpr int kValues = 2;            // value units kept per slot (of keys: one)
 constexpr int kNotes = 4;             // items whose notes are kept
 constexpr int kItemCost = 3;          // what an item's beginning and end take, in key tiles
 constexpr float kGrow = 8.f;          // growth of a maximum (log 2) that rescales O
@@ -65,7 +65,7 @@ constexpr int kBegins = 1, kEnds = 2;
 
 struct Slot {
   unsigned char q[kPanels][kQPanel];       // this CTA's 128 rows, 1024-aligned, swizzled panels
-  unsigned char key[kKeys][kKeyBytes];     // its 64 keys of a tile
+  unsigned char key[kKeyBytes];            // its 64 keys of a tile
   unsigned char value[kValues][kValueBytes];  // its 64 columns of a tile's values
 };
 
@@ -77,11 +77,11 @@ struct Smem {
   long long first_unit[2];                 // of the requests that hold the streams' first units
   int first_request[2];
   uint32_t tmem;
-  // this CTA's own
-  uint64_t key_empty[2][kKeys], value_full[2][kValues], value_empty[2][kValues], q_empty[2], s_full[2], o_done[2];
+  // this CTA's own (s_full says too that the keys have been read, o_done that the values have)
+  uint64_t value_full[2][kValues], s_full[2], o_done[2][kValues], q_empty[2];
   uint64_t part_full[2][kNotes], part_empty[2][kNotes], done;
   // the first CTA's (key_ready, q_ready: both CTAs' copies arrive; the others: both CTAs' warps)
-  uint64_t key_ready[2][kKeys], q_ready[2], value_ready[2][kValues], p_half[2], p_full[2];
+  uint64_t key_ready[2], q_ready[2], value_ready[2][kValues], p_half[2], p_full[2];
 };
 
 struct Pairing {  // a request: tokens q0 .. q0 + n - 1, keys k0 .. k0 + L - 1
@@ -173,19 +173,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int t = 0; t < 2; ++t) {
-      for (int s = 0; s < kKeys; ++s) {
-        mbar_init(&sm.key_empty[t][s], 1);
-        mbar_init(&sm.key_ready[t][s], 1);
-      }
+      mbar_init(&sm.key_ready[t], 1);
       for (int s = 0; s < kValues; ++s) {
         mbar_init(&sm.value_full[t][s], 1);
-        mbar_init(&sm.value_empty[t][s], 1);
+        mbar_init(&sm.o_done[t][s], 1);
         mbar_init(&sm.value_ready[t][s], 2);
       }
       mbar_init(&sm.q_empty[t], 1);
       mbar_init(&sm.q_ready[t], 1);
       mbar_init(&sm.s_full[t], 1);
-      mbar_init(&sm.o_done[t], 1);
       mbar_init(&sm.p_half[t], 8);
       mbar_init(&sm.p_full[t], 8);
       for (int s = 0; s < kNotes; ++s) {
@@ -375,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         l2 = __fadd2_rn(l2, __fadd2_rn(sum0, sum1));
       }
-      if (!ok || !wait(&sm.o_done[t], (task - 1) & 1)) break;
+      if (!ok || !wait(&sm.o_done[t][(task - 1) % kValues], ((task - 1) / kValues) & 1)) break;
       // ---- the end of this stream's part of the item
       tc_fence_after();
       const float l = l2.x + l2.y;
@@ -437,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = warp - kCopyWarp;
       Slot& slot = sm.slot[t];
       const long long u0 = starts[t], u1 = end_of(t);
-      const uint32_t key_ready = cluster_addr(&sm.key_ready[t][0], 0), q_ready = cluster_addr(&sm.q_ready[t], 0);
+      const uint32_t key_ready = cluster_addr(&sm.key_ready[t], 0), q_ready = cluster_addr(&sm.q_ready[t], 0);
       int key_put = 0, value_put = 0, item = 0;
       auto put_note = [&](const Part& part) {
         if (item >= kNotes) wait(&sm.part_empty[t][item % kNotes], (item / kNotes - 1) & 1);
@@ -529,17 +525,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d_pair(slot.q[lane], &q_map, q_ready, lane * 64, h, r.q0 + part.row0 + rank * kM);
           for (int i = 0; i < part.count; ++i) {
             // this CTA's half of the keys; both CTAs' copies arrive at the first's barrier
-            const int s = key_put % kKeys, v = value_put % kValues, at = r.k0 + (from + i) * kTile;
-            if (key_put >= kKeys) wait(&sm.key_empty[t][s], (key_put / kKeys - 1) & 1);
+            const int v = value_put % kValues, at = r.k0 + (from + i) * kTile;
+            if (key_put > 0) wait(&sm.s_full[t], (key_put - 1) & 1);
             if (!ok) break;
             ++key_put;
-            if (rank == 0 && lane == 0) mbar_expect_tx(&sm.key_ready[t][s], 2 * kKeyBytes);
+            if (rank == 0 && lane == 0) mbar_expect_tx(&sm.key_ready[t], 2 * kKeyBytes);
             __syncwarp();
             const int mine = at + rank * (kTile / 2);
-            if (lane < 2) tma_load_3d_pair(slot.key[s] + lane * kKeyPanel, &kv_map, key_ready + 8 * s, lane * 64, h, mine);
-            else if (lane == 2) tma_load_3d_pair(slot.key[s] + 2 * kKeyPanel, &pe_map, key_ready + 8 * s, 0, 0, mine);
+            if (lane < 2) tma_load_3d_pair(slot.key + lane * kKeyPanel, &kv_map, key_ready, lane * 64, h, mine);
+            else if (lane == 2) tma_load_3d_pair(slot.key + 2 * kKeyPanel, &pe_map, key_ready, 0, 0, mine);
             // its columns of all values
-            if (value_put >= kValues) wait(&sm.value_empty[t][v], (value_put / kValues - 1) & 1);
+            if (value_put >= kValues) wait(&sm.o_done[t][v], (value_put / kValues - 1) & 1);
             if (!ok) break;
             ++value_put;
             if (lane == 0) mbar_expect_tx(&sm.value_full[t][v], kValueBytes);
@@ -565,87 +561,77 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = max(0, value_put - kValues); u < value_put; ++u)
         mbar_wait(&sm.value_full[t][u % kValues], (u / kValues) & 1);
       if (rank == 0) {
-        for (int u = max(0, key_put - kKeys); u < key_put; ++u) mbar_wait(&sm.key_ready[t][u % kKeys], (u / kKeys) & 1);
+        if (key_put > 0) mbar_wait(&sm.key_ready[t], (key_put - 1) & 1);
         if (item > 0) mbar_wait(&sm.q_ready[t], (item - 1) & 1);
       }
     } else if (warp == kMmaWarp && rank == 0) {
       // ---- the products of both slots
       const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
       const uint32_t idesc_s = idesc_bf16(kTile, kRows, false, false), idesc_o = idesc_bf16(D, kRows, false, true);
+      // A slot's items begun, key tiles of the last one left, key tiles whose PV has been issued; whether an S
+      // is under way (then its PV comes next), the item's first one.
       struct State {
-        int item = 0, left = 0, tasks = 0;
-        bool live = false, first = false;
-      } state[2];
-      auto scores = [&](State& st, int t) {  // the slot's next S
-        st.live = false;
-        if (st.left == 0) {
-          if (st.item > 0) leave_part(t, st.item - 1);
-          Part part;
-          if (!read_part(t, st.item, part)) return;
-          st.left = __shfl_sync(0xffffffffu, part.count, 0);
-          st.first = true;
-          wait(&sm.q_ready[t], st.item & 1);
-          ++st.item;
-        }
-        const int s = st.tasks % kKeys;
-        if (!wait(&sm.key_ready[t][s], (st.tasks / kKeys) & 1)) return;
-        tc_fence_after();
-        --st.left;
-        if (elect_one()) {
-          const uint64_t a = smem_desc_sw128(smem_u32(sm.slot[t].q[0]), 16, 1024);
-          const uint64_t k = smem_desc_sw128(smem_u32(sm.slot[t].key[s]), 16, 1024);
-#pragma unroll
-          for (int j = 0; j < kKeyWidth / 16; ++j)  // 32 bytes on, or the next panel
-            mma_bf16_pair(base + t * kTile, a + (j & 3) * 2 + (j >> 2) * (kQPanel / 16),
-                          k + (j & 3) * 2 + (j >> 2) * (kKeyPanel / 16), idesc_s, j > 0 ? 1u : 0u);
-          mma_commit_pair(&sm.s_full[t]);
-          mma_commit_pair(&sm.key_empty[t][s]);
-          if (st.left == 0) mma_commit_pair(&sm.q_empty[t]);
-        }
-        __syncwarp();
-        st.live = true;
+        int item, left, tasks;
+        bool live, first;
       };
-      auto output = [&](State& st, int t) {  // PV of the slot's S under way
+      State here{0, 0, 0, true, false}, there{0, 0, 0, true, false};  // slot t's, the other's
+      const uint32_t one = elect_one() ? 1u : 0u;
+      auto scores = [&](int t) {  // the slot's next S
+        here.live = false;
+        if (here.left == 0) {
+          if (here.item > 0) leave_part(t, here.item - 1);
+          Part part;
+          if (!read_part(t, here.item, part)) return;
+          here.left = __shfl_sync(0xffffffffu, part.count, 0);
+          here.first = true;
+          wait(&sm.q_ready[t], here.item & 1);
+          ++here.item;
+        }
+        if (!wait(&sm.key_ready[t], here.tasks & 1)) return;
+        tc_fence_after();
+        --here.left;
+        const uint64_t a = smem_desc_sw128(smem_u32(sm.slot[t].q[0]), 16, 1024);
+        const uint64_t k = smem_desc_sw128(smem_u32(sm.slot[t].key), 16, 1024);
+#pragma unroll
+        for (int j = 0; j < kKeyWidth / 16; ++j)  // 32 bytes on, or the next panel
+          mma_bf16_pair_if(one, base + t * kTile, a + (j & 3) * 2 + (j >> 2) * (kQPanel / 16),
+                           k + (j & 3) * 2 + (j >> 2) * (kKeyPanel / 16), idesc_s, j > 0 ? 1u : 0u);
+        mma_commit_pair_if(one, &sm.s_full[t]);
+        if (here.left == 0) mma_commit_pair_if(one, &sm.q_empty[t]);
+        here.live = true;
+      };
+      auto output = [&](int t) {  // PV of the slot's S under way
+        const int s = here.tasks % kValues;
         const uint32_t d = base + kColO + t * D, pc = base + t * kTile + 64;
-        const int s = st.tasks % kValues;
         const uint64_t v = smem_desc_sw128(smem_u32(sm.slot[t].value[s]), kTile * 128, 1024);
-        wait(&sm.value_ready[t][s], (st.tasks / kValues) & 1);
+        wait(&sm.value_ready[t][s], (here.tasks / kValues) & 1);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          if (!wait(half ? &sm.p_full[t] : &sm.p_half[t], st.tasks & 1)) return;
+          if (!wait(half ? &sm.p_full[t] : &sm.p_half[t], here.tasks & 1)) return;
           tc_fence_after();
-          if (elect_one()) {
 #pragma unroll
-            for (int j = 4 * half; j < 4 * half + 4; ++j)
-              mma_bf16_pair_tmem_a(d, pc + 8 * j, v + ((j * 16 * 128) >> 4), idesc_o, !st.first || j > 0 ? 1u : 0u);
-            if (half) {
-              mma_commit_pair(&sm.o_done[t]);
-              mma_commit_pair(&sm.value_empty[t][s]);
-            }
-          }
-          __syncwarp();
+          for (int j = 4 * half; j < 4 * half + 4; ++j)
+            mma_bf16_pair_tmem_a_if(one, d, pc + 8 * j, v + ((j * 16 * 128) >> 4), idesc_o,
+                                    !here.first || j > 0 ? 1u : 0u);
         }
-        st.first = false;
-        ++st.tasks;
+        mma_commit_pair_if(one, &sm.o_done[t][s]);
+        here.first = false;
+        ++here.tasks;
       };
-      scores(state[0], 0);
-      if (ok) scores(state[1], 1);
-      while (ok && (state[0].live || state[1].live)) {
-        if (state[0].live) {
-          output(state[0], 0);
-          if (ok) scores(state[0], 0);
+#pragma unroll 1
+      for (int step = 0; ok && (here.live || there.live); ++step) {
+        const int t = __shfl_sync(0xffffffffu, step & 1, 0);
+        if (here.live) {
+          if (step > 1) output(t);
+          if (ok) scores(t);
         }
-        if (ok && state[1].live) {
-          output(state[1], 1);
-          if (ok) scores(state[1], 1);
-        }
+        const State x = here;
+        here = there;
+        there = x;
       }
       if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
-      if (elect_one()) mma_commit_pair(&sm.done);  // arrives when every product issued has completed
-      __syncwarp();
+      mma_commit_pair_if(one, &sm.done);  // arrives when every product issued has completed
       mbar_wait(&sm.done, 0);
-    } else if (warp == kMmaWarp) {
-      mbar_wait(&sm.done, 0, 1000 * kWaitLimitNs);
     } else if (warp == kValueWarp) {
       // ---- values that have arrived, without the entries that some row must not see; both slots' in
       // the order of their arrival
@@ -732,7 +718,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   cluster_sync();  // nothing of the pair is under way
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
+  if (warp == kMmaWarp) {
+    mbar_wait(&sm.done, 0);  // (the second CTA's word of it)
+    __syncwarp();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
   __syncwarp();
   cluster_sync();
 }

@@ -226,13 +226,14 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t tmem_d, uint64_t adesc, u
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
 }
 
-// The same with A in tensor memory (M = 256: each CTA's 128 rows in its own).
-__device__ __forceinline__ void mma_bf16_pair_tmem_a(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
-                                                     uint32_t idesc, uint32_t accumulate) {
+// The same in a warp that runs together, by the lane whose `one` is set: a branch around a few products
+// costs some hundred cycles of issue, a predicate none.
+__device__ __forceinline__ void mma_bf16_pair_if(uint32_t one, uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                                 uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate));
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one));
 }
 
 // Arrive once on `bar` of both CTAs when every MMA this thread issued so far has completed.
@@ -241,6 +242,24 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
       "h"((uint16_t)3)
+      : "memory");
+}
+
+// The same with A in tensor memory (M = 256: each CTA's 128 rows in its own).
+__device__ __forceinline__ void mma_bf16_pair_tmem_a_if(uint32_t one, uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one));
+}
+
+__device__ __forceinline__ void mma_commit_pair_if(uint32_t one, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
+      " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3), "r"(one)
       : "memory");
 }
 
