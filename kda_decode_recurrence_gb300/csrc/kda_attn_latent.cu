@@ -43,11 +43,10 @@ constexpr int kPanelBytes = kHalf * 128;
 // A unit of keys is three panels (64 keys x 192 entries), one of values four (64 keys x this CTA's 256
 // columns); the rings hold a key tile's.
 constexpr int kKeyPanels = 3, kKeys = kPanels / kKeyPanels, kKeyBytes = kKeyPanels * kPanelBytes;
-constexpr int kValuePanels = 4, kValues = 8 / kValuePanels, kValueBytes = kValuePanels * kPanelBytes;
-constexpr int kValueSplit = 4 / kValuePanels;  // units of half the keys
+constexpr int kValuePanels = 4, kValues = 2, kValueBytes = kValuePanels * kPanelBytes;
 constexpr int kAhead = 2;           // key tiles that are fetched into L2 before their copies
 constexpr int kNotes = 4;           // items whose notes are kept
-constexpr int kItemCost = 2;        // what an item's beginning and end take, in key tiles
+constexpr int kItemCost = 3;        // what an item's beginning and end take, in key tiles
 constexpr float kGrow = 8.f;        // growth of a maximum (log 2) that rescales O
 // Warps: 0-3 the softmax, 4 the products (of the pair's first CTA), 5 copies keys, 6 values, 7 finds the
 // share's items, 8-11 load queries and pass on values.
@@ -78,8 +77,9 @@ struct Smem {
   long long first_unit;                     // of the request that holds the share's first unit
   int first_request;
   uint32_t tmem;
-  // this CTA's own
-  uint64_t key_empty[kKeys], value_full[kValues], value_empty[kValues];
+  // this CTA's own (a key tile's last unit of keys has been read when S is there, its last of values when PV
+  // is done)
+  uint64_t key_empty[kKeys - 1], value_full[kValues], value_empty[kValues - 1];
   uint64_t part_full[kNotes], part_empty[kNotes];
   uint64_t s_full[2], o_done, q_empty, halves[2], done;
   // the first CTA's, arrived at by both (key_ready: by both CTAs' copies)
@@ -164,12 +164,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < kKeys; ++s) {
-      mbar_init(&sm.key_empty[s], 1);
+      if (s < kKeys - 1) mbar_init(&sm.key_empty[s], 1);
       mbar_init(&sm.key_ready[s], 1);
     }
     for (int s = 0; s < kValues; ++s) {
       mbar_init(&sm.value_full[s], 1);
-      mbar_init(&sm.value_empty[s], 1);
+      if (s < kValues - 1) mbar_init(&sm.value_empty[s], 1);
       mbar_init(&sm.value_ready[s], 8);
     }
     for (int s = 0; s < kNotes; ++s) {
@@ -405,7 +405,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int k = 0; k < kKeys && ok; ++k, ++put) {
             const int s = put % kKeys;
-            if (put >= kKeys) ok = wait_pair(&sm.key_empty[s], (put / kKeys - 1) & 1);
+            const int before = put / kKeys - 1;  // the key tile whose place this unit takes
+            if (before >= 0)
+              ok = s < kKeys - 1 ? wait_pair(&sm.key_empty[s], before & 1)
+                                 : wait_pair(&sm.s_full[before & 1], (before >> 1) & 1);
             if (!ok) break;
             if (rank == 0 && lane == 0) mbar_expect_tx(&sm.key_ready[s], 2 * kKeyBytes);
             __syncwarp();
@@ -420,14 +423,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int v = 0; v < kValues && ok; ++v, ++put) {
             const int s = put % kValues;
-            if (put >= kValues) ok = wait_pair(&sm.value_empty[s], (put / kValues - 1) & 1);
+            const int before = put / kValues - 1;
+            if (before >= 0) ok = wait_pair(s < kValues - 1 ? &sm.value_empty[s] : &sm.o_done, before & 1);
             if (!ok) break;
             if (lane == 0) mbar_expect_tx(&sm.value_full[s], kValueBytes);
             __syncwarp();
             if (panel < kValuePanels)
               tma_load_2d(sm.value[s] + panel * kPanelBytes + in * rows_per_box * 128, &rows_map, &sm.value_full[s],
-                          rank * (kLatent / 2) + (v % kValueSplit * kValuePanels + panel) * 64,
-                          v / kValueSplit ? row_hi : row_lo);
+                          rank * (kLatent / 2) + panel * 64, v ? row_hi : row_lo);
           }
         }
       }
@@ -446,7 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t q0 = smem_u32(sm.q[0]), key0 = smem_u32(sm.key[0]), value0 = smem_u32(sm.value[0]),
                    p0 = smem_u32(sm.p[0]);
     const uint32_t idesc_s = idesc_bf16(kTile, kRows, false, false), idesc_o = idesc_bf16(256, kRows, false, true);
-    int keys = 0, values = 0, task = 0;  // units and key tiles so far
+    const uint32_t one = elect_one() ? 1u : 0u;
+    int task = 0;  // key tiles so far
     Part part;
     for (int item = 0; read_part(item, part); leave_part(item), ++item) {
       if (rank != 0) continue;
@@ -456,50 +460,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i < count) {
           const uint32_t s_col = base + kColS + (uint32_t)((task + i) & 1) * kHalf;
 #pragma unroll 1
-          for (int k = 0; k < kKeys && ok; ++k, ++keys) {
-            const int s = keys % kKeys;
-            ok = wait_pair(&sm.key_ready[s], (keys / kKeys) & 1);
+          for (int k = 0; k < kKeys && ok; ++k) {
+            ok = wait_pair(&sm.key_ready[k], (task + i) & 1);
             if (!ok) break;
             tc_fence_after();
-            if (elect_one()) {
-              const uint64_t a = smem_desc_sw128(q0 + k * kKeyBytes, 16, 1024);
-              const uint64_t b = smem_desc_sw128(key0 + s * kKeyBytes, 16, 1024);
+            const uint64_t a = smem_desc_sw128(q0 + k * kKeyBytes, 16, 1024);
+            const uint64_t b = smem_desc_sw128(key0 + k * kKeyBytes, 16, 1024);
 #pragma unroll
-              for (int j = 0; j < 4 * kKeyPanels; ++j) {  // 32 bytes on, or the next panel
-                const uint64_t at = (j & 3) * 2 + (j >> 2) * (kPanelBytes / 16);
-                mma_bf16_pair(s_col, a + at, b + at, idesc_s, k + j > 0 ? 1u : 0u);
-              }
-              mma_commit_pair(&sm.key_empty[s]);
-              if (k == kKeys - 1) {
-                mma_commit_pair(&sm.s_full[(task + i) & 1]);
-                if (i == count - 1) mma_commit_pair(&sm.q_empty);
-              }
+            for (int j = 0; j < 4 * kKeyPanels; ++j) {  // 32 bytes on, or the next panel
+              const uint64_t at = (j & 3) * 2 + (j >> 2) * (kPanelBytes / 16);
+              mma_bf16_pair_if(one, s_col, a + at, b + at, idesc_s, k + j > 0 ? 1u : 0u);
             }
-            __syncwarp();
+            mma_commit_pair_if(one, k < kKeys - 1 ? &sm.key_empty[k] : &sm.s_full[(task + i) & 1]);
           }
+          if (i == count - 1) mma_commit_pair_if(one, &sm.q_empty);
         }
         if (i > 0 && ok) {
           const int g = task + i - 1;
           if (i == 1 && item > 0) ok = wait_pair(&sm.o_free, (item - 1) & 1);
           ok = ok && wait_pair(&sm.p_ready, g & 1);
 #pragma unroll 1
-          for (int v = 0; v < kValues && ok; ++v, ++values) {
-            const int s = values % kValues;
-            ok = wait_pair(&sm.value_ready[s], (values / kValues) & 1);
+          for (int v = 0; v < kValues && ok; ++v) {
+            ok = wait_pair(&sm.value_ready[v], g & 1);
             if (!ok) break;
             tc_fence_after();
-            if (elect_one()) {
-              const uint64_t a = smem_desc_sw128(p0 + v / kValueSplit * kPanelBytes, 16, 1024);
-              const uint64_t c = smem_desc_sw128(value0 + s * kValueBytes, kPanelBytes, 1024);
+            const uint64_t a = smem_desc_sw128(p0 + v * kPanelBytes, 16, 1024);
+            const uint64_t c = smem_desc_sw128(value0 + v * kValueBytes, kPanelBytes, 1024);
 #pragma unroll
-              for (int j = 0; j < 2 * kValuePanels; ++j)  // 16 keys, then this CTA's next 128 columns
-                mma_bf16_pair(base + kColO + (v % kValueSplit + (j >> 2)) * 128, a + 2 * (j & 3),
-                              c + (((j & 3) * 16 * 128) >> 4) + (j >> 2) * (2 * kPanelBytes / 16), idesc_o,
-                              i > 1 || v >= kValueSplit || (j & 3) > 0 ? 1u : 0u);
-              mma_commit_pair(&sm.value_empty[s]);
-              if (v == kValues - 1) mma_commit_pair(&sm.o_done);
-            }
-            __syncwarp();
+            for (int j = 0; j < 8; ++j)  // 16 keys, then this CTA's next 128 columns
+              mma_bf16_pair_if(one, base + kColO + (j >> 2) * 128, a + 2 * (j & 3),
+                               c + (((j & 3) * 16 * 128) >> 4) + (j >> 2) * (2 * kPanelBytes / 16), idesc_o,
+                               i > 1 || v > 0 || (j & 3) > 0 ? 1u : 0u);
+            mma_commit_pair_if(one, v < kValues - 1 ? &sm.value_empty[v] : &sm.o_done);
           }
         }
       }
@@ -507,8 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
     }
     if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
-    if (rank == 0 && elect_one()) mma_commit_pair(&sm.done);  // arrives when every product issued has completed
-    __syncwarp();
+    if (rank == 0) mma_commit_pair_if(one, &sm.done);  // arrives when every product issued has completed
     mbar_wait(&sm.done, 0);
   } else if (warp >= kValueWarp) {
     // ---- each item's queries; values that have arrived, without the entries that some row must not see
@@ -555,11 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // A quarter of the unit's 64 keys, four panels of eight chunks each.  0 x NaN would reach
             // rows that do not see it; rows that do have a score that is not finite.
 #pragma unroll 8
-            for (int k = 0; k < 4 * kValuePanels; ++k) {
+            for (int k = 0; k < 16; ++k) {
               const int n = k * 32 + lane, key = wv * 16 + ((n >> 3) & 15);
               uint4* x = reinterpret_cast<uint4*>(sm.value[s] + (n >> 7) * kPanelBytes + swizzled<128>(key, n & 7));
               const uint4 y = *x;
-              const uint4 z = start + v / kValueSplit * kHalf + key < part.L ? finite(y) : make_uint4(0, 0, 0, 0);
+              const uint4 z = start + v * kHalf + key < part.L ? finite(y) : make_uint4(0, 0, 0, 0);
               if (y.x != z.x || y.y != z.y || y.z != z.z || y.w != z.w) *x = z;
             }
             fence_proxy_async_smem();
