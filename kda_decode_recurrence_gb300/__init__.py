@@ -428,10 +428,26 @@ def kda_paged_attention(out, q, k_cache, v_cache, cu_seqlens, seq_lens, page_tab
 
 def _check_current(device) -> None:
     """The calls run on the current device: its kernels cannot take another's tensors."""
-    if device.type != "cuda":
+    index = device.index
+    if index is None:
         raise ValueError(f"expected CUDA tensors, got {device}")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {device}, but the current device is {torch.cuda.current_device()}")
+    if index != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on {device}, but the current device is {torch._C._cuda_getDevice()}")
+
+
+def _check_matrix(t: torch.Tensor, name: str, width: int, device) -> int:
+    """A [T, width] bf16 tensor whose rows may be strided; returns the elements between two."""
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected device {device}, got {t.device}")
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != width:
+        raise ValueError(f"{name} shape {tuple(shape)} != [T, {width}]")
+    s = t.stride()
+    if s[1] != 1:
+        raise ValueError(f"{name}: a row must be contiguous (strides {s})")
+    return s[0] if shape[0] > 1 else width
 
 
 def _check_outputs(out, lse, T, H, D, device) -> None:
@@ -534,9 +550,7 @@ def kda_latent_append(cache, rows, cu_seqlens, seq_lens, page_table, gamma=None,
     """
     dev = cache.device
     B, page, N, max_pages = _check_latent(cache, page_table, cu_seqlens, "cu_seqlens")
-    if rows.dim() != 2:
-        raise ValueError(f"rows shape {tuple(rows.shape)} != [T, {LATENT_ROW}]")
-    stride = _check_rows(rows.unsqueeze(1), "rows", 1, LATENT_ROW, dev)
+    stride = _check_matrix(rows, "rows", LATENT_ROW, dev)
     _check_lens(seq_lens, B, dev)
     if gamma is not None:
         _check(gamma, "gamma", torch.float32, dev)
@@ -607,14 +621,14 @@ def kda_latent_expanded(out, q, kv, k_pe, cu_q, cu_k, scale=None, causal=True, l
     latent_expanded_workspace_size(...) bytes; when None one is allocated here.
     """
     dev = q.device
-    if q.dim() != 3 or kv.dim() != 3 or k_pe.dim() != 2:
-        raise ValueError(f"q {tuple(q.shape)}, kv {tuple(kv.shape)}, k_pe {tuple(k_pe.shape)} must be "
-                         f"[Tq, H, {EXPANDED + LATENT_ROPE}], [Tk, H, {2 * EXPANDED}], [Tk, {LATENT_ROPE}]")
+    if q.dim() != 3 or kv.dim() != 3:
+        raise ValueError(f"q {tuple(q.shape)}, kv {tuple(kv.shape)} must be "
+                         f"[Tq, H, {EXPANDED + LATENT_ROPE}], [Tk, H, {2 * EXPANDED}]")
     Tq, H = q.shape[0], q.shape[1]
     Tk = kv.shape[0]
     qs = _check_rows(q, "q", H, EXPANDED + LATENT_ROPE, dev)
     ks = _check_rows(kv, "kv", H, 2 * EXPANDED, dev)
-    ps = _check_rows(k_pe.unsqueeze(1), "k_pe", 1, LATENT_ROPE, dev)
+    ps = _check_matrix(k_pe, "k_pe", LATENT_ROPE, dev)
     if k_pe.shape[0] != Tk:
         raise ValueError(f"kv has {Tk} tokens, k_pe {k_pe.shape[0]}")
     _check_outputs(out, lse, Tq, H, EXPANDED, dev)
