@@ -92,3 +92,213 @@ def test_shapes(shape, causal):
 def test_trees(shape):
     case, q = make(shape)
     check(case, q, tree=trees(case.n, seed=5))
+
+
+@pytest.mark.parametrize("shape", [SHAPES[4], SHAPES[7], SHAPES[12]], ids=["token", "window", "rows"])
+@pytest.mark.parametrize("amplitude,scale", [(1.0, 3.0), (30.0, 1.0), (1e4, 1.0), (1.0, -0.3), (1.0, 0.0)])
+def test_scores_of_other_sizes(shape, amplitude, scale):
+    case, q = make(shape, seed=31)
+    q.mul_(amplitude)
+    check(case, q, scale=scale)
+
+
+@pytest.mark.parametrize("amplitude", [2.0 ** -100, 2.0 ** 50])
+def test_latents_of_extreme_size(amplitude):
+    case, q = make(SHAPES[7], seed=32)
+    case.cache.mul_(amplitude)
+    check(case, (q.float() / amplitude).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("n,lens,H", [(5, 70, 40), (8, 200, 16), (40, 130, 24)])
+def test_a_bad_row_reaches_only_the_tokens_that_see_it(n, lens, H, bad):
+    """A later token's latent row, or its position part, that is not finite."""
+    for at in (5, 300, 540):
+        case, q = make(dict(n=[n], lens=[lens], H=H, page=16), seed=33)
+        want, wlse, _ = attend(case, q)
+        i = (2 * n) // 3
+        pos = lens - n + i
+        case.cache[int(case.table[0, pos // 16]), pos % 16, at] = bad
+        out, lse, status = attend(case, q)
+        assert status == 0 and torch.equal(out[:i], want[:i]) and torch.equal(lse[:i], wlse[:i])
+        if bad != bad:
+            assert bool(torch.isnan(out[i:]).all())
+
+
+def test_a_bad_node_reaches_only_the_nodes_that_see_it():
+    n, L, H = 37, 150, 12
+    case, q = make(dict(n=[n], lens=[L], H=H, page=16), seed=34)
+    tree = trees([n], seed=3)
+    mask = mask_of(tree, 2)
+    want, wlse, _ = attend(case, q, mask=mask)
+    bad = 11
+    pos = L - n + bad
+    case.cache[int(case.table[0, pos // 16]), pos % 16] = float("nan")
+    out, lse, status = attend(case, q, mask=mask)
+    sees = torch.tensor([bad in s for s in tree[0]], device="cuda")
+    assert status == 0 and bool(sees.any()) and bool((~sees).any())
+    assert torch.equal(out[~sees], want[~sees]) and torch.equal(lse[~sees], wlse[~sees])
+    assert bool(torch.isnan(out[sees]).all())
+
+
+def test_masks_of_nothing_and_of_everything():
+    """A mask without bits sees what was cached before; nothing at all without any; one with all bits (those
+    past the request's last token are nobody's) is as without causality."""
+    case, q = make(dict(n=[5, 33, 1], lens=[5, 133, 40], H=24, page=16), seed=35)
+    none = torch.zeros(case.T, 2, dtype=torch.int32, device="cuda")
+    out, lse, status = attend(case, q, mask=none)
+    assert status == 0
+    close(out, lse, reference(case, q, tree=[[set()] * k for k in case.n]))
+    assert bool((out[:5] == 0).all()) and bool(torch.isneginf(lse[:5]).all())
+    full, flse, _ = attend(case, q, mask=none - 1)
+    want, wlse, _ = attend(case, q, causal=False)
+    assert torch.equal(full, want) and torch.equal(flse, wlse)
+    check(case, q, tree=trees(case.n, seed=9), words=7)
+
+
+def test_too_many_nodes_for_the_mask_are_reported():
+    case, q = make(dict(n=[3, 40, 2], lens=[30, 60, 90], H=8, page=16), seed=36)
+    mask = mask_of(trees(case.n), 2)[:, :1].contiguous()
+    out, lse, status = attend(case, q, mask=mask)
+    assert status == kda.DEV_BAD_SEQLEN
+    assert bool(torch.isnan(out[3:43]).all()) and bool(torch.isfinite(out[:3]).all()) and bool(torch.isfinite(out[43:]).all())
+
+
+def test_without_lse_and_on_another_stream():
+    case, q = make(SHAPES[12], seed=37)
+    want, _, _ = attend(case, q)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    out, _, status = attend(case, q, with_lse=False, stream=stream)
+    assert status == 0 and torch.equal(out, want)
+
+
+def test_same_bits_and_graphs_that_share_a_workspace():
+    """The same call gives the same bits; two graphs with one workspace, replayed in turn, with other lengths
+    than captured."""
+    calls = []
+    work = torch.empty(kda.latent_attention_workspace_size(8, 100, 64), dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for shape, tree in ((SHAPES[7], False), (SHAPES[10], True)):
+        case, q = make(shape, seed=38)
+        mask = mask_of(trees(case.n), 1) if tree else None
+        want, wlse, _ = attend(case, q, mask=mask)
+        again, alse, _ = attend(case, q, mask=mask)
+        assert torch.equal(want, again) and torch.equal(wlse, alse)
+        shorter = torch.clamp(case.seq_lens - 1, min=1)
+        less, llse, _ = attend(case, q, mask=mask, seq_lens=shorter)
+        lens, out, lse = case.seq_lens.clone(), torch.zeros_like(want), torch.zeros_like(wlse)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            kda.kda_latent_attention(out, q, case.cache, case.cu, lens, case.table, tree_mask=mask, lse=lse,
+                                     workspace=work, dev_status=status)
+        calls.append((graph, lens, case.seq_lens, shorter, out, lse, (want, wlse), (less, llse), case, q, mask))
+    for _ in range(3):
+        for graph, lens, long, short, out, lse, full, less, *_ in calls:
+            for now, (o, e) in ((long, full), (short, less)):
+                lens.copy_(now)
+                out.zero_()
+                graph.replay()
+                torch.cuda.synchronize()
+                assert torch.equal(out, o) and torch.equal(lse, e) and int(status.item()) == 0
+
+
+@pytest.mark.parametrize("n,H", [(1, 128), (1, 16), (6, 32)])
+def test_same_bits_when_copies_arrive_late(n, H):
+    """Long caches read through a cold L2 and through a warm one."""
+    lens, page = 9000, 64
+    g = torch.Generator(device="cuda").manual_seed(39)
+    pages = 20 * (-(-lens // page))
+    cache = torch.randn(pages, page, ROW, device="cuda", generator=g, dtype=torch.bfloat16)
+    table = torch.randperm(pages, device="cuda", generator=g).to(torch.int32).view(20, -1)
+    q = torch.randn(20 * n, H, ROW, device="cuda", generator=g, dtype=torch.bfloat16)
+    cu = torch.arange(21, dtype=torch.int32, device="cuda") * n
+    seq = torch.full((20,), lens, dtype=torch.int32, device="cuda")
+    flush = torch.empty(300 << 20, dtype=torch.uint8, device="cuda")
+    first = None
+    for trial in range(8):
+        if trial % 2 == 0:
+            flush.fill_(trial)
+        out, lse = torch.zeros(20 * n, H, LATENT, device="cuda", dtype=torch.bfloat16), torch.zeros(20 * n, H, device="cuda")
+        assert int(kda.kda_latent_attention(out, q, cache, cu, seq, table, lse=lse).item()) == 0
+        first = first or (out, lse)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1]), f"trial {trial}"
+
+
+@pytest.mark.parametrize("shape", [SHAPES[2], SHAPES[7], SHAPES[12]], ids=["token", "window", "rows"])
+def test_a_bad_page_counts_as_zero_rows(shape):
+    case, q = make(shape, seed=40)
+    table = case.table.clone()
+    table[0, 0] = case.num_pages
+    table[case.B - 1, 0] = -5
+    out, lse, status = attend(case, q, table=table)
+    assert status == kda.DEV_BAD_PAGE
+    close(out, lse, reference(case, q, table=table))
+
+
+def test_bad_lengths_and_offsets_are_reported_and_skipped():
+    """(The others are served, not always with the same bits: the call is cut elsewhere.)"""
+    case, q = make(dict(n=[9, 4, 2], lens=[90, 40, 300], H=20, page=16), seed=41)
+    want = reference(case, q)
+
+    def served(out, lse, *rows):
+        for r in rows:
+            close(out[r], lse[r], [x[r] for x in want])
+
+    for bad in (case.max_pages * 16 + 1, -1):
+        lens = case.seq_lens.clone()
+        lens[1] = bad
+        out, lse, status = attend(case, q, seq_lens=lens)
+        assert status == kda.DEV_BAD_SEQLEN and bool(torch.isnan(out[9:13]).all())
+        served(out, lse, slice(0, 9), slice(13, 15))
+    # request 1 ends before it begins (request 2 has row 8 for its first then, which is not looked at)
+    out, lse, status = attend(case, q, cu=torch.tensor([0, 9, 8, 15], dtype=torch.int32, device="cuda"))
+    assert status == kda.DEV_BAD_SEQLEN
+    served(out, lse, slice(0, 8))
+    # the last two rows are nobody's
+    out, lse, status = attend(case, q, cu=torch.tensor([0, 9, 13, 13], dtype=torch.int32, device="cuda"))
+    assert status == kda.DEV_BAD_SEQLEN and bool(torch.isnan(out[13:]).all())
+    served(out, lse, slice(0, 13))
+
+
+@pytest.mark.parametrize("n", [1, 12])
+def test_offsets_beyond_32_bits(n):
+    """Pages past 2^32 bytes and 2^31 elements of the cache (the last of 5 GB)."""
+    small, q = make(dict(n=[n], lens=[400], H=32, page=128), seed=42, junk=0.0)
+    pages = 34000
+    big = torch.zeros(pages, 128, ROW, dtype=torch.bfloat16, device="cuda")
+    big[-small.num_pages:] = small.cache
+    table = torch.where(small.table >= 0, small.table + pages - small.num_pages, small.table)
+    want, _, _ = attend(small, q)
+    out, _, status = attend(small, q, cache=big, table=table)
+    assert status == 0 and torch.equal(out, want)
+    rows = torch.randn(n, ROW, device="cuda").to(torch.bfloat16)
+    kda.kda_latent_append(big, rows, small.cu, small.seq_lens, table, check_device=True)
+    at = torch.arange(400 - n, 400, device="cuda")
+    assert torch.equal(big[table[0].long()[at // 128], at % 128], rows)
+
+
+@pytest.mark.parametrize("B", [390, 1300])
+def test_many_requests(B):
+    """More requests than threads of a block, lengths from 0."""
+    g = torch.Generator().manual_seed(43)
+    lens = torch.randint(0, 60, (B,), generator=g).tolist()
+    case, q = make(dict(n=[min(1, x) for x in lens], lens=lens, H=3, page=16), seed=43)
+    check(case, q)
+
+
+@pytest.mark.parametrize("tree", [False, True])
+def test_long_sequences_in_many_pieces(tree):
+    """One request over all pairs of CTAs, and one beside it that is a few key tiles."""
+    case, q = make(dict(n=[7, 3], lens=[30000, 200], H=40, page=128), seed=44)
+    check(case, q, tree=trees(case.n) if tree else None)
+
+
+def test_empty_calls():
+    """No requests, no tokens: nothing is launched."""
+    case, q = make(dict(n=[2], lens=[20], H=4, page=16), seed=45)
+    out = torch.full((0, 4, LATENT), 1.0, device="cuda", dtype=torch.bfloat16)
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    assert int(kda.kda_latent_attention(out, q[:0], case.cache, zero, case.seq_lens, case.table).item()) == 0
+    out, _, status = attend(case, q, cu=zero[:1], seq_lens=zero[:0], table=case.table[:0])
+    assert status == 0 and bool(torch.isnan(out).all())

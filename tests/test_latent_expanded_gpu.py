@@ -76,3 +76,149 @@ IDS = [f"n{max(s['n'])}_L{max(s['lens'])}_H{s['H']}" for s in SHAPES]
 @pytest.mark.parametrize("shape", SHAPES, ids=IDS)
 def test_shapes(shape, causal):
     check(Prompts(**shape), causal)
+
+
+@pytest.mark.parametrize("amplitude,scale", [(1.0, 3.0), (30.0, 1.0), (1e4, 1.0), (1.0, -0.3), (1.0, 0.0)])
+def test_scores_of_other_sizes(amplitude, scale):
+    c = Prompts([100, 300], [220, 300], 3, seed=61)
+    c.q.mul_(amplitude)
+    check(c, scale=scale)
+
+
+@pytest.mark.parametrize("amplitude", [2.0 ** -110, 2.0 ** 110])
+def test_values_of_extreme_size(amplitude):
+    c = Prompts([100, 300], [220, 300], 3, seed=62)
+    c.kv[..., HEAD:] *= amplitude
+    check(c)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("n,L", [(5, 70), (90, 300), (300, 300), (600, 600)])
+def test_a_bad_value_reaches_only_the_tokens_that_see_it(n, L, bad):
+    """A later token's V that is not finite, in either half of the columns; a neighbour request is as before."""
+    for col in (5, 100):
+        c = Prompts([n, 40], [L, 90], 2, seed=63)
+        want, wlse, _ = attend(c)
+        i = (2 * n) // 3
+        c.kv[L - n + i, 1, HEAD + col] = bad
+        out, lse, status = attend(c)
+        assert status == 0 and torch.equal(lse, wlse)
+        assert torch.equal(out[:i], want[:i]) and torch.equal(out[n:], want[n:]) and torch.equal(out[:, 0], want[:, 0])
+        keep = torch.arange(HEAD, device="cuda") != col
+        assert torch.equal(out[i:n, 1][:, keep], want[i:n, 1][:, keep])
+        assert not bool(torch.isfinite(out[i:n, 1, col]).any())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_key_reaches_only_the_tokens_that_see_it(bad):
+    c = Prompts([200, 40], [300, 90], 2, seed=64)
+    want, wlse, _ = attend(c)
+    c.k_pe[240] = float("nan")                     # token 140's position part: all heads
+    c.kv[350:390] = bad                            # the second request's last 40 keys and values: its own tokens'
+    out, lse, status = attend(c)
+    assert status == 0 and torch.equal(out[:140], want[:140]) and torch.equal(lse[:140], wlse[:140])
+    assert bool(torch.isnan(out[140:200]).all())
+    # what lies behind a request's keys is the next one's
+    c = Prompts([200], [300], 2, seed=64, tail=100)
+    want, wlse, _ = attend(Prompts([200], [300], 2, seed=64, tail=100))
+    c.kv[300:] = bad
+    c.k_pe[300:] = bad
+    cu = c.cu_k.clone()
+    out, lse, status = attend(c)
+    assert status == kda.DEV_BAD_SEQLEN and torch.equal(cu, c.cu_k)         # (cu_k does not span the 400 keys)
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
+def test_no_keys_at_all():
+    c = Prompts([3, 2], [0, 0], 4, seed=65)
+    check(c)
+
+
+def test_without_lse_and_on_another_stream():
+    c = Prompts([33, 300], [50, 700], 5, seed=66)
+    want, _, _ = attend(c)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    out, _, status = attend(c, with_lse=False, stream=stream)
+    assert status == 0 and torch.equal(out, want)
+
+
+def test_same_bits_and_graph_replay():
+    c = Prompts([300, 40, 129], [700, 40, 300], 5, seed=67)
+    want, wlse, _ = attend(c)
+    again, alse, _ = attend(c)
+    assert torch.equal(want, again) and torch.equal(wlse, alse)
+    other = torch.tensor(cumulative([500, 240, 300]), dtype=torch.int32, device="cuda")
+    long = c.cu_k.clone()
+    c.cu_k.copy_(other)
+    less, llse, _ = attend(c)
+    out, lse = torch.zeros_like(want), torch.zeros_like(wlse)
+    work = torch.empty(kda.latent_expanded_workspace_size(3, 469, 5), dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kda.kda_latent_expanded(out, c.q, c.kv, c.k_pe, c.cu_q, c.cu_k, lse=lse, workspace=work, dev_status=status)
+    for now, (o, e) in ((other, (less, llse)), (long, (want, wlse)), (other, (less, llse))):
+        c.cu_k.copy_(now)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, o) and torch.equal(lse, e) and int(status.item()) == 0
+
+
+def test_same_bits_when_copies_arrive_late():
+    c = Prompts([1100, 700], [6000, 5000], 8, seed=68)
+    flush = torch.empty(300 << 20, dtype=torch.uint8, device="cuda")
+    first = None
+    for trial in range(8):
+        if trial % 2 == 0:
+            flush.fill_(trial)
+        out, lse, status = attend(c)
+        first = first or (out, lse)
+        assert status == 0 and torch.equal(out, first[0]) and torch.equal(lse, first[1]), f"trial {trial}"
+
+
+def test_bad_offsets_are_reported_and_skipped():
+    """(The others are served, not with the same bits: the call is cut elsewhere.)"""
+    c = Prompts([9, 40, 2], [90, 140, 30], 4, seed=69)
+    want = reference(c)
+
+    def served(out, lse, rows):
+        close(out[rows], lse[rows], [x[rows] for x in want])
+
+    for name, bad in (("cu_k", [0, 90, 20, 260]), ("cu_q", [0, 9, 8, 51])):      # the second ends before it begins
+        keep = getattr(c, name).clone()
+        getattr(c, name).copy_(torch.tensor(bad, dtype=torch.int32))
+        out, lse, status = attend(c)
+        assert status == kda.DEV_BAD_SEQLEN
+        served(out, lse, slice(0, 9 if name == "cu_k" else 8))
+        getattr(c, name).copy_(keep)
+    c.cu_q.copy_(torch.tensor([0, 9, 49, 49], dtype=torch.int32))                # the last two rows are nobody's
+    out, lse, status = attend(c)
+    assert status == kda.DEV_BAD_SEQLEN and bool(torch.isnan(out[49:]).all())
+    served(out, lse, slice(0, 49))
+
+
+def test_offsets_beyond_32_bits():
+    """Keys past 2^31 elements of kv, behind those of a request without new tokens."""
+    n, L, far, H = 130, 300, 90000, 100
+    g = torch.Generator(device="cuda").manual_seed(70)
+    kv = torch.zeros(far + L, H, 2 * HEAD, device="cuda", dtype=torch.bfloat16)
+    kv[far:] = torch.randn(L, H, 2 * HEAD, device="cuda", generator=g)
+    pe = torch.randn(far + L, ROPE, device="cuda", generator=g).to(torch.bfloat16)
+    q = torch.randn(n, H, HEAD + ROPE, device="cuda", generator=g).to(torch.bfloat16)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    out, want = torch.empty(2, n, H, HEAD, device="cuda", dtype=torch.bfloat16).unbind()
+    kda.kda_latent_expanded(out, q, kv, pe, ints([0, 0, n]), ints([0, far, far + L]), check_device=True)
+    kda.kda_latent_expanded(want, q, kv[far:], pe[far:], ints([0, n]), ints([0, L]), check_device=True)
+    assert torch.equal(out, want)
+
+
+def test_many_requests():
+    g = torch.Generator().manual_seed(71)
+    lens = torch.randint(0, 40, (800,), generator=g).tolist()
+    check(Prompts([min(x, i % 3) for i, x in enumerate(lens)], lens, 2, seed=71))
+
+
+def test_one_long_prompt_in_many_pieces():
+    check(Prompts([700], [9000], 1, seed=72))

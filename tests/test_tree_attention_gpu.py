@@ -73,3 +73,162 @@ def test_shapes(shape, cache):
     H = shape.pop("H")
     case = Case(**shape, cache=cache)
     check(case, queries(case, H), trees(case.n, seed=7))
+
+
+def make(shape, **kw):
+    shape = dict(shape)
+    H = shape.pop("H")
+    case = Case(**shape, **kw)
+    return case, queries(case, H)
+
+
+TREE = dict(n=[37, 9], lens=[150, 300], H=12, HKV=2, D=128, page=16)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_a_chain_is_as_causal(cache):
+    """A chain's mask sees what a causal chunk sees."""
+    case, q = make(dict(n=[20, 31], lens=[70, 400], H=16, HKV=2, D=128, page=32), cache=cache, seed=51)
+    chain = [[set(range(i + 1)) for i in range(k)] for k in case.n]
+    out, lse = check(case, q, chain)
+    caches, scales = case.args()
+    kda.kda_paged_attention(out, q, *caches, case.cu, case.seq_lens, case.table, 31, **scales, lse=lse, check_device=True)
+    # (not the same bits: causal items have fewer key tiles, and so the calls are cut elsewhere)
+    close(out, lse, reference(case, q, chain, 128 ** -0.5))
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_masks_of_nothing_and_of_everything(cache):
+    case, q = make(dict(n=[5, 33, 1], lens=[5, 133, 40], H=8, HKV=2, D=64, page=16), cache=cache, seed=52)
+    none = torch.zeros(case.T, 2, dtype=torch.int32, device="cuda")
+    out, lse, status = attend(case, q, none)
+    assert status == 0
+    close(out, lse, reference(case, q, [[set()] * k for k in case.n], 64 ** -0.5))
+    assert bool((out[:5] == 0).all()) and bool(torch.isneginf(lse[:5]).all())
+    out, lse, status = attend(case, q, none - 1)
+    assert status == 0
+    close(out, lse, reference(case, q, [[set(range(k))] * k for k in case.n], 64 ** -0.5))
+    check(case, q, trees(case.n, seed=9), words=7)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("G", [2, 6])
+def test_a_bad_value_reaches_only_the_nodes_that_see_it(bad, G):
+    case, q = make(dict(TREE, H=2 * G), seed=53)
+    tree = trees(case.n, seed=4)
+    mask = mask_of(tree, 2)
+    want, wlse, _ = attend(case, q, mask)
+    node, L, n = 11, case.lens[0], case.n[0]
+    pos = L - n + node
+    case.tensors["v"][0][int(case.table[0, pos // 16]), :, pos % 16, 5] = bad
+    out, lse, status = attend(case, q, mask)
+    sees = torch.tensor([node in s for s in tree[0]] + [False] * case.n[1], device="cuda")
+    assert status == 0 and bool(sees.any()) and torch.equal(lse, wlse)
+    assert torch.equal(out[~sees], want[~sees])
+    keep = torch.arange(128, device="cuda") != 5
+    assert torch.equal(out[sees][..., keep], want[sees][..., keep])
+    assert not bool(torch.isfinite(out[sees][..., 5]).any())
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_a_bad_key_reaches_only_the_nodes_that_see_it(cache):
+    case, q = make(TREE, cache=cache, seed=54)
+    tree = trees(case.n, seed=4)
+    mask = mask_of(tree, 2)
+    want, wlse, _ = attend(case, q, mask)
+    node, L, n = 11, case.lens[0], case.n[0]
+    pos = L - n + node
+    x, s = case.tensors["k"]
+    row = (int(case.table[0, pos // 16]), slice(None), pos % 16)
+    if s is None:
+        x[row] = float("nan")
+    else:
+        s[row] = float("nan")
+    out, lse, status = attend(case, q, mask)
+    sees = torch.tensor([node in t for t in tree[0]] + [False] * case.n[1], device="cuda")
+    assert status == 0 and torch.equal(out[~sees], want[~sees]) and torch.equal(lse[~sees], wlse[~sees])
+    assert bool(torch.isnan(out[sees]).all())
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_scores_of_other_sizes(cache):
+    for amplitude, scale in ((30.0, 1.0), (1e4, 1.0), (1.0, -0.3), (1.0, 0.0)):
+        case, q = make(TREE, cache=cache, seed=55)
+        check(case, (q.float() * amplitude).to(torch.bfloat16), trees(case.n), scale=scale)
+
+
+def test_on_another_stream_in_a_graph_and_again():
+    for cache in ("bf16", "e4m3"):
+        case, q = make(TREE, cache=cache, seed=56)
+        mask = mask_of(trees(case.n), 2)
+        want, wlse, _ = attend(case, q, mask)
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        out, _, status = attend(case, q, mask, with_lse=False, stream=stream)
+        assert status == 0 and torch.equal(out, want)
+        shorter = case.seq_lens - 13
+        less, llse, _ = attend(case, q, mask, seq_lens=shorter)
+        caches, scales = case.args()
+        lens, out, lse = case.seq_lens.clone(), torch.zeros_like(want), torch.zeros_like(wlse)
+        work = torch.empty(kda.tree_attention_workspace_size(case.B, case.T, 37, 12, 2, 128), dtype=torch.uint8, device="cuda")
+        word = torch.zeros(1, dtype=torch.int32, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            kda.kda_tree_attention(out, q, *caches, case.cu, lens, case.table, mask, 37, **scales, lse=lse, workspace=work,
+                                   dev_status=word)
+        for now, (o, e) in ((case.seq_lens, (want, wlse)), (shorter, (less, llse)), (case.seq_lens, (want, wlse))):
+            lens.copy_(now)
+            out.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, o) and torch.equal(lse, e) and int(word.item()) == 0
+
+
+def test_bad_pages_lengths_and_offsets():
+    case, q = make(dict(n=[9, 4, 2], lens=[90, 40, 300], H=20, HKV=2, D=128, page=16), seed=57)
+    tree = trees(case.n)
+    mask = mask_of(tree, 1)
+    table = case.table.clone()
+    table[0, 0], table[2, 3] = case.num_pages, -5
+    out, lse, status = attend(case, q, mask, table=table)
+    assert status == kda.DEV_BAD_PAGE
+    close(out, lse, reference(case, q, tree, 128 ** -0.5, table))
+    # (the others are served, not always with the same bits: the call is cut elsewhere)
+    exact = reference(case, q, tree, 128 ** -0.5)
+
+    def served(out, lse, *rows):
+        for r in rows:
+            close(out[r], lse[r], [x[r] for x in exact])
+
+    lens = case.seq_lens.clone()
+    lens[1] = case.max_pages * 16 + 1
+    out, lse, status = attend(case, q, mask, seq_lens=lens)
+    assert status == kda.DEV_BAD_SEQLEN and bool(torch.isnan(out[9:13]).all())
+    served(out, lse, slice(0, 9), slice(13, 15))
+    out, lse, status = attend(case, q, mask, max_tokens=5)
+    assert status == kda.DEV_BAD_SEQLEN and bool(torch.isnan(out[:9]).all())
+    served(out, lse, slice(9, 15))
+    out, lse, status = attend(case, q, mask, cu=torch.tensor([0, 9, 13, 13], dtype=torch.int32, device="cuda"))
+    assert status == kda.DEV_BAD_SEQLEN and bool(torch.isnan(out[13:]).all())
+    served(out, lse, slice(0, 13))
+
+
+def test_offsets_beyond_32_bits():
+    """Pages past 2^31 elements of the cache."""
+    small, q = make(dict(n=[20], lens=[200], H=16, HKV=8, D=128, page=128), seed=58, junk=0.0)
+    pages = 18400
+    big = [torch.zeros(pages, 8, 128, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for i, x in enumerate(big):
+        x[-small.num_pages:] = small.tensors["kv"[i]][0]
+    table = torch.where(small.table >= 0, small.table + pages - small.num_pages, small.table)
+    mask = mask_of(trees(small.n), 1)
+    want, _, _ = attend(small, q, mask)
+    out = torch.empty_like(want)
+    status = kda.kda_tree_attention(out, q, *big, small.cu, small.seq_lens, table, mask, 20)
+    assert int(status.item()) == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_long_sequences_in_many_pieces(cache):
+    case, q = make(dict(n=[11, 3], lens=[20000, 200], H=16, HKV=2, D=128, page=128), cache=cache, seed=59)
+    check(case, q, trees(case.n))
