@@ -63,6 +63,9 @@ struct Part {
 };
 constexpr int kBegins = 1, kEnds = 2;
 
+struct Pairing {  // a request: tokens q0 .. q0 + n - 1, keys k0 .. k0 + L - 1
+  int q0, n, k0, L;
+};
 struct Slot {
   unsigned char q[kPanels][kQPanel];       // this CTA's 128 rows, 1024-aligned, swizzled panels
   unsigned char key[kKeyBytes];            // its 64 keys of a tile
@@ -76,6 +79,7 @@ struct Smem {
   long long scan[2][kWarps];
   long long first_unit[2];                 // of the requests that hold the streams' first units
   int first_request[2];
+  Pairing first[2];                        // they
   uint32_t tmem;
   // this CTA's own (s_full says too that the keys have been read, o_done that the values have)
   uint64_t value_full[2][kValues], s_full[2], o_done[2][kValues], q_empty[2];
@@ -84,9 +88,6 @@ struct Smem {
   uint64_t key_ready[2], q_ready[2], value_ready[2][kValues], p_half[2], p_full[2];
 };
 
-struct Pairing {  // a request: tokens q0 .. q0 + n - 1, keys k0 .. k0 + L - 1
-  int q0, n, k0, L;
-};
 __device__ __forceinline__ Pairing load_request(const ExpandedArgs& p, int b, bool report) {
   Pairing r;
   r.q0 = fresh(p.cu_q + b);
@@ -204,9 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (rank == 0 && tid < 2) pieces.notes[2 * pair + tid].tokens = 0;
   const int passes = (p.B + kThreads - 1) / kThreads;
   long long mine = 0, before = 0, units = 0;
+  Pairing r{0, 0, 0, 0};
   for (int i = 0; i < passes; ++i) {
     const int b = i * kThreads + tid;
-    Pairing r{0, 0, 0, 0};
+    r = Pairing{0, 0, 0, 0};
     if (b < p.B) r = load_request(p, b, blockIdx.x == 0);
     mine = p.H * head_units(p, r, lane);
     long long all;
@@ -222,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int b = i * kThreads + tid;
     if (passes > 1) {  // counted again
       if (i == 0) units = 0;
-      Pairing r{0, 0, 0, 0};
+      r = Pairing{0, 0, 0, 0};
       if (b < p.B) r = load_request(p, b, false);
       mine = p.H * head_units(p, r, lane);
       long long all;
@@ -235,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (starts[t] >= before && starts[t] < before + mine) {
         sm.first_request[t] = b;
         sm.first_unit[t] = before;
+        sm.first[t] = r;
       }
   }
   __syncwarp();
@@ -473,8 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (u1 > u0) {
         b = sm.first_request[t];
         unit = sm.first_unit[t];
-        fetch();
-        take();
+        r = sm.first[t];
+        tiles = row_tiles(r);
+        base = b - 32;  // (the requests after it are fetched when they are wanted)
         // the head and the row tile that hold u0
         const long long each = __shfl_sync(0xffffffffu, head_units(p, r, lane), 0);
         h = (int)((u0 - unit) / each);

@@ -76,6 +76,7 @@ struct Smem {
   long long scan[2][kWarps];
   long long first_unit;                     // of the request that holds the share's first unit
   int first_request;
+  Request first;                            // it
   uint32_t tmem;
   // this CTA's own (a key tile's last unit of keys has been read when S is there, its last of values when PV
   // is done)
@@ -198,9 +199,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (rank == 0 && tid == 0) pieces.notes[pair].tokens = 0;
   const int passes = (p.B + kThreads - 1) / kThreads;
   long long mine = 0, before = 0, units = 0;
+  Request r{0, 0, 0};
   for (int i = 0; i < passes; ++i) {
     const int b = i * kThreads + tid;
-    Request r{0, 0, 0};
+    r = Request{0, 0, 0};
     if (b < p.B) r = load_request(p, b, blockIdx.x == 0);
     mine = request_units(p, r, lane);
     long long all;
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int b = i * kThreads + tid;
     if (passes > 1) {  // counted again
       if (i == 0) units = 0;
-      Request r{0, 0, 0};
+      r = Request{0, 0, 0};
       if (b < p.B) r = load_request(p, b, false);
       mine = request_units(p, r, lane);
       long long all;
@@ -225,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (u0 >= before && u0 < before + mine) {
       sm.first_request = b;
       sm.first_unit = before;
+      sm.first = r;
     }
   }
   __syncwarp();
@@ -285,10 +288,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (u1 > u0) {
       b = sm.first_request;
       unit = sm.first_unit;
-      fetch();
-      take();
+      r = sm.first;
+      tiles = row_tiles(p, r);
+      base = b - 32;  // (the requests after it are fetched when they are wanted)
       // the row tile that holds u0
-      if (!p.causal) {
+      if (tiles == 1) {
+        // it is the only one
+      } else if (!p.causal) {
         const int each = item_units(p, r, 0);
         tile = (int)((u0 - unit) / each);
         unit += (long long)tile * each;
@@ -329,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int pos0 = r.L - r.n, first = pos0 + part.row0 / p.H;
         part.whole = p.mask ? (first >= 0 ? pos0 : 0) : p.causal ? first + 1 : first >= 0 ? r.L : 0;
         part.flags = (from == 0 ? kBegins : 0) | (to == all ? kEnds : 0);
-        part.pieces = share_of(units, used, unit + kItemCost + all - 1) - pair + 1;
+        part.pieces = to == all ? 1 : share_of(units, used, unit + kItemCost + all - 1) - pair + 1;
         put_note(part);
       }
       unit += kItemCost + all;

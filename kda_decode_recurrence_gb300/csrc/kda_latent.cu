@@ -14,7 +14,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 2;
 
 __device__ __forceinline__ bool good_request(const LatentAppendArgs& p, int t0, int t1, int len) {
   return t0 >= 0 && t1 >= t0 && t1 <= p.T && len >= 0 && len <= (long long)p.c.max_pages * p.c.page_size;
@@ -126,8 +126,8 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
 }  // namespace
 
 cudaError_t launch_latent_append(const LatentAppendArgs& a, cudaStream_t stream) {
-  // Eight tokens to a warp where there are enough for all SMs, else one.
-  const int tokens = a.T >= 152 * 4 * kWarps * 2 ? 8 : 1;
+  // Four tokens to a warp where there are enough for all SMs, else one.
+  const int tokens = a.T >= 152 * 4 * kWarps * 2 ? 4 : 1;
   const long long per_cta = (long long)kWarps * tokens;
   const dim3 grid((unsigned)((a.T + per_cta - 1) / per_cta + 1));
   if (a.gamma) return launch(latent_append_kernel<true>, grid, dim3(kThreads), 0, stream, true, a, tokens);
