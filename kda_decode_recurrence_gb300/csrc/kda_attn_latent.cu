@@ -157,7 +157,8 @@ __device__ __forceinline__ uint4 finite(uint4 x) {
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    latent_kernel(const __grid_constant__ CUtensorMap rows_map, const LatentArgs p, const Pieces pieces) {
+    latent_kernel(const __grid_constant__ CUtensorMap key_map, const __grid_constant__ CUtensorMap value_map,
+                  const LatentArgs p, const Pieces pieces) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -350,7 +351,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- keys or values into their ring
     const int rows_per_box = min(p.c.page_size, kHalf);
     const int half_boxes = kHalf / rows_per_box, boxes = 2 * half_boxes;  // of a half, of a key tile
-    const int in = lane % half_boxes, panel = lane / half_boxes;          // of a unit's copies: lane's box and panel
+    // a unit's copies, by lane: all panels of 64 rows at once, or of fewer rows a panel each
+    const bool whole_unit = half_boxes == 1;
+    const int in = lane % half_boxes, panel = lane / half_boxes;
+    const int copies = whole_unit ? 1 : warp == kKeyWarp ? kKeyPanels : kValuePanels;
     const bool keys = warp == kKeyWarp;
     const uint32_t ready0 = cluster_addr(&sm.key_ready[0], 0);
     int put = 0;
@@ -418,9 +422,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             if (rank == 0 && lane == 0) mbar_expect_tx(&sm.key_ready[s], 2 * kKeyBytes);
             __syncwarp();
-            if (panel < kKeyPanels)
-              tma_load_2d_pair(sm.key[s] + panel * kPanelBytes + in * rows_per_box * 128, &rows_map, ready0 + 8 * s,
-                               (k * kKeyPanels + panel) * 64, row);
+            if (panel < copies)
+              tma_load_3d_pair(sm.key[s] + panel * kPanelBytes + in * rows_per_box * 128, &key_map, ready0 + 8 * s, 0,
+                               row, k * kKeyPanels + panel);
           }
           fetch_ahead(i);
         } else {
@@ -434,9 +438,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             if (lane == 0) mbar_expect_tx(&sm.value_full[s], kValueBytes);
             __syncwarp();
-            if (panel < kValuePanels)
-              tma_load_2d(sm.value[s] + panel * kPanelBytes + in * rows_per_box * 128, &rows_map, &sm.value_full[s],
-                          rank * (kLatent / 2) + panel * 64, v ? row_hi : row_lo);
+            if (panel < copies)
+              tma_load_3d(sm.value[s] + panel * kPanelBytes + in * rows_per_box * 128, &value_map, &sm.value_full[s], 0,
+                          v ? row_hi : row_lo, rank * kValuePanels + panel);
           }
         }
       }
@@ -786,17 +790,22 @@ size_t latent_workspace_bytes(int B, int T, int H) {
 
 cudaError_t launch_latent_attention(const LatentArgs& a, cudaStream_t stream) {
   static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "a CTA fits an SM");
-  CUtensorMap map;
-  const int rows_per_box = a.c.page_size < kHalf ? a.c.page_size : kHalf;
-  if (!make_map_2d(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.c.rows, kLatentRow,
-                   (uint64_t)a.c.num_pages * a.c.page_size, 64, rows_per_box))
-    return cudaErrorInvalidValue;
+  // The cache as [panel of 64 entries][row][64 entries]: a box of 64 rows and several panels lands as the
+  // panels' operand layout; rows of smaller pages take a box a panel (16 rows: 4234 cycles a key tile
+  // against 2950).
+  const uint32_t rows_per_box = a.c.page_size < kHalf ? a.c.page_size : kHalf;
+  const bool whole_unit = rows_per_box == kHalf;
+  CUtensorMap maps[2];
+  for (int i = 0; i < 2; ++i)
+    if (!make_map_3d_bf16(&maps[i], a.c.rows, 64, (uint64_t)a.c.num_pages * a.c.page_size, kPanels, kLatentRow * 2, 128,
+                          64, rows_per_box, whole_unit ? (i ? kValuePanels : kKeyPanels) : 1))
+      return cudaErrorInvalidValue;
   const size_t smem = sizeof(Smem) + 1024;
   static SmemSet set;
   cudaError_t e = allow_smem(latent_kernel, smem, set);
   if (e != cudaSuccess) return e;
   const Pieces pieces = pieces_at(a.workspace, kPairs, kRows);
-  e = launch_pairs(latent_kernel, dim3(2 * kPairs), dim3(kThreads), smem, stream, map, a, pieces);
+  e = launch_pairs(latent_kernel, dim3(2 * kPairs), dim3(kThreads), smem, stream, maps[0], maps[1], a, pieces);
   if (e != cudaSuccess) return e;
   return launch(latent_join_kernel, dim3(kPairs, kJoinY), dim3(128), 0, stream, true, a, pieces);
 }
