@@ -348,27 +348,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) put_note(Part{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0});
     if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
   } else if (warp == kKeyWarp || warp == kCopyWarp) {
-    // ---- keys or values into their ring
-    const int rows_per_box = min(p.c.page_size, kHalf);
-    const int half_boxes = kHalf / rows_per_box, boxes = 2 * half_boxes;  // of a half, of a key tile
+    // ---- keys or values into their ring.  (This chain is as long as a key tile takes: no division in it.)
+    const int page_shift = 31 - __clz(p.c.page_size), in_page = p.c.page_size - 1;
+    const int rows_per_box = min(p.c.page_size, kHalf), box_shift = min(page_shift, 6);
+    const int half_boxes = kHalf >> box_shift, boxes = 2 * half_boxes;  // of a half, of a key tile
+    const int nowhere = p.c.num_pages << page_shift;                    // a row past the end: zeros
     // a unit's copies, by lane: all panels of 64 rows at once, or of fewer rows a panel each
-    const bool whole_unit = half_boxes == 1;
-    const int in = lane % half_boxes, panel = lane / half_boxes;
-    const int copies = whole_unit ? 1 : warp == kKeyWarp ? kKeyPanels : kValuePanels;
     const bool keys = warp == kKeyWarp;
+    const int in = lane & (half_boxes - 1), panel = lane / half_boxes;
+    const int copies = half_boxes == 1 ? 1 : keys ? kKeyPanels : kValuePanels;
+    const uint32_t to = panel * kPanelBytes + in * rows_per_box * 128;
     const uint32_t ready0 = cluster_addr(&sm.key_ready[0], 0);
-    int put = 0;
+    int tasks = 0, put = 0;      // key tiles, units so far
     int soon = -1, soon_in = 0;  // page and position in it to be fetched into L2 next, by lane
     Part part;
     for (int item = 0; read_part(item, part); leave_part(item), ++item) {
       const int32_t* table = p.c.page_table + (size_t)part.b * p.c.max_pages;
-      const int box0 = part.tile0 * boxes, last = min(part.end, (part.tile0 + part.count) * kTile);
+      const int first = part.tile0 * kTile, last = min(part.end, (part.tile0 + part.count) * kTile);
       int page = -1;  // of the 32 boxes under way, by lane
       // row of the cache where `box` (per lane) of the part's key tile i starts; past the end: zeros
       auto cache_row = [&](int i, int box) {
-        const int at = i * boxes + box, pos = (box0 + at) * rows_per_box;
+        const int at = i * boxes + box, pos = first + (at << box_shift);
         const int pg = __shfl_sync(0xffffffffu, page, at & 31);
-        return pg >= 0 ? pg * p.c.page_size + pos % p.c.page_size : p.c.num_pages * p.c.page_size;
+        return pg >= 0 ? (pg << page_shift) + (pos & in_page) : nowhere;
       };
       // Rows of a later key tile (this part's, or the next one's where its note is there) are fetched into
       // L2: copies wait for room in the rings, which a key tile fills, and HBM is further away than that.
@@ -376,33 +378,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto fetch_ahead = [&](int i) {
         if (soon >= 0 && soon < p.c.num_pages)
           asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                           p.c.rows + ((size_t)soon * p.c.page_size + soon_in) * kLatentRow),
+                           p.c.rows + (((size_t)soon << page_shift) + soon_in) * kLatentRow),
                        "r"(rows_per_box * kLatentRow * 2)
                        : "memory");
         soon = -1;
-        int at = i + kAhead, b = part.b, tile0 = part.tile0, count = part.count, end = part.end;
-        if (at >= count) {
+        const int at = i + kAhead;
+        int pos = first + at * kTile + rank * kHalf + (lane << box_shift);
+        const int32_t* of = table;
+        bool some = pos < last;
+        if (at >= part.count) {
           if (!__all_sync(0xffffffffu, mbar_test(smem_u32(&sm.part_full[(item + 1) % kNotes]), ((item + 1) / kNotes) & 1)))
             return;
           const Part& next = sm.part[(item + 1) % kNotes];
-          at -= count;
-          b = next.b;
-          tile0 = next.tile0;
-          count = next.count;
-          end = next.end;
+          pos += (next.tile0 - part.tile0 - part.count) * kTile;
+          some = at - part.count < next.count && pos < next.end;
+          of = p.c.page_table + (size_t)next.b * p.c.max_pages;
         }
-        const int pos = (tile0 + at) * kTile + rank * kHalf + lane * rows_per_box;
-        if (at < count && lane < half_boxes && pos < end) {
-          soon = fresh(p.c.page_table + (size_t)b * p.c.max_pages + pos / p.c.page_size);
-          soon_in = pos % p.c.page_size;
+        if (some && lane < half_boxes) {
+          soon = fresh(of + (pos >> page_shift));
+          soon_in = pos & in_page;
         }
       };
-      for (int i = 0; i < part.count && ok; ++i) {
+      for (int i = 0; i < part.count && ok; ++i, ++tasks) {
         if (((i * boxes) & 31) == 0) {
-          const int pos = (box0 + i * boxes + lane) * rows_per_box;
+          const int pos = first + ((i * boxes + lane) << box_shift);
           page = -1;
           if (pos < last) {
-            page = fresh(table + pos / p.c.page_size);
+            page = fresh(table + (pos >> page_shift));
             if (page < 0 || page >= p.c.num_pages) {
               raise_status(p.dev_status, KDA_DEV_BAD_PAGE);
               page = -1;
@@ -412,35 +414,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (keys) {
           // this CTA's half of the keys, three panels at a time; both CTAs' copies arrive at the first's barrier
           const int row = cache_row(i, rank * half_boxes + in);
-#pragma unroll 1
-          for (int k = 0; k < kKeys && ok; ++k, ++put) {
-            const int s = put % kKeys;
-            const int before = put / kKeys - 1;  // the key tile whose place this unit takes
-            if (before >= 0)
-              ok = s < kKeys - 1 ? wait_pair(&sm.key_empty[s], before & 1)
-                                 : wait_pair(&sm.s_full[before & 1], (before >> 1) & 1);
+#pragma unroll
+          for (int k = 0; k < kKeys; ++k) {
+            if (tasks > 0 && ok)  // the key tile before has been read
+              ok = k < kKeys - 1 ? wait_pair(&sm.key_empty[k], (tasks - 1) & 1)
+                                 : wait_pair(&sm.s_full[(tasks - 1) & 1], ((tasks - 1) >> 1) & 1);
             if (!ok) break;
-            if (rank == 0 && lane == 0) mbar_expect_tx(&sm.key_ready[s], 2 * kKeyBytes);
+            if (rank == 0 && lane == 0) mbar_expect_tx(&sm.key_ready[k], 2 * kKeyBytes);
             __syncwarp();
             if (panel < copies)
-              tma_load_3d_pair(sm.key[s] + panel * kPanelBytes + in * rows_per_box * 128, &key_map, ready0 + 8 * s, 0,
-                               row, k * kKeyPanels + panel);
+              tma_load_3d_pair(sm.key[k] + to, &key_map, ready0 + 8 * k, 0, row, k * kKeyPanels + panel);
+            put = tasks * kKeys + k + 1;
           }
           fetch_ahead(i);
         } else {
           // this CTA's columns, half of the keys at a time
           const int row_lo = cache_row(i, in), row_hi = cache_row(i, half_boxes + in);
-#pragma unroll 1
-          for (int v = 0; v < kValues && ok; ++v, ++put) {
-            const int s = put % kValues;
-            const int before = put / kValues - 1;
-            if (before >= 0) ok = wait_pair(s < kValues - 1 ? &sm.value_empty[s] : &sm.o_done, before & 1);
+#pragma unroll
+          for (int v = 0; v < kValues; ++v) {
+            if (tasks > 0 && ok) ok = wait_pair(v < kValues - 1 ? &sm.value_empty[v] : &sm.o_done, (tasks - 1) & 1);
             if (!ok) break;
-            if (lane == 0) mbar_expect_tx(&sm.value_full[s], kValueBytes);
+            if (lane == 0) mbar_expect_tx(&sm.value_full[v], kValueBytes);
             __syncwarp();
             if (panel < copies)
-              tma_load_3d(sm.value[s] + panel * kPanelBytes + in * rows_per_box * 128, &value_map, &sm.value_full[s], 0,
-                          v ? row_hi : row_lo, rank * kValuePanels + panel);
+              tma_load_3d(sm.value[v] + to, &value_map, &sm.value_full[v], 0, v ? row_hi : row_lo,
+                          rank * kValuePanels + panel);
+            put = tasks * kValues + v + 1;
           }
         }
       }
