@@ -45,6 +45,7 @@ constexpr int kKeyBytes = kPanels * kKeyPanel, kValueBytes = kTile * 128;
 constexpr int kValues = 2;            // value units kept per slot (of keys: one)
 constexpr int kNotes = 4;             // items whose notes are kept
 constexpr int kItemCost = 3;          // what an item's beginning and end take, in key tiles
+constexpr unsigned long long kPartLimitNs = 60 * kWaitLimitNs;  // limit of a wait for a whole part
 constexpr float kGrow = 8.f;          // growth of a maximum (log 2) that rescales O
 constexpr float kRounds = 4194304.f;  // maxima past 2^22: half an fp32 step is more than 2^-2
 // Warps: 0-3 and 4-7 the slots' softmax, 8 the products, 9 and 10 the slots' copies, 11 passes on values.
@@ -439,7 +440,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t key_ready = cluster_addr(&sm.key_ready[t], 0), q_ready = cluster_addr(&sm.q_ready[t], 0);
       int key_put = 0, value_put = 0, item = 0;
       auto put_note = [&](const Part& part) {
-        if (item >= kNotes) wait(&sm.part_empty[t][item % kNotes], (item / kNotes - 1) & 1);
+        // (a part of a very long request may take more than a second)
+        if (item >= kNotes)
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(&sm.part_empty[t][item % kNotes], (item / kNotes - 1) & 1, kPartLimitNs));
         if (ok && lane == 0) {
           sm.part[t][item % kNotes] = part;
           sm.bad[t][item % kNotes] = 0;

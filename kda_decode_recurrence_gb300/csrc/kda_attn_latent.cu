@@ -47,6 +47,7 @@ constexpr int kValuePanels = 4, kValues = 2, kValueBytes = kValuePanels * kPanel
 constexpr int kAhead = 2;           // key tiles that are fetched into L2 before their copies
 constexpr int kNotes = 4;           // items whose notes are kept
 constexpr int kItemCost = 3;        // what an item's beginning and end take, in key tiles
+constexpr unsigned long long kPartLimitNs = 60 * kWaitLimitNs;  // limit of a wait for a whole part
 constexpr float kGrow = 8.f;        // growth of a maximum (log 2) that rescales O
 // Warps: 0-3 the softmax, 4 the products (of the pair's first CTA), 5 copies keys, 6 values, 7 finds the
 // share's items, 8-11 load queries and pass on values.
@@ -253,7 +254,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- the share's items
     int item = 0;
     auto put_note = [&](const Part& part) {
-      if (item >= kNotes) ok = wait_pair(&sm.part_empty[item % kNotes], (item / kNotes - 1) & 1);
+      // (a part over a very long cache may take more than a second)
+      if (item >= kNotes)
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.part_empty[item % kNotes], (item / kNotes - 1) & 1, kPartLimitNs));
       if (ok && lane == 0) {
         sm.part[item % kNotes] = part;
         mbar_arrive(&sm.part_full[item % kNotes]);

@@ -214,35 +214,21 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t base, uint32_t cols) {
                : "memory");
 }
 
-// ---- pairs of CTAs (cta_group::2, a cluster of two).  One thread of the pair's first CTA
-// issues; D's rows and A's are split between the CTAs, and so are B's: with M = 128 each CTA
-// holds 64 rows of A and half of the N rows of B.  D: a CTA's 64 rows in lanes 0 .. 63 with the first
-// half of N in consecutive columns, and again in lanes 64 .. 127 with the second half.
-__device__ __forceinline__ void mma_bf16_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
-                                              uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
-}
-
-// The same in a warp that runs together, by the lane whose `one` is set: a branch around a few products
-// costs some hundred cycles of issue, a predicate none.
+// ---- pairs of CTAs (cta_group::2, a cluster of two).  One thread of the pair's first CTA issues; D's rows
+// and A's are split between the CTAs, and so are B's N rows: each CTA holds half.  M = 256: a CTA's 128 rows of D
+// in its 128 lanes, N columns.  M = 128: a CTA's 64 rows in lanes 0 .. 63 with the first half of N in
+// consecutive columns, and again in lanes 64 .. 127 with the second half.  (Both operands from shared memory:
+// 32 and 64 cycles a step of 16 at M = 128, N = 128 and 256, twice that at M = 256: 4070 products a
+// cycle and SM.)
+//
+// The whole warp runs together, and the lane whose `one` is set issues: a branch around a few products costs a
+// hundred cycles of issue, a predicate none, a commit 80.
 __device__ __forceinline__ void mma_bf16_pair_if(uint32_t one, uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
                                                  uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
       " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one));
-}
-
-// Arrive once on `bar` of both CTAs when every MMA this thread issued so far has completed.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
 }
 
 // The same with A in tensor memory (M = 256: each CTA's 128 rows in its own).
@@ -254,6 +240,7 @@ __device__ __forceinline__ void mma_bf16_pair_tmem_a_if(uint32_t one, uint32_t t
       "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one));
 }
 
+// Arrive once on `bar` of both CTAs when every product that this thread issued so far has completed.
 __device__ __forceinline__ void mma_commit_pair_if(uint32_t one, uint64_t* bar) {
   asm volatile(
       "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
