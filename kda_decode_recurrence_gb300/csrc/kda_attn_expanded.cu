@@ -76,7 +76,7 @@ struct Slot {
 struct Smem {
   Slot slot[2];
   Part part[2][kNotes];
-  int bad[2][kNotes];                      // live entries of V were taken out of the item
+  int bad[2][kNotes];                      // item + 1: live entries of V were taken out of that item
   long long scan[2][kWarps];
   long long first_unit[2];                 // of the requests that hold the streams' first units
   int first_request[2];
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t out_row = (size_t)(part.q0 + row) * p.H + part.h;
       const size_t piece = ((size_t)stream_of(t) * 2 + (part.flags & kBegins ? 1 : 0)) * kRows + rank * kM + r;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const bool bad = sm.bad[t][item % kNotes] != 0;
+      const bool bad = sm.bad[t][item % kNotes] == item + 1;
       if (live) {
         if (!done) pieces.ml[piece] = make_float2(m, l);
         else if (p.lse) p.lse[out_row] = (m + log2f(l)) * kLn2;
@@ -446,7 +446,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                           mbar_wait(&sm.part_empty[t][item % kNotes], (item / kNotes - 1) & 1, kPartLimitNs));
         if (ok && lane == 0) {
           sm.part[t][item % kNotes] = part;
-          sm.bad[t][item % kNotes] = 0;
           mbar_arrive(&sm.part_full[t][item % kNotes]);
         }
         __syncwarp();
@@ -700,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the rows of either CTA add them at the item's end
                 if (lane < 2)
                   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&sm.bad[t][item[t] % kNotes], lane)),
-                               "r"(1)
+                               "r"(item[t] + 1)
                                : "memory");
                 asm volatile("fence.acq_rel.cluster;" ::: "memory");
               }
