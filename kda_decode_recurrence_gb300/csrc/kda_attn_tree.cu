@@ -1,7 +1,10 @@
-// kda_attn_tree.cu -- attention of drafted trees over a paged K/V cache: the chunk kernel with a
-// mask of the new tokens that each of them sees.
+// kda_attn_tree.cu -- attention of drafted trees over a paged K/V cache, by the size of a head.
 //
-// Trees of a few nodes take it too.  Their rows (nodes x query heads per key head) are mostly more
+// Heads of 128 have a kernel of pairs of CTAs (kda_attn_tree_pairs.cu).  Heads of 64 take the chunk kernel
+// with a mask of the new tokens that each of them sees: V would have 32 columns per CTA of a pair, half of
+// a swizzled row.
+//
+// Trees of a few nodes take these too.  Their rows (nodes x query heads per key head) are mostly more
 // than the 16 up to which the window kernel wins over bf16, and everything before the tree is seen by
 // every row, so that only the last key tiles differ from a chunk's.
 #include "kda_attn_chunk.cuh"
@@ -10,13 +13,14 @@ namespace kda {
 
 size_t tree_workspace_bytes(int B, int T, int max_tokens, int H, int HKV, int D) {
   if (B < 0 || T < 0 || max_tokens < 0 || H < 1 || HKV < 1 || H % HKV != 0 || (D != 64 && D != 128)) return 0;
-  return (pieces_bytes(kChunkCtas, kChunkRows, D) + 255) & ~(size_t)255;
+  return D == 128 ? tree_pairs_bytes() : (pieces_bytes(kChunkCtas, kChunkRows, D) + 255) & ~(size_t)255;
 }
 
 cudaError_t launch_tree_attention(const AttentionArgs& in, cudaStream_t stream) {
   AttentionArgs a = in;
   a.window_rows = 0;
-  return by_type<true>(a, stream);
+  if (a.c.D == 128) return launch_tree_pairs(a, stream);
+  return a.c.e4m3 ? by_pair<true, 64, true>(a, stream) : by_pair<true, 64, false>(a, stream);
 }
 
 }  // namespace kda

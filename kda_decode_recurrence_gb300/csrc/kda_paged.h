@@ -59,6 +59,8 @@ cudaError_t launch_paged_attention(const AttentionArgs& args, cudaStream_t strea
 
 size_t tree_workspace_bytes(int B, int T, int max_tokens, int H, int HKV, int D);
 cudaError_t launch_tree_attention(const AttentionArgs& args, cudaStream_t stream);
+size_t tree_pairs_bytes();
+cudaError_t launch_tree_pairs(const AttentionArgs& args, cudaStream_t stream);  // heads of 128
 
 struct VerifyArgs {
   int32_t* tokens;

@@ -232,3 +232,56 @@ def test_offsets_beyond_32_bits():
 def test_long_sequences_in_many_pieces(cache):
     case, q = make(dict(n=[11, 3], lens=[20000, 200], H=16, HKV=2, D=128, page=128), cache=cache, seed=59)
     check(case, q, trees(case.n))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_bad_scale_of_a_value_reaches_only_the_nodes_that_see_it(bad, D):
+    case, q = make(dict(TREE, D=D), cache="e4m3", seed=60)
+    tree = trees(case.n, seed=4)
+    mask = mask_of(tree, 2)
+    want, wlse, _ = attend(case, q, mask)
+    node, L, n = 11, case.lens[0], case.n[0]
+    pos = L - n + node
+    case.tensors["v"][1][int(case.table[0, pos // 16]), :, pos % 16] = bad
+    out, lse, status = attend(case, q, mask)
+    sees = torch.tensor([node in s for s in tree[0]] + [False] * case.n[1], device="cuda")
+    assert status == 0 and bool(sees.any()) and torch.equal(lse, wlse)
+    assert torch.equal(out[~sees], want[~sees])
+    assert not bool(torch.isfinite(out[sees]).any())
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_many_small_trees(cache):
+    """Several items to each stream of work, most of one key tile."""
+    g = torch.Generator().manual_seed(61)
+    n = torch.randint(0, 7, (420,), generator=g).tolist()
+    lens = [k + int(x) for k, x in zip(n, torch.randint(0, 260, (420,), generator=g))]
+    case, q = make(dict(n=n, lens=lens, H=10, HKV=2, D=128, page=32), cache=cache, seed=61)
+    check(case, q, trees(n, seed=3))
+
+
+def test_bad_values_of_many_small_trees():
+    """Each reaches the nodes of its own tree that see it, whatever shares the kernel's memory with it."""
+    g = torch.Generator().manual_seed(62)
+    n = torch.randint(1, 7, (420,), generator=g).tolist()
+    lens = [k + int(x) for k, x in zip(n, torch.randint(0, 260, (420,), generator=g))]
+    case, q = make(dict(n=n, lens=lens, H=10, HKV=2, D=128, page=32), seed=62)
+    tree = trees(n, seed=3)
+    mask = mask_of(tree, 1)
+    want, wlse, _ = attend(case, q, mask)
+    sees = []
+    for b in range(case.B):
+        if b % 3 == 1:
+            node = b % n[b]
+            pos = lens[b] - n[b] + node
+            case.tensors["v"][0][int(case.table[b, pos // 32]), :, pos % 32, 77] = float("nan")
+            sees += [node in s for s in tree[b]]
+        else:
+            sees += [False] * n[b]
+    out, lse, status = attend(case, q, mask)
+    sees = torch.tensor(sees, device="cuda")
+    assert status == 0 and torch.equal(lse, wlse) and torch.equal(out[~sees], want[~sees])
+    keep = torch.arange(128, device="cuda") != 77
+    assert torch.equal(out[sees][..., keep], want[sees][..., keep])
+    assert bool(torch.isnan(out[sees][..., 77]).all())
