@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (part.count == 0) break;
       const int L = part.L, n = part.n, token = part.token0 + rank * per_cta + tok_in;
       const bool live = tok_in < per_cta && token < n;
+      const bool idle = !__any_sync(0xffffffffu, live);  // (what is left in P stays in rows that nobody reads)
       const int row_hi = live && L - n + token >= 0 ? L : 0;
       const int32_t* words = p.tree + (size_t)(part.t0 + min(token, n - 1)) * p.tree_words;
       float m = -INFINITY;
@@ -247,6 +248,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool rounds = false;  // a maximum of the warp's is past kRounds
       for (int i = 0; i < part.count; ++i, ++task) {
         if (!wait_here(&sm.s_full[t][task % kRing], (task / kRing) & 1)) break;
+        if (idle) {
+          if (lane == 0) {
+            mbar_arrive_cluster(p_half);
+            mbar_arrive_cluster(p_full);
+          }
+          continue;
+        }
         tc_fence_after();
         const int start = (part.tile0 + i) * kTile;
         // whole key tiles of a bf16 cache take x = c S in one product with the subtraction
