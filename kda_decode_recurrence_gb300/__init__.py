@@ -31,6 +31,17 @@ Next to the KDA layers, for a model's full-attention layers and drafted tokens:
     paged_attention_workspace_size(B, T, max_tokens, H, HKV, D)
     kda_verify_draft(tokens, accepted, target_probs, draft_probs, draft_tokens,
                      accept_u, sample_u, cu_drafts)
+    kda_tree_attention(out, q, k_cache, v_cache, cu_seqlens, seq_lens,
+                       page_table, tree_mask, max_tokens)
+    tree_attention_workspace_size(B, T, max_tokens, H, HKV, D)
+
+and for layers whose heads share one latent row a token:
+
+    kda_latent_append(cache, rows, cu_seqlens, seq_lens, page_table, gamma, eps)
+    kda_latent_attention(out, q, cache, cu_seqlens, seq_lens, page_table, tree_mask)
+    latent_attention_workspace_size(B, T, H)
+    kda_latent_expanded(out, q, kv, k_pe, cu_q, cu_k)
+    latent_expanded_workspace_size(B, Tq, H)
 """
 from __future__ import annotations
 
@@ -460,11 +471,12 @@ def _check_outputs(out, lse, T, H, D, device) -> None:
             raise ValueError(f"lse shape {tuple(lse.shape)} != [{T}, {H}]")
 
 
-def _workspace(workspace, need, device, stream):
-    """The caller's workspace, or a new one on the call's stream."""
+def _workspace(workspace, size, sizes, device, stream):
+    """The caller's workspace, or a new one of size(*sizes) bytes on the call's stream."""
     if workspace is not None:
         _check(workspace, "workspace", torch.uint8, device)
         return workspace
+    need = size(*sizes)
     with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
         return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
 
@@ -509,7 +521,7 @@ def kda_tree_attention(out, q, k_cache, v_cache, cu_seqlens, seq_lens, page_tabl
     _check_lens(seq_lens, B, dev)
     words = _check_mask(tree_mask, T, dev)
     _check_current(dev)
-    workspace = _workspace(workspace, tree_attention_workspace_size(B, T, max_tokens, H, HKV, D), dev, stream)
+    workspace = _workspace(workspace, tree_attention_workspace_size, (B, T, max_tokens, H, HKV, D), dev, stream)
     status = _status_word(dev_status, dev, stream)
     rc = _lib.load().kda_tree_attention(
         out.data_ptr(), _ptr(lse), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
@@ -592,7 +604,7 @@ def kda_latent_attention(out, q, cache, cu_seqlens, seq_lens, page_table, scale=
     _check_lens(seq_lens, B, dev)
     words = _check_mask(tree_mask, T, dev) if tree_mask is not None else 0
     _check_current(dev)
-    workspace = _workspace(workspace, latent_attention_workspace_size(B, T, H), dev, stream)
+    workspace = _workspace(workspace, latent_attention_workspace_size, (B, T, H), dev, stream)
     status = _status_word(dev_status, dev, stream)
     rc = _lib.load().kda_latent_attention(
         out.data_ptr(), _ptr(lse), q.data_ptr(), cache.data_ptr(), cu_seqlens.data_ptr(),
@@ -638,7 +650,7 @@ def kda_latent_expanded(out, q, kv, k_pe, cu_q, cu_k, scale=None, causal=True, l
     if B < 0 or cu_k.numel() != B + 1:
         raise ValueError("cu_q and cu_k must have B + 1 entries")
     _check_current(dev)
-    workspace = _workspace(workspace, latent_expanded_workspace_size(B, Tq, H), dev, stream)
+    workspace = _workspace(workspace, latent_expanded_workspace_size, (B, Tq, H), dev, stream)
     status = _status_word(dev_status, dev, stream)
     rc = _lib.load().kda_latent_expanded(
         out.data_ptr(), _ptr(lse), q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), cu_q.data_ptr(),

@@ -19,6 +19,8 @@ def new_rows(case, seed=3, spread=1.0):
 
 def append(case, rows, gamma, eps=1e-5, **kw):
     cache = Guarded(case.cache.shape, torch.bfloat16, like=case.cache)
+    if "stream" in kw:  # (the buffers are filled on the current one)
+        kw["stream"].wait_stream(torch.cuda.current_stream())
     status = kda.kda_latent_append(cache.t, rows, case.cu, case.seq_lens, kw.pop("table", case.table), gamma=gamma, eps=eps, **kw)
     torch.cuda.synchronize()
     assert cache.intact()

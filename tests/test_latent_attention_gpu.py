@@ -24,6 +24,8 @@ def attend(case, q, causal=True, mask=None, scale=None, with_lse=True, **kw):
     out = Guarded((T, H, LATENT), torch.bfloat16, fill=float("nan"))
     lse = Guarded((T, H), torch.float32, fill=float("nan"))
     work = Guarded((kda.latent_attention_workspace_size(case.B, T, H),), torch.uint8, fill=0xFF)
+    if "stream" in kw:  # (the buffers are filled on the current one)
+        kw["stream"].wait_stream(torch.cuda.current_stream())
     status = kda.kda_latent_attention(out.t, q, kw.pop("cache", case.cache), kw.pop("cu", case.cu),
                                       kw.pop("seq_lens", case.seq_lens), kw.pop("table", case.table), scale=scale,
                                       causal=causal, tree_mask=mask, lse=lse.t if with_lse else None, workspace=work.t, **kw)

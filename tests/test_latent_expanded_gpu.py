@@ -32,6 +32,8 @@ def attend(c, causal=True, scale=None, with_lse=True, **kw):
     out = Guarded((T, H, HEAD), torch.bfloat16, fill=float("nan"))
     lse = Guarded((T, H), torch.float32, fill=float("nan"))
     work = Guarded((kda.latent_expanded_workspace_size(len(c.n), T, H),), torch.uint8, fill=0xFF)
+    if "stream" in kw:  # (the buffers are filled on the current one)
+        kw["stream"].wait_stream(torch.cuda.current_stream())
     status = kda.kda_latent_expanded(out.t, c.q, c.kv, c.k_pe, c.cu_q, c.cu_k, scale=scale, causal=causal,
                                      lse=lse.t if with_lse else None, workspace=work.t, **kw)
     torch.cuda.synchronize()

@@ -25,6 +25,8 @@ def attend(case, q, mask, scale=None, max_tokens=None, with_lse=True, **kw):
     most = max(case.n) if max_tokens is None else max_tokens
     work = Guarded((kda.tree_attention_workspace_size(case.B, T, most, H, case.HKV, D),), torch.uint8, fill=0xFF)
     caches, scales = case.args()
+    if "stream" in kw:  # (the buffers are filled on the current one)
+        kw["stream"].wait_stream(torch.cuda.current_stream())
     status = kda.kda_tree_attention(out.t, q, *caches, kw.pop("cu", case.cu), kw.pop("seq_lens", case.seq_lens),
                                     kw.pop("table", case.table), mask, most, scale=scale, **scales,
                                     lse=lse.t if with_lse else None, workspace=work.t, **kw)
@@ -285,3 +287,62 @@ def test_bad_values_of_many_small_trees():
     keep = torch.arange(128, device="cuda") != 77
     assert torch.equal(out[sees][..., keep], want[sees][..., keep])
     assert bool(torch.isnan(out[sees][..., 77]).all())
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_same_bits_when_copies_arrive_late(cache):
+    """Long caches read through a cold L2 and through a warm one, alone and beside calls on other streams."""
+    case, q = make(dict(n=[40] * 10, lens=[9001] * 10, H=24, HKV=4, D=128, page=64), cache=cache, seed=63)
+    mask = mask_of(trees(case.n), 2)
+    flush = torch.empty(300 << 20, dtype=torch.uint8, device="cuda")
+    first = None
+    for trial in range(4):
+        if trial % 2 == 0:
+            flush.fill_(trial)
+        out, lse, status = attend(case, q, mask)
+        first = first or (out, lse)
+        assert status == 0 and torch.equal(out, first[0]) and torch.equal(lse, first[1]), f"trial {trial}"
+    caches, scales = case.args()
+    got = [(torch.zeros_like(first[0]), torch.zeros_like(first[1]), torch.cuda.Stream()) for _ in range(3)]
+    torch.cuda.synchronize()
+    words = [kda.kda_tree_attention(out, q, *caches, case.cu, case.seq_lens, case.table, mask, 40, **scales, lse=lse, stream=s)
+             for _ in range(3) for out, lse, s in got]
+    torch.cuda.synchronize()
+    assert all(int(w.item()) == 0 for w in words)
+    assert all(torch.equal(out, first[0]) and torch.equal(lse, first[1]) for out, lse, _ in got)
+    close(first[0], first[1], reference(case, q, trees(case.n), 128 ** -0.5))
+
+
+def test_more_requests_than_threads():
+    g = torch.Generator().manual_seed(64)
+    n = torch.randint(0, 3, (1300,), generator=g).tolist()
+    lens = [k + int(x) for k, x in zip(n, torch.randint(0, 50, (1300,), generator=g))]
+    case, q = make(dict(n=n, lens=lens, H=3, HKV=1, D=128, page=16), seed=64)
+    check(case, q, trees(n, seed=3))
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured calls of other sizes, replayed in turns."""
+    cases = [make(dict(n=[20, 31], lens=[700, 4000], H=16, HKV=2, D=128, page=32), cache="e4m3", seed=65),
+             make(dict(n=[64], lens=[9000], H=32, HKV=8, D=128, page=64), seed=66)]
+    need = max(kda.tree_attention_workspace_size(c.B, c.T, max(c.n), q.shape[1], c.HKV, 128) for c, q in cases)
+    work = torch.empty(need, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for case, q in cases:
+        mask = mask_of(trees(case.n), 2)
+        want, wlse, _ = attend(case, q, mask)
+        caches, scales = case.args()
+        out, lse, word = torch.zeros_like(want), torch.zeros_like(wlse), torch.zeros(1, dtype=torch.int32, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            kda.kda_tree_attention(out, q, *caches, case.cu, case.seq_lens, case.table, mask, max(case.n), **scales,
+                                   lse=lse, workspace=work, dev_status=word)
+        graphs.append((graph, out, lse, word, want, wlse))
+    for turn in range(6):
+        for graph, out, lse, *_ in graphs:
+            out.zero_()
+            lse.zero_()
+            graph.replay()
+        torch.cuda.synchronize()
+        for graph, out, lse, word, want, wlse in graphs:
+            assert torch.equal(out, want) and torch.equal(lse, wlse) and int(word.item()) == 0
