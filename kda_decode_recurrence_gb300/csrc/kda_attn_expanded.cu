@@ -275,12 +275,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int item = 0; read_part(t, item, part); leave_part(t, item), ++item) {
       const int row = part.row0 + rank * kM + r, pos = part.L - part.n + row;
       const bool live = row < part.n;
+      const bool idle = !__any_sync(0xffffffffu, live);  // (what is left in P stays in rows that nobody reads)
       const int row_hi = pos < 0 ? 0 : p.causal ? min(pos + 1, part.L) : part.L;
       float m = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       bool rounds = false;  // a maximum of the warp's is past kRounds
       for (int i = 0; i < part.count; ++i, ++task) {
         if (!wait(&sm.s_full[t], task & 1)) break;
+        if (idle) {
+          if (lane == 0) {
+            mbar_arrive_cluster(p_half);
+            mbar_arrive_cluster(p_full);
+          }
+          continue;
+        }
         tc_fence_after();
         const int start = (part.tile0 + i) * kTile;
         // whole key tiles take x = c S in one product with the subtraction
@@ -321,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (plain) top *= c;
         // A larger maximum moves the sum and O; S came after the product before it, so O is at rest.
         const float now = fmaxf(m, top);
-        if (__any_sync(0xffffffffu, now > m + kGrow)) {
+        if (__any_sync(0xffffffffu, live && now > m + kGrow)) {  // (a row that is not live may hold anything)
           const float keep = exp2_approx(m - (now == -INFINITY ? 0.f : now));
           l2.x *= keep;
           l2.y *= keep;
@@ -338,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           m = now;
-          rounds = __any_sync(0xffffffffu, fabsf(m) > kRounds && m != -INFINITY);
+          rounds = __any_sync(0xffffffffu, live && fabsf(m) > kRounds && m != -INFINITY);
         }
         // c S is exact in the one product and the maximum rounded, by hundreds where scores are
         // billions: there both are rounded, so that the largest weight is 1

@@ -599,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int in = rank * kHalf + row, flat = part.row0 + in;
       const int token = flat / p.H, pos = L - n + token;
       const bool live = flat < (long long)n * p.H;
+      const bool idle = !__any_sync(0xffffffffu, live);  // (what is left in P stays in rows that nobody reads)
       const int row_hi = pos < 0 || !live ? 0 : p.causal ? min(pos + 1, L) : L;
       const int32_t* words = p.mask && live ? p.mask + (size_t)(part.t0 + token) * p.mask_words : nullptr;
       float m = -INFINITY;
@@ -606,6 +607,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < part.count; ++i, ++task) {
         ok = wait_pair(&sm.s_full[task & 1], (task >> 1) & 1);
         if (!ok) break;
+        if (idle) {
+          if (task > 0) ok = wait_pair(&sm.o_done, (task - 1) & 1);  // (no word twice of one product)
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_cluster(p_ready);
+          continue;
+        }
         tc_fence_after();
         const int start = (part.tile0 + i) * kTile + half * kHalf;
         float x[2][32];
@@ -638,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (task > 0) ok = ok && wait_pair(&sm.o_done, (task - 1) & 1);  // O and P are at rest
         if (!ok) break;
         // (both warps of a row decide alike: they have the same rows, maxima and so references)
-        if (__any_sync(0xffffffffu, now > m + kGrow)) {
+        if (__any_sync(0xffffffffu, live && now > m + kGrow)) {  // (a row that is not live may hold anything)
           const float keep = exp2_approx(m - (now == -INFINITY ? 0.f : now));
           l2.x *= keep;
           l2.y *= keep;
@@ -680,6 +687,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_cluster(p_ready);
       }
       if (!ok) break;
+      if (idle) {
+        ok = wait_pair(&sm.o_done, (task - 1) & 1);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_cluster(o_free);
+        continue;
+      }
       const float l_half = l2.x + l2.y, l = l_half + swap(l_half);
       ok = ok && wait_pair(&sm.o_done, (task - 1) & 1);
       if (!ok) break;

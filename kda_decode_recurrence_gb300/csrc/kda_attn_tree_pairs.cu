@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (plain) top *= c;
         // A larger maximum moves the sum and O; S came after the product before it, so O is at rest.
         const float now = fmaxf(m, top);
-        if (__any_sync(0xffffffffu, now > m + kGrow)) {
+        if (__any_sync(0xffffffffu, live && now > m + kGrow)) {  // (a row that is not live may hold anything)
           const float keep = exp2_approx(m - (now == -INFINITY ? 0.f : now));
           l2.x *= keep;
           l2.y *= keep;
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           m = now;
-          rounds = __any_sync(0xffffffffu, fabsf(m) > kRounds && m != -INFINITY);
+          rounds = __any_sync(0xffffffffu, live && fabsf(m) > kRounds && m != -INFINITY);
         }
         // c S is exact in the one product and the maximum rounded, by hundreds where scores are
         // billions: there both are rounded, so that the largest weight is 1

@@ -337,12 +337,12 @@ def test_graphs_that_share_a_workspace():
         with torch.cuda.graph(graph):
             kda.kda_tree_attention(out, q, *caches, case.cu, case.seq_lens, case.table, mask, max(case.n), **scales,
                                    lse=lse, workspace=work, dev_status=word)
-        graphs.append((graph, out, lse, word, want, wlse))
+        graphs.append((graph, out, lse, word, want, wlse, mask))  # (the graph reads the mask)
     for turn in range(6):
         for graph, out, lse, *_ in graphs:
             out.zero_()
             lse.zero_()
             graph.replay()
         torch.cuda.synchronize()
-        for graph, out, lse, word, want, wlse in graphs:
+        for graph, out, lse, word, want, wlse, _ in graphs:
             assert torch.equal(out, want) and torch.equal(lse, wlse) and int(word.item()) == 0
