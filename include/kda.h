@@ -42,7 +42,8 @@
  *     advanced (some requests skipped, or after KDA_DEV_TIMEOUT some tiles not
  *     written back) with no sign of it.  Pass a status word wherever the
  *     inputs are not known to be valid.
- *   - Calls that write the same state slots must not overlap in time.
+ *   - Calls that write the same state slots must not overlap in time, nor calls that
+ *     share a workspace.
  *
  * Page citations name the page title and the section it falls in:
  *   "KdaDecode"                       MAX Mojo builtin kernel, struct KdaDecode:

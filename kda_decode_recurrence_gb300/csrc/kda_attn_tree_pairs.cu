@@ -19,7 +19,8 @@
 // A slot's chain (S, a row's 128 exponentials, PV) is some 4000 cycles of a key tile beside 1024 of its
 // products, and two of them overlap: 16 trees of 60 nodes over 4060: DRAM 54 %, tensor cores 49 %.  e4m3 adds two
 // products per pair of scores; without the codes' widening the 194 us would be 187, without either scale 181.
-// Measured and left: an item's nodes dealt evenly to the two CTAs (128 -> 130 us), kItemCost of 1, 2 and 5.
+// Measured and left: an item's nodes dealt evenly to the two CTAs (128 -> 130 us), e4m3's S read twice from tensor
+// memory in place of 128 registers (194 -> 216), kItemCost of 1, 2 and 5.
 //
 // In key tiles with nodes, or the sequence's end, scores are masked, and entries of V that are not the
 // request's, or not finite, are taken out of shared memory first (0 x NaN would reach the rows that do not
