@@ -24,12 +24,12 @@
 // unfinished: its pieces are joined by a second kernel).  O is rescaled only when a row's
 // maximum has grown by more than 2^8.
 //
-// 128 tokens over 300-20000, 32 heads: 230 us, 5.9 TB/s of cache (240-253 while warps without a live row went
-// through the softmax); 64 over 1000-8000, 96 heads: 80 us, 4.4 TB/s.
+// 128 tokens over 300-20000, 32 heads: 226-246 us by box, 5.5-6.0 TB/s of cache (239 beside 228 when warps without
+// a live row go through the softmax); 64 over 1000-8000, 96 heads: 80-82 us, 4.4 TB/s.
 // A key tile takes some 2900 cycles of a pair: 2176 of products, 150 of their issue, 570 of waits for copies,
 // since the rings hold one key tile; an item's ends some 10000 (O through registers, 64 rows a CTA), a call's
 // beginning 11000 and the join 7-10 us.  (76 x 6001 positions: tensor cores 60 % of active cycles, DRAM 69 %.)
-// With pages of 16 a tile's 8 boxes per panel bound it: 4200 cycles a tile.
+// 32 windows of 1-8 over 200-6000, 64 heads, pages of 16: 69 us, the copies of smaller boxes in a tile's chain.
 // Measured and left: copies in units of one key panel (296 us against 251 then), four more warps for half of
 // the output (an item's ends 8000, a tile 100-200 more: 255 us against 250), kItemCost of 4 to 6.
 #include <cuda.h>
@@ -53,6 +53,17 @@ constexpr int kPanelBytes = kHalf * 128;
 // columns); the rings hold a key tile's.
 constexpr int kKeyPanels = 3, kKeys = kPanels / kKeyPanels, kKeyBytes = kKeyPanels * kPanelBytes;
 constexpr int kValuePanels = 4, kValues = 2, kValueBytes = kValuePanels * kPanelBytes;
+// A unit in shared memory: panels of 64 rows (panel after panel of 128-byte rows), or, grouped, panels of 8 rows
+// (8 rows of all its panels, then the next 8).  Grouped, a copy takes 8 rows of a whole unit, else a page's
+// rows, one panel each unless they are 64: a key tile of pages of 16 takes 40 copies in place of 68, of 32
+// 40 in place of 34, of 64 and more 40 in place of 5.  So only pages of 16 are grouped.
+// (32 windows of 1-8 over 200-6000, pages of 16: 73.4 -> 69.3 us.)
+template <bool kGrouped>
+constexpr int kPanelAt = kGrouped ? 1024 : kPanelBytes;            // between a unit's panels
+template <bool kGrouped>
+constexpr int kKeyGroup = kGrouped ? kKeyPanels * 1024 : 1024;     // between its groups of 8 rows
+template <bool kGrouped>
+constexpr int kValueGroup = kGrouped ? kValuePanels * 1024 : 1024;
 constexpr int kAhead = 2;           // key tiles that are fetched into L2 before their copies
 constexpr int kNotes = 4;           // items whose notes are kept
 constexpr int kItemCost = 3;        // what an item's beginning and end take, in key tiles
@@ -166,6 +177,7 @@ __device__ __forceinline__ uint4 finite(uint4 x) {
   return make_uint4(keep(x.x), keep(x.y), keep(x.z), keep(x.w));
 }
 
+template <bool kGrouped>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap key_map, const __grid_constant__ CUtensorMap value_map,
                   const LatentArgs p, const Pieces pieces) {
@@ -362,14 +374,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kKeyWarp || warp == kCopyWarp) {
     // ---- keys or values into their ring.  (This chain is as long as a key tile takes: no division in it.)
     const int page_shift = 31 - __clz(p.c.page_size), in_page = p.c.page_size - 1;
-    const int rows_per_box = min(p.c.page_size, kHalf), box_shift = min(page_shift, 6);
+    const int box_shift = kGrouped ? 3 : min(page_shift, 6), rows_per_box = 1 << box_shift;
     const int half_boxes = kHalf >> box_shift, boxes = 2 * half_boxes;  // of a half, of a key tile
     const int nowhere = p.c.num_pages << page_shift;                    // a row past the end: zeros
     // a unit's copies, by lane: all panels of 64 rows at once, or of fewer rows a panel each
     const bool keys = warp == kKeyWarp;
     const int in = lane & (half_boxes - 1), panel = lane / half_boxes;
-    const int copies = half_boxes == 1 ? 1 : keys ? kKeyPanels : kValuePanels;
-    const uint32_t to = panel * kPanelBytes + in * rows_per_box * 128;
+    const int panels = keys ? kKeyPanels : kValuePanels;
+    const int copies = kGrouped || half_boxes == 1 ? 1 : panels;
+    const uint32_t to = panel * kPanelBytes + in * rows_per_box * 128 * (kGrouped ? panels : 1);
     const uint32_t ready0 = cluster_addr(&sm.key_ready[0], 0);
     int tasks = 0, put = 0;      // key tiles, units so far
     int soon = -1, soon_in = 0;  // page and position in it to be fetched into L2 next, by lane
@@ -486,11 +499,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const uint64_t a = smem_desc_sw128(q0 + k * kKeyBytes, 16, 1024);
-            const uint64_t b = smem_desc_sw128(key0 + k * kKeyBytes, 16, 1024);
+            const uint64_t b = smem_desc_sw128(key0 + k * kKeyBytes, 16, kKeyGroup<kGrouped>);
 #pragma unroll
             for (int j = 0; j < 4 * kKeyPanels; ++j) {  // 32 bytes on, or the next panel
-              const uint64_t at = (j & 3) * 2 + (j >> 2) * (kPanelBytes / 16);
-              mma_bf16_pair_if(one, s_col, a + at, b + at, idesc_s, k + j > 0 ? 1u : 0u);
+              mma_bf16_pair_if(one, s_col, a + (j & 3) * 2 + (j >> 2) * (kPanelBytes / 16),
+                               b + (j & 3) * 2 + (j >> 2) * (kPanelAt<kGrouped> / 16), idesc_s, k + j > 0 ? 1u : 0u);
             }
             mma_commit_pair_if(one, k < kKeys - 1 ? &sm.key_empty[k] : &sm.s_full[(task + i) & 1]);
           }
@@ -506,11 +519,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const uint64_t a = smem_desc_sw128(p0 + v * kPanelBytes, 16, 1024);
-            const uint64_t c = smem_desc_sw128(value0 + v * kValueBytes, kPanelBytes, 1024);
+            const uint64_t c = smem_desc_sw128(value0 + v * kValueBytes, kPanelAt<kGrouped>, kValueGroup<kGrouped>);
 #pragma unroll
             for (int j = 0; j < 8; ++j)  // 16 keys, then this CTA's next 128 columns
               mma_bf16_pair_if(one, base + kColO + (j >> 2) * 128, a + 2 * (j & 3),
-                               c + (((j & 3) * 16 * 128) >> 4) + (j >> 2) * (2 * kPanelBytes / 16), idesc_o,
+                               c + (j & 3) * (2 * kValueGroup<kGrouped> / 16) + (j >> 2) * (2 * kPanelAt<kGrouped> / 16), idesc_o,
                                i > 1 || v > 0 || (j & 3) > 0 ? 1u : 0u);
             mma_commit_pair_if(one, v < kValues - 1 ? &sm.value_empty[v] : &sm.o_done);
           }
@@ -569,7 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 8
             for (int k = 0; k < 16; ++k) {
               const int n = k * 32 + lane, key = wv * 16 + ((n >> 3) & 15);
-              uint4* x = reinterpret_cast<uint4*>(sm.value[s] + (n >> 7) * kPanelBytes + swizzled<128>(key, n & 7));
+              uint4* x = reinterpret_cast<uint4*>(sm.value[s] + (n >> 7) * kPanelAt<kGrouped> + (key >> 3) * kValueGroup<kGrouped> +
+                                                  swizzled<128>(key & 7, n & 7));
               const uint4 y = *x;
               const uint4 z = start + v * kHalf + key < part.L ? finite(y) : make_uint4(0, 0, 0, 0);
               if (y.x != z.x || y.y != z.y || y.z != z.z || y.w != z.w) *x = z;
@@ -805,6 +819,27 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const LatentArgs p, co
   if (p.lse && cc == 0 && threadIdx.x < kHalf) p.lse[out_row] = (m + log2f(l)) * kLn2;
 }
 
+template <bool kGrouped>
+cudaError_t launch_latent(const LatentArgs& a, cudaStream_t stream) {
+  static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "a CTA fits an SM");
+  // The cache as [panel of 64 entries][row][64 entries]: a box of several panels lands as a unit's layout.
+  const uint32_t page_rows = a.c.page_size < kHalf ? a.c.page_size : kHalf;
+  const bool whole_unit = kGrouped || page_rows == kHalf;
+  CUtensorMap maps[2];
+  for (int i = 0; i < 2; ++i)
+    if (!make_map_3d_bf16(&maps[i], a.c.rows, 64, (uint64_t)a.c.num_pages * a.c.page_size, kPanels, kLatentRow * 2, 128,
+                          64, kGrouped ? 8 : page_rows, whole_unit ? (i ? kValuePanels : kKeyPanels) : 1))
+      return cudaErrorInvalidValue;
+  const size_t smem = sizeof(Smem) + 1024;
+  static SmemSet set;
+  cudaError_t e = allow_smem(latent_kernel<kGrouped>, smem, set);
+  if (e != cudaSuccess) return e;
+  const Pieces pieces = pieces_at(a.workspace, kPairs, kRows);
+  e = launch_pairs(latent_kernel<kGrouped>, dim3(2 * kPairs), dim3(kThreads), smem, stream, maps[0], maps[1], a, pieces);
+  if (e != cudaSuccess) return e;
+  return launch(latent_join_kernel, dim3(kPairs, kJoinY), dim3(128), 0, stream, true, a, pieces);
+}
+
 }  // namespace
 
 size_t latent_workspace_bytes(int B, int T, int H) {
@@ -813,25 +848,7 @@ size_t latent_workspace_bytes(int B, int T, int H) {
 }
 
 cudaError_t launch_latent_attention(const LatentArgs& a, cudaStream_t stream) {
-  static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "a CTA fits an SM");
-  // The cache as [panel of 64 entries][row][64 entries]: a box of 64 rows and several panels lands as the
-  // panels' operand layout; rows of smaller pages take a box a panel (16 rows: 4234 cycles a key tile
-  // against 2950).
-  const uint32_t rows_per_box = a.c.page_size < kHalf ? a.c.page_size : kHalf;
-  const bool whole_unit = rows_per_box == kHalf;
-  CUtensorMap maps[2];
-  for (int i = 0; i < 2; ++i)
-    if (!make_map_3d_bf16(&maps[i], a.c.rows, 64, (uint64_t)a.c.num_pages * a.c.page_size, kPanels, kLatentRow * 2, 128,
-                          64, rows_per_box, whole_unit ? (i ? kValuePanels : kKeyPanels) : 1))
-      return cudaErrorInvalidValue;
-  const size_t smem = sizeof(Smem) + 1024;
-  static SmemSet set;
-  cudaError_t e = allow_smem(latent_kernel, smem, set);
-  if (e != cudaSuccess) return e;
-  const Pieces pieces = pieces_at(a.workspace, kPairs, kRows);
-  e = launch_pairs(latent_kernel, dim3(2 * kPairs), dim3(kThreads), smem, stream, maps[0], maps[1], a, pieces);
-  if (e != cudaSuccess) return e;
-  return launch(latent_join_kernel, dim3(kPairs, kJoinY), dim3(128), 0, stream, true, a, pieces);
+  return a.c.page_size == 16 ? launch_latent<true>(a, stream) : launch_latent<false>(a, stream);
 }
 
 }  // namespace kda
