@@ -1,5 +1,5 @@
 // kda_attn_chunk.cuh -- attention of chunks: the requests with more rows (new tokens x
-// query heads per key head) than the window kernel takes, and drafted trees (kTree).
+// query heads per key head) than the window kernel takes, and drafted trees over heads of 64 (kTree).
 //
 // Such a request does 4 D operations per row and cached position on 4 D bytes per
 // position: with hundreds of rows the tensor cores bound it.  One CTA per SM
@@ -815,7 +815,10 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, kPair>::kThreads, 1)
       // the masks of a tree's tokens (rows beyond it have a token's, and are not written)
       auto words_of = [&](int of) { return p.tree + (size_t)(w.r.t0 + min(of, n - 1)) * p.tree_words; };
       [[maybe_unused]] const int32_t* words = kTree ? words_of(token) : nullptr;
-      float m = -INFINITY;
+      // A row of no token holds what was there before: its maximum never grows, so that it has no say in when the
+      // warp rescales.
+      auto least = [&](int in) { return in / p.G < per_tile && token0 + in / p.G < n ? -INFINITY : INFINITY; };
+      float m = least(r);
       float2 l2 = make_float2(0.f, 0.f);
       bool begun = false;
       [[maybe_unused]] bool rounds = false;  // a maximum of the warp's is past kRounds
@@ -828,7 +831,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, kPair>::kThreads, 1)
           const int at = L - n + token0 + (32 * (warp & 3) + 8 * k + (lane >> 2)) / p.G;
           lo4[k] = seen_lo(p, at);
           hi4[k] = min(seen_hi(p, at, L), L);
-          m4[k] = -INFINITY;
+          m4[k] = least(32 * (warp & 3) + 8 * k + (lane >> 2));
           l4[k] = 0.f;
         }
       }
@@ -890,7 +893,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, kPair>::kThreads, 1)
               }
             }
             m = now;
-            rounds = __any_sync(0xffffffffu, fabsf(m) > kRounds && m != -INFINITY);
+            rounds = __any_sync(0xffffffffu, fabsf(m) > kRounds && fabsf(m) < INFINITY);
           }
           begun = true;
         };
@@ -1226,11 +1229,6 @@ template <bool kTree, int D, bool kE4m3>
 cudaError_t by_pair(const AttentionArgs& a, cudaStream_t stream) {
   return a.max_tokens > kM / a.G ? launch_chunk<D, kE4m3, true, kTree>(a, stream)
                                  : launch_chunk<D, kE4m3, false, kTree>(a, stream);
-}
-template <bool kTree>
-cudaError_t by_type(const AttentionArgs& a, cudaStream_t stream) {
-  if (a.c.D == 128) return a.c.e4m3 ? by_pair<kTree, 128, true>(a, stream) : by_pair<kTree, 128, false>(a, stream);
-  return a.c.e4m3 ? by_pair<kTree, 64, true>(a, stream) : by_pair<kTree, 64, false>(a, stream);
 }
 
 }  // namespace

@@ -346,3 +346,31 @@ def test_graphs_that_share_a_workspace():
         torch.cuda.synchronize()
         for graph, out, lse, word, want, wlse, _ in graphs:
             assert torch.equal(out, want) and torch.equal(lse, wlse) and int(word.item()) == 0
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_bits_do_not_depend_on_what_ran_before(D, cache):
+    """126 of a row tile's 128 rows are used (6 heads a group): what the others hold is left over from the call before,
+    here of queries of another size.  Trees, and a chunk of the same tokens."""
+    case, q = make(dict(n=[40] * 6, lens=[3001] * 6, H=24, HKV=4, D=D, page=64), cache=cache, seed=67)
+    mask = mask_of(trees(case.n), 2)
+    full, fq = make(dict(n=[64] * 20, lens=[1100] * 20, H=32, HKV=8, D=D, page=64), cache=cache, seed=68)
+    fmask = mask_of(trees(full.n), 2)
+    caches, scales = case.args()
+    fcaches, fscales = full.args()
+
+    def chunk(c, q, caches, scales, most):
+        out = torch.zeros(c.T, q.shape[1], D, device="cuda", dtype=torch.bfloat16)
+        kda.kda_paged_attention(out, q, *caches, c.cu, c.seq_lens, c.table, most, **scales, check_device=True)
+        return out
+
+    want = None
+    for amplitude in (1e-3, 1.0, 30.0, 1e3):
+        before = (fq.float() * amplitude).to(torch.bfloat16)
+        attend(full, before, fmask)
+        tree = attend(case, q, mask)[0].clone()
+        chunk(full, before, fcaches, fscales, 64)
+        line = chunk(case, q, caches, scales, 40)
+        want = want or (tree, line)
+        assert torch.equal(tree, want[0]) and torch.equal(line, want[1]), f"after queries of {amplitude}"
