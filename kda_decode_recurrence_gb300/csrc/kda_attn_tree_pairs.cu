@@ -18,7 +18,7 @@
 // masks: 134); 16 of 4-32 over 500-12000, 96 / 8 heads, e4m3: 194 us (270); one of 13 nodes over 517: 16 us.
 // A slot's chain (S, a row's 128 exponentials, PV) is some 4000 cycles of a key tile beside 1024 of its
 // products, and two of them overlap: 16 trees of 60 nodes over 4060: DRAM 54 %, tensor cores 49 %.  e4m3 adds two
-// products per pair of scores; without the codes' widening the 194 us would be 187, without either scale 181.
+// products per pair of scores; without the codes' widening the 194 us would be 187, with one scale less 181-183.
 // Measured and left: an item's nodes dealt evenly to the two CTAs (128 -> 130 us), e4m3's S read twice from tensor
 // memory in place of 128 registers (194 -> 216), kItemCost of 1, 2 and 5.
 //
