@@ -492,8 +492,9 @@ kda_status kda_latent_append(kda_bf16* cache, const kda_bf16* rows, const float*
  *   out = sum_j e^(x_j - m) c_j / sum_j e^(x_j - m),  m = max_j x_j;   lse = ln sum_j e^(x_j)
  * A token that sees nothing gets out = 0, lse = -inf.  Scores, sums and outputs are accumulated in
  * fp32; the weights are rounded to bf16 for the product with c, 2^-8 of each at most.  What a row
- * holds that a token does not see (not a number, an infinity) has no influence on it; rows that it
- * sees must be finite (one with a NaN makes its output NaN).
+ * holds that a token does not see (not a number, an infinity) has no influence on it; what it sees
+ * goes by the formula: a score that is +infinity or no number makes the token's output no number,
+ * one of -infinity (weight 0) the entries where the row is infinite.
  *
  *   out          [T, H, 512] bf16, written.  Alignment 16 B.
  *   lse          [T, H] fp32, written, or NULL.

@@ -94,6 +94,7 @@ struct Smem {
   unsigned char p[2][kPanelBytes];          // 64 rows x 64 keys, twice
   Part part[kNotes];
   float red[2][2 * kHalf];
+  int bad[kNotes];                          // item + 1: live entries of values were taken out of that item
   long long scan[2][kWarps];
   long long first_unit;                     // of the request that holds the share's first unit
   int first_request;
@@ -177,10 +178,36 @@ __device__ __forceinline__ uint4 finite(uint4 x) {
   return make_uint4(keep(x.x), keep(x.y), keep(x.z), keep(x.w));
 }
 
+// Adds the live entries of the latents that were taken out of an item's partly seen key tiles to columns
+// col .. col + 31 of one row's output: the weight of each is found again from the query and the row in memory.
+// (Rare: values that are not finite.)
+__device__ __noinline__ void add_bad_latents(const LatentArgs& p, int b, int L, int n, int from, int to,
+                                             const int32_t* words, const kda_bf16* q, float m, int col, float* o) {
+  const int32_t* table = p.c.page_table + (size_t)b * p.c.max_pages;
+  auto value = [](kda_bf16 x) { return __uint_as_float((uint32_t)x << 16); };
+  for (int j = from; j < to; ++j) {
+    if (words && !(tree_bits(words, p.mask_words, n, j - (L - n)) & 1)) continue;
+    const int page = table[j / p.c.page_size];
+    if (page < 0 || page >= p.c.num_pages) continue;
+    const kda_bf16* row = p.c.rows + ((size_t)page * p.c.page_size + j % p.c.page_size) * kLatentRow;
+    float w = -1.f;
+    for (int d = 0; d < 32; ++d) {
+      const kda_bf16 v = row[col + d];
+      if ((v & 0x7f80u) != 0x7f80u) continue;
+      if (w < 0.f) {
+        float x = 0.f;
+        for (int e = 0; e < kLatentRow; ++e) x = fmaf(value(q[e]), value(row[e]), x);
+        w = exp2_approx(x * (p.scale * kLog2E) - m);
+      }
+      o[d] = fmaf(w, value(v), o[d]);
+    }
+  }
+}
+
 template <bool kGrouped>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap key_map, const __grid_constant__ CUtensorMap value_map,
-                  const LatentArgs p, const Pieces pieces) {
+                  const __grid_constant__ LatentArgs p, const Pieces pieces) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -199,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kNotes; ++s) {
       mbar_init(&sm.part_full[s], 1);
       mbar_init(&sm.part_empty[s], 11);  // warps that read notes
+      sm.bad[s] = 0;
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.s_full[s], 1);
@@ -578,15 +606,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           if (start + kTile > part.whole) {
             // A quarter of the unit's 64 keys, four panels of eight chunks each.  0 x NaN would reach
-            // rows that do not see it; rows that do have a score that is not finite.
+            // rows that do not see it; those that do add it at the item's end.
+            bool bad = false;
 #pragma unroll 8
             for (int k = 0; k < 16; ++k) {
               const int n = k * 32 + lane, key = wv * 16 + ((n >> 3) & 15);
               uint4* x = reinterpret_cast<uint4*>(sm.value[s] + (n >> 7) * kPanelAt<kGrouped> + (key >> 3) * kValueGroup<kGrouped> +
                                                   swizzled<128>(key & 7, n & 7));
               const uint4 y = *x;
-              const uint4 z = start + v * kHalf + key < part.L ? finite(y) : make_uint4(0, 0, 0, 0);
-              if (y.x != z.x || y.y != z.y || y.z != z.z || y.w != z.w) *x = z;
+              const bool live = start + v * kHalf + key < part.L;
+              const uint4 z = live ? finite(y) : make_uint4(0, 0, 0, 0);
+              if (y.x != z.x || y.y != z.y || y.z != z.z || y.w != z.w) {
+                *x = z;
+                bad |= live;
+              }
+            }
+            if (__any_sync(0xffffffffu, bad)) {  // for the rows of both CTAs
+              if (lane < 2)
+                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&sm.bad[item % kNotes], lane)),
+                             "r"(item + 1)
+                             : "memory");
+              asm volatile("fence.acq_rel.cluster;" ::: "memory");
             }
             fence_proxy_async_smem();
           }
@@ -725,6 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t out_row = (size_t)part.t0 * p.H + flat;
       const size_t piece = ((size_t)pair * 2 + (part.flags & kBegins ? 1 : 0)) * kRows + in;
       const float inv = l == 0.f ? 0.f : 1.f / l;
+      const bool bad = sm.bad[item % kNotes] == item + 1;
       if (live && half == 0) {
         if (!done) pieces.ml[piece] = make_float2(m, l);
         else if (p.lse) p.lse[out_row] = (m + log2f(l)) * kLn2;
@@ -741,6 +782,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_32cols(lanes + kColO + cc, o);
         tmem_ld_wait();
         const int col = half * 256 + cc;
+        if (bad && live) {
+          float y[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = o[e];
+          add_bad_latents(p, part.b, L, n, max(part.tile0, part.whole / kTile) * kTile,
+                          min(row_hi, (part.tile0 + part.count) * kTile), words,
+                          p.q + (part.t0 + token) * p.q_stride + (size_t)(flat - token * p.H) * kLatentRow,
+                          m == -INFINITY ? 0.f : m, col, y);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = y[e];
+        }
+        __syncwarp();
         if (done) {
           uint4 y[4];
 #pragma unroll

@@ -304,3 +304,26 @@ def test_empty_calls():
     assert int(kda.kda_latent_attention(out, q[:0], case.cache, zero, case.seq_lens, case.table).item()) == 0
     out, _, status = attend(case, q, cu=zero[:1], seq_lens=zero[:0], table=case.table[:0])
     assert status == 0 and bool(torch.isnan(out).all())
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("n,lens,pos,H,kind", [
+    (1, 70, 20, 16, "causal"), (1, 300, 20, 16, "causal"), (1, 300, 290, 3, "causal"), (5, 200, 100, 16, "causal"),
+    (5, 200, 150, 40, "full"), (40, 130, 60, 24, "causal"), (40, 130, 100, 24, "causal"), (3, 9000, 100, 8, "causal"),
+    (3, 9000, 8980, 8, "causal"), (2, 9000, 8998, 64, "full"), (37, 150, 20, 12, "tree"), (37, 150, 124, 12, "tree")])
+def test_an_infinity_of_weight_zero(n, lens, pos, H, kind, bad):
+    """A latent with an infinite entry whose score is -infinity: the products with that entry are 0 x infinity, no number, for
+    every token that sees the row, wherever a key tile's border lies; the other entries are as without the row."""
+    for col in (7, 400):
+        case, q = make(dict(n=[n], lens=[lens], H=H, page=32), seed=46)
+        q[..., col] = -(q[..., col].abs() + 0.5) if bad > 0 else q[..., col].abs() + 0.5
+        tree = trees(case.n, seed=3) if kind == "tree" else None
+        see = seen_by(n, lens, kind == "causal", tree[0] if tree else None)
+        case.cache[int(case.table[0, pos // 32]), pos % 32, col] = bad
+        out, lse, status = attend(case, q, kind == "causal", mask_of(tree, 2) if tree else None)
+        rows, sees = case.dense(0), see[:, pos].clone()
+        see[:, pos] = False
+        want = softmax64(q, rows[:, None], rows[:, None, :LATENT], see, SCALE)
+        assert status == 0 and bool(sees.any()) and bool(torch.isnan(out[sees][..., col]).all())
+        out[sees, :, col] = want[0][sees, :, col].to(torch.bfloat16)
+        close(out, lse, want)
