@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kNotes; ++s) {
       mbar_init(&sm.part_full[s], 1);
-      mbar_init(&sm.part_empty[s], 11);  // warps that read notes
+      mbar_init(&sm.part_empty[s], rank == 0 ? 11 : 10);  // warps that read notes
       sm.bad[s] = 0;
     }
     for (int s = 0; s < 2; ++s) {
@@ -505,8 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = max(0, put - kValues); u < put; ++u) mbar_wait(&sm.value_full[u % kValues], (u / kValues) & 1);
     else if (rank == 0)
       for (int u = max(0, put - kKeys); u < put; ++u) mbar_wait(&sm.key_ready[u % kKeys], (u / kKeys) & 1);
-  } else if (warp == kMmaWarp) {
-    // ---- the products
+  } else if (warp == kMmaWarp && rank == 0) {
+    // ---- the products.  (The second CTA's warp would run ahead of the notes, and wait for a long part's end.)
     const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t q0 = smem_u32(sm.q[0]), key0 = smem_u32(sm.key[0]), value0 = smem_u32(sm.value[0]),
                    p0 = smem_u32(sm.p[0]);
@@ -515,7 +515,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     int task = 0;  // key tiles so far
     Part part;
     for (int item = 0; read_part(item, part); leave_part(item), ++item) {
-      if (rank != 0) continue;
       const int count = __shfl_sync(0xffffffffu, part.count, 0);
       ok = wait_pair(&sm.q_ready, item & 1);
       for (int i = 0; i <= count && ok; ++i) {
@@ -561,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
     }
     if (!ok && lane == 0) raise_status(p.dev_status, KDA_DEV_TIMEOUT);
-    if (rank == 0) mma_commit_pair_if(one, &sm.done);  // arrives when every product issued has completed
+    mma_commit_pair_if(one, &sm.done);  // arrives when every product issued has completed
     mbar_wait(&sm.done, 0);
   } else if (warp >= kValueWarp) {
     // ---- each item's queries; values that have arrived, without the entries that some row must not see
@@ -823,7 +822,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   cluster_sync();  // nothing of the pair is under way
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
+  if (warp == kMmaWarp) {
+    mbar_wait(&sm.done, 0);  // (the second CTA's word of it)
+    __syncwarp();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
   __syncwarp();
   cluster_sync();
 }

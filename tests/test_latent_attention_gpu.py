@@ -327,3 +327,28 @@ def test_an_infinity_of_weight_zero(n, lens, pos, H, kind, bad):
         assert status == 0 and bool(sees.any()) and bool(torch.isnan(out[sees][..., col]).all())
         out[sees, :, col] = want[0][sees, :, col].to(torch.bfloat16)
         close(out, lse, want)
+
+
+def test_a_part_of_more_than_a_second():
+    """A share that begins with a part of some 1.2 million key tiles (1.4 s at the products' rate) and goes on with seven short
+    ones: no warp may give up on a note while it waits for the first.  The pages repeat, and in each period of
+    them one row has a score 40 above the others: out is that row, and e^-40 of the others vanishes."""
+    page, period, longest = 128, 64, 1 << 30
+    lens = [150_000_000] + [400 + 130 * i for i in range(6)] + [longest] * 12
+    B, share = len(lens), sum(lens) / 128 / 76                 # key tiles of a pair of CTAs
+    assert lens[0] / 128 < share - 200 and lens[0] / 128 > 1.1e6 and share < 1.5e6
+    g = torch.Generator(device="cuda").manual_seed(47)
+    top = torch.where(torch.rand(ROW, device="cuda", generator=g) < 0.5, -1.0, 1.0)
+    cache = torch.randn(period, page, ROW, device="cuda", generator=g).mul_(0.01).to(torch.bfloat16)
+    cache[2, 17] = top.to(torch.bfloat16)                      # position 273 of every 8192
+    table = (torch.arange(longest // page, dtype=torch.int32, device="cuda") % period).expand(B, -1).contiguous()
+    q = (top * 2.0 ** -4).to(torch.bfloat16).expand(B, 1, ROW).contiguous()    # q . top = 36, of the others 0.014 and less
+    cu, seq = torch.arange(B + 1, dtype=torch.int32, device="cuda"), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out, lse = torch.full((B, 1, LATENT), float("nan"), dtype=torch.bfloat16, device="cuda"), torch.empty(B, 1, device="cuda")
+    status = kda.kda_latent_attention(out, q, cache, cu, seq, table, scale=40 / 36, lse=lse)
+    assert int(status.item()) == 0
+    assert torch.equal(out[:, 0], top[:LATENT].to(torch.bfloat16).expand(B, -1))
+    count = torch.tensor([-(-(x - 273) // 8192) for x in lens], dtype=torch.float64)
+    off = (lse[:, 0].double().cpu() - (40 + torch.log(count))).abs()
+    # the score, its factor and the sum's logarithm: a few fp32 roundings of 60; the others: at most 2^30 e^-39
+    assert bool((off < 60 * 8 * 2.0 ** -24 + 2.0 ** 30 * 1.2e-17).all())
