@@ -162,17 +162,19 @@ __device__ __forceinline__ void transpose4(uint4 (&x)[4], int lane) {
 
 // A wait of a whole warp; what follows when the phase is not there at once is out of
 // line, so that the product warps' waits take little room in the instruction cache.
+template <bool kCluster = false>
 static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity) {
   const unsigned long long t0 = global_ns();
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 16; ++i)
-      if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+      if (__all_sync(0xffffffffu, mbar_try<kCluster>(bar, parity))) return true;
     if (__any_sync(0xffffffffu, global_ns() - t0 > kWaitLimitNs)) return false;
   }
 }
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_together(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_try(bar, parity)) || wait_on(bar, parity);
+  return __all_sync(0xffffffffu, mbar_try<kCluster>(bar, parity)) || wait_on<kCluster>(bar, parity);
 }
 
 // A role's share of the registers that the block was launched with.

@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool ok = true;
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    ok = ok && wait_together(smem_u32(bar), parity);
+    ok = ok && wait_together<true>(smem_u32(bar), parity);
     return ok;
   };
   auto read_part = [&](int t, int item, Part& part) {
@@ -714,10 +714,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     *chunk(i) = make_uint4(x.x & ~out.x, x.y & ~out.y, x.z & ~out.z, x.w & ~out.w);
                 }
                 // the rows of either CTA add them at the item's end
-                if (lane < 2)
-                  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&sm.bad[t][item[t] % kNotes], lane)),
-                               "r"(item[t] + 1)
-                               : "memory");
+                if (lane == 0)
+                  for (int to = 0; to < 2; ++to)
+                    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&sm.bad[t][item[t] % kNotes], to)),
+                                 "r"(item[t] + 1)
+                                 : "memory");
                 asm volatile("fence.acq_rel.cluster;" ::: "memory");
               }
               fence_proxy_async_smem();
@@ -743,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();  // nothing of the pair is under way
   tc_fence_after();
   if (warp == kMmaWarp) {
-    mbar_wait(&sm.done, 0);  // (the second CTA's word of it)
+    mbar_wait<true>(&sm.done, 0);  // (the second CTA's word of it)
     __syncwarp();
     tmem_dealloc_pair(tmem, kTmemCols);
   }

@@ -163,11 +163,10 @@ __device__ __forceinline__ long long request_units(const LatentArgs& p, const Re
   return sum;
 }
 
-// A bounded wait of a whole warp.  Barriers of the first CTA that the other one arrives at carry no
-// data between the CTAs: what their arrivals stand for (a copy, P, an O that has been read) is in the
-// arriving SM's own memory, complete or fenced for its tensor core before the arrival.
+// A bounded wait of a whole warp.  What the other CTA's arrivals stand for (a copy, P, an O that has been read)
+// is in its own memory, complete or fenced for its tensor core, and released to the cluster by the arrival.
 __device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity) {
-  return wait_together(smem_u32(bar), parity);
+  return wait_together<true>(smem_u32(bar), parity);
 }
 
 // The entries of x (eight bf16) that are not finite become zeros.
@@ -621,10 +620,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             if (__any_sync(0xffffffffu, bad)) {  // for the rows of both CTAs
-              if (lane < 2)
-                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&sm.bad[item % kNotes], lane)),
-                             "r"(item + 1)
-                             : "memory");
+              if (lane == 0)
+                for (int to = 0; to < 2; ++to)
+                  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&sm.bad[item % kNotes], to)),
+                               "r"(item + 1)
+                               : "memory");
               asm volatile("fence.acq_rel.cluster;" ::: "memory");
             }
             fence_proxy_async_smem();
@@ -823,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();  // nothing of the pair is under way
   tc_fence_after();
   if (warp == kMmaWarp) {
-    mbar_wait(&sm.done, 0);  // (the second CTA's word of it)
+    mbar_wait<true>(&sm.done, 0);  // (the second CTA's word of it)
     __syncwarp();
     tmem_dealloc_pair(tmem, kTmemCols);
   }

@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool ok = true;
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    ok = ok && wait_together(smem_u32(bar), parity);
+    ok = ok && wait_together<true>(smem_u32(bar), parity);
     return ok;
   };
   auto read_part = [&](int t, int item, Part& part) {
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     more_registers<kSoftmaxRegs>();
     // (a call in a wait would bound the registers that this role may take)
     auto wait_here = [&](uint64_t* bar, uint32_t parity) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity));
+      ok = ok && __all_sync(0xffffffffu, mbar_wait<true>(bar, parity));
       return ok;
     };
     const int t = warp >> 2, r = tid & (kM - 1);
@@ -747,10 +747,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (__any_sync(0xffffffffu, bad)) {  // the rows of either CTA add them at the item's end
-            if (lane < 2)
-              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&sm.bad[t][item % kNotes], lane)),
-                           "r"(item + 1)
-                           : "memory");
+            if (lane == 0)
+              for (int to = 0; to < 2; ++to)
+                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&sm.bad[t][item % kNotes], to)),
+                             "r"(item + 1)
+                             : "memory");
             asm volatile("fence.acq_rel.cluster;" ::: "memory");
           }
           __syncwarp();
@@ -766,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();  // nothing of the pair is under way
   tc_fence_after();
   if (warp == kMmaWarp) {
-    mbar_wait(&sm.done, 0);  // (the second CTA's word of it)
+    mbar_wait<true>(&sm.done, 0);  // (the second CTA's word of it)
     __syncwarp();
     tmem_dealloc_pair(tmem, kTmemCols);
   }
