@@ -135,3 +135,16 @@ def test_stream_and_graph():
     torch.cuda.synchronize()
     want, _ = append(case, rows, gamma)
     assert torch.equal(cache[used], want[used]) and int(status.item()) == 0
+
+
+@pytest.mark.parametrize("size", [2.0 ** -126, 2.0 ** -128, 2.0 ** -131, 2.0 ** -133, 2.0 ** 126])
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -149, 2.0 ** -91, 2.0 ** -90])
+def test_rows_at_the_ends_of_bf16(size, eps):
+    """The smallest bf16 numbers, whose reciprocal root mean square passes fp32, and the largest."""
+    case = LatentCase([5], [40], 16)
+    rows = (torch.randn(5, ROW, generator=torch.Generator().manual_seed(2)).clamp(-3.5, 3.5) * size).to(torch.bfloat16).cuda()
+    assert bool((rows[:, :LATENT] != 0).any(1).all())
+    gamma = (1 + 0.2 * torch.randn(LATENT, generator=torch.Generator().manual_seed(3))).cuda()
+    got, status = append(case, rows, gamma, eps)
+    assert status == 0
+    check(case, rows, gamma, got, eps)
