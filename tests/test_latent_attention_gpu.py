@@ -352,3 +352,19 @@ def test_a_part_of_more_than_a_second():
     off = (lse[:, 0].double().cpu() - (40 + torch.log(count))).abs()
     # the score, its factor and the sum's logarithm: a few fp32 roundings of 60; the others: at most 2^30 e^-39
     assert bool((off < 60 * 8 * 2.0 ** -24 + 2.0 ** 30 * 1.2e-17).all())
+
+
+@pytest.mark.parametrize("n,lens,H", [([4, 6, 3], [2, 0, 50], 40), ([40, 9], [33, 300], 24), ([3, 1, 70], [1, 900, 60], 8)])
+@pytest.mark.parametrize("kind", ["causal", "full", "tree"])
+def test_queries_of_padding_tokens_have_no_influence(n, lens, H, kind):
+    """Tokens before position 0 hold anything: huge numbers, infinities, NaN.  Their rows stand in the same tiles, and in
+    the same warps, as those of tokens that see something."""
+    case, q = make(dict(n=n, lens=lens, H=H, page=16), seed=48)
+    mask = mask_of(trees(n, seed=2), 3) if kind == "tree" else None
+    want, wlse, _ = attend(case, q, kind == "causal", mask)
+    at = cumulative(n)
+    for junk in (3e38, float("inf"), float("nan")):
+        for b in range(case.B):
+            q[at[b]:at[b] + max(0, n[b] - lens[b])] = junk
+        out, lse, status = attend(case, q, kind == "causal", mask)
+        assert status == 0 and torch.equal(out, want) and torch.equal(lse, wlse)

@@ -224,3 +224,32 @@ def test_many_requests():
 
 def test_one_long_prompt_in_many_pieces():
     check(Prompts([700], [9000], 1, seed=72))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_queries_of_padding_tokens_have_no_influence(causal):
+    """Tokens before position 0 hold anything: huge numbers, infinities, NaN.  Their rows stand in the same warps as those of
+    tokens that see something."""
+    c = Prompts([50, 9, 300], [33, 0, 290], 3, seed=73)
+    want, wlse, _ = attend(c, causal)
+    at = cumulative(c.n)
+    for junk in (3e38, float("inf"), float("nan")):
+        for b in range(3):
+            c.q[at[b]:at[b] + max(0, c.n[b] - c.lens[b])] = junk
+        out, lse, status = attend(c, causal)
+        assert status == 0 and torch.equal(out, want) and torch.equal(lse, wlse)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_key_of_the_second_request(bad):
+    """Keys and values that its later tokens see: the earlier ones, and the first request, keep their bits."""
+    c = Prompts([200, 140], [300, 490], 2, seed=74)
+    want, wlse, _ = attend(c)
+    c.kv[700:710, 1] = bad                          # positions 400 .. 409: the second request's tokens from 50 on
+    out, lse, status = attend(c)
+    assert status == 0 and torch.equal(out[:250], want[:250]) and torch.equal(lse[:250], wlse[:250])
+    assert torch.equal(out[:, 0], want[:, 0]) and torch.equal(lse[:, 0], wlse[:, 0])
+    if bad != bad:
+        assert bool(torch.isnan(out[250:, 1]).all()) and bool(torch.isnan(lse[250:, 1]).all())
+    else:                                           # (scores of -infinity leave their own values' columns only)
+        assert not bool(torch.isfinite(out[250:, 1]).any())

@@ -374,3 +374,20 @@ def test_bits_do_not_depend_on_what_ran_before(D, cache):
         line = chunk(case, q, caches, scales, 40)
         want = want or (tree, line)
         assert torch.equal(tree, want[0]) and torch.equal(line, want[1]), f"after queries of {amplitude}"
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_queries_of_padding_tokens_have_no_influence(D, cache):
+    """Tokens before position 0 hold anything: huge numbers, infinities, NaN.  Their rows stand in the same warps as those of
+    nodes that see something."""
+    case, q = make(dict(n=[4, 6, 40], lens=[2, 0, 33], H=12, HKV=2, D=D, page=16), cache=cache, seed=69)
+    mask = mask_of(trees(case.n, seed=2), 2)
+    q = q.contiguous()
+    want, wlse, _ = attend(case, q, mask)
+    at = cumulative(case.n)
+    for junk in (3e38, float("inf"), float("nan")):
+        for b in range(case.B):
+            q[at[b]:at[b] + max(0, case.n[b] - case.lens[b])] = junk
+        out, lse, status = attend(case, q, mask)
+        assert status == 0 and torch.equal(out, want) and torch.equal(lse, wlse)
