@@ -473,7 +473,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (b < p.B) {
           r = load_request(p, b, false);
           if (r.n > 0) break;
-          ++b;
+          // (32 at a time: a million one by one would take longer than the others wait for a note)
+          const unsigned some = __ballot_sync(0xffffffffu, b + lane < p.B && load_request(p, b + lane, false).n > 0);
+          b += some ? __ffs(some) - 1 : 32;
         }
         h = tile = 0;
         tiles = (r.n + nodes - 1) / nodes;

@@ -391,3 +391,23 @@ def test_queries_of_padding_tokens_have_no_influence(D, cache):
             q[at[b]:at[b] + max(0, case.n[b] - case.lens[b])] = junk
         out, lse, status = attend(case, q, mask)
         assert status == 0 and torch.equal(out, want) and torch.equal(lse, wlse)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_millions_of_requests_without_nodes(cache):
+    """Between two that have some: no warp may give up on a note while they are passed over."""
+    B, page = 6_000_001, 16
+    case, q = make(dict(n=[5, 40], lens=[150, 300], H=12, HKV=2, D=128, page=page), cache=cache, seed=70)
+    mask = mask_of(trees(case.n), 2)
+    want, wlse, _ = attend(case, q, mask)
+    at = torch.zeros(B, dtype=torch.int64, device="cuda")
+    at[-1] = 1
+    n = torch.zeros(B, dtype=torch.int32, device="cuda")
+    n[0], n[-1] = case.n
+    cu = torch.cat([torch.zeros(1, dtype=torch.int32, device="cuda"), n.cumsum(0).to(torch.int32)])
+    lens = torch.where(n > 0, case.seq_lens[at], 0)
+    table = case.table[at].contiguous()
+    out, lse = torch.zeros_like(want), torch.zeros_like(wlse)
+    caches, scales = case.args()
+    status = kda.kda_tree_attention(out, q, *caches, cu, lens, table, mask, 40, **scales, lse=lse)
+    assert int(status.item()) == 0 and torch.equal(out, want) and torch.equal(lse, wlse)
