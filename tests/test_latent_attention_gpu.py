@@ -368,3 +368,28 @@ def test_queries_of_padding_tokens_have_no_influence(n, lens, H, kind):
             q[at[b]:at[b] + max(0, n[b] - lens[b])] = junk
         out, lse, status = attend(case, q, kind == "causal", mask)
         assert status == 0 and torch.equal(out, want) and torch.equal(lse, wlse)
+
+
+def test_infinities_of_many_small_requests():
+    """Each reaches the tokens of its own request that see it, whatever shares the kernel's memory with it."""
+    g = torch.Generator().manual_seed(49)
+    n = torch.randint(1, 7, (420,), generator=g).tolist()
+    lens = [k + int(x) for k, x in zip(n, torch.randint(0, 260, (420,), generator=g))]
+    case, q = make(dict(n=n, lens=lens, H=10, page=32), seed=49)
+    q[..., 300] = -(q[..., 300].abs() + 0.5)
+    want, wlse, _ = attend(case, q)
+    parts, hit, cu = [], torch.zeros(case.T, dtype=torch.bool, device="cuda"), cumulative(n)
+    for b in range(1, case.B, 3):
+        pos = lens[b] - n[b] + b % n[b]
+        case.cache[int(case.table[b, pos // 32]), pos % 32, 300] = float("inf")
+        see, rows = seen_by(n[b], lens[b]), case.dense(b)
+        hit[cu[b]:cu[b + 1]] = see[:, pos]
+        see[:, pos] = False
+        parts.append((softmax64(q[cu[b]:cu[b + 1]], rows[:, None], rows[:, None, :LATENT], see, SCALE), slice(cu[b], cu[b + 1])))
+    out, lse, status = attend(case, q)
+    assert status == 0 and torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], wlse[~hit])
+    assert bool(torch.isnan(out[hit][..., 300]).all())
+    for exact, at in parts:
+        x = out[at].clone()
+        x[hit[at], :, 300] = exact[0][hit[at], :, 300].to(torch.bfloat16)
+        close(x, lse[at], exact)
