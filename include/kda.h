@@ -389,8 +389,11 @@ kda_status kda_cache_read(kda_bf16* k_rows, kda_bf16* v_rows, const void* k_cach
  * are accumulated in fp32; the weights (over an e4m3 cache times v's scale) are
  * rounded for the product with V: to bf16, 2^-8 of each at most, or, for requests
  * with few rows over an e4m3 cache whose v scales are of one size, to f16, 2^-11 of
- * each or 2^-25 of the row's largest.  What a position beyond seq_lens[b] or
- * outside every token's window holds (not a number, an infinity) has no influence.
+ * each or 2^-25 of the row's largest.  (bf16 and its products end at 2^-133: values of
+ * an e4m3 cache below some 2^-110 lose bits.  The sum is divided by the weights' at the
+ * end: it may be infinite where the sum of a row's |v_j| passes 2^-8 of fp32's range.)  What a
+ * position beyond seq_lens[b] or outside every token's window holds (not a number, an
+ * infinity) has no influence.
  *
  *   out          [T, H, D] bf16, written.  Alignment 16 B.
  *   lse          [T, H] fp32, written, or NULL.
@@ -515,7 +518,8 @@ kda_status kda_latent_attention(kda_bf16* out, float* lse, const kda_bf16* q, co
                                 size_t workspace_bytes, int32_t* dev_status, void* stream);
 
 /* Bytes of device workspace kda_latent_attention needs for these sizes (0 when the sizes are
- * invalid).  Host-only, no CUDA call. */
+ * invalid; else some 40 MB: what it is needed for depends on the lengths, which the device
+ * knows).  Host-only, no CUDA call. */
 size_t kda_latent_attention_workspace_size(int B, int T, int H);
 
 /*

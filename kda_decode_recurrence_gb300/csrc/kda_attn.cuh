@@ -74,16 +74,16 @@ __device__ __forceinline__ int share_of(long long units, int ctas, long long u) 
 // Pieces in the workspace: per CTA a note of the item it begins but does not
 // finish, then per CTA and place kRows maxima and sums, then kRows x D outputs.
 struct PieceNote {
-  int row0;     // first row of the item's outputs: token * H + first head
-  int tokens;   // its tokens (0: this CTA begins no shared item)
-  int pieces;   // CTAs that share it
-  int pad;
+  int row0;     // first row of the item's outputs: token * H + first head (expanded: its first token)
+  int tokens;   // its tokens (absorbed: its rows; 0: this CTA begins no shared item)
+  int pieces;   // CTAs, pairs or streams that share it
+  int head;     // expanded: its head
 };
 
 struct Pieces {
   PieceNote* notes;
   float2* ml;   // [ctas][2][rows]: maximum (in units of log 2), sum
-  float* o;     // [ctas][2][rows][D]
+  float* o;     // [ctas][2][rows x D], a piece's in the order in which its kernel's threads hold them
 };
 
 inline size_t pieces_bytes(int ctas, int rows, int D) {

@@ -18,8 +18,8 @@
 // Streams take even shares of all key tiles; items that are cut are left in pieces for a second kernel.
 // O is rescaled only when a row's maximum has grown by more than 2^8.
 //
-// 2048 new tokens over 6001 before them, 96 heads: 637-665 us by box, 1.33-1.39 PFLOP/s of a cuBLAS product's
-// 1.74 held for long (the clock falls to 1.6 GHz under the power limit); 5 prompts of 33-1500, 16 heads: 53 us.
+// 2048 new tokens over 6001 before them, 96 heads: 640-673 us by box, 1.31-1.38 PFLOP/s of a cuBLAS product's
+// 1.74 held for long (the clock falls to 1.6 GHz under the power limit); 5 prompts of 33-1500, 16 heads: 54 us.
 // A slot's chain (S, a row's 128 exponentials, PV) is some 4000 cycles beside 1280 of its products, and two
 // of them overlap: tensor cores 57 % of active cycles, exponentials 23 %, issue 33 %.  Of the 4000: 240 until
 // S is in registers, 650 to its maximum, 1000 for the weights, 1600 until the next S.
@@ -784,7 +784,7 @@ __global__ void __launch_bounds__(128) expanded_join_kernel(const ExpandedArgs p
       o[e].w = fmaf(w, x[e].w, o[e].w * keep);
     }
   }
-  const size_t out_row = (size_t)(note.row0 + row) * p.H + note.pad;
+  const size_t out_row = (size_t)(note.row0 + row) * p.H + note.head;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint4* to = reinterpret_cast<uint4*>(p.out + out_row * D + 16 * cc);
 #pragma unroll

@@ -24,12 +24,12 @@
 // unfinished: its pieces are joined by a second kernel).  O is rescaled only when a row's
 // maximum has grown by more than 2^8.
 //
-// 128 tokens over 300-20000, 32 heads: 226-246 us by box, 5.5-6.0 TB/s of cache (239 beside 228 when warps without
-// a live row go through the softmax); 64 over 1000-8000, 96 heads: 80-82 us, 4.4 TB/s.
+// 128 tokens over 300-20000, 32 heads: 233-245 us by box, 5.5-5.8 TB/s of cache (on one box 239 beside 228 when warps
+// without a live row go through the softmax); 64 over 1000-8000, 96 heads: 81-82 us, 4.3-4.4 TB/s.
 // A key tile takes some 2900 cycles of a pair: 2176 of products, 150 of their issue, 570 of waits for copies,
 // since the rings hold one key tile; an item's ends some 10000 (O through registers, 64 rows a CTA), a call's
 // beginning 11000 and the join 7-10 us.  (76 x 6001 positions: tensor cores 60 % of active cycles, DRAM 69 %.)
-// 32 windows of 1-8 over 200-6000, 64 heads, pages of 16: 69 us, the copies of smaller boxes in a tile's chain.
+// 32 windows of 1-8 over 200-6000, 64 heads, pages of 16: 70 us, the copies of smaller boxes in a tile's chain.
 // Measured and left: copies in units of one key panel (296 us against 251 then), four more warps for half of
 // the output (an item's ends 8000, a tile 100-200 more: 255 us against 250), kItemCost of 4 to 6.
 #include <cuda.h>

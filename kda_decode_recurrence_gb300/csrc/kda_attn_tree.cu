@@ -2,7 +2,9 @@
 //
 // Heads of 128 have a kernel of pairs of CTAs (kda_attn_tree_pairs.cu).  Heads of 64 take the chunk kernel
 // with a mask of the new tokens that each of them sees: V would have 32 columns per CTA of a pair, half of
-// a swizzled row.
+// a swizzled row.  (32 trees of 8-60 nodes over 1000-8000, 32 / 8 heads of 64, bf16: 114 us; 16 of 4-32 over 500-12000,
+// 96 / 8, e4m3: 219 us; one of 13 over 517: 16 us.  DRAM 27 and 8 %, tensor cores 24 and 15 %, issue 36 and 46 %: a row
+// tile's chain bounds it, which takes as long as with heads of 128 for half of the products.)
 //
 // Trees of a few nodes take these too.  Their rows (nodes x query heads per key head) are mostly more
 // than the 16 up to which the window kernel wins over bf16, and everything before the tree is seen by

@@ -14,8 +14,8 @@
 //
 // Streams take even shares of all key tiles; items that are cut are left in pieces for a second kernel.
 //
-// 32 trees of 8-60 nodes over 1000-8000, 32 / 8 heads, bf16: 128-130 us, 4.4 TB/s of cache (the chunk kernel with
-// masks: 134); 16 of 4-32 over 500-12000, 96 / 8 heads, e4m3: 194 us (270); one of 13 nodes over 517: 16 us.
+// 32 trees of 8-60 nodes over 1000-8000, 32 / 8 heads, bf16: 130-133 us by box, 4.3-4.4 TB/s of cache (the chunk
+// kernel with masks: 134); 16 of 4-32 over 500-12000, 96 / 8 heads, e4m3: 196 us (270); one of 13 nodes over 517: 16 us.
 // A slot's chain (S, a row's 128 exponentials, PV) is some 4000 cycles of a key tile beside 1024 of its
 // products, and two of them overlap: 16 trees of 60 nodes over 4060: DRAM 54 %, tensor cores 49 %.  e4m3 adds two
 // products per pair of scores; without the codes' widening the 194 us would be 187, with one scale less 181-183.
