@@ -9,6 +9,8 @@
 // stream of items (request, up to 2 (128 / G) nodes, key head), key tiles of 128 positions, with
 // products of the pair (cta_group::2, M = 256, each CTA 128 rows, half of the keys for S and half of V's
 // columns for PV): S and P share tensor memory, one warp issues for both slots in turns.
+// P is in bf16 because V is, and a product takes one type: 2^-8 of a weight at most, as the output's own rounding
+// (errors against 64 bits 0.0019-0.0024, of outputs rounded once 0.0017).
 // Over e4m3 two warps a slot widen the codes to bf16 on the way (exactly), each CTA its half: a key's scale
 // multiplies its column of S, a value's its column of P before the rounding.
 //
