@@ -27,8 +27,8 @@
 // unfinished: its pieces are joined by a second kernel).  O is rescaled only when a row's
 // maximum has grown by more than 2^8.
 //
-// 128 tokens over 300-20000, 32 heads: 233-245 us by box, 5.5-5.8 TB/s of cache (on one box 239 beside 228 when warps
-// without a live row go through the softmax); 64 over 1000-8000, 96 heads: 81-82 us, 4.3-4.4 TB/s.
+// 128 tokens over 300-20000, 32 heads: 233-246 us by box, 5.5-5.8 TB/s of cache (on one box 239 beside 228 when warps
+// without a live row go through the softmax); 64 over 1000-8000, 96 heads: 81-83 us, 4.3-4.4 TB/s.
 // A key tile takes some 2900 cycles of a pair: 2176 of products, 150 of their issue, 570 of waits for copies,
 // since the rings hold one key tile; an item's ends some 10000 (O through registers, 64 rows a CTA), a call's
 // beginning 11000 and the join 7-10 us.  (76 x 6001 positions: tensor cores 60 % of active cycles, DRAM 69 %.)
